@@ -274,6 +274,106 @@ int specdec_verify_attention(const void* q, const void* k_cache, const void* v_c
                              size_t workspace_bytes, void* stream);
 
 /*
+ * An 8-bit key/value cache. A cache tensor (one for K, one for V) holds e4m3
+ * codes [B, Lmax, Hkv, D] and fp32 scales [B, Hkv, ceil(Lmax / 32)]: the
+ * value of row j of head h is code * scale[b][h][j / SPECDEC_KV8_BLOCK].
+ *
+ * specdec_kv8_append() quantises the bf16 keys and values of new positions
+ * into it:
+ *   k_new, v_new [B, n, Hkv, D]  bf16   row i of sequence b at element
+ *                                       (b * n + i) * stride (the strides are
+ *                                       multiples of 8, at least Hkv * D, so
+ *                                       a slice of a fused projection serves)
+ *   start        [B]   int32 (device)   the first cache row to write
+ *   counts       [B]   int32 (device)   rows to write, or NULL: n for all; a
+ *                                       sequence with a count <= 0 is skipped
+ *   rows         [B, n] int32 (device)  which rows of k_new and v_new to take,
+ *                                       in order, or NULL: 0, 1, 2, ... With
+ *                                       counts = n_accepted and rows =
+ *                                       out_nodes of specdec_verify_tree()
+ *                                       and start one past the root's row,
+ *                                       the accepted path's rows replace the
+ *                                       tree's. Only the first counts[b]
+ *                                       entries of row b are read.
+ *   k_cache, v_cache, k_scale, v_scale  as above; the codes of rows start ..
+ *                                       start + count - 1 and the scales of
+ *                                       their blocks are written
+ * A block's scale is 2^e with the smallest e in [-40, 40] such that its new
+ * rows' finite magnitudes are at most 448 * 2^e; magnitudes above that (and
+ * infinities) become +-448 codes and NaN stays NaN. When the block already
+ * holds rows before `start`, the scale is the larger of that and its own, and
+ * if that grows those rows' codes are encoded again (round to nearest even).
+ * Rows at and after start + count are left as they were: they are not part of
+ * the cache any more, so append drafts again after a rejection from the first
+ * rejected row. Both K and V, all blocks, in one kernel.
+ * A start or count outside the cache, or a count above n, sets
+ * SPECDEC_ERR_INVALID_ARG in the status word and skips that sequence; a rows
+ * entry outside [0, n) does the same for the block of 32 cache rows it would
+ * go to. Limits: D = 64, 128 or 256; Lmax <= 2^30; B * Lmax * Hkv * D < 2^40;
+ * B * Hkv * (n / 32 + 2) < 2^31; bf16 and code pointers 16-byte aligned. The sources and the caches must not overlap. Asynchronous; the
+ * workspace holds the status word only.
+ */
+#define SPECDEC_KV8_BLOCK 32
+size_t specdec_kv8_append_workspace_size(void);
+int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new, long long v_stride,
+                       const int32_t* start, const int32_t* counts, const int32_t* rows, int B,
+                       int n, int Hkv, int D, int Lmax, void* k_cache, void* v_cache,
+                       float* k_scale, float* v_scale, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Verify-step attention with a cap on the scores, a bias by distance, a
+ * sliding window and a token tree: over the 8-bit cache above
+ * (specdec_verify_attention_kv8) or a bf16 cache (.._masked). Arguments as
+ * specdec_verify_attention(), and:
+ *   q        [B, n_new, Hq, D]   bf16   position i of sequence b at element
+ *                                       (b * n_new + i) * q_stride (a multiple
+ *                                       of 8, at least Hq * D)
+ *   k_scale, v_scale                    of the 8-bit cache: positive, within
+ *                                       [2^-40, 2^40]
+ *   seq_lens [B]                 int32  (device) rows of the sequence with the
+ *                                       n_new new ones; 0 marks an unused slot
+ *                                       of the batch, whose output is 0
+ *   parent   [n_new] int32, HOST, or NULL: the new positions are the nodes of
+ *                                       a tree as in specdec_verify_tree();
+ *                                       a node sees the cached rows before
+ *                                       the new ones, its ancestors and
+ *                                       itself. NULL: a chain.
+ *   slopes   [Hq] fp32 (device) or NULL: the bias -slopes[h] * distance
+ *   softcap  > 0: scores become softcap * tanh(score / softcap); 0: none
+ *   window   > 0: a position sees distances 0 .. window - 1; 0: all
+ *   out      [B, n_new, Hq, D]   bf16
+ * Score of query i of head h on row j: scale * q . k_j (scale <= 0 selects
+ * 1/sqrt(D)), capped, then biased. Distance is the difference of positions:
+ * row j before the new ones stands at j, new position i at seq_lens[b] - n_new
+ * + i, or, in a tree, + the depth of node i. Rows that a position does not see
+ * never reach its output, whatever they hold. Softmax and sums in fp32; the
+ * probabilities enter the value product as f16 (kv8) or bf16 (masked).
+ * Limits: D = 64, 128 or 256, 1 <= n_new <= SPECDEC_MAX_TREE_NODES, Hq % Hkv
+ * == 0, n_new * Hq <= 2^20, B * n_new * Hq < 2^31, n_new <= Lmax <= 2^30,
+ * B * Lmax * Hkv * D < 2^40; q, caches and out 16-byte aligned. A length that is neither 0 nor within
+ * [n_new, Lmax] sets SPECDEC_ERR_INVALID_ARG in the status word and that
+ * sequence's output is 0. The workspace does not grow with B or Lmax.
+ * Asynchronous.
+ */
+size_t specdec_verify_attention_kv8_workspace_size(int B, int n_new, int Hq, int Hkv, int D,
+                                                   int Lmax);
+int specdec_verify_attention_kv8(const void* q, long long q_stride, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 const int32_t* seq_lens, const int32_t* parent,
+                                 const float* slopes, int B, int n_new, int Hq, int Hkv, int D,
+                                 int Lmax, float scale, float softcap, int window, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+size_t specdec_verify_attention_masked_workspace_size(int B, int n_new, int Hq, int Hkv, int D,
+                                                      int Lmax);
+int specdec_verify_attention_masked(const void* q, long long q_stride, const void* k_cache,
+                                    const void* v_cache, const int32_t* seq_lens,
+                                    const int32_t* parent, const float* slopes, int B, int n_new,
+                                    int Hq, int Hkv, int D, int Lmax, float scale, float softcap,
+                                    int window, void* out, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
  * The drafter's clustered LM head ("多詞元預測視覺化指南", section 高效嵌入器):
  * cluster logits y = h E^T, the top_k clusters of every row (largest y, ties
  * to the lower index), token logits z = h . W_r for the kept clusters'

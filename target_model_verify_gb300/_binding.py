@@ -22,6 +22,7 @@ SPECDEC_BF16 = 0
 SPECDEC_FP32 = 1
 SPECDEC_MAX_GAMMA = 32
 SPECDEC_MAX_TREE_NODES = 128
+SPECDEC_KV8_BLOCK = 32
 
 SPECDEC_OK = 0
 SPECDEC_ERR_INVALID_ARG = -1
@@ -35,6 +36,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _u64 = ctypes.c_uint64
+_ll = ctypes.c_longlong
 _sz = ctypes.c_size_t
 
 _CORE = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _u64, _i, _vp, _vp, _vp, _sz, _vp]
@@ -59,6 +61,15 @@ _SIGNATURES = {
     "specdec_verify_attention_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "specdec_verify_attention": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _vp,
                                       _sz, _vp]),
+    "specdec_kv8_append_workspace_size": (_sz, []),
+    "specdec_kv8_append": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp,
+                                _vp, _vp, _vp, _sz, _vp]),
+    "specdec_verify_attention_kv8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "specdec_verify_attention_kv8": (_i, [_vp, _ll] + [_vp] * 7 + [_i] * 6 + [_f, _f, _i, _vp, _vp,
+                                                                              _sz, _vp]),
+    "specdec_verify_attention_masked_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "specdec_verify_attention_masked": (_i, [_vp, _ll] + [_vp] * 5 + [_i] * 6 + [_f, _f, _i, _vp, _vp,
+                                                                                 _sz, _vp]),
     "specdec_shard_record_bytes": (_sz, [_i, _i]),
     "specdec_shard_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "specdec_shard_score": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp,
@@ -165,6 +176,32 @@ def specdec_verify_attention_workspace_size(B, n_new, Hq, Hkv, D, Lmax) -> int:
 
 def specdec_verify_attention(*args) -> int:
     return int(lib().specdec_verify_attention(*args))
+
+
+def specdec_kv8_append_workspace_size() -> int:
+    return int(lib().specdec_kv8_append_workspace_size())
+
+
+def specdec_kv8_append(*args) -> int:
+    return int(lib().specdec_kv8_append(*args))
+
+
+def specdec_verify_attention_kv8_workspace_size(B, n_new, Hq, Hkv, D, Lmax) -> int:
+    return int(lib().specdec_verify_attention_kv8_workspace_size(B, n_new, Hq, Hkv, D, Lmax))
+
+
+def specdec_verify_attention_kv8(*args) -> int:
+    """Attention over the 8-bit cache (the parent array is a host int32 array)."""
+    return int(lib().specdec_verify_attention_kv8(*args))
+
+
+def specdec_verify_attention_masked_workspace_size(B, n_new, Hq, Hkv, D, Lmax) -> int:
+    return int(lib().specdec_verify_attention_masked_workspace_size(B, n_new, Hq, Hkv, D, Lmax))
+
+
+def specdec_verify_attention_masked(*args) -> int:
+    """Masked attention over a bf16 cache (the parent array is a host int32 array)."""
+    return int(lib().specdec_verify_attention_masked(*args))
 
 
 def specdec_cluster_head_workspace_size(M, n_c, top_k, max_cluster) -> int:

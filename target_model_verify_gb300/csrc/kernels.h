@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -185,6 +186,56 @@ cudaError_t launch_attention(const AttnLaunch& A, const CUtensorMap& tmap_k,
                              const CUtensorMap& tmap_v, cudaStream_t stream);
 int attn_n_stages(int B, int n_new, int Hq, int Hkv);
 int attn_smem_bytes(int n_mt, int n_stages);
+
+// Verify-step attention with caps, biases, windows and token trees, over a
+// bf16 or an e4m3 cache (cache_attention.cuh).
+constexpr int kCacheAttnCtas = 304;  // CTAs at most: two per SM of a 152-SM part
+struct CacheAttnLaunch {
+  int B, n_new, Hq, Hkv, G, R, Lmax; // G = Hq / Hkv, R = n_new * G query rows per KV head
+  int n_groups, group_rows;          // the R rows in equal groups
+  int window;                        // a position sees distances below it (0: all)
+  int tree;                          // 1: anc and depth describe the new positions
+  int max_depth;                     // of the new positions (n_new - 1 for a chain)
+  int n_scale;                       // scales per (sequence, KV head)
+  float scale, cap, cap_exp;         // cap_exp = 2 log2(e) / cap
+  long long q_stride;                // elements from one position's queries to the next's
+  const __nv_bfloat16* q;            // [B, n_new, Hq, D]
+  const float* k_scale;              // [B, Hkv, n_scale] (e4m3 cache)
+  const float* v_scale;
+  const float* slopes;               // [Hq] or null
+  const int32_t* seq_lens;           // [B]
+  __nv_bfloat16* out;                // [B, n_new, Hq, D]
+  float* part_o;                     // [2 kCacheAttnCtas, rows, D]
+  float* part_ml;                    // [2 kCacheAttnCtas, rows, 2]
+  int* status;
+  uint32_t anc[SPECDEC_MAX_TREE_NODES][4];   // bit a of row i: node i sees node a
+  uint8_t depth[SPECDEC_MAX_TREE_NODES];
+};
+// Keys per TMA box, bytes per box row: what the tensor maps are encoded with.
+constexpr int cache_attn_block(bool e4m3, int D) { return e4m3 && D != 256 ? 128 : 64; }
+// Query rows per CTA at most: 64, or 32 at 256 dims.
+constexpr int cache_attn_max_rows(int D) { return D == 256 ? 32 : 64; }
+cudaError_t launch_cache_attention_kv8(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
+                                       const CUtensorMap& tmap_v, cudaStream_t stream);
+cudaError_t launch_cache_attention_bf16(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
+                                        const CUtensorMap& tmap_v, cudaStream_t stream);
+
+// Quantise new positions' keys and values into an e4m3 cache.
+struct Kv8AppendLaunch {
+  int B, n, Hkv, D, Lmax, n_scale, max_blocks;
+  const __nv_bfloat16* src[2];       // k_new, v_new [B, n, Hkv, D]
+  long long stride[2];               // elements from one position to the next
+  uint8_t* cache[2];                 // [B, Lmax, Hkv, D] e4m3
+  float* scale[2];                   // [B, Hkv, n_scale]
+  const int32_t* start;              // [B]
+  const int32_t* counts;             // [B] or null (n)
+  const int32_t* rows;               // [B, n] or null (0, 1, ...)
+  int* status;
+};
+cudaError_t launch_kv8_append(const Kv8AppendLaunch& A, cudaStream_t stream);
+
+// The driver's tensor-map encoder (null when the driver lacks it).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // The drafter's clustered LM head.
 struct ClusterLaunch {
