@@ -350,7 +350,7 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
  * never reach its output, whatever they hold. Softmax and sums in fp32; the
  * probabilities enter the value product as f16 (kv8) or bf16 (masked).
  * Limits: D = 64, 128 or 256, 1 <= n_new <= SPECDEC_MAX_TREE_NODES, Hq % Hkv
- * == 0, n_new * Hq <= 2^20, B * n_new * Hq < 2^31, n_new <= Lmax <= 2^30,
+ * == 0, Hq / Hkv <= 128, Hq <= 2^20, q_stride < 2^31, B * n_new * Hq < 2^31, n_new <= Lmax <= 2^30,
  * B * Lmax * Hkv * D < 2^40; q, caches and out 16-byte aligned. A length that is neither 0 nor within
  * [n_new, Lmax] sets SPECDEC_ERR_INVALID_ARG in the status word and that
  * sequence's output is 0. The workspace does not grow with B or Lmax.

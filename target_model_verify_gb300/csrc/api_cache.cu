@@ -18,7 +18,7 @@ int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
   if (B < 0 || n_new < 1 || n_new > SPECDEC_MAX_TREE_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
       !head_dim_ok(D) || Lmax < n_new || Lmax > (1 << 30))
     return SPECDEC_ERR_UNSUPPORTED;
-  if ((long long)n_new * Hq > (1 << 20)) return SPECDEC_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 128 || Hq > (1 << 20)) return SPECDEC_ERR_UNSUPPORTED;
   if ((__int128)B * Lmax * Hkv * D >= ((__int128)1 << 40)) return SPECDEC_ERR_UNSUPPORTED;
   // (sequence, KV head, row group) tiles are a grid dimension
   if ((long long)B * Hq * n_new >= (1ll << 31)) return SPECDEC_ERR_UNSUPPORTED;
@@ -26,20 +26,21 @@ int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
 }
 
 struct AttnPlan {
-  int n_groups, group_rows, tile_rows;
+  int n_groups, group_pos;
   size_t off_ml, off_o, total;
 };
 
-// Query rows of one KV head in equal groups; the partials of the tiles that
-// the CTAs share, two per CTA, whatever the batch and the lengths.
+// The new positions in equal groups of at most 128 query rows per KV head;
+// the partials of the tiles that the CTAs share, two per CTA, whatever the
+// batch and the lengths.
 AttnPlan make_plan(int n_new, int G, int D) {
   AttnPlan p;
-  const int R = n_new * G, most = cache_attn_max_rows(D);
-  p.n_groups = (R + most - 1) / most;
-  p.group_rows = (R + p.n_groups - 1) / p.n_groups;
-  p.tile_rows = p.group_rows <= 16 ? 16 : p.group_rows <= 32 ? 32 : 64;
+  const int most = 128 / G;
+  p.n_groups = (n_new + most - 1) / most;
+  p.group_pos = (n_new + p.n_groups - 1) / p.n_groups;
+  p.n_groups = (n_new + p.group_pos - 1) / p.group_pos;
   size_t off = align_up(sizeof(WsHeader));
-  const size_t rows = (size_t)2 * kCacheAttnCtas * p.tile_rows;
+  const size_t rows = (size_t)2 * kCacheAttnCtas * cache_attn_rows(p.group_pos * G);
   p.off_ml = off;
   off = align_up(off + rows * 2 * sizeof(float));
   p.off_o = off;
@@ -65,6 +66,21 @@ bool encode_cache(CUtensorMap* map, const void* base, bool e4m3, int B, int Lmax
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as a 4-D tensor {D, Hq, n_new, B}; box: 64 dims of a group's
+// rows of one KV head, positions past n_new read as zeros.
+bool encode_queries(CUtensorMap* map, const void* q, long long q_stride, int B, int n_new, int Hq, int G, int D,
+                    int group_pos) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)n_new, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2, (cuuint64_t)q_stride * 2 * n_new};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)group_pos, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache, const void* v_cache,
               const float* k_scale, const float* v_scale, const int32_t* seq_lens, const int32_t* parent,
               const float* slopes, int B, int n_new, int Hq, int Hkv, int D, int Lmax, float scale,
@@ -79,7 +95,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
     return SPECDEC_ERR_INVALID_ARG;
   if (((((uintptr_t)k_scale | (uintptr_t)v_scale | (uintptr_t)slopes | (uintptr_t)seq_lens)) & 3u) != 0)
     return SPECDEC_ERR_INVALID_ARG;
-  if (q_stride < (long long)Hq * D || q_stride % 8 != 0) return SPECDEC_ERR_INVALID_ARG;
+  if (q_stride < (long long)Hq * D || q_stride % 8 != 0 || q_stride >= (1ll << 31)) return SPECDEC_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
     return SPECDEC_ERR_INVALID_ARG;
   CacheAttnLaunch A;
@@ -109,10 +125,9 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.Hq = Hq;
   A.Hkv = Hkv;
   A.G = G;
-  A.R = n_new * G;
   A.Lmax = Lmax;
   A.n_groups = pl.n_groups;
-  A.group_rows = pl.group_rows;
+  A.group_pos = pl.group_pos;
   A.window = window;
   A.n_scale = (Lmax + SPECDEC_KV8_BLOCK - 1) / SPECDEC_KV8_BLOCK;
   A.scale = scale > 0.f ? scale : 1.f / std::sqrt((float)D);
@@ -120,6 +135,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.cap_exp = softcap > 0.f ? 2.f * kLog2e / softcap : 0.f;
   A.q_stride = q_stride;
   A.q = static_cast<const __nv_bfloat16*>(q);
+  A.v = v_cache;
   A.k_scale = k_scale;
   A.v_scale = v_scale;
   A.slopes = slopes;
@@ -128,12 +144,16 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.part_ml = reinterpret_cast<float*>(ws + pl.off_ml);
   A.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   A.status = reinterpret_cast<int*>(ws);
-  CUtensorMap tk, tv;
+  CUtensorMap tk, tv, tq;
   if (!encode_cache(&tk, k_cache, e4m3, B, Lmax, Hkv, D) || !encode_cache(&tv, v_cache, e4m3, B, Lmax, Hkv, D))
     return SPECDEC_ERR_CUDA;
+  if (e4m3)
+    tq = tk;                                   // not read: the kernel converts the queries itself
+  else if (!encode_queries(&tq, q, q_stride, B, n_new, Hq, G, D, pl.group_pos))
+    return SPECDEC_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  const cudaError_t e = e4m3 ? launch_cache_attention_kv8(A, D, tk, tv, stream)
-                             : launch_cache_attention_bf16(A, D, tk, tv, stream);
+  const cudaError_t e = e4m3 ? launch_cache_attention_kv8(A, D, tk, tv, tq, stream)
+                             : launch_cache_attention_bf16(A, D, tk, tv, tq, stream);
   return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 

@@ -6,35 +6,40 @@
 //   s_rj = cap * tanh(s_rj / cap)       when a cap is set
 //   x_rj = log2(e) * (s_rj - slope_h * (pos_i - pos_j))
 //   o_r  = sum_j 2^x_rj v_j / sum_j 2^x_rj   over the rows j that i sees
-// with one pass over the cache, the running maximum and sum of the softmax
-// in fp32. The scale of an e4m3 value block enters the exponent: with
-// y_rj = x_rj + log2(s_v), o = sum 2^(y - M) code_j / sum (2^(y - M) / s_v),
-// M the running maximum of y, so weights of every block share one range.
+// with one pass over the cache and the softmax statistics in fp32. The scale
+// of an e4m3 value block enters the exponent: with y_rj = x_rj + log2(s_v),
+// o = sum 2^(y - M) code_j / sum (2^(y - M) / s_v), M a reference near the
+// running maximum of y, so weights of every block share one range.
 //
-// Bound: HBM (each K and V row is read once per group of up to 64 query
-// rows; R = n_new * G query rows give 2 R flops per cache byte at 16 bits
-// and 4 R at 8).
+// Bound: HBM (each K and V row is read once per group of up to 128 query
+// rows).
 //
 // Schedule. The (sequence, KV head, row group) tiles, each a run of cache
 // blocks as long as its own sequence (or window), are laid end to end and
-// the run of blocks is cut into equal parts, one per CTA, on the device from
-// seq_lens, so ragged batches keep every SM busy to the end. A tile that
-// lies inside one part is finished by its CTA; the others leave (maximum,
-// sum, unnormalised output) partials that combine_kernel merges.
+// the run of blocks is cut into equal parts, one per CTA (one CTA per SM), on
+// the device from seq_lens, so ragged batches keep every SM busy to the end.
+// A tile that lies inside one part is finished by its CTA; the others leave
+// (maximum, sum, unnormalised output) partials that combine_kernel merges.
 //
-// CTA: one producer thread feeds a ring of slots, alternately a block of K
-// and a block of V (TMA boxes of up to 128 bytes x kBlk rows, swizzled);
-// four consumer warps each take a quarter of the block's keys for S = Q K^T,
-// exchange row maxima and the probabilities through shared memory, and each
-// take a quarter of the head's dims for O += P V. So every K and V byte is
-// read from shared memory (and, for e4m3, widened to f16) once per CTA
-// whatever the number of query rows, and the output needs no merge between
-// warps. Contractions are mma.sync m16n8k16 with fp32 accumulation, e4m3
-// codes widened to f16 (exact) in registers; queries enter as f16 scaled by
-// a power of two per row (exact down to 2^-28 of the row's maximum), so the
-// only rounding before the output is that of the probabilities: to f16 (11
-// bits) over an e4m3 cache, and to bf16 over a bf16 one, whose values need
-// its range.
+// CTA: warps 0-3 softmax, 4-7 auxiliary, 8 TMA producer, 9 tcgen05 issuer.
+//   S = Q K^T: tcgen05.mma, M = 128 query rows, N = a block of keys, into one
+//     of two tensor-memory buffers, a block ahead of the softmax. bf16:
+//     kind::f16. e4m3: kind::f8f6f4 on the codes as they lie; the query row,
+//     scaled by a power of two to below 256, is the sum of two e4m3 terms
+//     (4 + 4 significant bits hold a bf16 value exactly down to 2^-10 of the
+//     row's largest, and to 2^-18 of it below), so two products accumulate.
+//   softmax: lane = query row, so maxima and sums need no exchange. With
+//     R <= 64 query rows the 128 lanes hold 128 / RP copies of the rows (RP =
+//     32 or 64) and each copy takes its own share of every block's keys; its
+//     probabilities go to its share's columns of the P operand, whose other
+//     columns stay zero, so the copies are independent online softmaxes,
+//     merged once per tile. The reference M moves only when a row's maximum
+//     passes it by 2^8 (the exponents have that headroom), so the output in
+//     tensor memory is rarely rescaled.
+//   O += P V: P from tensor memory, V the MN-major operand, kind::f16. e4m3
+//     values are widened to f16 (exact) by the auxiliary warps into a second
+//     shared-memory tile, since P needs f16's 11 bits and both operands share
+//     a type; bf16 values are used as they land.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -46,35 +51,39 @@
 namespace specdec {
 namespace cache_attn {
 
-constexpr int kConsumers = 4;                  // warps that compute
-constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kSoftWarps = 4;
+constexpr int kAuxWarps = 4;
+constexpr int kProducer = 8, kIssuer = 9;     // warp indices
+constexpr int kThreads = 320;
 constexpr unsigned long long kDrainNs = 1000000000ull;
+constexpr float kHeadroom = 8.f;              // log2 by which a maximum may pass its reference
+constexpr int kSmemLimit = 227 * 1024;
 
-template <bool kE4m3, int kD, int kMt>
+template <bool kE4m3, int kD, int kRP>
 struct Shape {
   static constexpr int kElem = kE4m3 ? 1 : 2;
-  // keys per block: 16 KB of K at head dim 128 either way
-  static constexpr int kBlk = cache_attn_block(kE4m3, kD);
+  static constexpr int kBlk = cache_attn_block(kE4m3, kD);   // keys per block
   static constexpr int kRowBytes = kD * kElem;
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;   // one TMA box row
   static constexpr int kPanels = kRowBytes / kPanelBytes;
-  static constexpr int kSlotBytes = kBlk * kRowBytes;
-  static constexpr int kNt = kBlk / kConsumers / 8;       // key n-tiles per warp in Q K^T
-  static constexpr int kKs = kD / 16;                     // k steps of Q K^T
-  static constexpr int kDw = kD / kConsumers;             // dims per warp in P V
-  static constexpr int kNd = kDw / 8;                     // dim n-tiles per warp in P V
-  static constexpr int kKk = kBlk / 16;                   // k steps of P V
-  static constexpr int kRows = 16 * kMt;
-  static constexpr int kQBytes = kMt * kKs * 512;         // fragment order
-  static constexpr int kPBytes = kMt * kKk * 512;
-  // row tables: reduction [kRows][4], position, index, scale, slope; tree: 128 x (4 words + depth)
-  static constexpr int kTabBytes = kRows * 16 + 4 * kRows * 4 + 128 * 16 + 128 * 4;
-  static constexpr int kFixed = 1024 + kQBytes + kPBytes + kTabBytes + 256;
-  // two CTAs per SM (228 KB, 1 KB reserved each)
-  static constexpr int kSlots = (113 * 1024 - kFixed) / kSlotBytes < 8
-                                    ? (113 * 1024 - kFixed) / kSlotBytes : 8;
-  static constexpr int kSmem = kFixed + kSlots * kSlotBytes;
-  static_assert(kSlots >= 2, "a K and a V block must fit");
+  static constexpr int kSlotBytes = kBlk * kRowBytes;        // a block of K, or of V, as it lands
+  static constexpr int kCopies = 128 / kRP;                  // copies of the query rows
+  static constexpr int kKpl = kBlk / kCopies;                // keys per lane and block
+  static constexpr int kTerms = kE4m3 ? 2 : 1;
+  static constexpr int kQTerm = 128 * kRowBytes;             // 128 query rows in the K operand's type
+  static constexpr int kQBytes = kTerms * kQTerm;
+  static constexpr int kQBufs = kElem * kD >= (kE4m3 ? 128 : 512) ? 1 : 2;
+  static constexpr int kV16Bytes = kE4m3 ? kBlk * kD * 2 : 0;   // widened V, two of them
+  static constexpr int kStageBytes = kCopies > 1 ? 128 * 33 * 4 : 0;   // merge of the copies
+  static constexpr int kTabBytes = 2 * 128 * 4 + 128 * 8 + 128 * 16 + 128 * 4;  // q scales, (m, l), tree
+  static constexpr int kFixed = 1024 + 2 * kV16Bytes + kQBufs * kQBytes + kStageBytes + kTabBytes + 512;
+  static constexpr int kRingMax = (kSmemLimit - kFixed) / (2 * kSlotBytes);
+  static constexpr int kRing = kRingMax < 6 ? kRingMax : 6;  // K blocks (and V blocks) in flight
+  static constexpr int kSmem = kFixed + 2 * kRing * kSlotBytes;
+  static_assert(kRing >= 2, "two K and two V blocks must fit");
+  // tensor memory columns: two score buffers, the output, two P operands
+  static constexpr int kColS = 0, kColO = 2 * kBlk, kColP = kColO + kD;
+  static_assert(kColP + kBlk <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -90,57 +99,23 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void lds64(uint32_t a, uint32_t& x, uint32_t& y) {
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
-}
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-// d += a (16 x 16) b (16 x 8); f16 operands for an e4m3 cache, bf16 otherwise.
-template <bool kF16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  if constexpr (kF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 // Two e4m3 codes (16 bits) to two f16 values; every e4m3 value is an f16 value.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
@@ -148,9 +123,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
   return h;
 }
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = e4m3x2_to_f16x2((uint16_t)w);
-  hi = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+__device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+  return c;
 }
 template <bool kF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -175,6 +151,144 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   while (!mbar_try_wait(bar, parity))
     if (globaltimer() - t0 > kDrainNs) return false;
   return true;
+}
+
+// Shared-memory operand descriptor, swizzled rows of kPanel = 128 or 64
+// bytes in groups of 8. K-major: the k extent of one MMA lies inside a row.
+// MN-major (V): a row is one k, its bytes run along N; `lead` is the distance
+// to the next panel of N and 8 k rows follow every 8 * kPanel bytes.
+template <int kPanel>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)((8u * kPanel) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(kPanel == 128 ? 2 : 4) << 61;
+  return d;
+}
+// Instruction descriptor fields: D fp32; operand types (f16 0, bf16 1 under
+// kind::f16; e4m3 0 under kind::f8f6f4); B transposed (MN-major).
+__host__ __device__ constexpr uint32_t instr_desc(int type, bool b_mn, int N) {
+  return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | (b_mn ? 1u << 16 : 0u) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+// D (+)= A B^T with A and B in shared memory.
+template <bool kF8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (kF8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    tc_mma_bf16(d, a, b, idesc, acc);
+}
+// The same with A in tensor memory (f16 or bf16 pairs, one row per lane).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Tensor memory: each thread of a warp reads or writes consecutive 32-bit
+// columns of its lane. Loads return with the values there.
+template <int kN>
+struct Cols {};
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+      "}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
+        "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
+        "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+      : "r"(taddr + 0)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
+        "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
+        "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
+        "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
+        "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]),
+        "=r"(x[30]), "=r"(x[31])
+      : "r"(taddr + 0)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+      "}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
+        "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
+        "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
+        "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
+        "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]),
+        "=r"(x[30]), "=r"(x[31]), "=r"(x[32]), "=r"(x[33]), "=r"(x[34]), "=r"(x[35]),
+        "=r"(x[36]), "=r"(x[37]), "=r"(x[38]), "=r"(x[39]), "=r"(x[40]), "=r"(x[41]),
+        "=r"(x[42]), "=r"(x[43]), "=r"(x[44]), "=r"(x[45]), "=r"(x[46]), "=r"(x[47]),
+        "=r"(x[48]), "=r"(x[49]), "=r"(x[50]), "=r"(x[51]), "=r"(x[52]), "=r"(x[53]),
+        "=r"(x[54]), "=r"(x[55]), "=r"(x[56]), "=r"(x[57]), "=r"(x[58]), "=r"(x[59]),
+        "=r"(x[60]), "=r"(x[61]), "=r"(x[62]), "=r"(x[63])
+      : "r"(taddr + 0), "r"(taddr + 32)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Cols<8>) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8};"
+      ::"r"(taddr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+        "r"(x[6]), "r"(x[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Cols<16>) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+        "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]),
+        "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Cols<32>) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(taddr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+        "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]),
+        "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(x[16]), "r"(x[17]),
+        "r"(x[18]), "r"(x[19]), "r"(x[20]), "r"(x[21]), "r"(x[22]), "r"(x[23]),
+        "r"(x[24]), "r"(x[25]), "r"(x[26]), "r"(x[27]), "r"(x[28]), "r"(x[29]),
+        "r"(x[30]), "r"(x[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Cols<64>) {
+  tmem_store(taddr, x, Cols<32>{});
+  tmem_store(taddr + 32, x + 32, Cols<32>{});
+}
+__device__ __forceinline__ void tmem_wait_store() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // Blocks of kBlk cache rows that a sequence of L rows reads, and the first
@@ -286,37 +400,94 @@ struct Walk {
   }
 };
 
-template <bool kE4m3, int kD, int kMt, bool kExtra>
-__global__ void __launch_bounds__(kThreads, 2)
+// The visible rows among 32 of the cache, for one query row: the cached
+// prefix (rows below P0, bounded below by the window) and the new rows' own
+// mask, 128 bits from row P0 on.
+struct Sight {
+  int P0, low;            // first new row; lowest prefix row seen
+  uint32_t v[4];
+  __device__ __forceinline__ uint32_t word(int k) const {
+    return k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : k == 3 ? v[3] : 0u;
+  }
+  __device__ __forceinline__ uint32_t mask(int j) const {
+    const int p = P0 - j, lo = low - j;
+    uint32_t m = p <= 0 ? 0u : p >= 32 ? 0xffffffffu : (1u << p) - 1u;
+    if (lo > 0) m &= lo >= 32 ? 0u : 0xffffffffu << lo;
+    const int off = -p;
+    if (off > -32 && off < 128) {
+      if (off < 0)
+        m |= v[0] << -off;
+      else
+        m |= __funnelshift_r(word(off >> 5), word((off >> 5) + 1), off & 31);
+    }
+    return m;
+  }
+};
+
+template <bool kE4m3, int kD, int kRP, bool kExtra>
+__global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnLaunch A, const __grid_constant__ CUtensorMap tmap_k,
-                      const __grid_constant__ CUtensorMap tmap_v) {
-  using S = Shape<kE4m3, kD, kMt>;
-  constexpr int kBlk = S::kBlk, kNt = S::kNt, kNd = S::kNd;
+                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_q) {
+  using S = Shape<kE4m3, kD, kRP>;
+  constexpr int kBlk = S::kBlk, kKpl = S::kKpl, kR = S::kRing, kNq = S::kQBufs;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t slot0 = (raw + 1023u) & ~1023u;
-  const uint32_t qs = slot0 + S::kSlots * S::kSlotBytes;
-  const uint32_t ps = qs + S::kQBytes;
-  const uint32_t red = ps + S::kPBytes;                  // [kRows][4] fp32
-  const uint32_t tab = red + S::kRows * 16;              // pos, index, scale, slope: [kRows] each
-  const uint32_t tree = tab + 4 * S::kRows * 4;          // [128][4] ancestor words, then depth [128]
+  const uint32_t ring_k = (raw + 1023u) & ~1023u;
+  const uint32_t ring_v = ring_k + kR * S::kSlotBytes;
+  const uint32_t v16 = ring_v + kR * S::kSlotBytes;
+  const uint32_t qb = v16 + 2 * S::kV16Bytes;
+  const uint32_t stage = qb + kNq * S::kQBytes;
+  const uint32_t q_tab = stage + S::kStageBytes;           // query row scales [kNq][128]
+  const uint32_t ml_tab = q_tab + 2 * 128 * 4;             // (reference, sum) of every lane
+  const uint32_t tree = ml_tab + 128 * 8;                  // [128][4] ancestor words, then depth [128]
   const uint32_t bars = tree + 128 * 16 + 128 * 4;
-  auto full_bar = [&](int s) { return bars + 8u * (uint32_t)s; };
-  auto empty_bar = [&](int s) { return bars + 8u * (uint32_t)(S::kSlots + s); };
-  uint8_t* gen = smem_raw - raw;                         // generic address of a shared offset
-  volatile int* abort = reinterpret_cast<volatile int*>(gen + bars + 16 * S::kSlots);
-  volatile int* shared_b = abort + 1;
-  volatile long long* shared_u = reinterpret_cast<volatile long long*>(gen + bars + 16 * S::kSlots + 8);
+  auto k_full = [&](int s) { return bars + 8u * (uint32_t)s; };
+  auto k_empty = [&](int s) { return bars + 8u * (uint32_t)(kR + s); };
+  auto v_full = [&](int s) { return bars + 8u * (uint32_t)(2 * kR + s); };
+  auto v_empty = [&](int s) { return bars + 8u * (uint32_t)(3 * kR + s); };
+  auto v_clean = [&](int s) { return bars + 8u * (uint32_t)(4 * kR + s); };
+  const uint32_t bars2 = bars + 8u * 5 * kR;
+  auto s_full = [&](int s) { return bars2 + 8u * (uint32_t)s; };
+  auto p_full = [&](int s) { return bars2 + 8u * (uint32_t)(2 + s); };
+  auto q_full = [&](int s) { return bars2 + 8u * (uint32_t)(4 + s); };
+  auto q_empty = [&](int s) { return bars2 + 8u * (uint32_t)(6 + s); };
+  auto v16_full = [&](int s) { return bars2 + 8u * (uint32_t)(8 + s); };
+  auto v16_empty = [&](int s) { return bars2 + 8u * (uint32_t)(10 + s); };
+  // One per block parity: when a block's scores are there, the product two
+  // blocks back is done, so a wait for the one before it is never a phase off.
+  auto o_done = [&](int s) { return bars2 + 8u * (uint32_t)(12 + s); };
+  const uint32_t drained = bars2 + 8u * 14;
+  uint8_t* const words = smem_raw + (bars2 + 8u * 16 - raw);
+  volatile int* const abort = reinterpret_cast<volatile int*>(words);
+  volatile int* const odd = abort + 1;                     // a value that is no number was held back
+  volatile uint32_t* const tmem_slot = reinterpret_cast<volatile uint32_t*>(words) + 2;
+  volatile int* const shared_b = abort + 3;
+  volatile long long* const shared_u = reinterpret_cast<volatile long long*>(words + 16);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kSlots; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), kConsumers);
+    for (int s = 0; s < kR; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), kE4m3 ? kAuxWarps : 1 + kAuxWarps);   // bf16: the product reads it too
+      mbar_init(v_clean(s), kAuxWarps);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full(s), 1);
+      mbar_init(o_done(s), 1);
+      mbar_init(p_full(s), kSoftWarps);
+      mbar_init(q_full(s), kE4m3 ? kAuxWarps : 1);
+      mbar_init(q_empty(s), kE4m3 ? 1 + kSoftWarps : 1);
+      mbar_init(v16_full(s), kAuxWarps);
+      mbar_init(v16_empty(s), 1);
+    }
+    mbar_init(drained, 1);
     *abort = 0;
+    *odd = 0;
     fence_mbar_init();
   }
+  if (warp == kIssuer) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
   if (A.tree) {
     for (int e = threadIdx.x; e < A.n_new; e += kThreads) {
       sts128(tree + e * 16, A.anc[e][0], A.anc[e][1], A.anc[e][2], A.anc[e][3]);
@@ -340,557 +511,685 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (blockIdx.x == 0) *A.status = any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   Walk<kBlk> w;
   w.start(A, *shared_b, shared_u[0], shared_u[1], shared_u[2]);
   const long long part0 = shared_u[1];
+  // A warp's wait: all lanes agree on whether it ran out.
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, A.status));
+  };
+  // Whether every new position sees every row of block ib of the walk's tile.
+  auto is_clean = [&](const Walk<kBlk>& t, int ib) {
+    const int j0 = (t.first + t.blk + ib) * kBlk, P0 = t.L - A.n_new;
+    return j0 + kBlk <= P0 + 1 && (A.window <= 0 || j0 > P0 + A.max_depth - A.window);
+  };
+  uint32_t issued[3] = {0, 0, 0}, issued_phase[3] = {0, 0, 0};   // producer: K, V, Q copies in flight
 
-  uint32_t issued_mask = 0, issued_phase = 0;
-  if (warp == kConsumers) {
+  if (warp == kProducer) {
     // ---------------------------------------------------------- producer --
     if (lane == 0) {
       const uint64_t pol = policy_evict_first();
+      auto mark = [&](int what, int s, uint32_t ph) {
+        issued[what] |= 1u << s;
+        issued_phase[what] = (issued_phase[what] & ~(1u << s)) | (ph << s);
+      };
       int s = 0;
-      uint32_t ph = 0;
+      uint32_t ph = 0, nt = 0;
       bool ok = true;
-      for (; ok && !w.done(); w.next(A)) {
-        for (int i = 0; ok && i < 2 * w.n_here; ++i) {
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, abort, A.status)) {
-            ok = false;
-            break;
-          }
-          const int j0 = (w.first + w.blk + (i >> 1)) * kBlk;
-          mbar_arrive_expect_tx(full_bar(s), (uint32_t)S::kSlotBytes);
-          const uint32_t st = slot0 + (uint32_t)s * S::kSlotBytes;
+      for (; ok && !w.done(); w.next(A), ++nt) {
+        if constexpr (!kE4m3) {
+          // the tile's query rows, once per copy
+          const int qs = nt % kNq;
+          const uint32_t qph = (nt / kNq) & 1;
+          if (!(ok = mbar_wait(q_empty(qs), qph ^ 1u, abort, A.status))) break;
+          const uint32_t box = (uint32_t)(A.group_pos * A.G) * 128u;
+          mbar_arrive_expect_tx(q_full(qs), box * (kD / 64) * S::kCopies);
+          for (int c = 0; c < S::kCopies; ++c)
+            for (int p = 0; p < kD / 64; ++p)
+              tma_load_4d(qb + qs * S::kQBytes + p * 128 * 128 + c * kRP * 128, &tmap_q, q_full(qs), p * 64,
+                          w.h * A.G, w.g * A.group_pos, w.b, policy_evict_normal());
+          mark(2, qs, qph);
+        }
+        for (int i = 0; i < w.n_here; ++i) {
+          const int j0 = (w.first + w.blk + i) * kBlk;
+          if (!(ok = mbar_wait(k_empty(s), ph ^ 1u, abort, A.status))) break;
+          mbar_arrive_expect_tx(k_full(s), (uint32_t)S::kSlotBytes);
 #pragma unroll
           for (int p = 0; p < S::kPanels; ++p)
-            tma_load_4d(st + p * kBlk * S::kPanelBytes, (i & 1) ? &tmap_v : &tmap_k, full_bar(s),
+            tma_load_4d(ring_k + s * S::kSlotBytes + p * kBlk * S::kPanelBytes, &tmap_k, k_full(s),
                         p * (S::kPanelBytes / S::kElem), w.h, j0, w.b, pol);
-          issued_mask |= 1u << s;
-          issued_phase = (issued_phase & ~(1u << s)) | (ph << s);
-          if (++s == S::kSlots) {
+          mark(0, s, ph);
+          if (!(ok = mbar_wait(v_empty(s), ph ^ 1u, abort, A.status))) break;
+          mbar_arrive_expect_tx(v_full(s), (uint32_t)S::kSlotBytes);
+#pragma unroll
+          for (int p = 0; p < S::kPanels; ++p)
+            tma_load_4d(ring_v + s * S::kSlotBytes + p * kBlk * S::kPanelBytes, &tmap_v, v_full(s),
+                        p * (S::kPanelBytes / S::kElem), w.h, j0, w.b, pol);
+          mark(1, s, ph);
+          if (++s == kR) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
     }
-  } else {
-    // --------------------------------------------------------- consumers --
-    const int g = lane >> 2, t = lane & 3;
-    int s = 0;
-    uint32_t ph = 0;
-    bool dead = false;      // a wait ran out: keep to the barriers, compute nothing
-    auto advance = [&]() {
-      if (++s == S::kSlots) {
-        s = 0;
-        ph ^= 1u;
-      }
-    };
-    // Address of 16-byte chunk c of row r of a slot (the TMA swizzle: chunk
-    // index XOR the row inside 8 rows of 128 bytes, or 4 pairs of rows of 64).
-    auto chunk = [&](uint32_t base, int r, int c) {
-      constexpr int per = S::kPanelBytes / 16;
-      const int p = c / per, cc = c % per;
-      const int x = S::kPanelBytes == 128 ? (r & 7) : ((r >> 1) & 3);
-      return base + (uint32_t)(p * kBlk * S::kPanelBytes + r * S::kPanelBytes + ((cc ^ x) << 4));
-    };
-    for (; !w.done(); w.next(A)) {
-      const int P0 = w.L - A.n_new;              // cache row (and position) of the first new row
-      const int row_base = w.g * A.group_rows;
-      const int rows_here = min(A.group_rows, A.R - row_base);
-      // ---- queries into fragment order, with the rows' tables ----
-      constexpr int kCh = kD / 8;                // 16-byte chunks of a query row
-      for (int e = threadIdx.x; e < S::kRows * kCh; e += 32 * kConsumers) {
-        const int r = e / kCh, c = e % kCh;
-        uint4 val = make_uint4(0u, 0u, 0u, 0u);
-        int i = 0, gq = 0;
-        if (r < rows_here) {
-          i = (row_base + r) / A.G;
-          gq = (row_base + r) % A.G;
-          val = __ldg(reinterpret_cast<const uint4*>(A.q + ((size_t)w.b * A.n_new + i) * A.q_stride +
-                                                     (size_t)(w.h * A.G + gq) * kD + c * 8));
-        }
-        const uint32_t wv[4] = {val.x, val.y, val.z, val.w};
-        uint32_t out[4];
-        float q_scale = 1.f;
-        if constexpr (kE4m3) {
-          float f[8], amax = 0.f;
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ issuer --
+    if (lane == 0 && !w.done()) {
+      constexpr uint32_t id_qk = instr_desc(kE4m3 ? 0 : 1, false, kBlk);
+      constexpr uint32_t id_pv = instr_desc(kE4m3 ? 0 : 1, true, kD);
+      Walk<kBlk> wq = w;                 // the tile whose scores come next
+      int iq = 0, sq = 0;
+      uint32_t phq = 0, nq = 0, tq = 0;
+      auto issue_scores = [&]() {
+        const int qs = tq % kNq;
+        if (iq == 0 && !mbar_wait<true>(q_full(qs), (tq / kNq) & 1, abort, A.status)) return false;
+        if (!mbar_wait<true>(k_full(sq), phq, abort, A.status)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + S::kColS + (nq & 1) * kBlk;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[2 * k] = __uint_as_float(wv[k] << 16);
-            f[2 * k + 1] = __uint_as_float(wv[k] & 0xffff0000u);
+        for (int term = 0; term < S::kTerms; ++term)
+#pragma unroll
+          for (int p = 0; p < S::kPanels; ++p)
+#pragma unroll
+            for (int k = 0; k < S::kPanelBytes / 32; ++k)
+              mma_ss<kE4m3>(d,
+                            operand_desc<S::kPanelBytes>(qb + qs * S::kQBytes + term * S::kQTerm +
+                                                             p * 128 * S::kPanelBytes + k * 32, 16),
+                            operand_desc<S::kPanelBytes>(ring_k + sq * S::kSlotBytes +
+                                                             p * kBlk * S::kPanelBytes + k * 32, 16),
+                            id_qk, term + p + k > 0);
+        tc_commit(k_empty(sq));
+        tc_commit(s_full(nq & 1));
+        if (++sq == kR) {
+          sq = 0;
+          phq ^= 1u;
+        }
+        ++nq;
+        if (++iq == wq.n_here) {
+          tc_commit(q_empty(qs));
+          iq = 0;
+          ++tq;
+          wq.next(A);
+        }
+        return true;
+      };
+      bool ok = issue_scores();
+      int s = 0;
+      uint32_t ph = 0, n = 0, clean_ph = 0;
+      for (; ok && !w.done(); w.next(A))
+        for (int i = 0; i < w.n_here; ++i, ++n) {
+          // Scores run a block ahead. Into a new tile they do so only with a
+          // second query buffer: with one, they would wait for the refill.
+          const bool more = !wq.done(), early = more && (kNq == 2 || iq != 0);
+          if (early && !(ok = issue_scores())) break;
+          if (!(ok = mbar_wait<true>(p_full(n & 1), (n >> 1) & 1, abort, A.status))) break;
+          uint32_t vb;
+          if constexpr (kE4m3) {
+            vb = v16 + (n & 1) * S::kV16Bytes;
+            if (!(ok = mbar_wait<true>(v16_full(n & 1), (n >> 1) & 1, abort, A.status))) break;
+          } else {
+            vb = ring_v + s * S::kSlotBytes;
+            if (!(ok = mbar_wait<true>(v_full(s), ph, abort, A.status))) break;
+            if (!is_clean(w, i)) {
+              if (!(ok = mbar_wait<true>(v_clean(s), (clean_ph >> s) & 1, abort, A.status))) break;
+              clean_ph ^= 1u << s;
+            }
           }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kBlk / 16; ++k)
+            mma_ts(tmem + S::kColO, tmem + S::kColP + (n & 1) * (kBlk / 2) + k * 8,
+                   operand_desc<128>(vb + k * 2048, kBlk * 128), id_pv, i > 0 || k > 0);
+          tc_commit(kE4m3 ? v16_empty(n & 1) : v_empty(s));
+          tc_commit(o_done(n & 1));
+          if (more && !early && !(ok = issue_scores())) break;
+          if (++s == kR) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      // every product has to be done before the tensor memory is given back
+      tc_commit(drained);
+      wait_drain(drained, 0);
+    }
+  } else if (warp >= kSoftWarps) {
+    // --------------------------------------------------------- auxiliary --
+    const int at = threadIdx.x - 32 * kSoftWarps;      // 0 .. 127
+    bool ok = true;
+    if constexpr (kE4m3) {
+      Walk<kBlk> wl = w;                               // the tile whose queries come next
+      uint32_t tl = 0;
+      auto load_queries = [&]() {
+        const int qs = tl % kNq;
+        if (!warp_wait(q_empty(qs), ((tl / kNq) & 1) ^ 1u)) return false;
+        constexpr int kCh = kD / 8;                    // lanes per row, 8 dims each
+        const int pos0 = wl.g * A.group_pos;
+        const int rows = min(A.group_pos, A.n_new - pos0) * A.G;
+        for (int e = at; e < kRP * kCh; e += 32 * kAuxWarps) {
+          const int r = e / kCh, c = e % kCh;
+          uint4 val = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows)
+            val = __ldg(reinterpret_cast<const uint4*>(
+                A.q + ((size_t)wl.b * A.n_new + pos0 + r / A.G) * A.q_stride +
+                (size_t)(wl.h * A.G + r % A.G) * kD + c * 8));
+          const uint32_t wv[4] = {val.x, val.y, val.z, val.w};
+          float f[8], amax = 0.f;
+          bool fine = true;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float a = fabsf(f[k]);
-            if (a < INFINITY) amax = fmaxf(amax, a);
+            f[k] = __uint_as_float(k & 1 ? wv[k >> 1] & 0xffff0000u : wv[k >> 1] << 16);
+            amax = fmaxf(amax, fabsf(f[k]));
+            fine &= fabsf(f[k]) < INFINITY;
           }
-          // the row's kCh lanes are neighbours in the warp
 #pragma unroll
-          for (int o = kCh / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // amax -> [2^14, 2^15): the exponent field moves to 127 + 14
-          const int ex = (int)(__float_as_uint(amax) >> 23);
-          const int down = amax > 0.f ? min(max(ex - 141, -100), 113) : 0;
+          for (int o = kCh / 2; o; o >>= 1) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            fine &= __shfl_xor_sync(0xffffffffu, (int)fine, o) != 0;
+          }
+          // largest magnitude -> [2^7, 2^8); a row that holds no numbers is NaN
+          const int down = amax > 0.f && fine ? min(max((int)(__float_as_uint(amax) >> 23) - 134, -100), 120) : 0;
           const float mul = __uint_as_float((uint32_t)(127 - down) << 23);
-          q_scale = __uint_as_float((uint32_t)(127 + down) << 23);
+          uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) out[k] = pack2<true>(f[2 * k] * mul, f[2 * k + 1] * mul);
-        } else {
+          for (int k = 0; k < 2; ++k) {
+            uint32_t ph[2], pl[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) out[k] = wv[k];
-        }
-        const int mt = r >> 4, rr = r & 15;
-        const uint32_t hi_row = rr >= 8 ? 4u : 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // dims 8c + 2k, +1: step, lane column and word of the A fragment
-          int step, tt, word;
-          if constexpr (kE4m3) {
-            // lane column tt owns whole 16-byte code chunks (see the K loads)
-            const int cc = c >> 1;
-            const int ci = kD == 64 ? 0 : (cc & 1) + 2 * (cc >> 3);
-            tt = kD == 64 ? cc : (cc & 7) >> 1;
-            step = ci * 4 + (c & 1) * 2 + (k >> 1);
-            word = (k & 1) * 2;
-          } else {
-            step = c >> 1;
-            tt = k;
-            word = (c & 1) * 2;
-          }
-          sts32(qs + (uint32_t)((mt * S::kKs + step) * 32 + (rr & 7) * 4 + tt) * 16 + word * 4 + hi_row,
-                out[k]);
-        }
-        if (c == 0) {
-          const int dep = A.tree ? (int)lds32(tree + 128 * 16 + i * 4) : i;
-          sts32(tab + r * 4, (uint32_t)dep);
-          sts32(tab + S::kRows * 4 + r * 4, (uint32_t)i);
-          sts32(tab + 2 * S::kRows * 4 + r * 4, __float_as_uint(A.scale * q_scale));
-          if (kExtra)
-            sts32(tab + 3 * S::kRows * 4 + r * 4,
-                  __float_as_uint(A.slopes && r < rows_here ? A.slopes[w.h * A.G + gq] * kLog2e : 0.f));
-        }
-      }
-      named_bar_sync(1, 32 * kConsumers);
-
-      float m_run[kMt][2], l_run[kMt][2], o[kMt][kNd][4], cq[kMt][2];
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          m_run[mt][h] = -INFINITY;
-          l_run[mt][h] = 0.f;
-          cq[mt][h] = __uint_as_float(lds32(tab + 2 * S::kRows * 4 + (mt * 16 + g + 8 * h) * 4));
-        }
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-        for (int n = 0; n < kNd; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
-
-      // Whether row r of the group sees cache row j (j in [0, L) or beyond).
-      auto sees = [&](int r, int j) {
-        if (j >= w.L) return false;
-        const int dep = (int)lds32(tab + r * 4);
-        if (j < P0) return A.window <= 0 || P0 + dep - j < A.window;
-        const int a = j - P0, i = (int)lds32(tab + S::kRows * 4 + r * 4);
-        if (!A.tree) return a <= i && (A.window <= 0 || i - a < A.window);
-        if (!((lds32(tree + i * 16 + (a >> 5) * 4) >> (a & 31)) & 1u)) return false;
-        return A.window <= 0 || dep - (int)lds32(tree + 128 * 16 + a * 4) < A.window;
-      };
-
-      const int key_w = warp * (kBlk / kConsumers);      // this warp's first key in a block
-      const float* ksp = nullptr;
-      const float* vsp = nullptr;
-      float sk_next = 1.f, sv_next = 1.f;
-      auto load_scales = [&](int j) {                    // of the 32-row block that holds row j
-        if constexpr (kE4m3) {
-          if (j < w.L) {
-            sk_next = __ldg(ksp + j / SPECDEC_KV8_BLOCK);
-            sv_next = __ldg(vsp + j / SPECDEC_KV8_BLOCK);
-          } else {
-            sk_next = sv_next = 1.f;
-          }
-        }
-      };
-      if constexpr (kE4m3) {
-        const size_t so = ((size_t)w.b * A.Hkv + w.h) * A.n_scale;
-        ksp = A.k_scale + so;
-        vsp = A.v_scale + so;
-      }
-      load_scales((w.first + w.blk) * kBlk + key_w);
-
-      for (int ib = 0; ib < w.n_here; ++ib) {
-        const int j0 = (w.first + w.blk + ib) * kBlk;
-        const float sk = sk_next, sv = sv_next;
-        if (ib + 1 < w.n_here) load_scales(j0 + kBlk + key_w);
-        const bool clean = j0 + kBlk <= P0 + 1 &&
-                           (A.window <= 0 || j0 > P0 + A.max_depth - A.window);
-        // ---- S = Q K^T over this warp's keys ----
-        float sc[kMt][kNt][4];
-#pragma unroll
-        for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-          for (int n = 0; n < kNt; ++n) sc[mt][n][0] = sc[mt][n][1] = sc[mt][n][2] = sc[mt][n][3] = 0.f;
-        if (!dead && !mbar_wait(full_bar(s), ph, abort, A.status)) dead = true;
-        if (!dead) {
-          const uint32_t kb = slot0 + (uint32_t)s * S::kSlotBytes;
-          if constexpr (kE4m3) {
-            // Lane (g, t) takes key g of every n-tile, and of it whole 16-byte
-            // chunks: 2t, 2t + 1 of every 128-byte panel (t at 64 dims). The
-            // dims of a k step are spread over the lanes accordingly, alike
-            // for Q; eight lanes of a load phase then hit all 32 banks.
-#pragma unroll
-            for (int ci = 0; ci < kD / 64; ++ci) {
-              uint4 kw[kNt];
-#pragma unroll
-              for (int n = 0; n < kNt; ++n)
-                kw[n] = lds128(chunk(kb, key_w + n * 8 + g,
-                                     kD == 64 ? t : 2 * t + (ci & 1) + 8 * (ci >> 1)));
-#pragma unroll
-              for (int k4 = 0; k4 < 4; ++k4) {
-                uint4 a[kMt];
-#pragma unroll
-                for (int mt = 0; mt < kMt; ++mt)
-                  a[mt] = lds128(qs + (uint32_t)((mt * S::kKs + ci * 4 + k4) * 32 + lane) * 16);
-#pragma unroll
-                for (int n = 0; n < kNt; ++n) {
-                  const uint32_t word = k4 == 0 ? kw[n].x : k4 == 1 ? kw[n].y : k4 == 2 ? kw[n].z : kw[n].w;
-                  uint32_t b0, b1;
-                  widen4(word, b0, b1);
-#pragma unroll
-                  for (int mt = 0; mt < kMt; ++mt) mma16816<true>(sc[mt][n], a[mt], b0, b1);
-                }
-              }
+            for (int x = 0; x < 2; ++x) {
+              const float a = f[4 * k + 2 * x] * mul, b = f[4 * k + 2 * x + 1] * mul;
+              ph[x] = f32_to_e4m3x2(a, b);
+              const uint32_t back = e4m3x2_to_f16x2((uint16_t)ph[x]);
+              const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&back));
+              pl[x] = f32_to_e4m3x2(a - r2.x, b - r2.y);
             }
-          } else {
-#pragma unroll
-            for (int ks = 0; ks < S::kKs; ++ks) {
-              uint4 a[kMt];
-#pragma unroll
-              for (int mt = 0; mt < kMt; ++mt)
-                a[mt] = lds128(qs + (uint32_t)((mt * S::kKs + ks) * 32 + lane) * 16);
-#pragma unroll
-              for (int n = 0; n < kNt; n += 2) {
-                uint32_t r[4];
-                ldsm_x4(chunk(kb, key_w + n * 8 + (lane & 7) + ((lane >> 4) << 3),
-                              ks * 2 + ((lane >> 3) & 1)), r);
-#pragma unroll
-                for (int mt = 0; mt < kMt; ++mt) {
-                  mma16816<false>(sc[mt][n], a[mt], r[0], r[1]);
-                  mma16816<false>(sc[mt][n + 1], a[mt], r[2], r[3]);
-                }
-              }
-            }
+            hi[k] = ph[0] | (ph[1] << 16);
+            lo[k] = pl[0] | (pl[1] << 16);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty_bar(s));
+          const int d0 = c * 8, p = d0 / S::kPanelBytes, cc = (d0 % S::kPanelBytes) / 16;
+#pragma unroll
+          for (int copy = 0; copy < S::kCopies; ++copy) {
+            const int rr = copy * kRP + r;
+            const int x = S::kPanelBytes == 128 ? (rr & 7) : ((rr >> 1) & 3);
+            const uint32_t dst = qb + qs * S::kQBytes + p * 128 * S::kPanelBytes + rr * S::kPanelBytes +
+                                 ((cc ^ x) << 4) + (d0 & 8);
+            sts64(dst, hi[0], hi[1]);
+            sts64(dst + S::kQTerm, lo[0], lo[1]);
+          }
+          if (c == 0)
+            sts32(q_tab + (qs * 128 + r) * 4,
+                  fine ? (uint32_t)(127 + down) << 23 : 0x7fffffffu);
         }
-        advance();
-
-        // ---- exponents, masks, row maxima ----
-        const float lv = kE4m3 ? __log2f(sv) : 0.f;
-        const float inv_sv = kE4m3 ? rcp(sv) : 1.f;
-        float bmax[kMt][2];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(qs));
+        ++tl;
+        wl.next(A);
+        return true;
+      };
+      for (int k = 0; k < kNq; ++k)
+        if (ok && !wl.done()) ok = load_queries();
+      int s = 0;
+      uint32_t ph = 0, n = 0;
+      for (; ok && !w.done(); w.next(A)) {
+        for (int i = 0; i < w.n_here; ++i, ++n) {
+          const bool clean = is_clean(w, i);
+          const int j0 = (w.first + w.blk + i) * kBlk;
+          if (!(ok = warp_wait(v_full(s), ph))) break;
+          if (!(ok = warp_wait(v16_empty(n & 1), ((n >> 1) & 1) ^ 1u))) break;
+          // A warp takes 8 keys x 4 chunks of 16 codes at a time: rows p and
+          // p ^ 5 side by side keep both the reads and the writes free of
+          // bank conflicts under their swizzles.
+          const uint32_t src = ring_v + s * S::kSlotBytes, dst = v16 + (n & 1) * S::kV16Bytes;
+          const int pr = lane >> 3, row8 = (lane & 4) ? pr ^ 5 : pr;
+          constexpr int kQuads = kD / 64;
+#pragma unroll 4
+          for (int e = warp - kSoftWarps; e < kBlk / 8 * kQuads; e += kAuxWarps) {
+            const int j = (e / kQuads) * 8 + row8, c = (e % kQuads) * 4 + (lane & 3);
+            constexpr int per = S::kPanelBytes / 16;
+            const int x = S::kPanelBytes == 128 ? (j & 7) : ((j >> 1) & 3);
+            const uint4 v = lds128(src + (c / per) * kBlk * S::kPanelBytes + j * S::kPanelBytes +
+                                   (((c % per) ^ x) << 4));
+            const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[8];
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = mt * 16 + g + 8 * h;
-            float m = -INFINITY;
-            if constexpr (kExtra) {
-              const float ck = cq[mt][h] * sk;
-              const float slope = __uint_as_float(lds32(tab + 3 * S::kRows * 4 + r * 4));
-              const int dep = (int)lds32(tab + r * 4);
-#pragma unroll
-              for (int n = 0; n < kNt; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float y = sc[mt][n][2 * h + e] * ck;
-                  // cap * tanh(y / cap) = cap * (1 - 2 / (1 + e^(2 y / cap)))
-                  if (A.cap > 0.f) y = A.cap * (1.f - 2.f * rcp(1.f + ex2(y * A.cap_exp)));
-                  int pj = j0 + key_w + n * 8 + 2 * t + e;
-                  if (A.tree && pj >= P0 && pj < w.L) pj = P0 + (int)lds32(tree + 128 * 16 + (pj - P0) * 4);
-                  y = fmaf(y, kLog2e, lv) - slope * (float)(P0 + dep - pj);
-                  sc[mt][n][2 * h + e] = y;
-                }
-            } else {
-              const float ck = cq[mt][h] * sk * kLog2e;
-#pragma unroll
-              for (int n = 0; n < kNt; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) sc[mt][n][2 * h + e] = fmaf(sc[mt][n][2 * h + e], ck, lv);
+            for (int k = 0; k < 4; ++k) {
+              h[2 * k] = e4m3x2_to_f16x2((uint16_t)wv[k]);
+              h[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(wv[k] >> 16));
             }
             if (!clean) {
+              // Rows past the sequence hold anything, and a NaN in a row that
+              // not every query sees would pass a zero probability: neither
+              // enters the product. The epilogue adds the NaN where seen.
 #pragma unroll
-              for (int n = 0; n < kNt; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (!sees(r, j0 + key_w + n * 8 + 2 * t + e)) sc[mt][n][2 * h + e] = -INFINITY;
-            }
-#pragma unroll
-            for (int n = 0; n < kNt; ++n) m = fmaxf(m, fmaxf(sc[mt][n][2 * h], sc[mt][n][2 * h + 1]));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            bmax[mt][h] = m;
-            if (t == 0) sts32(red + r * 16 + warp * 4, __float_as_uint(m));
-          }
-        named_bar_sync(1, 32 * kConsumers);
-
-        // ---- probabilities to shared memory, in fragment order ----
-        bool moved = false;
-        float alpha[kMt][2];
-#pragma unroll
-        for (int mt = 0; mt < kMt; ++mt) {
-          float mu[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 m4 = lds128(red + (mt * 16 + g + 8 * h) * 16);
-            const float m_new =
-                fmaxf(fmaxf(m_run[mt][h], fmaxf(__uint_as_float(m4.x), __uint_as_float(m4.y))),
-                      fmaxf(__uint_as_float(m4.z), __uint_as_float(m4.w)));
-            mu[h] = m_new == -INFINITY ? 0.f : m_new;          // nothing seen yet
-            alpha[mt][h] = ex2(m_run[mt][h] - mu[h]);
-            m_run[mt][h] = m_new;
-            moved |= alpha[mt][h] != 1.f;
-            // f16 probabilities fill the range up to 2^15: small weights keep their bits
-            if constexpr (kE4m3) mu[h] -= 15.f;
-          }
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int n = 0; n < kNt; n += 2) {
-            uint32_t pk[4];                    // rows g, g + 8 of n-tile n, then of n + 1
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float lo = ex2(sc[mt][n + (x >> 1)][(x & 1) * 2] - mu[x & 1]);
-              const float hi = ex2(sc[mt][n + (x >> 1)][(x & 1) * 2 + 1] - mu[x & 1]);
-              pk[x] = pack2<kE4m3>(lo, hi);
-              // The sum takes bf16 weights as rounded: their error then moves
-              // the output by w (v - o) only. The f16 rounding is left out of it.
-              const float sum = kE4m3 ? lo + hi
-                                      : __uint_as_float(pk[x] << 16) + __uint_as_float(pk[x] & 0xffff0000u);
-              if (x & 1) sum1 += sum; else sum0 += sum;
-            }
-            sts128(ps + (uint32_t)(((key_w / 16 + n / 2) * kMt + mt) * 32 + lane) * 16, pk[0], pk[1], pk[2], pk[3]);
-          }
-          l_run[mt][0] = fmaf(l_run[mt][0], alpha[mt][0], sum0 * inv_sv);
-          l_run[mt][1] = fmaf(l_run[mt][1], alpha[mt][1], sum1 * inv_sv);
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-          for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-            for (int n = 0; n < kNd; ++n) {
-              o[mt][n][0] *= alpha[mt][0];
-              o[mt][n][1] *= alpha[mt][0];
-              o[mt][n][2] *= alpha[mt][1];
-              o[mt][n][3] *= alpha[mt][1];
-            }
-        }
-        named_bar_sync(1, 32 * kConsumers);
-
-        // ---- O += P V over this warp's dims ----
-        if (!dead && !mbar_wait(full_bar(s), ph, abort, A.status)) dead = true;
-        if (!dead) {
-          const uint32_t vb = slot0 + (uint32_t)s * S::kSlotBytes;
-          // Rows past the sequence hold anything and a row that not every
-          // query sees may hold an infinity or a NaN, which a zero
-          // probability would not silence: both are kept out of the product.
-          uint32_t odd = 0;
-          auto guard = [&](uint32_t v, int j) {          // values of rows j (low half) and j + 1
-            constexpr uint32_t ex = kE4m3 ? 0x7c00u : 0x7f80u;
-            if (j >= w.L) v &= 0xffff0000u;
-            if (j + 1 >= w.L) v &= 0x0000ffffu;
-            if ((v & ex) == ex) {
-              v &= 0xffff0000u;
-              odd = 1;
-            }
-            if ((v & (ex << 16)) == (ex << 16)) {
-              v &= 0x0000ffffu;
-              odd = 1;
-            }
-            return v;
-          };
-#pragma unroll
-          for (int kk = 0; kk < S::kKk; ++kk) {
-            uint4 a[kMt];
-#pragma unroll
-            for (int mt = 0; mt < kMt; ++mt)
-              a[mt] = lds128(ps + (uint32_t)((kk * kMt + mt) * 32 + lane) * 16);
-            uint32_t b0[kNd], b1[kNd];
-            if constexpr (kE4m3) {
-              // Lane (g, t): kNd neighbouring dims of keys 2t, 2t + 1 and
-              // 8 further; bytes of the two keys pair up into f16x2.
-              const int d0 = warp * S::kDw + g * kNd;
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const int r0 = kk * 16 + hf * 8 + 2 * t;
-                uint32_t x[2], y[2];
-                const uint32_t a0 = chunk(vb, r0, d0 >> 4) + (d0 & 15);
-                const uint32_t a1 = chunk(vb, r0 + 1, d0 >> 4) + (d0 & 15);
-                if constexpr (kNd == 8) {
-                  lds64(a0, x[0], x[1]);
-                  lds64(a1, y[0], y[1]);
-                } else if constexpr (kNd == 4) {
-                  x[0] = lds32(a0);
-                  y[0] = lds32(a1);
-                } else {
-                  x[0] = lds16(a0);
-                  y[0] = lds16(a1);
+              for (int k = 0; k < 8; ++k) {
+                if (j0 + j >= w.L) h[k] = 0u;
+                if ((h[k] & 0x7c00u) == 0x7c00u) {
+                  h[k] &= 0xffff0000u;
+                  *odd = 1;
                 }
-                uint32_t(&b)[kNd] = hf ? b1 : b0;
-#pragma unroll
-                for (int q4 = 0; q4 < (kNd + 3) / 4; ++q4) {
-                  widen4(__byte_perm(x[q4], y[q4], 0x5140), b[q4 * 4], b[q4 * 4 + 1]);
-                  if constexpr (kNd >= 4)
-                    widen4(__byte_perm(x[q4], y[q4], 0x7362), b[q4 * 4 + 2], b[q4 * 4 + 3]);
+                if ((h[k] & 0x7c000000u) == 0x7c000000u) {
+                  h[k] &= 0x0000ffffu;
+                  *odd = 1;
                 }
               }
-            } else {
-#pragma unroll
-              for (int n = 0; n < kNd; n += 2) {
-                uint32_t r[4];
-                ldsm_x4_t(chunk(vb, kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3),
-                                warp * (S::kDw / 8) + n + (lane >> 4)), r);
-                b0[n] = r[0];
-                b1[n] = r[1];
-                b0[n + 1] = r[2];
-                b1[n + 1] = r[3];
-              }
             }
-            if (!clean) {
-#pragma unroll
-              for (int n = 0; n < kNd; ++n) {
-                b0[n] = guard(b0[n], j0 + kk * 16 + 2 * t);
-                b1[n] = guard(b1[n], j0 + kk * 16 + 8 + 2 * t);
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < kNd; ++n)
-#pragma unroll
-              for (int mt = 0; mt < kMt; ++mt) mma16816<kE4m3>(o[mt][n], a[mt], b0[n], b1[n]);
+            const uint32_t to = dst + (c >> 2) * kBlk * 128 + j * 128;
+            const int c2 = (2 * c) & 7;
+            sts128(to + ((c2 ^ (j & 7)) << 4), h[0], h[1], h[2], h[3]);
+            sts128(to + (((c2 + 1) ^ (j & 7)) << 4), h[4], h[5], h[6], h[7]);
           }
-          if (!clean && __any_sync(0xffffffffu, odd)) {
-            // Rare: the infinities and NaN left out above, for the rows that see them.
-            for (int key = 0; key < kBlk && j0 + key < w.L; ++key) {
-#pragma unroll
-              for (int n = 0; n < kNd; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int d = kE4m3 ? warp * S::kDw + (2 * t + e) * kNd + n
-                                      : warp * S::kDw + n * 8 + 2 * t + e;
-                  const int byte = d * S::kElem;
-                  const uint32_t at = chunk(vb, key, byte >> 4) + (byte & 15);
-                  float v;
-                  bool is_odd;
-                  if constexpr (kE4m3) {
-                    is_odd = (lds8(at) & 0x7fu) == 0x7fu;
-                    v = __uint_as_float(0x7fffffffu);
-                  } else {
-                    const uint32_t u = lds16(at);
-                    is_odd = (u & 0x7f80u) == 0x7f80u;
-                    v = __uint_as_float(u << 16);
-                  }
-                  if (!is_odd) continue;
-#pragma unroll
-                  for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                      const int r = mt * 16 + g + 8 * h;
-                      if (r >= rows_here || !sees(r, j0 + key)) continue;
-                      const uint32_t pu =
-                          lds16(ps + (uint32_t)(((key >> 4) * kMt + mt) * 32 + g * 4 + ((key & 7) >> 1)) * 16 +
-                                (h + ((key >> 3) & 1) * 2) * 4 + (key & 1) * 2);
-                      const float pv = kE4m3 ? __half2float(__ushort_as_half((unsigned short)pu))
-                                             : __uint_as_float(pu << 16);
-                      o[mt][n][2 * h + e] += pv * v;
-                    }
-                }
-            }
-          }
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(empty_bar(s));
+          if (lane == 0) {
+            mbar_arrive(v_empty(s));
+            mbar_arrive(v16_full(n & 1));
+          }
+          if (++s == kR) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        advance();
+        if (ok && !wl.done()) ok = load_queries();
       }
-
-      // ---- the tile's sums over the warps, then the output or a partial ----
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          l_run[mt][h] += __shfl_xor_sync(0xffffffffu, l_run[mt][h], 1);
-          l_run[mt][h] += __shfl_xor_sync(0xffffffffu, l_run[mt][h], 2);
-          if (t == 0) sts32(red + (mt * 16 + g + 8 * h) * 16 + warp * 4, __float_as_uint(l_run[mt][h]));
-        }
-      named_bar_sync(1, 32 * kConsumers);
-      const bool whole = w.blk == 0 && w.n_here == w.nb;
-      const size_t slot = (size_t)blockIdx.x * 2 + (w.u == part0 ? 0 : 1);
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = mt * 16 + g + 8 * h;
-          if (r >= rows_here || dead) continue;
-          const uint4 l4 = lds128(red + r * 16);
-          const float l = (__uint_as_float(l4.x) + __uint_as_float(l4.y)) +
-                          (__uint_as_float(l4.z) + __uint_as_float(l4.w));
-          if (whole) {
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
-            const int i = (row_base + r) / A.G, gq = (row_base + r) % A.G;
-            __nv_bfloat16* dst =
-                A.out + (((size_t)w.b * A.n_new + i) * A.Hq + (size_t)w.h * A.G + gq) * kD + warp * S::kDw;
-            if constexpr (kE4m3) {
-              // dims (2t) kNd .. (2t + 2) kNd - 1 are this lane's
-              uint32_t pk[kNd];
-#pragma unroll
-              for (int n = 0; n < kNd; n += 2) {
-                pk[n / 2] = pack2<false>(o[mt][n][2 * h] * inv, o[mt][n + 1][2 * h] * inv);
-                pk[kNd / 2 + n / 2] = pack2<false>(o[mt][n][2 * h + 1] * inv, o[mt][n + 1][2 * h + 1] * inv);
+    } else {
+      // bf16 values are multiplied as they land; only blocks with rows that
+      // not every query sees are gone over first (see above).
+      int s = 0;
+      uint32_t ph = 0;
+      for (; ok && !w.done(); w.next(A))
+        for (int i = 0; i < w.n_here; ++i) {
+          // every block is waited for, and released, so that this loop and the
+          // ring never part by more than the ring's length
+          if (!(ok = warp_wait(v_full(s), ph))) break;
+          if (!is_clean(w, i)) {
+            const int j0 = (w.first + w.blk + i) * kBlk;
+            for (int e = at; e < S::kSlotBytes / 16; e += 32 * kAuxWarps) {
+              const int j = (e >> 3) % kBlk;
+              const uint32_t a = ring_v + s * S::kSlotBytes + e * 16;
+              uint4 v = lds128(a);
+              uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+              bool put = false;
+              if (j0 + j >= w.L) {
+                wv[0] = wv[1] = wv[2] = wv[3] = 0u;
+                put = true;
               }
-              uint32_t* d32 = reinterpret_cast<uint32_t*>(dst + 2 * t * kNd);
-              if constexpr (kNd >= 4) {
 #pragma unroll
-                for (int n = 0; n < kNd; n += 4)
-                  *reinterpret_cast<uint4*>(d32 + n) = make_uint4(pk[n], pk[n + 1], pk[n + 2], pk[n + 3]);
-              } else {
-                *reinterpret_cast<uint2*>(d32) = make_uint2(pk[0], pk[1]);
+              for (int k = 0; k < 4; ++k) {
+                if ((wv[k] & 0x7f80u) == 0x7f80u) {
+                  wv[k] &= 0xffff0000u;
+                  put = true;
+                  *odd = 1;
+                }
+                if ((wv[k] & 0x7f800000u) == 0x7f800000u) {
+                  wv[k] &= 0x0000ffffu;
+                  put = true;
+                  *odd = 1;
+                }
               }
-            } else {
-#pragma unroll
-              for (int n = 0; n < kNd; ++n)
-                *reinterpret_cast<uint32_t*>(dst + n * 8 + 2 * t) =
-                    pack2<false>(o[mt][n][2 * h] * inv, o[mt][n][2 * h + 1] * inv);
+              if (put) sts128(a, wv[0], wv[1], wv[2], wv[3]);
             }
-          } else {
-            float* po = A.part_o + (slot * S::kRows + r) * kD + warp * S::kDw;
-#pragma unroll
-            for (int n = 0; n < kNd; ++n) {
-              if constexpr (kE4m3) {
-                po[2 * t * kNd + n] = o[mt][n][2 * h];
-                po[(2 * t + 1) * kNd + n] = o[mt][n][2 * h + 1];
-              } else {
-                *reinterpret_cast<float2*>(po + n * 8 + 2 * t) = make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
-              }
-            }
-            if (warp == 0 && t == 0)
-              *reinterpret_cast<float2*>(A.part_ml + (slot * S::kRows + r) * 2) = make_float2(m_run[mt][h], l);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_clean(s));
+          }
+          if (lane == 0) mbar_arrive(v_empty(s));
+          if (++s == kR) {
+            s = 0;
+            ph ^= 1u;
           }
         }
     }
+  } else {
+    // ----------------------------------------------------------- softmax --
+    const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);      // this warp's lanes
+    const int row = (warp * 32 + lane) % kRP, copy = warp * 32 / kRP;
+    constexpr int kSub = kKpl > 32 ? kKpl / 32 : 1;                // 32-row pieces of a lane's keys
+    constexpr int kSubKeys = kKpl / kSub;
+    bool dead = false;                   // a wait ran out: keep to the barriers, compute nothing
+    uint32_t n = 0, nt = 0;
+    if constexpr (S::kCopies > 1) {
+      const uint32_t zero[32] = {};
+#pragma unroll
+      for (int c = 0; c < kBlk; c += 32) tmem_store(tl + S::kColP + c, zero, Cols<32>{});
+      tmem_wait_store();
+    }
+    for (; !w.done(); w.next(A), ++nt) {
+      const int P0 = w.L - A.n_new, pos0 = w.g * A.group_pos;
+      const int rows_here = min(A.group_pos, A.n_new - pos0) * A.G;
+      const bool mine = row < rows_here;
+      const int idx = mine ? pos0 + row / A.G : 0, gq = mine ? row % A.G : 0;
+      const int dep = A.tree ? (int)lds32(tree + 128 * 16 + idx * 4) : idx;
+      Sight sight;
+      sight.P0 = P0;
+      sight.low = A.window > 0 ? P0 + dep - A.window + 1 : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (A.tree) {
+          sight.v[k] = lds32(tree + idx * 16 + k * 4);
+        } else {
+          const int top = idx - 32 * k, low = A.window > 0 ? idx - A.window + 1 - 32 * k : 0;
+          uint32_t m = top < 0 ? 0u : top >= 31 ? 0xffffffffu : (2u << top) - 1u;
+          if (low > 0) m &= low >= 32 ? 0u : 0xffffffffu << low;
+          sight.v[k] = m;
+        }
+      }
+      if (A.tree && A.window > 0 && A.window <= A.max_depth) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          for (int a = 0; a < 32 && 32 * k + a < A.n_new; ++a)
+            if (dep - (int)lds32(tree + 128 * 16 + (32 * k + a) * 4) >= A.window) sight.v[k] &= ~(1u << a);
+      }
+      float ck = A.scale;
+      if constexpr (kE4m3) {
+        const int qs = nt % kNq;
+        if (!dead && !warp_wait(q_full(qs), (nt / kNq) & 1)) dead = true;
+        ck *= __uint_as_float(lds32(q_tab + (qs * 128 + row) * 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty(qs));
+      }
+      if (!kExtra) ck *= kLog2e;
+      const float slope = kExtra && A.slopes ? A.slopes[w.h * A.G + gq] * kLog2e : 0.f;
+
+      float m_ref = -INFINITY, l = 0.f;
+      const int key0 = copy * kKpl;                                // this copy's first key of a block
+      float sk_next[kSub], sv_next[kSub];
+      auto load_scales = [&](int j) {
+        if constexpr (kE4m3) {
+          const size_t so = ((size_t)w.b * A.Hkv + w.h) * A.n_scale;
+#pragma unroll
+          for (int x = 0; x < kSub; ++x) {
+            const int jj = j + x * kSubKeys;
+            sk_next[x] = jj < w.L ? __ldg(A.k_scale + so + jj / SPECDEC_KV8_BLOCK) : 1.f;
+            sv_next[x] = jj < w.L ? __ldg(A.v_scale + so + jj / SPECDEC_KV8_BLOCK) : 1.f;
+          }
+        }
+      };
+      load_scales((w.first + w.blk) * kBlk + key0);
+
+      for (int ib = 0; ib < w.n_here; ++ib, ++n) {
+        const int j0 = (w.first + w.blk + ib) * kBlk + key0;
+        const bool clean = is_clean(w, ib);
+        float sk[kSub], sv[kSub];
+        if constexpr (kE4m3) {
+#pragma unroll
+          for (int x = 0; x < kSub; ++x) {
+            sk[x] = sk_next[x];
+            sv[x] = sv_next[x];
+          }
+          if (ib + 1 < w.n_here) load_scales(j0 + kBlk);
+        }
+        if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
+        if (dead) continue;
+        tc_fence_after();
+        // ---- this lane's scores, as exponents ----
+        union {
+          uint32_t u[kKpl];
+          float f[kKpl];
+        } x;
+        {
+          const uint32_t from = tl + S::kColS + (n & 1) * kBlk + key0;
+          if constexpr (kKpl == 128) {
+            tmem_load(from, *reinterpret_cast<uint32_t(*)[64]>(&x.u[0]));
+            tmem_load(from + 64, *reinterpret_cast<uint32_t(*)[64]>(&x.u[64]));
+          } else {
+            tmem_load(from, x.u);
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          float* const y = x.f + sub * kSubKeys;
+          const float lv = kE4m3 ? __log2f(sv[sub]) : 0.f;
+          const float c = kE4m3 ? ck * sk[sub] : ck;
+          const int js = j0 + sub * kSubKeys;
+          if constexpr (kExtra) {
+#pragma unroll
+            for (int k = 0; k < kSubKeys; ++k) {
+              float z = y[k] * c;
+              // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
+              if (A.cap > 0.f) z = A.cap * (1.f - 2.f * rcp(1.f + ex2(z * A.cap_exp)));
+              y[k] = fmaf(z, kLog2e, lv);
+            }
+            if (A.slopes) {
+              // bias slope * (pos_j - pos_i); tree nodes stand at their depth
+              const float base = (float)(js - P0 - dep);
+              if (clean || !A.tree) {
+#pragma unroll
+                for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(slope, base + (float)k, y[k]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < kSubKeys; ++k) {
+                  int pj = js + k - P0;
+                  if (pj >= 0) pj = (int)lds32(tree + 128 * 16 + min(pj, A.n_new - 1) * 4);
+                  y[k] = fmaf(slope, (float)(pj - dep), y[k]);
+                }
+              }
+            }
+          } else if constexpr (kE4m3) {
+#pragma unroll
+            for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(y[k], c, lv);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kSubKeys; ++k) y[k] *= c;
+          }
+          if (!clean) {
+            const uint32_t m = sight.mask(js);
+#pragma unroll
+            for (int k = 0; k < kSubKeys; ++k) y[k] = (m >> k) & 1u ? y[k] : -INFINITY;
+          }
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < kSubKeys; ++k) t4[k & 3] = fmaxf(t4[k & 3], y[k]);
+          top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+        }
+        // ---- the reference follows the maximum when it has to ----
+        const bool need = mine && top > m_ref + kHeadroom;
+        if (__any_sync(0xffffffffu, need)) {
+          const float to = need ? top : m_ref;
+          const float alpha = need ? ex2(m_ref - to) : 1.f;
+          l *= alpha;
+          m_ref = to;
+          if (ib > 0) {
+            if (!warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) {
+              dead = true;
+              continue;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kD; c += 32) {
+              uint32_t v[32];
+              tmem_load(tl + S::kColO + c, v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+              tmem_store(tl + S::kColO + c, v, Cols<32>{});
+            }
+            tmem_wait_store();
+          }
+        }
+        // ---- probabilities ----
+        // f16 ones are kept 2^7 high: the headroom's 2^8 above that still fits,
+        // and small weights stay normal numbers down to 2^-21.
+        const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - (kE4m3 ? 7.f : 0.f);
+        uint32_t pk[kKpl / 2];
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < kSubKeys; k += 2) {
+            const float p0 = ex2(x.f[sub * kSubKeys + k] - mu), p1 = ex2(x.f[sub * kSubKeys + k + 1] - mu);
+            const uint32_t u = pack2<kE4m3>(p0, p1);
+            pk[(sub * kSubKeys + k) / 2] = u;
+            // The sum takes bf16 weights as rounded: their error then moves
+            // the output by w (v - o) only. The f16 rounding is left out of it.
+            if constexpr (kE4m3) {
+              sum[0] += p0;
+              sum[1] += p1;
+            } else {
+              sum[0] += __uint_as_float(u << 16);
+              sum[1] += __uint_as_float(u & 0xffff0000u);
+            }
+          }
+          if constexpr (kE4m3)
+            l = fmaf(sum[0] + sum[1], rcp(sv[sub]), l);
+          else
+            l += sum[0] + sum[1];
+        }
+        tmem_store(tl + S::kColP + (n & 1) * (kBlk / 2) + key0 / 2, pk, Cols<kKpl / 2>{});
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(n & 1));
+      }
+
+      // ---- the tile's output, or this part's share of it ----
+      if (!dead && !warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
+      tc_fence_after();
+      const bool whole = w.blk == 0 && w.n_here == w.nb;
+      const size_t slot = (size_t)blockIdx.x * 2 + (w.u == part0 ? 0 : 1);
+      // Infinities and NaN that were held back from the product (rare), for
+      // the rows that see them.
+      auto add_odd = [&](float (&v)[32], int c0) {
+        for (int ib = 0; ib < w.n_here; ++ib) {
+          if (is_clean(w, ib)) continue;
+          const int j0 = (w.first + w.blk + ib) * kBlk + key0;
+          for (int k = 0; k < kKpl && j0 + k < w.L; ++k) {
+            const bool seen = mine && (sight.mask(j0 + k) & 1u);
+            const size_t from = (((size_t)w.b * A.Lmax + j0 + k) * A.Hkv + w.h) * kD + c0;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              float val;
+              if constexpr (kE4m3) {
+                const uint8_t code = static_cast<const uint8_t*>(A.v)[from + c];
+                val = (code & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : 0.f;
+              } else {
+                const uint32_t u = static_cast<const uint16_t*>(A.v)[from + c];
+                val = (u & 0x7f80u) == 0x7f80u ? __uint_as_float(u << 16) : 0.f;
+              }
+              if (seen && val != 0.f) v[c] += val;
+            }
+          }
+        }
+      };
+      const bool has_odd = *odd != 0;
+      if constexpr (S::kCopies == 1) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);       // NaN stays
+        const size_t at_row =
+            (((size_t)w.b * A.n_new + idx) * A.Hq + (size_t)w.h * A.G + gq) * kD;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kD; c0 += 32) {
+          if (dead) break;
+          uint32_t u[32];
+          tmem_load(tl + S::kColO + c0, u);
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
+          if (has_odd) add_odd(v, c0);
+          if (!mine) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(A.out + at_row + c0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(pack2<false>(v[8 * k] * inv, v[8 * k + 1] * inv),
+                                  pack2<false>(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                                  pack2<false>(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                                  pack2<false>(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(A.part_o + (slot * kRP + row) * kD + c0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+        }
+        if (!whole && mine && !dead)
+          *reinterpret_cast<float2*>(A.part_ml + (slot * kRP + row) * 2) = make_float2(m_ref, l);
+      } else {
+        // Merge the copies through shared memory, 32 columns at a time.
+        const int lg = warp * 32 + lane;
+        sts64(ml_tab + lg * 8, __float_as_uint(m_ref), __float_as_uint(l));
+        named_bar_sync(1, 32 * kSoftWarps);
+        float M = -INFINITY, lt = 0.f;
+#pragma unroll
+        for (int c = 0; c < S::kCopies; ++c)
+          M = fmaxf(M, __uint_as_float(lds32(ml_tab + (c * kRP + row) * 8)));
+        const float Mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int c = 0; c < S::kCopies; ++c)
+          lt += __uint_as_float(lds32(ml_tab + (c * kRP + row) * 8 + 4)) *
+                ex2(__uint_as_float(lds32(ml_tab + (c * kRP + row) * 8)) - Mu);
+        const float wgt = ex2(m_ref - Mu);
+        const float inv = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);
+        constexpr int kPer = 32 / S::kCopies;                    // columns a thread sums
+        const size_t at_row =
+            (((size_t)w.b * A.n_new + idx) * A.Hq + (size_t)w.h * A.G + gq) * kD;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kD; c0 += 32) {
+          if (!dead) {
+            uint32_t u[32];
+            tmem_load(tl + S::kColO + c0, u);
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
+            if (has_odd) add_odd(v, c0);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sts32(stage + (lg * 33 + k) * 4, __float_as_uint(v[k] * wgt));
+          }
+          named_bar_sync(1, 32 * kSoftWarps);
+          // thread (row, copy) sums columns copy * kPer ..
+          float v[kPer];
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            v[k] = 0.f;
+#pragma unroll
+            for (int c = 0; c < S::kCopies; ++c)
+              v[k] += __uint_as_float(lds32(stage + ((c * kRP + row) * 33 + copy * kPer + k) * 4));
+          }
+          if (mine && !dead) {
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(A.out + at_row + c0 + copy * kPer);
+#pragma unroll
+              for (int k = 0; k < kPer / 8; ++k)
+                dst[k] = make_uint4(pack2<false>(v[8 * k] * inv, v[8 * k + 1] * inv),
+                                    pack2<false>(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                                    pack2<false>(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                                    pack2<false>(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+            } else {
+              float4* dst =
+                  reinterpret_cast<float4*>(A.part_o + (slot * kRP + row) * kD + c0 + copy * kPer);
+#pragma unroll
+              for (int k = 0; k < kPer / 4; ++k)
+                dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+          named_bar_sync(1, 32 * kSoftWarps);
+        }
+        if (!whole && mine && !dead && copy == 0)
+          *reinterpret_cast<float2*>(A.part_ml + (slot * kRP + row) * 2) = make_float2(M, lt);
+      }
+    }
   }
+  tc_fence_before();
   __syncthreads();   // every role has left its loop
-  if (*abort && warp == kConsumers && lane == 0)
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
+  if (*abort && warp == kProducer && lane == 0)
     // A wait gave up: let every copy already issued land before the CTA exits.
-    for (int s = 0; s < S::kSlots; ++s)
-      if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u);
+    for (int s = 0; s < kR; ++s) {
+      if (issued[0] & (1u << s)) wait_drain(k_full(s), (issued_phase[0] >> s) & 1u);
+      if (issued[1] & (1u << s)) wait_drain(v_full(s), (issued_phase[1] >> s) & 1u);
+      if (!kE4m3 && s < kNq && (issued[2] & (1u << s))) wait_drain(q_full(s), (issued_phase[2] >> s) & 1u);
+    }
 }
 
 // Merges the partials of the tiles that more than one CTA worked on, and
 // zeroes the outputs of sequences without blocks. One warp per query row:
 // blockIdx.x = tile, blockIdx.y * 8 + warp = row of its group.
-template <bool kE4m3, int kD, int kMt>
+template <bool kE4m3, int kD, int kRP>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CacheAttnLaunch A, int n_ctas) {
-  using S = Shape<kE4m3, kD, kMt>;
+  constexpr int kBlk = cache_attn_block(kE4m3, kD);
   __shared__ long long sh_before[8], sh_total[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x;
@@ -902,7 +1201,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
   for (int x = threadIdx.x; x < A.B; x += 256) {
     int first;
     bool bad;
-    const int nb = seq_blocks<S::kBlk>(A, A.seq_lens[x], first, bad);
+    const int nb = seq_blocks<kBlk>(A, A.seq_lens[x], first, bad);
     total += nb;
     if (x < b) before += nb;
   }
@@ -924,16 +1223,17 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
   }
   int first;
   bool bad;
-  const int nb = seq_blocks<S::kBlk>(A, A.seq_lens[b], first, bad);
+  const int nb = seq_blocks<kBlk>(A, A.seq_lens[b], first, bad);
   const long long per = (long long)A.Hkv * A.n_groups;
   total *= per;
   const long long u0 = before * per + (long long)(h * A.n_groups + grp) * nb;
+  const int pos0 = grp * A.group_pos;
   const int r = blockIdx.y * 8 + warp;
-  const int rr = grp * A.group_rows + r;
-  if (r >= A.group_rows || rr >= A.R) return;
+  if (r >= min(A.group_pos, A.n_new - pos0) * A.G) return;
   constexpr int kPer = kD / 32;
-  __nv_bfloat16* dst =
-      A.out + (((size_t)b * A.n_new + rr / A.G) * A.Hq + (size_t)h * A.G + rr % A.G) * kD + lane * kPer;
+  __nv_bfloat16* dst = A.out +
+                       (((size_t)b * A.n_new + pos0 + r / A.G) * A.Hq + (size_t)h * A.G + r % A.G) * kD +
+                       lane * kPer;
   float acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
@@ -948,7 +1248,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
       const long long pb = part_begin(total, c, n_ctas);
       if (pb == part_begin(total, c + 1, n_ctas)) continue;
       const size_t slot = (size_t)c * 2 + (c == c0 && pb != u0 ? 1 : 0);
-      M = fmaxf(M, A.part_ml[(slot * S::kRows + r) * 2]);
+      M = fmaxf(M, A.part_ml[(slot * kRP + r) * 2]);
     }
     M = warp_max(M);
     const float mu = M == -INFINITY ? 0.f : M;
@@ -958,10 +1258,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
       const long long pb = part_begin(total, c, n_ctas);
       if (pb == part_begin(total, c + 1, n_ctas)) continue;
       const size_t slot = (size_t)c * 2 + (c == c0 && pb != u0 ? 1 : 0);
-      const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + (slot * S::kRows + r) * 2);
+      const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + (slot * kRP + r) * 2);
       const float wgt = ex2(ml.x - mu);
       l += ml.y * wgt;
-      const float* po = A.part_o + (slot * S::kRows + r) * kD + lane * kPer;
+      const float* po = A.part_o + (slot * kRP + r) * kD + lane * kPer;
 #pragma unroll
       for (int k = 0; k < kPer; k += 2) {
         const float2 v = *reinterpret_cast<const float2*>(po + k);
@@ -976,16 +1276,16 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
     *reinterpret_cast<uint32_t*>(dst + k) = pack2<false>(acc[k] * inv, acc[k + 1] * inv);
 }
 
-template <bool kE4m3, int kD, int kMt, bool kExtra>
+template <bool kE4m3, int kD, int kRP, bool kExtra>
 cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CUtensorMap& tv,
-                       cudaStream_t stream) {
-  using S = Shape<kE4m3, kD, kMt>;
+                       const CUtensorMap& tq, cudaStream_t stream) {
+  using S = Shape<kE4m3, kD, kRP>;
   static std::atomic<int> smem_set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !smem_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(cache_attn_kernel<kE4m3, kD, kMt, kExtra>,
+    e = cudaFuncSetAttribute(cache_attn_kernel<kE4m3, kD, kRP, kExtra>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
@@ -1003,31 +1303,30 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<kE4m3, kD, kMt, kExtra>, A, tk, tv);
+  e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<kE4m3, kD, kRP, kExtra>, A, tk, tv, tq);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)tiles, (A.group_rows + 7) / 8);
+  cfg.gridDim = dim3((unsigned)tiles, (A.group_pos * A.G + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<kE4m3, kD, kMt>, A, grid);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<kE4m3, kD, kRP>, A, grid);
 }
 
-template <bool kE4m3, int kD, int kMt>
+template <bool kE4m3, int kD, int kRP>
 cudaError_t launch_extra(const CacheAttnLaunch& A, const CUtensorMap& tk, const CUtensorMap& tv,
-                         cudaStream_t stream) {
-  return A.cap > 0.f || A.slopes ? launch_one<kE4m3, kD, kMt, true>(A, tk, tv, stream)
-                                 : launch_one<kE4m3, kD, kMt, false>(A, tk, tv, stream);
+                         const CUtensorMap& tq, cudaStream_t stream) {
+  return A.cap > 0.f || A.slopes ? launch_one<kE4m3, kD, kRP, true>(A, tk, tv, tq, stream)
+                                 : launch_one<kE4m3, kD, kRP, false>(A, tk, tv, tq, stream);
 }
 
-// Row tiles per CTA: the fewest of 1, 2 and 4 (2 at 256 dims) that hold a group.
+// Rows per copy: the fewest of 32, 64 and 128 lanes that hold a group.
 template <bool kE4m3, int kD>
 cudaError_t launch_rows(const CacheAttnLaunch& A, const CUtensorMap& tk, const CUtensorMap& tv,
-                        cudaStream_t stream) {
-  if (A.group_rows <= 16) return launch_extra<kE4m3, kD, 1>(A, tk, tv, stream);
-  if constexpr (kD == 256)
-    return launch_extra<kE4m3, kD, 2>(A, tk, tv, stream);
-  else
-    return A.group_rows <= 32 ? launch_extra<kE4m3, kD, 2>(A, tk, tv, stream)
-                              : launch_extra<kE4m3, kD, 4>(A, tk, tv, stream);
+                        const CUtensorMap& tq, cudaStream_t stream) {
+  switch (cache_attn_rows(A.group_pos * A.G)) {
+    case 32: return launch_extra<kE4m3, kD, 32>(A, tk, tv, tq, stream);
+    case 64: return launch_extra<kE4m3, kD, 64>(A, tk, tv, tq, stream);
+    default: return launch_extra<kE4m3, kD, 128>(A, tk, tv, tq, stream);
+  }
 }
 
 }  // namespace cache_attn

@@ -189,10 +189,10 @@ int attn_smem_bytes(int n_mt, int n_stages);
 
 // Verify-step attention with caps, biases, windows and token trees, over a
 // bf16 or an e4m3 cache (cache_attention.cuh).
-constexpr int kCacheAttnCtas = 304;  // CTAs at most: two per SM of a 152-SM part
+constexpr int kCacheAttnCtas = 152;  // CTAs at most: one per SM
 struct CacheAttnLaunch {
-  int B, n_new, Hq, Hkv, G, R, Lmax; // G = Hq / Hkv, R = n_new * G query rows per KV head
-  int n_groups, group_rows;          // the R rows in equal groups
+  int B, n_new, Hq, Hkv, G, Lmax;    // G = Hq / Hkv
+  int n_groups, group_pos;           // the new positions in equal groups of at most 128 rows
   int window;                        // a position sees distances below it (0: all)
   int tree;                          // 1: anc and depth describe the new positions
   int max_depth;                     // of the new positions (n_new - 1 for a chain)
@@ -200,6 +200,7 @@ struct CacheAttnLaunch {
   float scale, cap, cap_exp;         // cap_exp = 2 log2(e) / cap
   long long q_stride;                // elements from one position's queries to the next's
   const __nv_bfloat16* q;            // [B, n_new, Hq, D]
+  const void* v;                     // the value cache
   const float* k_scale;              // [B, Hkv, n_scale] (e4m3 cache)
   const float* v_scale;
   const float* slopes;               // [Hq] or null
@@ -211,14 +212,18 @@ struct CacheAttnLaunch {
   uint32_t anc[SPECDEC_MAX_TREE_NODES][4];   // bit a of row i: node i sees node a
   uint8_t depth[SPECDEC_MAX_TREE_NODES];
 };
-// Keys per TMA box, bytes per box row: what the tensor maps are encoded with.
+// Keys per block (and TMA box).
 constexpr int cache_attn_block(bool e4m3, int D) { return e4m3 && D != 256 ? 128 : 64; }
-// Query rows per CTA at most: 64, or 32 at 256 dims.
-constexpr int cache_attn_max_rows(int D) { return D == 256 ? 32 : 64; }
+// Lanes that a group of query rows takes: 32, 64 or 128.
+constexpr int cache_attn_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// tmap_q: the queries as a bf16 tensor {D, Hq, n_new, B} with a box of 64
+// dims x G heads x group_pos positions, 128-byte swizzle (bf16 cache only).
 cudaError_t launch_cache_attention_kv8(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
-                                       const CUtensorMap& tmap_v, cudaStream_t stream);
+                                       const CUtensorMap& tmap_v, const CUtensorMap& tmap_q,
+                                       cudaStream_t stream);
 cudaError_t launch_cache_attention_bf16(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
-                                        const CUtensorMap& tmap_v, cudaStream_t stream);
+                                        const CUtensorMap& tmap_v, const CUtensorMap& tmap_q,
+                                        cudaStream_t stream);
 
 // Quantise new positions' keys and values into an e4m3 cache.
 struct Kv8AppendLaunch {

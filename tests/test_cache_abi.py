@@ -50,18 +50,18 @@ def _attend(fn, q=P, qs=4096, kc=P, vc=P, sk=P, sv=P, lens=P, parent=None, slope
 def test_attention_argument_errors(name):
     fn, size = getattr(b, name), getattr(b, name + "_workspace_size")
     need = size(1, 5, 32, 8, 128, 64)
-    assert need >= 2 * 304 * 20 * 130 * 4
+    assert need >= 2 * 152 * 20 * 130 * 4
     assert size(1024, 5, 32, 8, 128, 1 << 19) == need                  # grows with neither B nor Lmax
     assert _attend(fn, B=0, q=0, ws=0) == b.SPECDEC_OK
     for bad in ({"D": 96}, {"n": 0}, {"n": 129}, {"Hq": 30}, {"Hq": 4}, {"H": 0}, {"B": -1}, {"Lmax": 4},
-                {"Lmax": (1 << 30) + 1}, {"B": 1 << 20, "Lmax": 1 << 20}, {"Hq": 1 << 18},
+                {"Lmax": (1 << 30) + 1}, {"B": 1 << 20, "Lmax": 1 << 20}, {"Hq": 129 * 8},
                 {"B": 1 << 25, "Lmax": 5}):
         assert _attend(fn, **bad) == b.SPECDEC_ERR_UNSUPPORTED, bad
         shape = dict(B=1, n=5, Hq=32, H=8, D=128, Lmax=64)
         shape.update(bad)
         assert size(*shape.values()) == 0, bad
     for bad in ({"q": 0}, {"kc": 0}, {"vc": 0}, {"lens": 0}, {"out": 0}, {"q": P + 8}, {"out": P + 2},
-                {"lens": P + 2}, {"slopes": P + 1}, {"qs": 4095}, {"qs": 4088}, {"qs": 4100},
+                {"lens": P + 2}, {"slopes": P + 1}, {"qs": 4095}, {"qs": 4088}, {"qs": 4100}, {"qs": 1 << 31},
                 {"scale": float("nan")}, {"cap": -1.0}, {"cap": float("inf")}, {"window": -1},
                 {"parent": (0, 0, 0, 0, 0)}, {"parent": (-1, 1, 0, 0, 0)}, {"parent": (-1, 0, 0, 3, 0)},
                 {"parent": (-1, 0, -1, 0, 0)}):

@@ -56,10 +56,17 @@ def _values(cache):
     return _f(cache[0]), _f(cache[1])
 
 
-def _call(kind, q, cache, lens, **how):
+def _call(kind, q, cache, lens, workspace=None, **how):
+    """The call; unless the caller brings a workspace, no device-side error is expected of it."""
     import target_model_verify_gb300 as tv
     fn = tv.verify_attention_kv8 if kind == "kv8" else tv.verify_attention_masked
-    return fn(q, *cache, lens, **how)
+    if workspace is not None or torch.cuda.is_current_stream_capturing() or "stream" in how:
+        return fn(q, *cache, lens, workspace=workspace, **how)
+    n = tv.cache_attention_workspace_bytes(*q.shape[:3], cache[0].shape[2], q.shape[3], cache[0].shape[1])
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    out = fn(q, *cache, lens, workspace=ws, **how)
+    assert tv.read_status(ws) == 0
+    return out
 
 
 def _check(kind, q, cache, lens, out, seqs=None, **how):
@@ -133,6 +140,20 @@ def test_lengths_around_the_blocks(kind):
     lens = [3, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 0, 258, 0]
     q, cache, lens = _inputs(kind, 11, len(lens), 3, 4, 2, 128, 258, lens=lens)
     _check(kind, q, cache, lens, _call(kind, q, cache, lens))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("how", [{}, {"window": 2500}], ids=str)
+def test_long_ragged_batch(kind, how):
+    """Many blocks that every position sees between those with masks, several tiles per CTA."""
+    import target_model_verify_gb300 as tv
+    lens = [6000, 40, 5111, 3, 2600, 1, 0, 4097] * 4
+    q, cache, lens = _inputs(kind, 22, len(lens), 1, 16, 8, 64, 6000, lens=lens)
+    ws = torch.empty(tv.cache_attention_workspace_bytes(len(lens), 1, 16, 8, 64, 6000), dtype=torch.uint8,
+                     device=DEV)
+    out = _call(kind, q, cache, lens, workspace=ws, **how)
+    assert tv.read_status(ws) == 0
+    _check(kind, q, cache, lens, out, seqs=[0, 2, 3, 15, 28, 30, 31], **how)
 
 
 @pytest.mark.parametrize("kind", KINDS)
