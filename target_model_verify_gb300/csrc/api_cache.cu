@@ -22,6 +22,8 @@ int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
   if ((__int128)B * Lmax * Hkv * D >= ((__int128)1 << 40)) return SPECDEC_ERR_UNSUPPORTED;
   // (sequence, KV head, row group) tiles are a grid dimension
   if ((long long)B * Hq * n_new >= (1ll << 31)) return SPECDEC_ERR_UNSUPPORTED;
+  // and their blocks of 64 keys or more are counted in 32 bits
+  if ((__int128)B * Hkv * n_new * (Lmax / 64 + 8) >= ((__int128)1 << 31)) return SPECDEC_ERR_UNSUPPORTED;
   return SPECDEC_OK;
 }
 

@@ -21,7 +21,9 @@
 // A tile that lies inside one part is finished by its CTA; the others leave
 // (maximum, sum, unnormalised output) partials that combine_kernel merges.
 //
-// CTA: warps 0-3 softmax, 4-7 auxiliary, 8 TMA producer, 9 tcgen05 issuer.
+// CTA: warps 0-3 softmax, 4-7 auxiliary, 8 and 9 TMA producers (K with Q,
+// and V, whose slots free up at different times), 10 and 11 tcgen05 issuers (one per product: a thread takes 50 to 100 cycles for each MMA, as
+// long as the MMA itself, and more for each wait).
 //   S = Q K^T: tcgen05.mma, M = 128 query rows, N = a block of keys, into one
 //     of two tensor-memory buffers, a block ahead of the softmax. bf16:
 //     kind::f16. e4m3: kind::f8f6f4 on the codes as they lie; the query row,
@@ -53,11 +55,13 @@ namespace cache_attn {
 
 constexpr int kSoftWarps = 4;
 constexpr int kAuxWarps = 4;
-constexpr int kProducer = 8, kIssuer = 9;     // warp indices
-constexpr int kThreads = 320;
+constexpr int kProducer = 8, kProducerV = 9, kIssuerS = 10, kIssuerO = 11;   // warp indices
+constexpr int kThreads = 384;
 constexpr unsigned long long kDrainNs = 1000000000ull;
+constexpr int kStagePitch = 36 * 4;           // bytes: 32 floats, 16-byte accesses free of bank conflicts
 constexpr float kHeadroom = 8.f;              // log2 by which a maximum may pass its reference
 constexpr int kSmemLimit = 227 * 1024;
+constexpr int kTileCost = 3;                  // units of work that a tile costs besides its blocks
 
 template <bool kE4m3, int kD, int kRP>
 struct Shape {
@@ -70,20 +74,25 @@ struct Shape {
   static constexpr int kCopies = 128 / kRP;                  // copies of the query rows
   static constexpr int kKpl = kBlk / kCopies;                // keys per lane and block
   static constexpr int kTerms = kE4m3 ? 2 : 1;
-  static constexpr int kQTerm = 128 * kRowBytes;             // 128 query rows in the K operand's type
-  static constexpr int kQBytes = kTerms * kQTerm;
-  static constexpr int kQBufs = kElem * kD >= (kE4m3 ? 128 : 512) ? 1 : 2;
+  // Queries: e4m3 terms sit in tensor memory where it has room for them
+  // (shared memory bandwidth is what the e4m3 products compete for), else
+  // 128 rows in the K operand's layout in shared memory.
+  static constexpr bool kQTmem = kE4m3 && kD <= 128;
+  static constexpr int kQTerm = 128 * kRowBytes;
+  static constexpr int kQBytes = kQTmem ? 0 : kTerms * kQTerm;
+  static constexpr int kQBufs = !kE4m3 && kD <= 128 ? 2 : 1;
+  static constexpr int kPBufs = kQTmem ? 1 : 2;
   static constexpr int kV16Bytes = kE4m3 ? kBlk * kD * 2 : 0;   // widened V, two of them
-  static constexpr int kStageBytes = kCopies > 1 ? 128 * 33 * 4 : 0;   // merge of the copies
-  static constexpr int kTabBytes = 2 * 128 * 4 + 128 * 8 + 128 * 16 + 128 * 4;  // q scales, (m, l), tree
+  static constexpr int kStageBytes = 128 * kStagePitch;      // 32 output columns of every lane
+  static constexpr int kTabBytes = 128 * 4 + 128 * 8 + 128 * 16 + 128 * 4;  // q scales, (m, l), tree
   static constexpr int kFixed = 1024 + 2 * kV16Bytes + kQBufs * kQBytes + kStageBytes + kTabBytes + 512;
   static constexpr int kRingMax = (kSmemLimit - kFixed) / (2 * kSlotBytes);
   static constexpr int kRing = kRingMax < 6 ? kRingMax : 6;  // K blocks (and V blocks) in flight
   static constexpr int kSmem = kFixed + 2 * kRing * kSlotBytes;
   static_assert(kRing >= 2, "two K and two V blocks must fit");
-  // tensor memory columns: two score buffers, the output, two P operands
-  static constexpr int kColS = 0, kColO = 2 * kBlk, kColP = kColO + kD;
-  static_assert(kColP + kBlk <= 512, "tensor memory");
+  // tensor memory columns: two score buffers, the output, P, the query terms
+  static constexpr int kColS = 0, kColO = 2 * kBlk, kColP = kColO + kD, kColQ = kColP + kPBufs * (kBlk / 2);
+  static_assert(kColQ + (kQTmem ? kTerms * (kD / 4) : 0) <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -173,6 +182,16 @@ __host__ __device__ constexpr uint32_t instr_desc(int type, bool b_mn, int N) {
   return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | (b_mn ? 1u << 16 : 0u) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // D (+)= A B^T with A and B in shared memory.
 template <bool kF8>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -186,14 +205,48 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
   else
     tc_mma_bf16(d, a, b, idesc, acc);
 }
-// The same with A in tensor memory (f16 or bf16 pairs, one row per lane).
+// The same with A in tensor memory: a row per lane, 32-bit columns of two
+// 16-bit or four 8-bit elements along k.
+template <bool kF8>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+  if constexpr (kF8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma2(float& a, float& b, float c, float d) {   // (a, b) * c + d
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {   // (a, b) + (c, d)
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+  const uint4 v = lds128(a);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
 // Tensor memory: each thread of a warp reads or writes consecutive 32-bit
@@ -291,10 +344,10 @@ __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Blocks of kBlk cache rows that a sequence of L rows reads, and the first
-// of them: all rows, or those inside the window of the first new position
-// (the one that sees furthest back). A length of 0 marks an unused batch
-// slot; *bad reports lengths that the cache cannot hold.
+// What the schedule knows of a sequence: the blocks of kBlk cache rows it
+// reads, all or those inside the window of its first new position (the one
+// that sees furthest back), and the first of them. A length of 0 marks an
+// unused batch slot; bad: a length that the cache cannot hold.
 template <int kBlk>
 __device__ __forceinline__ int seq_blocks(const CacheAttnLaunch& A, int L, int& first, bool& bad) {
   bad = L != 0 && (L < A.n_new || L > A.Lmax);
@@ -304,55 +357,63 @@ __device__ __forceinline__ int seq_blocks(const CacheAttnLaunch& A, int L, int& 
   return (L + kBlk - 1) / kBlk - first;
 }
 
-// The part of the block run that CTA c of n takes.
-__device__ __forceinline__ long long part_begin(long long total, int c, int n) {
-  return total * c / n;
+// Units of work of a tile of nb blocks: starting and writing out a tile
+// costs about kTileCost blocks, which come first.
+__device__ __forceinline__ int tile_units(int nb) { return nb > 0 ? nb + kTileCost : 0; }
+
+// The first unit of CTA c's part, of n: equal parts to within a unit.
+__device__ __forceinline__ int part_begin(int total, int c, int n) {
+  return total / n * c + (int)((unsigned)(total % n) * (unsigned)c / (unsigned)n);
 }
 
-// One warp: the number of block units in the batch, and where unit `at` lies:
-// sequence b and offset inside it (b = B when at >= total).
+// One warp: the batch's units, and where unit part_begin(c) lies: sequence b
+// (B when there is none) and offset inside it.
+struct Place {
+  int total, u0, u1, b, off;
+  bool any_bad;
+};
 template <int kBlk>
-__device__ __forceinline__ long long total_units(const CacheAttnLaunch& A, int lane, bool& any_bad) {
-  long long sum = 0;
-  bool bad_seen = false;
+__device__ __forceinline__ Place find_part(const CacheAttnLaunch& A, int lane, int c, int n) {
+  const int per = A.Hkv * A.n_groups;
+  Place p;
+  int first, units0 = 0, sum = 0;
+  bool bad, bad_seen = false;
   for (int b = lane; b < A.B; b += 32) {
-    int first;
-    bool bad;
-    sum += seq_blocks<kBlk>(A, A.seq_lens[b], first, bad);
+    const int u = per * tile_units(seq_blocks<kBlk>(A, A.seq_lens[b], first, bad));
+    if (b < 32) units0 = u;                    // the first 32 sequences stay at hand
+    sum += u;
     bad_seen |= bad;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  any_bad = __any_sync(0xffffffffu, bad_seen);
-  return sum * A.Hkv * A.n_groups;
-}
-template <int kBlk>
-__device__ __forceinline__ void locate_unit(const CacheAttnLaunch& A, int lane, long long at, int& b_out,
-                                            long long& off_out) {
-  const long long per = (long long)A.Hkv * A.n_groups;
-  long long before = 0;
-  b_out = A.B;
-  off_out = 0;
+  p.any_bad = __any_sync(0xffffffffu, bad_seen);
+  p.total = sum;
+  p.u0 = part_begin(sum, c, n);
+  p.u1 = part_begin(sum, c + 1, n);
+  p.b = A.B;
+  p.off = 0;
+  if (p.u0 >= p.u1) return p;
+  int before = 0;
   for (int b0 = 0; b0 < A.B; b0 += 32) {
     const int b = b0 + lane;
-    int first;
-    bool bad;
-    const long long mine = b < A.B ? per * seq_blocks<kBlk>(A, A.seq_lens[b], first, bad) : 0;
-    long long run = mine;
+    const int mine = b0 == 0 ? units0
+                     : b < A.B ? per * tile_units(seq_blocks<kBlk>(A, A.seq_lens[b], first, bad)) : 0;
+    int run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, run, o);
+      const int x = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += x;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, at < before + run);
+    const unsigned hit = __ballot_sync(0xffffffffu, p.u0 < before + run);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      b_out = b0 + l;
-      off_out = at - before - __shfl_sync(0xffffffffu, run - mine, l);
-      return;
+      p.b = b0 + l;
+      p.off = p.u0 - before - __shfl_sync(0xffffffffu, run - mine, l);
+      return p;
     }
     before += __shfl_sync(0xffffffffu, run, 31);
   }
+  return p;
 }
 
 // Walks the tiles of a part: (b, h, group) and the block range inside each.
@@ -361,42 +422,56 @@ struct Walk {
   int b, h, g;        // tile
   int blk, n_here;    // first block inside the tile, blocks of this part
   int nb, first, L;   // the tile's blocks, its first cache block, its length
-  long long u, end;
+  int clean_lo, clean_hi;   // the tile's blocks that every new position sees whole
+  int u, end, tile0;  // this part's first unit in the tile, the part's end, the tile's first unit
 
   __device__ __forceinline__ void load(const CacheAttnLaunch& A) {
     bool bad;
     L = A.seq_lens[b];
     nb = seq_blocks<kBlk>(A, L, first, bad);
+    const int P0 = L - A.n_new;               // row and position of the first new one
+    clean_hi = (P0 + 1) / kBlk - first;
+    clean_lo = A.window > 0 ? (max(0, P0 + A.max_depth - A.window + 1) + kBlk - 1) / kBlk - first : 0;
   }
-  __device__ __forceinline__ void start(const CacheAttnLaunch& A, int b0, long long off, long long u0,
-                                        long long u1) {
+  __device__ __forceinline__ void cut() {
+    const int to = min(tile0 + tile_units(nb), end);
+    blk = max(0, u - tile0 - kTileCost);
+    n_here = max(0, to - tile0 - kTileCost) - blk;
+  }
+  __device__ __forceinline__ void start(const CacheAttnLaunch& A, int b0, int off, int u0, int u1) {
     u = u0;
     end = u1;
     b = b0;
     if (u >= end) return;
     load(A);
-    blk = (int)(off % nb);
-    const int t = (int)(off / nb);
+    const int units = tile_units(nb), t = off / units;
+    tile0 = u - (off - t * units);
     g = t % A.n_groups;
     h = t / A.n_groups;
-    n_here = (int)min((long long)(nb - blk), end - u);
+    cut();
+    if (n_here == 0) next(A);
   }
   __device__ __forceinline__ bool done() const { return u >= end; }
+  // To the next tile, and past one of which this part has only the leading units.
   __device__ __forceinline__ void next(const CacheAttnLaunch& A) {
-    u += n_here;
-    if (u >= end) return;
-    blk = 0;
-    if (++g == A.n_groups) {
-      g = 0;
-      if (++h == A.Hkv) {
-        h = 0;
-        do {
-          ++b;
-          load(A);
-        } while (nb == 0);
+    do {
+      u = tile0 = tile0 + tile_units(nb);
+      if (u >= end) return;
+      if (++g == A.n_groups) {
+        g = 0;
+        if (++h == A.Hkv) {
+          h = 0;
+          do {
+            ++b;
+            load(A);
+          } while (nb == 0);
+        }
       }
-    }
-    n_here = (int)min((long long)nb, end - u);
+      cut();
+    } while (n_here == 0);
+  }
+  __device__ __forceinline__ bool clean(int ib) const {
+    return blk + ib >= clean_lo && blk + ib < clean_hi;
   }
 };
 
@@ -438,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t v16 = ring_v + kR * S::kSlotBytes;
   const uint32_t qb = v16 + 2 * S::kV16Bytes;
   const uint32_t stage = qb + kNq * S::kQBytes;
-  const uint32_t q_tab = stage + S::kStageBytes;           // query row scales [kNq][128]
-  const uint32_t ml_tab = q_tab + 2 * 128 * 4;             // (reference, sum) of every lane
+  const uint32_t q_tab = stage + S::kStageBytes;           // query row scales, by lane
+  const uint32_t ml_tab = q_tab + 128 * 4;                 // (reference, sum) of every lane
   const uint32_t tree = ml_tab + 128 * 8;                  // [128][4] ancestor words, then depth [128]
   const uint32_t bars = tree + 128 * 16 + 128 * 4;
   auto k_full = [&](int s) { return bars + 8u * (uint32_t)s; };
@@ -454,16 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto q_empty = [&](int s) { return bars2 + 8u * (uint32_t)(6 + s); };
   auto v16_full = [&](int s) { return bars2 + 8u * (uint32_t)(8 + s); };
   auto v16_empty = [&](int s) { return bars2 + 8u * (uint32_t)(10 + s); };
-  // One per block parity: when a block's scores are there, the product two
-  // blocks back is done, so a wait for the one before it is never a phase off.
+  // One per block parity: the softmax takes note of every phase of each.
   auto o_done = [&](int s) { return bars2 + 8u * (uint32_t)(12 + s); };
   const uint32_t drained = bars2 + 8u * 14;
   uint8_t* const words = smem_raw + (bars2 + 8u * 16 - raw);
   volatile int* const abort = reinterpret_cast<volatile int*>(words);
   volatile int* const odd = abort + 1;                     // a value that is no number was held back
   volatile uint32_t* const tmem_slot = reinterpret_cast<volatile uint32_t*>(words) + 2;
-  volatile int* const shared_b = abort + 3;
-  volatile long long* const shared_u = reinterpret_cast<volatile long long*>(words + 16);
+  volatile int* const place = abort + 4;                   // find_part's answer
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kR; ++s) {
@@ -482,12 +555,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(v16_full(s), kAuxWarps);
       mbar_init(v16_empty(s), 1);
     }
-    mbar_init(drained, 1);
+    mbar_init(drained, 2);
     *abort = 0;
     *odd = 0;
     fence_mbar_init();
   }
-  if (warp == kIssuer) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+  if (warp == kIssuerO) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
   if (A.tree) {
     for (int e = threadIdx.x; e < A.n_new; e += kThreads) {
       sts128(tree + e * 16, A.anc[e][0], A.anc[e][1], A.anc[e][2], A.anc[e][3]);
@@ -495,53 +568,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   grid_dependency_wait();
+  grid_launch_dependents();          // the merge may get ready on idle SMs
   if (warp == 0) {
-    bool any_bad;
-    const long long total = total_units<kBlk>(A, lane, any_bad);
-    const long long u0 = part_begin(total, blockIdx.x, gridDim.x);
-    const long long u1 = part_begin(total, blockIdx.x + 1, gridDim.x);
-    int b0 = A.B;
-    long long off = 0;
-    if (u0 < u1) locate_unit<kBlk>(A, lane, u0, b0, off);
+    const Place pl = find_part<kBlk>(A, lane, blockIdx.x, gridDim.x);
     if (lane == 0) {
-      *shared_b = b0;
-      shared_u[0] = off;
-      shared_u[1] = u0;
-      shared_u[2] = u1;
-      if (blockIdx.x == 0) *A.status = any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
+      place[0] = pl.b;
+      place[1] = pl.off;
+      place[2] = pl.u0;
+      place[3] = pl.u1;
+      if (blockIdx.x == 0) *A.status = pl.any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int part0 = place[2];
   Walk<kBlk> w;
-  w.start(A, *shared_b, shared_u[0], shared_u[1], shared_u[2]);
-  const long long part0 = shared_u[1];
+  w.start(A, place[0], place[1], part0, place[3]);
   // A warp's wait: all lanes agree on whether it ran out.
   auto warp_wait = [&](uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, A.status));
+    return __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort, A.status));
   };
-  // Whether every new position sees every row of block ib of the walk's tile.
-  auto is_clean = [&](const Walk<kBlk>& t, int ib) {
-    const int j0 = (t.first + t.blk + ib) * kBlk, P0 = t.L - A.n_new;
-    return j0 + kBlk <= P0 + 1 && (A.window <= 0 || j0 > P0 + A.max_depth - A.window);
-  };
-  uint32_t issued[3] = {0, 0, 0}, issued_phase[3] = {0, 0, 0};   // producer: K, V, Q copies in flight
+  uint32_t issued = 0, issued_phase = 0, issued_q = 0, issued_q_phase = 0;   // producers: copies in flight
 
-  if (warp == kProducer) {
-    // ---------------------------------------------------------- producer --
+  if (warp == kProducer || warp == kProducerV) {
+    // --------------------------------------- producers: K and Q; V --
     if (lane == 0) {
+      const bool is_v = warp == kProducerV;
       const uint64_t pol = policy_evict_first();
-      auto mark = [&](int what, int s, uint32_t ph) {
-        issued[what] |= 1u << s;
-        issued_phase[what] = (issued_phase[what] & ~(1u << s)) | (ph << s);
-      };
+      const CUtensorMap* const map = is_v ? &tmap_v : &tmap_k;
+      const uint32_t ring = is_v ? ring_v : ring_k;
       int s = 0;
       uint32_t ph = 0, nt = 0;
       bool ok = true;
       for (; ok && !w.done(); w.next(A), ++nt) {
-        if constexpr (!kE4m3) {
+        if (!kE4m3 && !is_v) {
           // the tile's query rows, once per copy
           const int qs = nt % kNq;
           const uint32_t qph = (nt / kNq) & 1;
@@ -552,24 +614,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = 0; p < kD / 64; ++p)
               tma_load_4d(qb + qs * S::kQBytes + p * 128 * 128 + c * kRP * 128, &tmap_q, q_full(qs), p * 64,
                           w.h * A.G, w.g * A.group_pos, w.b, policy_evict_normal());
-          mark(2, qs, qph);
+          issued_q |= 1u << qs;
+          issued_q_phase = (issued_q_phase & ~(1u << qs)) | (qph << qs);
         }
         for (int i = 0; i < w.n_here; ++i) {
           const int j0 = (w.first + w.blk + i) * kBlk;
-          if (!(ok = mbar_wait(k_empty(s), ph ^ 1u, abort, A.status))) break;
-          mbar_arrive_expect_tx(k_full(s), (uint32_t)S::kSlotBytes);
+          const uint32_t full = is_v ? v_full(s) : k_full(s);
+          if (!(ok = mbar_wait(is_v ? v_empty(s) : k_empty(s), ph ^ 1u, abort, A.status))) break;
+          mbar_arrive_expect_tx(full, (uint32_t)S::kSlotBytes);
 #pragma unroll
           for (int p = 0; p < S::kPanels; ++p)
-            tma_load_4d(ring_k + s * S::kSlotBytes + p * kBlk * S::kPanelBytes, &tmap_k, k_full(s),
+            tma_load_4d(ring + s * S::kSlotBytes + p * kBlk * S::kPanelBytes, map, full,
                         p * (S::kPanelBytes / S::kElem), w.h, j0, w.b, pol);
-          mark(0, s, ph);
-          if (!(ok = mbar_wait(v_empty(s), ph ^ 1u, abort, A.status))) break;
-          mbar_arrive_expect_tx(v_full(s), (uint32_t)S::kSlotBytes);
-#pragma unroll
-          for (int p = 0; p < S::kPanels; ++p)
-            tma_load_4d(ring_v + s * S::kSlotBytes + p * kBlk * S::kPanelBytes, &tmap_v, v_full(s),
-                        p * (S::kPanelBytes / S::kElem), w.h, j0, w.b, pol);
-          mark(1, s, ph);
+          issued |= 1u << s;
+          issued_phase = (issued_phase & ~(1u << s)) | (ph << s);
           if (++s == kR) {
             s = 0;
             ph ^= 1u;
@@ -577,166 +635,223 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == kIssuer) {
-    // ------------------------------------------------------------ issuer --
-    if (lane == 0 && !w.done()) {
-      constexpr uint32_t id_qk = instr_desc(kE4m3 ? 0 : 1, false, kBlk);
-      constexpr uint32_t id_pv = instr_desc(kE4m3 ? 0 : 1, true, kD);
-      Walk<kBlk> wq = w;                 // the tile whose scores come next
-      int iq = 0, sq = 0;
-      uint32_t phq = 0, nq = 0, tq = 0;
-      auto issue_scores = [&]() {
-        const int qs = tq % kNq;
-        if (iq == 0 && !mbar_wait<true>(q_full(qs), (tq / kNq) & 1, abort, A.status)) return false;
-        if (!mbar_wait<true>(k_full(sq), phq, abort, A.status)) return false;
+  } else if (warp == kIssuerS) {
+    // --------------------------------------------------- issuer of Q K^T --
+    // Scores run up to two blocks ahead of the softmax's answer.
+    constexpr uint32_t id_qk = instr_desc(kE4m3 ? 0 : 1, false, kBlk);
+    const uint64_t q_desc = operand_desc<S::kPanelBytes>(qb, 16);
+    const uint64_t k_desc = operand_desc<S::kPanelBytes>(ring_k, 16);
+    int s = 0;
+    uint32_t ph = 0, n = 0, nt = 0;
+    bool ok = true;
+    for (; ok && !w.done(); w.next(A), ++nt) {
+      const int qs = nt % kNq;
+      if (!(ok = warp_wait(q_full(qs), (nt / kNq) & 1))) break;
+      const uint64_t qd = q_desc + (uint64_t)((uint32_t)(qs * S::kQBytes) >> 4);
+      for (int i = 0; i < w.n_here; ++i, ++n) {
+        if (!(ok = warp_wait(k_full(s), ph))) break;
+        // the buffer's previous scores have been read
+        if (n >= 2 && !(ok = warp_wait(p_full(n & 1), ((n - 2) >> 1) & 1))) break;
         tc_fence_after();
-        const uint32_t d = tmem + S::kColS + (nq & 1) * kBlk;
+        const uint64_t kd = k_desc + (uint64_t)((uint32_t)(s * S::kSlotBytes) >> 4);
+        const uint32_t d = tmem + S::kColS + (n & 1) * kBlk;
+        if (elect_one()) {
 #pragma unroll
-        for (int term = 0; term < S::kTerms; ++term)
+          for (int term = 0; term < S::kTerms; ++term)
 #pragma unroll
-          for (int p = 0; p < S::kPanels; ++p)
+            for (int p = 0; p < S::kPanels; ++p)
 #pragma unroll
-            for (int k = 0; k < S::kPanelBytes / 32; ++k)
-              mma_ss<kE4m3>(d,
-                            operand_desc<S::kPanelBytes>(qb + qs * S::kQBytes + term * S::kQTerm +
-                                                             p * 128 * S::kPanelBytes + k * 32, 16),
-                            operand_desc<S::kPanelBytes>(ring_k + sq * S::kSlotBytes +
-                                                             p * kBlk * S::kPanelBytes + k * 32, 16),
-                            id_qk, term + p + k > 0);
-        tc_commit(k_empty(sq));
-        tc_commit(s_full(nq & 1));
-        if (++sq == kR) {
-          sq = 0;
-          phq ^= 1u;
+              for (int k = 0; k < S::kPanelBytes / 32; ++k) {
+                const uint64_t b = kd + (uint64_t)((p * kBlk * S::kPanelBytes + k * 32) >> 4);
+                if constexpr (S::kQTmem)
+                  mma_ts<true>(d, tmem + S::kColQ + term * (kD / 4) + p * (S::kPanelBytes / 4) + k * 8, b, id_qk,
+                               term + p + k > 0);
+                else
+                  mma_ss<kE4m3>(d, qd + (uint64_t)((term * S::kQTerm + p * 128 * S::kPanelBytes + k * 32) >> 4), b,
+                                id_qk, term + p + k > 0);
+              }
+          tc_commit(s_full(n & 1));
+          tc_commit(k_empty(s));
+          if (i + 1 == w.n_here) tc_commit(q_empty(qs));
         }
-        ++nq;
-        if (++iq == wq.n_here) {
-          tc_commit(q_empty(qs));
-          iq = 0;
-          ++tq;
-          wq.next(A);
+        __syncwarp();
+        if (++s == kR) {
+          s = 0;
+          ph ^= 1u;
         }
-        return true;
-      };
-      bool ok = issue_scores();
-      int s = 0;
-      uint32_t ph = 0, n = 0, clean_ph = 0;
-      for (; ok && !w.done(); w.next(A))
-        for (int i = 0; i < w.n_here; ++i, ++n) {
-          // Scores run a block ahead. Into a new tile they do so only with a
-          // second query buffer: with one, they would wait for the refill.
-          const bool more = !wq.done(), early = more && (kNq == 2 || iq != 0);
-          if (early && !(ok = issue_scores())) break;
-          if (!(ok = mbar_wait<true>(p_full(n & 1), (n >> 1) & 1, abort, A.status))) break;
-          uint32_t vb;
-          if constexpr (kE4m3) {
-            vb = v16 + (n & 1) * S::kV16Bytes;
-            if (!(ok = mbar_wait<true>(v16_full(n & 1), (n >> 1) & 1, abort, A.status))) break;
-          } else {
-            vb = ring_v + s * S::kSlotBytes;
-            if (!(ok = mbar_wait<true>(v_full(s), ph, abort, A.status))) break;
-            if (!is_clean(w, i)) {
-              if (!(ok = mbar_wait<true>(v_clean(s), (clean_ph >> s) & 1, abort, A.status))) break;
-              clean_ph ^= 1u << s;
-            }
+      }
+    }
+    if (elect_one()) tc_commit(drained);
+    wait_drain(drained, 0);
+  } else if (warp == kIssuerO) {
+    // ----------------------------------------------------- issuer of P V --
+    constexpr uint32_t id_pv = instr_desc(kE4m3 ? 0 : 1, true, kD);
+    const uint64_t v_desc = operand_desc<128>(kE4m3 ? v16 : ring_v, kBlk * 128);
+    int s = 0;
+    uint32_t ph = 0, n = 0, clean_ph = 0;
+    bool ok = true;
+    for (; ok && !w.done(); w.next(A))
+      for (int i = 0; i < w.n_here; ++i, ++n) {
+        uint64_t vd;
+        if constexpr (kE4m3) {
+          vd = v_desc + (uint64_t)((uint32_t)((n & 1) * S::kV16Bytes) >> 4);
+          if (!(ok = warp_wait(v16_full(n & 1), (n >> 1) & 1))) break;
+        } else {
+          vd = v_desc + (uint64_t)((uint32_t)(s * S::kSlotBytes) >> 4);
+          if (!(ok = warp_wait(v_full(s), ph))) break;
+          if (!w.clean(i)) {
+            if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) break;
+            clean_ph ^= 1u << s;
           }
-          tc_fence_after();
+        }
+        if (!(ok = warp_wait(p_full(n & 1), (n >> 1) & 1))) break;
+        tc_fence_after();
+        const uint32_t pa = tmem + S::kColP + (S::kPBufs == 2 ? (n & 1) * (kBlk / 2) : 0);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBlk / 16; ++k)
-            mma_ts(tmem + S::kColO, tmem + S::kColP + (n & 1) * (kBlk / 2) + k * 8,
-                   operand_desc<128>(vb + k * 2048, kBlk * 128), id_pv, i > 0 || k > 0);
-          tc_commit(kE4m3 ? v16_empty(n & 1) : v_empty(s));
+            mma_ts<false>(tmem + S::kColO, pa + k * 8, vd + (uint64_t)(k * 2048 >> 4), id_pv, i > 0 || k > 0);
           tc_commit(o_done(n & 1));
-          if (more && !early && !(ok = issue_scores())) break;
-          if (++s == kR) {
-            s = 0;
-            ph ^= 1u;
-          }
+          tc_commit(kE4m3 ? v16_empty(n & 1) : v_empty(s));
         }
-      // every product has to be done before the tensor memory is given back
-      tc_commit(drained);
-      wait_drain(drained, 0);
-    }
+        __syncwarp();
+        if (++s == kR) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    // every product has to be done before the tensor memory is given back
+    if (elect_one()) tc_commit(drained);
+    wait_drain(drained, 0);
   } else if (warp >= kSoftWarps) {
     // --------------------------------------------------------- auxiliary --
     const int at = threadIdx.x - 32 * kSoftWarps;      // 0 .. 127
     bool ok = true;
     if constexpr (kE4m3) {
-      Walk<kBlk> wl = w;                               // the tile whose queries come next
-      uint32_t tl = 0;
-      auto load_queries = [&]() {
-        const int qs = tl % kNq;
-        if (!warp_wait(q_empty(qs), ((tl / kNq) & 1) ^ 1u)) return false;
-        constexpr int kCh = kD / 8;                    // lanes per row, 8 dims each
-        const int pos0 = wl.g * A.group_pos;
-        const int rows = min(A.group_pos, A.n_new - pos0) * A.G;
-        for (int e = at; e < kRP * kCh; e += 32 * kAuxWarps) {
-          const int r = e / kCh, c = e % kCh;
-          uint4 val = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows)
-            val = __ldg(reinterpret_cast<const uint4*>(
-                A.q + ((size_t)wl.b * A.n_new + pos0 + r / A.G) * A.q_stride +
-                (size_t)(wl.h * A.G + r % A.G) * kD + c * 8));
-          const uint32_t wv[4] = {val.x, val.y, val.z, val.w};
-          float f[8], amax = 0.f;
-          bool fine = true;
+      // A tile's query rows as two e4m3 terms each. In tensor memory: thread
+      // = lane = row, 16 dims at a time; its scale from all of the row first.
+      uint32_t nt = 0;
+      auto load_queries = [&](const Walk<kBlk>& t) {
+        if (!warp_wait(q_empty(0), (nt & 1) ^ 1u)) return false;
+        if constexpr (S::kQTmem) {
+          const int row = at % kRP, pos0 = t.g * A.group_pos;
+          const bool mine = row < min(A.group_pos, A.n_new - pos0) * A.G;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              A.q + ((size_t)t.b * A.n_new + pos0 + (mine ? row / A.G : 0)) * A.q_stride +
+              (size_t)(t.h * A.G + (mine ? row % A.G : 0)) * kD);
+          uint32_t wv[kD / 2];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            f[k] = __uint_as_float(k & 1 ? wv[k >> 1] & 0xffff0000u : wv[k >> 1] << 16);
-            amax = fmaxf(amax, fabsf(f[k]));
-            fine &= fabsf(f[k]) < INFINITY;
+          for (int c = 0; c < kD / 8; ++c) {
+            const uint4 v = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            wv[4 * c] = v.x;
+            wv[4 * c + 1] = v.y;
+            wv[4 * c + 2] = v.z;
+            wv[4 * c + 3] = v.w;
           }
+          uint32_t top = 0;                    // largest magnitude, as bf16 bits
 #pragma unroll
-          for (int o = kCh / 2; o; o >>= 1) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            fine &= __shfl_xor_sync(0xffffffffu, (int)fine, o) != 0;
-          }
-          // largest magnitude -> [2^7, 2^8); a row that holds no numbers is NaN
-          const int down = amax > 0.f && fine ? min(max((int)(__float_as_uint(amax) >> 23) - 134, -100), 120) : 0;
+          for (int k = 0; k < kD / 2; ++k)
+            top = max(top, max(wv[k] & 0x7fffu, (wv[k] >> 16) & 0x7fffu));
+          const bool fine = top < 0x7f80u;     // else the row holds no numbers: NaN
+          // largest magnitude -> [2^7, 2^8)
+          const int down = top > 0 && fine ? min(max((int)(top >> 7) - 134, -100), 120) : 0;
           const float mul = __uint_as_float((uint32_t)(127 - down) << 23);
-          uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t ph[2], pl[2];
+          for (int c = 0; c < kD / 4; c += 8) {
+            uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float a = f[4 * k + 2 * x] * mul, b = f[4 * k + 2 * x + 1] * mul;
-              ph[x] = f32_to_e4m3x2(a, b);
-              const uint32_t back = e4m3x2_to_f16x2((uint16_t)ph[x]);
-              const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&back));
-              pl[x] = f32_to_e4m3x2(a - r2.x, b - r2.y);
+            for (int k = 0; k < 8; ++k) {
+              uint32_t ph[2], pl[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t u = wv[(c + k) * 2 + x];
+                const float a = __uint_as_float(u << 16) * mul, b = __uint_as_float(u & 0xffff0000u) * mul;
+                ph[x] = f32_to_e4m3x2(a, b);
+                const uint32_t back = e4m3x2_to_f16x2((uint16_t)ph[x]);
+                const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                pl[x] = f32_to_e4m3x2(a - r2.x, b - r2.y);
+              }
+              hi[k] = ph[0] | (ph[1] << 16);
+              lo[k] = pl[0] | (pl[1] << 16);
             }
-            hi[k] = ph[0] | (ph[1] << 16);
-            lo[k] = pl[0] | (pl[1] << 16);
+            const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kColQ + c;
+            tmem_store(to, hi, Cols<8>{});
+            tmem_store(to + kD / 4, lo, Cols<8>{});
           }
-          const int d0 = c * 8, p = d0 / S::kPanelBytes, cc = (d0 % S::kPanelBytes) / 16;
+          sts32(q_tab + at * 4, fine ? (uint32_t)(127 + down) << 23 : 0x7fffffffu);
+          tmem_wait_store();
+          tc_fence_before();
+        } else {
+          constexpr int kCh = kD / 8;                    // lanes per row, 8 dims each
+          const int pos0 = t.g * A.group_pos;
+          const int rows = min(A.group_pos, A.n_new - pos0) * A.G;
+          for (int e = at; e < kRP * kCh; e += 32 * kAuxWarps) {
+            const int r = e / kCh, c = e % kCh;
+            uint4 val = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows)
+              val = __ldg(reinterpret_cast<const uint4*>(
+                  A.q + ((size_t)t.b * A.n_new + pos0 + r / A.G) * A.q_stride +
+                  (size_t)(t.h * A.G + r % A.G) * kD + c * 8));
+            const uint32_t wv[4] = {val.x, val.y, val.z, val.w};
+            float f[8], amax = 0.f;
+            bool fine = true;
 #pragma unroll
-          for (int copy = 0; copy < S::kCopies; ++copy) {
-            const int rr = copy * kRP + r;
-            const int x = S::kPanelBytes == 128 ? (rr & 7) : ((rr >> 1) & 3);
-            const uint32_t dst = qb + qs * S::kQBytes + p * 128 * S::kPanelBytes + rr * S::kPanelBytes +
-                                 ((cc ^ x) << 4) + (d0 & 8);
-            sts64(dst, hi[0], hi[1]);
-            sts64(dst + S::kQTerm, lo[0], lo[1]);
+            for (int k = 0; k < 8; ++k) {
+              f[k] = __uint_as_float(k & 1 ? wv[k >> 1] & 0xffff0000u : wv[k >> 1] << 16);
+              amax = fmaxf(amax, fabsf(f[k]));
+              fine &= fabsf(f[k]) < INFINITY;
+            }
+#pragma unroll
+            for (int o = kCh / 2; o; o >>= 1) {
+              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+              fine &= __shfl_xor_sync(0xffffffffu, (int)fine, o) != 0;
+            }
+            // largest magnitude -> [2^7, 2^8); a row that holds no numbers is NaN
+            const int down = amax > 0.f && fine ? min(max((int)(__float_as_uint(amax) >> 23) - 134, -100), 120) : 0;
+            const float mul = __uint_as_float((uint32_t)(127 - down) << 23);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t ph[2], pl[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float a = f[4 * k + 2 * x] * mul, b = f[4 * k + 2 * x + 1] * mul;
+                ph[x] = f32_to_e4m3x2(a, b);
+                const uint32_t back = e4m3x2_to_f16x2((uint16_t)ph[x]);
+                const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                pl[x] = f32_to_e4m3x2(a - r2.x, b - r2.y);
+              }
+              hi[k] = ph[0] | (ph[1] << 16);
+              lo[k] = pl[0] | (pl[1] << 16);
+            }
+            const int d0 = c * 8, p = d0 / S::kPanelBytes, cc = (d0 % S::kPanelBytes) / 16;
+#pragma unroll
+            for (int copy = 0; copy < S::kCopies; ++copy) {
+              const int rr = copy * kRP + r;
+              const int x = S::kPanelBytes == 128 ? (rr & 7) : ((rr >> 1) & 3);
+              const uint32_t dst = qb + p * 128 * S::kPanelBytes + rr * S::kPanelBytes +
+                                   ((cc ^ x) << 4) + (d0 & 8);
+              sts64(dst, hi[0], hi[1]);
+              sts64(dst + S::kQTerm, lo[0], lo[1]);
+            }
+            if (c == 0)
+#pragma unroll
+              for (int copy = 0; copy < S::kCopies; ++copy)
+                sts32(q_tab + (copy * kRP + r) * 4, fine ? (uint32_t)(127 + down) << 23 : 0x7fffffffu);
           }
-          if (c == 0)
-            sts32(q_tab + (qs * 128 + r) * 4,
-                  fine ? (uint32_t)(127 + down) << 23 : 0x7fffffffu);
+  fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(qs));
-        ++tl;
-        wl.next(A);
+        if (lane == 0) mbar_arrive(q_full(0));
+        ++nt;
         return true;
       };
-      for (int k = 0; k < kNq; ++k)
-        if (ok && !wl.done()) ok = load_queries();
+      if (!w.done()) ok = load_queries(w);
       int s = 0;
       uint32_t ph = 0, n = 0;
       for (; ok && !w.done(); w.next(A)) {
         for (int i = 0; i < w.n_here; ++i, ++n) {
-          const bool clean = is_clean(w, i);
+          const bool clean = w.clean(i);
           const int j0 = (w.first + w.blk + i) * kBlk;
           if (!(ok = warp_wait(v_full(s), ph))) break;
           if (!(ok = warp_wait(v16_empty(n & 1), ((n >> 1) & 1) ^ 1u))) break;
@@ -745,42 +860,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           // bank conflicts under their swizzles.
           const uint32_t src = ring_v + s * S::kSlotBytes, dst = v16 + (n & 1) * S::kV16Bytes;
           const int pr = lane >> 3, row8 = (lane & 4) ? pr ^ 5 : pr;
-          constexpr int kQuads = kD / 64;
-#pragma unroll 4
-          for (int e = warp - kSoftWarps; e < kBlk / 8 * kQuads; e += kAuxWarps) {
-            const int j = (e / kQuads) * 8 + row8, c = (e % kQuads) * 4 + (lane & 3);
-            constexpr int per = S::kPanelBytes / 16;
-            const int x = S::kPanelBytes == 128 ? (j & 7) : ((j >> 1) & 3);
-            const uint4 v = lds128(src + (c / per) * kBlk * S::kPanelBytes + j * S::kPanelBytes +
-                                   (((c % per) ^ x) << 4));
-            const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[8];
+          constexpr int kQuads = kD / 64, kPer = S::kPanelBytes / 16;
+          constexpr int kSteps = kBlk / 8 * kQuads / kAuxWarps, kBatch = kSteps < 8 ? kSteps : 8;
+#pragma unroll 1
+          for (int e0 = warp - kSoftWarps; e0 < kBlk / 8 * kQuads; e0 += kAuxWarps * kBatch) {
+            uint4 v[kBatch];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              h[2 * k] = e4m3x2_to_f16x2((uint16_t)wv[k]);
-              h[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(wv[k] >> 16));
+            for (int x = 0; x < kBatch; ++x) {
+              const int e = e0 + x * kAuxWarps, j = (e / kQuads) * 8 + row8, c = (e % kQuads) * 4 + (lane & 3);
+              const int sw = S::kPanelBytes == 128 ? (j & 7) : ((j >> 1) & 3);
+              v[x] = lds128(src + (c / kPer) * kBlk * S::kPanelBytes + j * S::kPanelBytes +
+                            (((c % kPer) ^ sw) << 4));
             }
-            if (!clean) {
-              // Rows past the sequence hold anything, and a NaN in a row that
-              // not every query sees would pass a zero probability: neither
-              // enters the product. The epilogue adds the NaN where seen.
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                if (j0 + j >= w.L) h[k] = 0u;
-                if ((h[k] & 0x7c00u) == 0x7c00u) {
-                  h[k] &= 0xffff0000u;
-                  *odd = 1;
-                }
-                if ((h[k] & 0x7c000000u) == 0x7c000000u) {
-                  h[k] &= 0x0000ffffu;
-                  *odd = 1;
+            for (int x = 0; x < kBatch; ++x) {
+              const int e = e0 + x * kAuxWarps, j = (e / kQuads) * 8 + row8, c = (e % kQuads) * 4 + (lane & 3);
+              const uint32_t wv[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+              uint32_t h[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                h[2 * k] = e4m3x2_to_f16x2((uint16_t)wv[k]);
+                h[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(wv[k] >> 16));
+              }
+              if (!clean) {
+                // Rows past the sequence hold anything, and a NaN in a row that
+                // not every query sees would pass a zero probability: neither
+                // enters the product. The epilogue adds the NaN where seen.
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  if (j0 + j >= w.L) h[k] = 0u;
+                  if ((h[k] & 0x7c00u) == 0x7c00u) {
+                    h[k] &= 0xffff0000u;
+                    *odd = 1;
+                  }
+                  if ((h[k] & 0x7c000000u) == 0x7c000000u) {
+                    h[k] &= 0x0000ffffu;
+                    *odd = 1;
+                  }
                 }
               }
+              const uint32_t to = dst + (c >> 2) * kBlk * 128 + j * 128;
+              const int c2 = (2 * c) & 7;
+              sts128(to + ((c2 ^ (j & 7)) << 4), h[0], h[1], h[2], h[3]);
+              sts128(to + (((c2 + 1) ^ (j & 7)) << 4), h[4], h[5], h[6], h[7]);
             }
-            const uint32_t to = dst + (c >> 2) * kBlk * 128 + j * 128;
-            const int c2 = (2 * c) & 7;
-            sts128(to + ((c2 ^ (j & 7)) << 4), h[0], h[1], h[2], h[3]);
-            sts128(to + (((c2 + 1) ^ (j & 7)) << 4), h[4], h[5], h[6], h[7]);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -793,7 +916,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1u;
           }
         }
-        if (ok && !wl.done()) ok = load_queries();
+        if (!ok) break;
+        Walk<kBlk> then = w;
+        then.next(A);
+        if (!then.done()) ok = load_queries(then);
       }
     } else {
       // bf16 values are multiplied as they land; only blocks with rows that
@@ -805,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // every block is waited for, and released, so that this loop and the
           // ring never part by more than the ring's length
           if (!(ok = warp_wait(v_full(s), ph))) break;
-          if (!is_clean(w, i)) {
+          if (!w.clean(i)) {
             const int j0 = (w.first + w.blk + i) * kBlk;
             for (int e = at; e < S::kSlotBytes / 16; e += 32 * kAuxWarps) {
               const int j = (e >> 3) % kBlk;
@@ -846,15 +972,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ----------------------------------------------------------- softmax --
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);      // this warp's lanes
-    const int row = (warp * 32 + lane) % kRP, copy = warp * 32 / kRP;
-    constexpr int kSub = kKpl > 32 ? kKpl / 32 : 1;                // 32-row pieces of a lane's keys
-    constexpr int kSubKeys = kKpl / kSub;
+    const int lg = warp * 32 + lane, row = lg % kRP, copy = warp * 32 / kRP;
+    // A lane's keys of a block: at once up to 64, in pieces of 32 above (a
+    // piece's scores are read twice then, rather than held).
+    constexpr int kPiece = kKpl <= 64 ? kKpl : 32, kPieces = kKpl / kPiece;
+    constexpr int kSubKeys = kKpl < 32 ? kKpl : 32, kSubs = kKpl / kSubKeys;   // runs with one scale
     bool dead = false;                   // a wait ran out: keep to the barriers, compute nothing
     uint32_t n = 0, nt = 0;
     if constexpr (S::kCopies > 1) {
       const uint32_t zero[32] = {};
 #pragma unroll
-      for (int c = 0; c < kBlk; c += 32) tmem_store(tl + S::kColP + c, zero, Cols<32>{});
+      for (int c = 0; c < S::kPBufs * (kBlk / 2); c += 32) tmem_store(tl + S::kColP + c, zero, Cols<32>{});
       tmem_wait_store();
     }
     for (; !w.done(); w.next(A), ++nt) {
@@ -883,109 +1011,113 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int a = 0; a < 32 && 32 * k + a < A.n_new; ++a)
             if (dep - (int)lds32(tree + 128 * 16 + (32 * k + a) * 4) >= A.window) sight.v[k] &= ~(1u << a);
       }
-      float ck = A.scale;
-      if constexpr (kE4m3) {
-        const int qs = nt % kNq;
-        if (!dead && !warp_wait(q_full(qs), (nt / kNq) & 1)) dead = true;
-        ck *= __uint_as_float(lds32(q_tab + (qs * 128 + row) * 4));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_empty(qs));
-      }
-      if (!kExtra) ck *= kLog2e;
       const float slope = kExtra && A.slopes ? A.slopes[w.h * A.G + gq] * kLog2e : 0.f;
-
-      float m_ref = -INFINITY, l = 0.f;
       const int key0 = copy * kKpl;                                // this copy's first key of a block
-      float sk_next[kSub], sv_next[kSub];
+      const float* ks = nullptr;
+      const float* vs = nullptr;
+      float sk_next[kSubs], sv_next[kSubs];
       auto load_scales = [&](int j) {
         if constexpr (kE4m3) {
-          const size_t so = ((size_t)w.b * A.Hkv + w.h) * A.n_scale;
 #pragma unroll
-          for (int x = 0; x < kSub; ++x) {
+          for (int x = 0; x < kSubs; ++x) {
             const int jj = j + x * kSubKeys;
-            sk_next[x] = jj < w.L ? __ldg(A.k_scale + so + jj / SPECDEC_KV8_BLOCK) : 1.f;
-            sv_next[x] = jj < w.L ? __ldg(A.v_scale + so + jj / SPECDEC_KV8_BLOCK) : 1.f;
+            sk_next[x] = jj < w.L ? __ldg(ks + jj / SPECDEC_KV8_BLOCK) : 1.f;
+            sv_next[x] = jj < w.L ? __ldg(vs + jj / SPECDEC_KV8_BLOCK) : 1.f;
           }
         }
       };
-      load_scales((w.first + w.blk) * kBlk + key0);
+      float ck = A.scale;
+      if constexpr (kE4m3) {
+        const size_t so = ((size_t)w.b * A.Hkv + w.h) * A.n_scale;
+        ks = A.k_scale + so;
+        vs = A.v_scale + so;
+        load_scales((w.first + w.blk) * kBlk + key0);
+        if (!dead && !warp_wait(q_full(0), nt & 1)) dead = true;
+        ck *= __uint_as_float(lds32(q_tab + lg * 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty(0));
+      }
+      if (!kExtra) ck *= kLog2e;
 
-      for (int ib = 0; ib < w.n_here; ++ib, ++n) {
-        const int j0 = (w.first + w.blk + ib) * kBlk + key0;
-        const bool clean = is_clean(w, ib);
-        float sk[kSub], sv[kSub];
-        if constexpr (kE4m3) {
+      float m_ref = -INFINITY, l = 0.f;
+      int j0 = (w.first + w.blk) * kBlk + key0;
+      for (int ib = 0; ib < w.n_here; ++ib, ++n, j0 += kBlk) {
+        const bool clean = w.clean(ib);
+        float cs[kSubs], lv[kSubs], inv_sv[kSubs];                 // per run: score factor, log2 s_v, 1 / s_v
 #pragma unroll
-          for (int x = 0; x < kSub; ++x) {
-            sk[x] = sk_next[x];
-            sv[x] = sv_next[x];
+        for (int x = 0; x < kSubs; ++x) {
+          cs[x] = ck;
+          lv[x] = 0.f;
+          inv_sv[x] = 1.f;
+          if constexpr (kE4m3) {
+            cs[x] = ck * sk_next[x];
+            if (cs[x] < 1e-37f) cs[x] = 1e-37f;                    // -inf times it stays -inf (NaN stays too)
+            lv[x] = __log2f(sv_next[x]);
+            inv_sv[x] = rcp(sv_next[x]);
           }
-          if (ib + 1 < w.n_here) load_scales(j0 + kBlk);
         }
+        if (kE4m3 && ib + 1 < w.n_here) load_scales(j0 + kBlk);
         if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
         if (dead) continue;
         tc_fence_after();
-        // ---- this lane's scores, as exponents ----
+        const uint32_t from = tl + S::kColS + (n & 1) * kBlk + key0;
         union {
-          uint32_t u[kKpl];
-          float f[kKpl];
+          uint32_t u[kPiece];
+          float f[kPiece];
         } x;
-        {
-          const uint32_t from = tl + S::kColS + (n & 1) * kBlk + key0;
-          if constexpr (kKpl == 128) {
-            tmem_load(from, *reinterpret_cast<uint32_t(*)[64]>(&x.u[0]));
-            tmem_load(from + 64, *reinterpret_cast<uint32_t(*)[64]>(&x.u[64]));
-          } else {
-            tmem_load(from, x.u);
-          }
-        }
+        // ---- masks, cap and bias; the lane's largest exponent ----
         float top = -INFINITY;
 #pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          float* const y = x.f + sub * kSubKeys;
-          const float lv = kE4m3 ? __log2f(sv[sub]) : 0.f;
-          const float c = kE4m3 ? ck * sk[sub] : ck;
-          const int js = j0 + sub * kSubKeys;
-          if constexpr (kExtra) {
+        for (int pc = 0; pc < kPieces; ++pc) {
+          tmem_load(from + pc * kPiece, x.u);
 #pragma unroll
-            for (int k = 0; k < kSubKeys; ++k) {
-              float z = y[k] * c;
-              // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
-              if (A.cap > 0.f) z = A.cap * (1.f - 2.f * rcp(1.f + ex2(z * A.cap_exp)));
-              y[k] = fmaf(z, kLog2e, lv);
-            }
-            if (A.slopes) {
-              // bias slope * (pos_j - pos_i); tree nodes stand at their depth
-              const float base = (float)(js - P0 - dep);
-              if (clean || !A.tree) {
+          for (int sub = 0; sub < kPiece / kSubKeys; ++sub) {
+            float* const y = x.f + sub * kSubKeys;
+            const int xs = pc * (kPiece / kSubKeys) + sub, js = j0 + xs * kSubKeys;
+            if constexpr (kExtra) {
+              if (A.cap > 0.f) {
+                // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
+                const float in = cs[xs] * A.cap_exp, out = -2.f * A.cap * kLog2e, add = A.cap * kLog2e + lv[xs];
 #pragma unroll
-                for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(slope, base + (float)k, y[k]);
+                for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(out, rcp(1.f + ex2(y[k] * in)), add);
               } else {
 #pragma unroll
-                for (int k = 0; k < kSubKeys; ++k) {
-                  int pj = js + k - P0;
-                  if (pj >= 0) pj = (int)lds32(tree + 128 * 16 + min(pj, A.n_new - 1) * 4);
-                  y[k] = fmaf(slope, (float)(pj - dep), y[k]);
+                for (int k = 0; k < kSubKeys; k += 2) fma2(y[k], y[k + 1], cs[xs] * kLog2e, lv[xs]);
+              }
+              if (A.slopes) {
+                // bias slope * (pos_j - pos_i); tree nodes stand at their depth
+                if (!A.tree || js + kSubKeys <= P0) {
+                  const float base = (float)(js - P0 - dep);
+#pragma unroll
+                  for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(slope, base + (float)k, y[k]);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < kSubKeys; ++k) {
+                    int pj = js + k - P0;
+                    if (pj >= 0) pj = (int)lds32(tree + 128 * 16 + min(pj, A.n_new - 1) * 4);
+                    y[k] = fmaf(slope, (float)(pj - dep), y[k]);
+                  }
                 }
               }
             }
-          } else if constexpr (kE4m3) {
+            if (!clean) {
+              const uint32_t m = sight.mask(js);
 #pragma unroll
-            for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(y[k], c, lv);
-          } else {
+              for (int k = 0; k < kSubKeys; ++k) y[k] = (m >> k) & 1u ? y[k] : -INFINITY;
+            }
+            float t0 = max3(y[0], y[1], y[2]), t1 = max3(y[3], y[4], y[5]);
 #pragma unroll
-            for (int k = 0; k < kSubKeys; ++k) y[k] *= c;
+            for (int k = 6; k + 3 < kSubKeys; k += 4) {
+              t0 = max3(t0, y[k], y[k + 1]);
+              t1 = max3(t1, y[k + 2], y[k + 3]);
+            }
+            t0 = max3(t0, y[kSubKeys - 2], y[kSubKeys - 1]);
+            t0 = fmaxf(t0, t1);
+            top = fmaxf(top, kExtra ? t0 : fmaf(t0, cs[xs], lv[xs]));
           }
-          if (!clean) {
-            const uint32_t m = sight.mask(js);
-#pragma unroll
-            for (int k = 0; k < kSubKeys; ++k) y[k] = (m >> k) & 1u ? y[k] : -INFINITY;
-          }
-          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int k = 0; k < kSubKeys; ++k) t4[k & 3] = fmaxf(t4[k & 3], y[k]);
-          top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+          if (kPieces > 1 && (kExtra || !clean)) tmem_store(from + pc * kPiece, x.u, Cols<kPiece>{});
         }
+        if (kPieces > 1 && (kExtra || !clean)) tmem_wait_store();
         // ---- the reference follows the maximum when it has to ----
         const bool need = mine && top > m_ref + kHeadroom;
         if (__any_sync(0xffffffffu, need)) {
@@ -999,13 +1131,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < kD; c += 32) {
-              uint32_t v[32];
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) {
+              uint32_t v[16];
               tmem_load(tl + S::kColO + c, v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-              tmem_store(tl + S::kColO + c, v, Cols<32>{});
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+              tmem_store(tl + S::kColO + c, v, Cols<16>{});
             }
             tmem_wait_store();
           }
@@ -1014,31 +1146,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         // f16 ones are kept 2^7 high: the headroom's 2^8 above that still fits,
         // and small weights stay normal numbers down to 2^-21.
         const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - (kE4m3 ? 7.f : 0.f);
-        uint32_t pk[kKpl / 2];
+        // Exponents of 2^20 and more are rounded before the subtraction, as the
+        // reference was: a fused one would bring out the reference's rounding.
+        const bool large = !kExtra && __any_sync(0xffffffffu, fabsf(mu) >= 1048576.f);
 #pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          float sum[2] = {0.f, 0.f};
+        for (int pc = 0; pc < kPieces; ++pc) {
+          if (kPieces > 1) tmem_load(from + pc * kPiece, x.u);
+          uint32_t pk[kPiece / 2];
 #pragma unroll
-          for (int k = 0; k < kSubKeys; k += 2) {
-            const float p0 = ex2(x.f[sub * kSubKeys + k] - mu), p1 = ex2(x.f[sub * kSubKeys + k + 1] - mu);
-            const uint32_t u = pack2<kE4m3>(p0, p1);
-            pk[(sub * kSubKeys + k) / 2] = u;
-            // The sum takes bf16 weights as rounded: their error then moves
-            // the output by w (v - o) only. The f16 rounding is left out of it.
-            if constexpr (kE4m3) {
-              sum[0] += p0;
-              sum[1] += p1;
-            } else {
-              sum[0] += __uint_as_float(u << 16);
-              sum[1] += __uint_as_float(u & 0xffff0000u);
+          for (int sub = 0; sub < kPiece / kSubKeys; ++sub) {
+            float* const y = x.f + sub * kSubKeys;
+            const int xs = pc * (kPiece / kSubKeys) + sub;
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < kSubKeys; k += 2) {
+              if (!kExtra && !large) {
+                fma2(y[k], y[k + 1], cs[xs], lv[xs] - mu);
+              } else {
+                if (!kExtra) fma2(y[k], y[k + 1], cs[xs], lv[xs]);
+                add2(y[k], y[k + 1], -mu, -mu);
+              }
+              const float p0 = ex2(y[k]), p1 = ex2(y[k + 1]);
+              const uint32_t u = pack2<kE4m3>(p0, p1);
+              pk[(sub * kSubKeys + k) / 2] = u;
+              // The sum takes bf16 weights as rounded: their error then moves
+              // the output by w (v - o) only. The f16 rounding is left out of it.
+              if constexpr (kE4m3)
+                add2(s0, s1, p0, p1);
+              else
+                add2(s0, s1, __uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
             }
+            l = kE4m3 ? fmaf(s0 + s1, inv_sv[xs], l) : l + (s0 + s1);
           }
-          if constexpr (kE4m3)
-            l = fmaf(sum[0] + sum[1], rcp(sv[sub]), l);
-          else
-            l += sum[0] + sum[1];
+          // the product that last read this P buffer is done
+          if (pc == 0 && n >= S::kPBufs &&
+              !warp_wait(o_done((n - S::kPBufs) & 1), ((n - S::kPBufs) >> 1) & 1)) {
+            dead = true;
+            break;
+          }
+          tmem_store(tl + S::kColP + (S::kPBufs == 2 ? (n & 1) * (kBlk / 2) : 0) + (key0 + pc * kPiece) / 2, pk,
+                     Cols<kPiece / 2>{});
         }
-        tmem_store(tl + S::kColP + (n & 1) * (kBlk / 2) + key0 / 2, pk, Cols<kKpl / 2>{});
+        if (dead) continue;
         tmem_wait_store();
         tc_fence_before();
         __syncwarp();
@@ -1046,72 +1195,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- the tile's output, or this part's share of it ----
-      if (!dead && !warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
-      tc_fence_after();
       const bool whole = w.blk == 0 && w.n_here == w.nb;
       const size_t slot = (size_t)blockIdx.x * 2 + (w.u == part0 ? 0 : 1);
-      // Infinities and NaN that were held back from the product (rare), for
-      // the rows that see them.
-      auto add_odd = [&](float (&v)[32], int c0) {
-        for (int ib = 0; ib < w.n_here; ++ib) {
-          if (is_clean(w, ib)) continue;
-          const int j0 = (w.first + w.blk + ib) * kBlk + key0;
-          for (int k = 0; k < kKpl && j0 + k < w.L; ++k) {
-            const bool seen = mine && (sight.mask(j0 + k) & 1u);
-            const size_t from = (((size_t)w.b * A.Lmax + j0 + k) * A.Hkv + w.h) * kD + c0;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              float val;
-              if constexpr (kE4m3) {
-                const uint8_t code = static_cast<const uint8_t*>(A.v)[from + c];
-                val = (code & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : 0.f;
-              } else {
-                const uint32_t u = static_cast<const uint16_t*>(A.v)[from + c];
-                val = (u & 0x7f80u) == 0x7f80u ? __uint_as_float(u << 16) : 0.f;
-              }
-              if (seen && val != 0.f) v[c] += val;
-            }
-          }
-        }
-      };
-      const bool has_odd = *odd != 0;
-      if constexpr (S::kCopies == 1) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);       // NaN stays
-        const size_t at_row =
-            (((size_t)w.b * A.n_new + idx) * A.Hq + (size_t)w.h * A.G + gq) * kD;
-#pragma unroll 1
-        for (int c0 = 0; c0 < kD; c0 += 32) {
-          if (dead) break;
-          uint32_t u[32];
-          tmem_load(tl + S::kColO + c0, u);
-          float v[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
-          if (has_odd) add_odd(v, c0);
-          if (!mine) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(A.out + at_row + c0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[k] = make_uint4(pack2<false>(v[8 * k] * inv, v[8 * k + 1] * inv),
-                                  pack2<false>(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                                  pack2<false>(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
-                                  pack2<false>(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(A.part_o + (slot * kRP + row) * kD + c0);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          }
-        }
-        if (!whole && mine && !dead)
-          *reinterpret_cast<float2*>(A.part_ml + (slot * kRP + row) * 2) = make_float2(m_ref, l);
-      } else {
-        // Merge the copies through shared memory, 32 columns at a time.
-        const int lg = warp * 32 + lane;
+      float wgt = 1.f, lt = l, M = m_ref;
+      if constexpr (S::kCopies > 1) {
+        // merge the copies: weights from their references
         sts64(ml_tab + lg * 8, __float_as_uint(m_ref), __float_as_uint(l));
         named_bar_sync(1, 32 * kSoftWarps);
-        float M = -INFINITY, lt = 0.f;
+        M = -INFINITY;
+        lt = 0.f;
 #pragma unroll
         for (int c = 0; c < S::kCopies; ++c)
           M = fmaxf(M, __uint_as_float(lds32(ml_tab + (c * kRP + row) * 8)));
@@ -1120,67 +1212,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < S::kCopies; ++c)
           lt += __uint_as_float(lds32(ml_tab + (c * kRP + row) * 8 + 4)) *
                 ex2(__uint_as_float(lds32(ml_tab + (c * kRP + row) * 8)) - Mu);
-        const float wgt = ex2(m_ref - Mu);
-        const float inv = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);
-        constexpr int kPer = 32 / S::kCopies;                    // columns a thread sums
-        const size_t at_row =
-            (((size_t)w.b * A.n_new + idx) * A.Hq + (size_t)w.h * A.G + gq) * kD;
+        wgt = ex2(m_ref - Mu);
+      }
+      if (whole) wgt *= lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);     // NaN stays
+      if (!whole && mine && !dead && copy == 0)
+        *reinterpret_cast<float2*>(A.part_ml + (slot * kRP + row) * 2) = make_float2(M, lt);
+      if (!dead && !warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
+      tc_fence_after();
+      const bool has_odd = *odd != 0;
+      // 32 columns at a time through shared memory, so that copies add up and
+      // rows are written in whole lines: thread (r4, c4) writes 4 columns.
 #pragma unroll 1
-        for (int c0 = 0; c0 < kD; c0 += 32) {
-          if (!dead) {
-            uint32_t u[32];
-            tmem_load(tl + S::kColO + c0, u);
-            float v[32];
+      for (int c0 = 0; c0 < kD; c0 += 32) {
+        if (!dead) {
+          uint32_t u[32];
+          tmem_load(tl + S::kColO + c0, u);
+          if (has_odd) {
+            // Infinities and NaN that were held back from the product (rare),
+            // for the rows that see them.
+            for (int ib = 0; ib < w.n_here; ++ib) {
+              if (w.clean(ib)) continue;
+              const int jb = (w.first + w.blk + ib) * kBlk + key0;
+              for (int k = 0; k < kKpl && jb + k < w.L; ++k) {
+                const bool seen = mine && (sight.mask(jb + k) & 1u);
+                const size_t at = (((size_t)w.b * A.Lmax + jb + k) * A.Hkv + w.h) * kD + c0;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
-            if (has_odd) add_odd(v, c0);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) sts32(stage + (lg * 33 + k) * 4, __float_as_uint(v[k] * wgt));
-          }
-          named_bar_sync(1, 32 * kSoftWarps);
-          // thread (row, copy) sums columns copy * kPer ..
-          float v[kPer];
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            v[k] = 0.f;
-#pragma unroll
-            for (int c = 0; c < S::kCopies; ++c)
-              v[k] += __uint_as_float(lds32(stage + ((c * kRP + row) * 33 + copy * kPer + k) * 4));
-          }
-          if (mine && !dead) {
-            if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(A.out + at_row + c0 + copy * kPer);
-#pragma unroll
-              for (int k = 0; k < kPer / 8; ++k)
-                dst[k] = make_uint4(pack2<false>(v[8 * k] * inv, v[8 * k + 1] * inv),
-                                    pack2<false>(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                                    pack2<false>(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
-                                    pack2<false>(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
-            } else {
-              float4* dst =
-                  reinterpret_cast<float4*>(A.part_o + (slot * kRP + row) * kD + c0 + copy * kPer);
-#pragma unroll
-              for (int k = 0; k < kPer / 4; ++k)
-                dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                for (int c = 0; c < 32; ++c) {
+                  uint32_t bits;
+                  bool is_odd;
+                  if constexpr (kE4m3) {
+                    is_odd = (static_cast<const uint8_t*>(A.v)[at + c] & 0x7fu) == 0x7fu;
+                    bits = 0x7fffffffu;
+                  } else {
+                    bits = (uint32_t)static_cast<const uint16_t*>(A.v)[at + c] << 16;
+                    is_odd = (bits & 0x7f800000u) == 0x7f800000u;
+                  }
+                  if (seen && is_odd) u[c] = __float_as_uint(__uint_as_float(u[c]) + __uint_as_float(bits));
+                }
+              }
             }
           }
-          named_bar_sync(1, 32 * kSoftWarps);
+          const uint32_t to = stage + lg * kStagePitch;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            sts128(to + k * 4, __float_as_uint(__uint_as_float(u[k]) * wgt),
+                   __float_as_uint(__uint_as_float(u[k + 1]) * wgt),
+                   __float_as_uint(__uint_as_float(u[k + 2]) * wgt),
+                   __float_as_uint(__uint_as_float(u[k + 3]) * wgt));
         }
-        if (!whole && mine && !dead && copy == 0)
-          *reinterpret_cast<float2*>(A.part_ml + (slot * kRP + row) * 2) = make_float2(M, lt);
+        if constexpr (S::kCopies > 1)
+          named_bar_sync(1, 32 * kSoftWarps);
+        else
+          __syncwarp();
+        const int c4 = (lane & 7) * 4;
+        constexpr int kRowStep = S::kCopies > 1 ? 16 : 4;        // rows written at a time by who shares them
+        const int r0 = S::kCopies > 1 ? warp * 4 : warp * 32;
+        const int r_end = min(rows_here, S::kCopies > 1 ? kRP : warp * 32 + 32);
+        for (int r = r0 + (lane >> 3); r < r_end; r += kRowStep) {
+          float4 v = lds128f(stage + r * kStagePitch + c4 * 4);
+#pragma unroll
+          for (int c = 1; c < S::kCopies; ++c) {
+            const float4 y = lds128f(stage + (c * kRP + r) * kStagePitch + c4 * 4);
+            v.x += y.x;
+            v.y += y.y;
+            v.z += y.z;
+            v.w += y.w;
+          }
+          if (dead) continue;
+          if (whole) {
+            const int i = pos0 + r / A.G;
+            *reinterpret_cast<uint2*>(A.out + (((size_t)w.b * A.n_new + i) * A.Hq + (size_t)w.h * A.G + r % A.G) * kD +
+                                      c0 + c4) = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+          } else {
+            *reinterpret_cast<float4*>(A.part_o + (slot * kRP + r) * kD + c0 + c4) = v;
+          }
+        }
+        if constexpr (S::kCopies > 1)
+          named_bar_sync(1, 32 * kSoftWarps);
+        else
+          __syncwarp();
       }
     }
   }
   tc_fence_before();
   __syncthreads();   // every role has left its loop
   tc_fence_after();
-  if (warp == kIssuer) tmem_dealloc(tmem, 512);
-  if (*abort && warp == kProducer && lane == 0)
+  if (warp == kIssuerO) tmem_dealloc(tmem, 512);
+  if (*abort && lane == 0)
     // A wait gave up: let every copy already issued land before the CTA exits.
     for (int s = 0; s < kR; ++s) {
-      if (issued[0] & (1u << s)) wait_drain(k_full(s), (issued_phase[0] >> s) & 1u);
-      if (issued[1] & (1u << s)) wait_drain(v_full(s), (issued_phase[1] >> s) & 1u);
-      if (!kE4m3 && s < kNq && (issued[2] & (1u << s))) wait_drain(q_full(s), (issued_phase[2] >> s) & 1u);
+      if (issued & (1u << s))
+        wait_drain(warp == kProducerV ? v_full(s) : k_full(s), (issued_phase >> s) & 1u);
+      if (issued_q & (1u << s)) wait_drain(q_full(s), (issued_q_phase >> s) & 1u);
     }
 }
 
@@ -1190,21 +1313,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool kE4m3, int kD, int kRP>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CacheAttnLaunch A, int n_ctas) {
   constexpr int kBlk = cache_attn_block(kE4m3, kD);
-  __shared__ long long sh_before[8], sh_total[8];
+  __shared__ int sh_before[8], sh_total[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x;
   const int grp = tile % A.n_groups;
   const int h = tile / A.n_groups % A.Hkv;
   const int b = tile / A.n_groups / A.Hkv;
-  grid_dependency_wait();
-  long long before = 0, total = 0;
+  // The schedule again (the lengths were there before the attention kernel
+  // let this one start), then its partials.
+  int before = 0, total = 0, first;
+  bool bad;
   for (int x = threadIdx.x; x < A.B; x += 256) {
-    int first;
-    bool bad;
-    const int nb = seq_blocks<kBlk>(A, A.seq_lens[x], first, bad);
-    total += nb;
-    if (x < b) before += nb;
+    const int u = tile_units(seq_blocks<kBlk>(A, A.seq_lens[x], first, bad));
+    total += u;
+    if (x < b) before += u;
   }
+  const int nb = seq_blocks<kBlk>(A, A.seq_lens[b], first, bad);
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -1221,14 +1345,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
     before += sh_before[x];
     total += sh_total[x];
   }
-  int first;
-  bool bad;
-  const int nb = seq_blocks<kBlk>(A, A.seq_lens[b], first, bad);
-  const long long per = (long long)A.Hkv * A.n_groups;
+  const int per = A.Hkv * A.n_groups;
   total *= per;
-  const long long u0 = before * per + (long long)(h * A.n_groups + grp) * nb;
+  const int u0 = before * per + (h * A.n_groups + grp) * tile_units(nb);
   const int pos0 = grp * A.group_pos;
   const int r = blockIdx.y * 8 + warp;
+  grid_dependency_wait();
   if (r >= min(A.group_pos, A.n_new - pos0) * A.G) return;
   constexpr int kPer = kD / 32;
   __nv_bfloat16* dst = A.out +
@@ -1239,25 +1361,24 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
   float inv = 0.f;
   if (nb > 0) {
-    // CTA c owns unit u iff part_begin(c) <= u < part_begin(c + 1)
-    const int c0 = (int)(((u0 + 1) * n_ctas - 1) / total);
-    const int c1 = (int)(((u0 + nb) * n_ctas - 1) / total);
+    // CTA c owns unit u iff part_begin(c) <= u < part_begin(c + 1); the tile's
+    // blocks are its units from u0 + kTileCost on.
+    auto owner = [&](int u) { return (int)(((long long)(u + 1) * n_ctas - 1) / total); };
+    const int c0 = owner(u0 + kTileCost), c1 = owner(u0 + kTileCost + nb - 1);
     if (c0 == c1) return;                        // its CTA wrote the output
+    // CTA c0's part may have begun before the tile: then it is its second partial
+    auto slot_of = [&](int c) { return (size_t)c * 2 + (c == c0 && part_begin(total, c, n_ctas) < u0 ? 1 : 0); };
+    auto empty = [&](int c) { return part_begin(total, c, n_ctas) == part_begin(total, c + 1, n_ctas); };
     float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const long long pb = part_begin(total, c, n_ctas);
-      if (pb == part_begin(total, c + 1, n_ctas)) continue;
-      const size_t slot = (size_t)c * 2 + (c == c0 && pb != u0 ? 1 : 0);
-      M = fmaxf(M, A.part_ml[(slot * kRP + r) * 2]);
-    }
+    for (int c = c0 + lane; c <= c1; c += 32)
+      if (!empty(c)) M = fmaxf(M, A.part_ml[(slot_of(c) * kRP + r) * 2]);
     M = warp_max(M);
     const float mu = M == -INFINITY ? 0.f : M;
     float l = 0.f;
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
-      const long long pb = part_begin(total, c, n_ctas);
-      if (pb == part_begin(total, c + 1, n_ctas)) continue;
-      const size_t slot = (size_t)c * 2 + (c == c0 && pb != u0 ? 1 : 0);
+      if (empty(c)) continue;
+      const size_t slot = slot_of(c);
       const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + (slot * kRP + r) * 2);
       const float wgt = ex2(ml.x - mu);
       l += ml.y * wgt;
@@ -1291,7 +1412,7 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
     if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
   }
   const long long tiles = (long long)A.B * A.Hkv * A.n_groups;
-  const long long most = tiles * ((A.Lmax + S::kBlk - 1) / S::kBlk);
+  const long long most = tiles * ((A.Lmax + S::kBlk - 1) / S::kBlk + kTileCost);
   const int grid = (int)(most < kCacheAttnCtas ? most : kCacheAttnCtas);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
