@@ -6,9 +6,6 @@ the call a user makes.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
-
 import torch
 
 from . import _binding as _b
@@ -211,60 +208,6 @@ def verify_attention(q, k_cache, v_cache, seq_lens, scale=0.0, out=None, workspa
 KV8_BLOCK = _b.SPECDEC_KV8_BLOCK
 
 
-def _on(dev, stream):
-    """Context in which a call allocates and launches: the caller's stream, else the current stream
-    of the tensors' device. (Scratch allocated here belongs to that stream.)"""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
-
-
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on one CUDA device")
-
-
-def _row_stride(t, what):
-    """Elements between consecutive positions of t [B, n, H, D], whose sequences follow each other
-    at n times that (a contiguous tensor, or a slice of a fused projection)."""
-    B, n, H, D = t.shape
-    sb, sn, sh, sd = t.stride()
-    if n == 1 and B > 1:
-        sn = sb
-    elif n == 1:
-        sn = H * D
-    if ((sd != 1 and D > 1) or (sh != D and H > 1) or (sb != n * sn and B > 1) or sn < H * D
-            or sn % 8 != 0):
-        raise ValueError(f"{what}: the heads of a position must be contiguous, positions a multiple "
-                         "of 8 elements apart and sequences n positions apart")
-    return sn
-
-
-def _check_kv8_cache(k_cache, v_cache, k_scale, v_scale):
-    for t in (k_cache, v_cache):
-        if t.dtype != torch.float8_e4m3fn or t.dim() != 4 or not t.is_contiguous() or not t.is_cuda:
-            raise TypeError("the caches must be contiguous float8_e4m3fn CUDA tensors [B, Lmax, Hkv, D]")
-    B, Lmax, Hkv, _ = k_cache.shape
-    want = (B, Hkv, -(-Lmax // KV8_BLOCK))
-    for t in (k_scale, v_scale):
-        if t.dtype != torch.float32 or not t.is_contiguous():
-            raise TypeError("the scales must be contiguous float32 CUDA tensors")
-        if t.shape != want:
-            raise ValueError(f"the scales must have shape [B, Hkv, ceil(Lmax / {KV8_BLOCK})]")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape")
-
-
-def _check_ints(t, shape, what):
-    if t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda:
-        raise TypeError(f"{what} must be a contiguous int32 CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {list(shape)}")
-
-
 def alloc_kv8_cache(B, Lmax, Hkv, D, device=None):
     """(k_cache, v_cache, k_scale, v_scale) of an empty 8-bit cache: float8_e4m3fn codes
     [B, Lmax, Hkv, D] and float32 scales [B, Hkv, ceil(Lmax / KV8_BLOCK)]."""
@@ -287,28 +230,10 @@ def append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts=N
     verified tree's rows by its accepted path's. Writes the cache in place and returns
     (k_cache, v_cache, k_scale, v_scale).
     """
-    if k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16 or not k_new.is_cuda:
-        raise TypeError("k_new and v_new must be bfloat16 CUDA tensors")
-    _check_kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    B, n, Hkv, D = k_new.shape
-    Lmax = k_cache.shape[1]
-    if v_new.shape != k_new.shape or k_cache.shape != (B, Lmax, Hkv, D):
-        raise ValueError("k_new and v_new must be [B, n, Hkv, D] for a cache [B, Lmax, Hkv, D]")
-    _check_ints(start, (B,), "start")
-    if counts is not None:
-        _check_ints(counts, (B,), "counts")
-    if rows is not None:
-        _check_ints(rows, (B, n), "rows")
-    dev = k_new.device
-    _same_device(dev, v_new, k_cache, v_cache, k_scale, v_scale, start, counts, rows, workspace)
-    ks, vs = _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new")
-    with _on(dev, stream):
-        if workspace is None:
-            workspace = torch.empty(_b.specdec_kv8_append_workspace_size(), dtype=torch.uint8, device=dev)
-        rc = _b.specdec_kv8_append(k_new.data_ptr(), ks, v_new.data_ptr(), vs, start.data_ptr(),
-                                   _ptr(counts), _ptr(rows), B, n, Hkv, D, Lmax, k_cache.data_ptr(),
-                                   v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                   workspace.data_ptr(), workspace.numel(), _stream_ptr(None))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts, rows, workspace)
+    rc = _b.native().append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts, rows, workspace)
     if rc != 0:
         _b._check(rc, "specdec_kv8_append")
     return k_cache, v_cache, k_scale, v_scale
@@ -317,48 +242,6 @@ def append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts=N
 def cache_attention_workspace_bytes(B, n_new, Hq, Hkv, D, Lmax) -> int:
     """Workspace of verify_attention_kv8 and verify_attention_masked."""
     return _b.specdec_verify_attention_kv8_workspace_size(B, n_new, Hq, Hkv, D, Lmax)
-
-
-def _cache_attention(fn, name, q, k_cache, v_cache, scales, seq_lens, scale, softcap, window, slopes,
-                     parent, out, workspace, stream):
-    if q.dtype != torch.bfloat16 or not q.is_cuda or q.dim() != 4:
-        raise TypeError("q must be a bfloat16 CUDA tensor [B, n_new, Hq, D]")
-    B, n_new, Hq, D = q.shape
-    Bc, Lmax, Hkv, Dc = k_cache.shape
-    if Bc != B or Dc != D:
-        raise ValueError("q [B, n_new, Hq, D] and the cache [B, Lmax, Hkv, D] do not fit")
-    _check_ints(seq_lens, (B,), "seq_lens")
-    if slopes is not None:
-        if slopes.dtype != torch.float32 or not slopes.is_contiguous():
-            raise TypeError("slopes must be a contiguous float32 CUDA tensor")
-        if slopes.shape != (Hq,):
-            raise ValueError("slopes must have one entry per query head")
-    par = None
-    if parent is not None:
-        if len(parent) != n_new:
-            raise ValueError("parent must have one entry per new position")
-        par = (ctypes.c_int32 * n_new)(*(int(p) for p in parent))
-    dev = q.device
-    _same_device(dev, k_cache, v_cache, *scales, seq_lens, slopes, out, workspace)
-    stride = _row_stride(q, "q")
-    if out is not None and (out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
-        raise TypeError("out must be a contiguous bfloat16 CUDA tensor of q's shape")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(B, n_new, Hq, D, dtype=torch.bfloat16, device=dev)
-        if workspace is None:
-            nbytes = cache_attention_workspace_bytes(B, n_new, Hq, Hkv, D, Lmax)
-            if nbytes == 0:
-                raise SpecdecError(_b.SPECDEC_ERR_UNSUPPORTED, "cache_attention_workspace_bytes")
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        rc = fn(q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(),
-                *(t.data_ptr() for t in scales), seq_lens.data_ptr(),
-                0 if par is None else ctypes.addressof(par), _ptr(slopes), B, n_new, Hq, Hkv, D, Lmax,
-                float(scale), float(softcap), int(window), out.data_ptr(), workspace.data_ptr(),
-                workspace.numel(), _stream_ptr(None))
-    if rc != 0:
-        _b._check(rc, name)
-    return out
 
 
 def verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale=0.0, softcap=0.0,
@@ -371,23 +254,29 @@ def verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale=
     the distance, slopes [Hq] float32 bias by distance, and parent (n_new ints as in verify_tree)
     makes the new positions a token tree. Returns out [B, n_new, Hq, D] bf16.
     """
-    _check_kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    return _cache_attention(_b.specdec_verify_attention_kv8, "specdec_verify_attention_kv8", q, k_cache,
-                            v_cache, (k_scale, v_scale), seq_lens, scale, softcap, window, slopes, parent,
-                            out, workspace, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
+                                        slopes, parent, out, workspace)
+    rc, out = _b.native().cache_attention(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
+                                          slopes, parent, out, workspace)
+    if rc != 0:
+        _b._check(rc, "specdec_verify_attention_kv8")
+    return out
 
 
 def verify_attention_masked(q, k_cache, v_cache, seq_lens, scale=0.0, softcap=0.0, window=0, slopes=None,
                             parent=None, out=None, workspace=None, stream=None):
     """verify_attention_kv8() over a bf16 cache k_cache, v_cache [B, Lmax, Hkv, D]."""
-    for t in (k_cache, v_cache):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous() or not t.is_cuda:
-            raise TypeError("the caches must be contiguous bfloat16 CUDA tensors [B, Lmax, Hkv, D]")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape")
-    return _cache_attention(_b.specdec_verify_attention_masked, "specdec_verify_attention_masked", q,
-                            k_cache, v_cache, (), seq_lens, scale, softcap, window, slopes, parent, out,
-                            workspace, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_attention_masked(q, k_cache, v_cache, seq_lens, scale, softcap, window, slopes, parent,
+                                           out, workspace)
+    rc, out = _b.native().cache_attention(q, k_cache, v_cache, None, None, seq_lens, scale, softcap, window, slopes,
+                                          parent, out, workspace)
+    if rc != 0:
+        _b._check(rc, "specdec_verify_attention_masked")
+    return out
 
 
 def cluster_head(hidden, cluster_emb, W_sorted, starts, token_of_row, top_k=1, max_cluster=None,

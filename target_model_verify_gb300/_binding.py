@@ -109,6 +109,26 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_native = None
+
+
+def native():
+    """The compiled module that marshals the cache operators (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        lib()
+        path = os.path.join(os.path.dirname(LIB_PATH), "_native.so")
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing: build it with `python -m target_model_verify_gb300.build`")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("_native", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native = module
+    return _native
+
+
 def header_functions() -> list[str]:
     """Names of the functions include/specdec_verify.h declares."""
     with open(HEADER, encoding="utf-8") as f:
