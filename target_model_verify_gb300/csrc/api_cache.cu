@@ -35,14 +35,15 @@ struct AttnPlan {
 // The new positions in equal groups of at most 128 query rows per KV head;
 // the partials of the tiles that the CTAs share, two per CTA, whatever the
 // batch and the lengths.
-AttnPlan make_plan(int n_new, int G, int D) {
+AttnPlan make_plan(bool e4m3, int n_new, int G, int D) {
   AttnPlan p;
   const int most = 128 / G;
   p.n_groups = (n_new + most - 1) / most;
   p.group_pos = (n_new + p.n_groups - 1) / p.n_groups;
   p.n_groups = (n_new + p.group_pos - 1) / p.group_pos;
   size_t off = align_up(sizeof(WsHeader));
-  const size_t rows = (size_t)2 * kCacheAttnCtas * cache_attn_rows(p.group_pos * G);
+  const int ctas = cache_attn_by_keys(e4m3, D, p.group_pos * G) ? kCacheAttnMaxCtas : kCacheAttnCtas;
+  const size_t rows = (size_t)2 * ctas * cache_attn_rows(p.group_pos * G);
   p.off_ml = off;
   off = align_up(off + rows * 2 * sizeof(float));
   p.off_o = off;
@@ -118,7 +119,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
     }
   }
   const int G = Hq / Hkv;
-  const AttnPlan pl = make_plan(n_new, G, D);
+  const AttnPlan pl = make_plan(e4m3, n_new, G, D);
   if (!workspace || ((uintptr_t)workspace % kAlign) != 0 || workspace_bytes < pl.total)
     return SPECDEC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
@@ -214,7 +215,7 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
 
 size_t specdec_verify_attention_kv8_workspace_size(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
   if (check_shape(B, n_new, Hq, Hkv, D, Lmax) != SPECDEC_OK) return 0;
-  return make_plan(n_new, Hq / Hkv, D).total;
+  return make_plan(true, n_new, Hq / Hkv, D).total;
 }
 
 int specdec_verify_attention_kv8(const void* q, long long q_stride, const void* k_cache, const void* v_cache,

@@ -1,0 +1,683 @@
+// The cache attention (cache_attention.cuh) over an e4m3 cache of head dim
+// 128 for up to 32 query rows per KV head, with the cache on the M side of
+// both products.
+//
+// With few query rows the row-per-lane form pays for 128 of them: its products
+// and their operand reads, and widening V to f16, take as long as the cache
+// takes to arrive. Here
+//   S^T = K Q^T:   M = 128 keys, N = 64: the rows' two e4m3 query terms side
+//                  by side (K is read from shared memory once; the terms'
+//                  scores are added in registers);
+//   O^T += V^T P^T: M = 128 dims, N = 96: the rows' probabilities as three
+//                  e4m3 terms, p = hi + mid / 16 + lo / 256, with an
+//                  accumulator each. The terms are those of p rounded to f16,
+//                  exact down to 2^-20 of a row's largest weight, and V is
+//                  multiplied as it lies in the cache.
+// Lane = key in the softmax, so a row's statistics run over lanes and warps.
+// Only its reference does not follow every maximum: it is set 2^2 above the
+// row's first and moved when an exponent passes it by 2^4, which one
+// barrier with a vote per block finds out; sums stay with the keys' threads
+// until the tile ends.
+//
+// Two CTAs per SM (256 tensor memory columns each). Warps 0-3 softmax, 4
+// producer, 5 and 6 issuers, 7 queries, row tables and the check of V blocks
+// that not every query sees whole.
+#pragma once
+
+#include "cache_attention.cuh"
+
+namespace specdec {
+namespace cache_attn {
+
+constexpr int kKeyThreads = 256;
+constexpr int kKeyD = 128, kKeyBlk = 128, kKeyRows = 32, kKeyRing = 2;
+constexpr int kKeySlot = kKeyBlk * kKeyD;
+constexpr int kKeyPTerm = kKeyBlk * kKeyRows;           // [keys][32 rows] codes of one term
+constexpr int kKeyQBytes = 2 * kKeyRows * kKeyD;        // [hi rows, lo rows][dims]
+constexpr int kKeyColS = 0, kKeyColO = 128;
+constexpr float kRise = 4.f, kLift = 2.f, kBase = 4.f;  // log2: see above; p at the reference is 2^kBase
+// row tables per query buffer: score factor, slope, depth, index [32] each
+constexpr int kKeyTab = 4 * kKeyRows * 4;
+constexpr int kKeySmem = 1024 + 2 * kKeyRing * kKeySlot + 2 * 3 * kKeyPTerm + 2 * kKeyQBytes + 2 * kKeyTab +
+                         2 * kKeyRows * 4 + 4 * kKeyRows * 4 + 128 * 16 + 128 * 4 + 512;
+static_assert(2 * (kKeySmem + 1024) <= 228 * 1024, "two CTAs per SM");
+
+// MN-major operand of 32-byte rows (32 codes along N), 32-byte swizzle.
+__device__ __forceinline__ uint64_t operand_desc32(uint32_t saddr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)((8u * 32) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)6 << 61;
+  return d;
+}
+__device__ __forceinline__ bool bar_any(int id, int nthreads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+  return c;
+}
+// (h - back) * 16, elementwise; exact for back the e4m3 rounding of h.
+__device__ __forceinline__ uint32_t rest16(uint32_t h, uint32_t back) {
+  const __half2 s = __float2half2_rn(16.f);
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&back)), s);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <bool kExtra>
+__global__ void __launch_bounds__(kKeyThreads, 2)
+    cache_attn_keys_kernel(const __grid_constant__ CacheAttnLaunch A, const __grid_constant__ CUtensorMap tmap_k,
+                           const __grid_constant__ CUtensorMap tmap_v) {
+  constexpr int kBlk = kKeyBlk, kD = kKeyD, kR = kKeyRing, kRows = kKeyRows;
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring_k = (raw + 1023u) & ~1023u;
+  const uint32_t ring_v = ring_k + kR * kKeySlot;
+  const uint32_t pb = ring_v + kR * kKeySlot;              // probabilities: [2][3 terms]
+  const uint32_t qb = pb + 2 * 3 * kKeyPTerm;
+  const uint32_t tab = qb + 2 * kKeyQBytes;
+  const uint32_t ref = tab + 2 * kKeyTab;                  // references, then factors for what moved
+  const uint32_t red = ref + 2 * kRows * 4;                // [4 warps][32 rows]
+  const uint32_t tree = red + 4 * kRows * 4;
+  const uint32_t bars = tree + 128 * 16 + 128 * 4;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  auto k_full = [&](int s) { return bar(s); };
+  auto k_empty = [&](int s) { return bar(2 + s); };
+  auto v_full = [&](int s) { return bar(4 + s); };
+  auto v_empty = [&](int s) { return bar(6 + s); };
+  auto v_clean = [&](int s) { return bar(8 + s); };
+  auto s_full = [&](int s) { return bar(10 + s); };
+  auto p_full = [&](int s) { return bar(12 + s); };
+  auto o_done = [&](int s) { return bar(14 + s); };
+  auto q_full = [&](int s) { return bar(16 + s); };
+  auto q_empty = [&](int s) { return bar(18 + s); };
+  const uint32_t drained = bar(20);
+  uint8_t* const words = smem_raw + (bar(22) - raw);
+  volatile int* const abort = reinterpret_cast<volatile int*>(words);
+  volatile int* const odd = abort + 1;
+  volatile uint32_t* const tmem_slot = reinterpret_cast<volatile uint32_t*>(words) + 2;
+  volatile int* const place = abort + 4;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 2);          // the product and the checking warp
+      mbar_init(v_clean(s), 1);
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), kSoftWarps);
+      mbar_init(o_done(s), 1);
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 1 + kSoftWarps);
+    }
+    mbar_init(drained, 2);
+    *abort = 0;
+    *odd = 0;
+    fence_mbar_init();
+  }
+  if (warp == 6) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 256);
+  if (A.tree) {
+    for (int e = threadIdx.x; e < A.n_new; e += kKeyThreads) {
+      sts128(tree + e * 16, A.anc[e][0], A.anc[e][1], A.anc[e][2], A.anc[e][3]);
+      sts32(tree + 128 * 16 + e * 4, A.depth[e]);
+    }
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();          // the merge may get ready on idle SMs
+  if (warp == 0) {
+    const Place pl = find_part<kBlk>(A, lane, blockIdx.x, gridDim.x);
+    if (lane == 0) {
+      place[0] = pl.b;
+      place[1] = pl.off;
+      place[2] = pl.u0;
+      place[3] = pl.u1;
+      if (blockIdx.x == 0) *A.status = pl.any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int part0 = place[2];
+  Walk<kBlk> w;
+  w.start(A, place[0], place[1], part0, place[3]);
+  auto warp_wait = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait<true>(b, parity, abort, A.status));
+  };
+  uint32_t issued_k = 0, issued_v = 0, phase_k = 0, phase_v = 0;   // producer: copies in flight
+
+  if (warp == 4) {
+    // ---------------------------------------------------------- producer --
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_first();
+      uint32_t n = 0;
+      bool ok = true;
+      for (; ok && !w.done(); w.next(A))
+        for (int i = 0; i < w.n_here; ++i, ++n) {
+          const int s = n & 1, j0 = (w.first + w.blk + i) * kBlk;
+          const uint32_t ph = (n >> 1) & 1;
+          if (!(ok = mbar_wait(k_empty(s), ph ^ 1u, abort, A.status))) break;
+          mbar_arrive_expect_tx(k_full(s), kKeySlot);
+          tma_load_4d(ring_k + s * kKeySlot, &tmap_k, k_full(s), 0, w.h, j0, w.b, pol);
+          issued_k |= 1u << s;
+          phase_k = (phase_k & ~(1u << s)) | (ph << s);
+          if (!(ok = mbar_wait(v_empty(s), ph ^ 1u, abort, A.status))) break;
+          mbar_arrive_expect_tx(v_full(s), kKeySlot);
+          tma_load_4d(ring_v + s * kKeySlot, &tmap_v, v_full(s), 0, w.h, j0, w.b, pol);
+          issued_v |= 1u << s;
+          phase_v = (phase_v & ~(1u << s)) | (ph << s);
+        }
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------- issuer of K Q^T --
+    constexpr uint32_t id = instr_desc(0, false, 2 * kRows);
+    const uint64_t k_desc = operand_desc<128>(ring_k, 16), q_desc = operand_desc<128>(qb, 16);
+    uint32_t n = 0, nt = 0;
+    bool ok = true;
+    for (; ok && !w.done(); w.next(A), ++nt) {
+      const uint32_t qs = nt & 1;
+      if (!(ok = warp_wait(q_full(qs), (nt >> 1) & 1))) break;
+      const uint64_t qd = q_desc + (uint64_t)(qs * (kKeyQBytes >> 4));
+      for (int i = 0; i < w.n_here; ++i, ++n) {
+        const uint32_t s = n & 1;
+        if (!(ok = warp_wait(k_full(s), (n >> 1) & 1))) break;
+        if (n >= 2 && !(ok = warp_wait(p_full(s), ((n - 2) >> 1) & 1))) break;   // scores two blocks ago are read
+        tc_fence_after();
+        const uint64_t kd = k_desc + (uint64_t)(s * (kKeySlot >> 4));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kD / 32; ++k)
+            mma_ss<true>(tmem + kKeyColS + s * 64, kd + 2 * k, qd + 2 * k, id, k > 0);
+          tc_commit(s_full(s));
+          tc_commit(k_empty(s));
+          if (i + 1 == w.n_here) tc_commit(q_empty(qs));
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) tc_commit(drained);
+    wait_drain(drained, 0);
+  } else if (warp == 6) {
+    // ----------------------------------------------- issuer of V^T P^T --
+    constexpr uint32_t id = instr_desc(0, true, 3 * kRows) | (1u << 15);     // A (V^T) is M-major too
+    const uint64_t v_desc = operand_desc<128>(ring_v, 16), p_desc = operand_desc32(pb, kKeyPTerm);
+    uint32_t n = 0, clean_ph = 0;
+    bool ok = true;
+    for (; ok && !w.done(); w.next(A))
+      for (int i = 0; i < w.n_here; ++i, ++n) {
+        const uint32_t s = n & 1;
+        if (!(ok = warp_wait(v_full(s), (n >> 1) & 1))) break;
+        if (!w.clean(i)) {
+          if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) break;
+          clean_ph ^= 1u << s;
+        }
+        if (!(ok = warp_wait(p_full(s), (n >> 1) & 1))) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + (uint64_t)(s * (kKeySlot >> 4));
+        const uint64_t pd = p_desc + (uint64_t)(s * (3 * kKeyPTerm >> 4));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kBlk / 32; ++k)
+            mma_ss<true>(tmem + kKeyColO, vd + k * (32 * 128 >> 4), pd + k * (32 * 32 >> 4), id, i > 0 || k > 0);
+          tc_commit(o_done(s));
+          tc_commit(v_empty(s));
+        }
+        __syncwarp();
+      }
+    // every product has to be done before the tensor memory is given back
+    if (elect_one()) tc_commit(drained);
+    wait_drain(drained, 0);
+  } else if (warp == 7) {
+    // ------------------------------ queries, row tables, odd values of V --
+    Walk<kBlk> wl = w;                   // the tile whose queries come next
+    uint32_t tl = 0, n = 0;
+    bool ok = true;
+    auto load_queries = [&]() {
+      const uint32_t qs = tl & 1;
+      if (!warp_wait(q_empty(qs), ((tl >> 1) & 1) ^ 1u)) return false;
+      // lane = row: two e4m3 terms of its 128 dims
+      const int pos0 = wl.g * A.group_pos, row = lane;
+      const bool mine = row < min(A.group_pos, A.n_new - pos0) * A.G;
+      const int idx = mine ? pos0 + row / A.G : 0, head = wl.h * A.G + (mine ? row % A.G : 0);
+      const uint4* src = reinterpret_cast<const uint4*>(A.q + ((size_t)wl.b * A.n_new + idx) * A.q_stride +
+                                                        (size_t)head * kD);
+      uint32_t wv[kD / 2];
+#pragma unroll
+      for (int c = 0; c < kD / 8; ++c) {
+        const uint4 v = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        wv[4 * c] = v.x;
+        wv[4 * c + 1] = v.y;
+        wv[4 * c + 2] = v.z;
+        wv[4 * c + 3] = v.w;
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < kD / 2; ++k) top = max(top, max(wv[k] & 0x7fffu, (wv[k] >> 16) & 0x7fffu));
+      const bool fine = top < 0x7f80u;
+      const int down = top > 0 && fine ? min(max((int)(top >> 7) - 134, -100), 120) : 0;
+      const float mul = __uint_as_float((uint32_t)(127 - down) << 23);
+      const uint32_t hi_row = qb + qs * kKeyQBytes + row * kD, lo_row = hi_row + kRows * kD;
+#pragma unroll
+      for (int c = 0; c < kD / 16; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t ph[2], pl[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t u = wv[8 * c + 2 * k + x];
+            const float a = __uint_as_float(u << 16) * mul, b = __uint_as_float(u & 0xffff0000u) * mul;
+            ph[x] = f32_to_e4m3x2(a, b);
+            const uint32_t back = e4m3x2_to_f16x2((uint16_t)ph[x]);
+            const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            pl[x] = f32_to_e4m3x2(a - r2.x, b - r2.y);
+          }
+          hi[k] = ph[0] | (ph[1] << 16);
+          lo[k] = pl[0] | (pl[1] << 16);
+        }
+        const uint32_t at = (uint32_t)((c ^ (row & 7)) << 4);
+        sts128(hi_row + at, hi[0], hi[1], hi[2], hi[3]);
+        sts128(lo_row + at, lo[0], lo[1], lo[2], lo[3]);
+      }
+      const uint32_t t = tab + qs * kKeyTab + row * 4;
+      const float q_scale = fine ? __uint_as_float((uint32_t)(127 + down) << 23) : __uint_as_float(0x7fffffffu);
+      sts32(t, __float_as_uint(A.scale * q_scale * (kExtra ? 1.f : kLog2e)));
+      sts32(t + kRows * 4, __float_as_uint(kExtra && A.slopes ? A.slopes[head] * kLog2e : 0.f));
+      sts32(t + 2 * kRows * 4, (uint32_t)(A.tree ? (int)lds32(tree + 128 * 16 + idx * 4) : idx));
+      sts32(t + 3 * kRows * 4, (uint32_t)idx);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(qs));
+      ++tl;
+      wl.next(A);
+      return true;
+    };
+    for (int k = 0; k < 2; ++k)
+      if (ok && !wl.done()) ok = load_queries();
+    for (uint32_t nt = 0; ok && !w.done(); w.next(A), ++nt) {
+      for (int i = 0; i < w.n_here; ++i, ++n) {
+        const uint32_t s = n & 1;
+        if (!(ok = warp_wait(v_full(s), (n >> 1) & 1))) break;
+        if (!w.clean(i)) {
+          // Rows past the sequence hold anything, and a NaN in a row that not
+          // every query sees would pass a zero probability: neither stays in
+          // the product. The epilogue adds the NaN where seen.
+          const int j0 = (w.first + w.blk + i) * kBlk;
+          for (int e = lane; e < kKeySlot / 16; e += 32) {
+            const uint32_t a = ring_v + s * kKeySlot + e * 16;
+            const uint4 v = lds128(a);
+            uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            bool put = false;
+            if (j0 + (e >> 3) >= w.L) {
+              x[0] = x[1] = x[2] = x[3] = 0u;
+              put = true;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // bytes whose low seven bits are all ones
+              const uint32_t nan = __vcmpeq4(x[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              if (nan) {
+                x[k] &= ~nan;
+                put = true;
+                *odd = 1;
+              }
+            }
+            if (put) sts128(a, x[0], x[1], x[2], x[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_clean(s));
+        }
+        if (lane == 0) mbar_arrive(v_empty(s));
+        // the next tile's queries, once the last tile's buffer is about free
+        if (i == 0 && nt > 0 && !wl.done() && !(ok = load_queries())) break;
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- softmax --
+    const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+    const int kl = warp * 32 + lane;         // this thread's key of a block, and its dim of the output
+    bool dead = false;
+    uint32_t n = 0, nt = 0;
+    for (; !w.done(); w.next(A), ++nt) {
+      const int P0 = w.L - A.n_new, pos0 = w.g * A.group_pos;
+      const int rows_here = min(A.group_pos, A.n_new - pos0) * A.G;
+      const uint32_t qs = nt & 1, t0 = tab + qs * kKeyTab;
+      const size_t so = ((size_t)w.b * A.Hkv + w.h) * A.n_scale;
+      const float* ks = A.k_scale + so;
+      const float* vs = A.v_scale + so;
+      int j = (w.first + w.blk) * kBlk + kl;           // this thread's cache row
+      float sk_next, sv_next;
+      auto load_scales = [&](int jw) {
+        sk_next = jw < w.L ? __ldg(ks + jw / SPECDEC_KV8_BLOCK) : 1.f;
+        sv_next = jw < w.L ? __ldg(vs + jw / SPECDEC_KV8_BLOCK) : 1.f;
+      };
+      load_scales(j - lane);
+      float l[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) l[r] = 0.f;
+      if (warp == 0) sts32(ref + lane * 4, __float_as_uint(-INFINITY));
+      if (!dead && !warp_wait(q_full(qs), (nt >> 1) & 1)) dead = true;
+      named_bar_sync(1, 32 * kSoftWarps);
+
+      for (int ib = 0; ib < w.n_here; ++ib, ++n, j += kBlk) {
+        const bool clean = w.clean(ib);
+        const float sk = sk_next, lv = __log2f(sv_next), inv_sv = rcp(sv_next);
+        if (ib + 1 < w.n_here) load_scales(j - lane + kBlk);
+        if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
+        tc_fence_after();
+        float y[kRows];
+        // Exponents of this key for every row, less `base` minus the rows'
+        // references (with_ref) or as they are.
+        auto exponents = [&](bool with_ref) {
+          const uint32_t from = tl + kKeyColS + (n & 1) * 64;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t a[16], b[16];
+            tmem_load(from + 16 * hf, a);
+            tmem_load(from + 32 + 16 * hf, b);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              y[16 * hf + k] = __uint_as_float(a[k]);
+              y[16 * hf + k + 1] = __uint_as_float(a[k + 1]);
+              add2(y[16 * hf + k], y[16 * hf + k + 1], __uint_as_float(b[k]), __uint_as_float(b[k + 1]));
+            }
+          }
+          float pj = 0.f;
+          if (kExtra && A.slopes) {
+            int p = j - P0;                            // position from the first new one's
+            if (A.tree && p >= 0) p = (int)lds32(tree + 128 * 16 + min(p, A.n_new - 1) * 4);
+            pj = (float)p;
+          }
+#pragma unroll
+          for (int r = 0; r < kRows; r += 4) {
+            const float4 c = lds128f(t0 + r * 4);
+            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (with_ref) m = lds128f(ref + r * 4);
+            const float cc[4] = {c.x, c.y, c.z, c.w};
+            const float bb[4] = {lv + kBase - m.x, lv + kBase - m.y, lv + kBase - m.z, lv + kBase - m.w};
+            if constexpr (kExtra) {
+              const float4 sl = lds128f(t0 + kRows * 4 + r * 4);
+              const uint4 dp = lds128(t0 + 2 * kRows * 4 + r * 4);
+              const float ss[4] = {sl.x, sl.y, sl.z, sl.w};
+              const float dd[4] = {(float)(int)dp.x, (float)(int)dp.y, (float)(int)dp.z, (float)(int)dp.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float z = y[r + k] * (cc[k] * sk);
+                float e;
+                if (A.cap > 0.f)       // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
+                  e = fmaf(-2.f * A.cap * kLog2e, rcp(1.f + ex2(z * A.cap_exp)), A.cap * kLog2e);
+                else
+                  e = z * kLog2e;
+                y[r + k] = fmaf(ss[k], pj - dd[k], e) + bb[k];
+              }
+            } else {
+              // the product is rounded before the reference comes off, so that
+              // exponents of any size agree with it
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[r + k] = fmaf(y[r + k], cc[k] * sk, 0.f) + bb[k];
+            }
+          }
+          if (!clean) {
+            const int a = j - P0;
+            const int da = A.tree && a >= 0 ? (int)lds32(tree + 128 * 16 + min(a, A.n_new - 1) * 4) : a;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+              const int dep = (int)lds32(t0 + 2 * kRows * 4 + r * 4);
+              bool seen = j < w.L && (A.window <= 0 || dep - da < A.window);
+              if (a >= 0) {
+                const int idx = (int)lds32(t0 + 3 * kRows * 4 + r * 4);
+                if (A.tree)
+                  seen = seen && ((lds32(tree + idx * 16 + (min(a, 127) >> 5) * 4) >> (a & 31)) & 1u);
+                else
+                  seen = seen && a <= idx;
+              }
+              if (!seen) y[r] = -INFINITY;
+            }
+          }
+        };
+        if (!dead) exponents(true);
+        float top = -INFINITY;
+        if (!dead) {
+#pragma unroll
+          for (int r = 0; r < kRows; r += 4) top = max3(max3(top, y[r], y[r + 1]), y[r + 2], y[r + 3]);
+        }
+        if (bar_any(1, 32 * kSoftWarps, top > kBase + kRise)) {
+          // ---- some row's reference has to move: all rows' maxima ----
+          if (!dead) exponents(false);
+          if (dead) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) y[r] = -INFINITY;
+          }
+          // halve the rows a lane carries five times: lane r ends up with row r
+#pragma unroll
+          for (int o = 16, cnt = 16; o; o >>= 1, cnt >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int k = 0; k < cnt; ++k) {
+              const float give = up ? y[k] : y[k + cnt], keep = up ? y[k + cnt] : y[k];
+              y[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+            }
+          }
+          sts32(red + kl * 4, __float_as_uint(y[0] - kBase));
+          named_bar_sync(1, 32 * kSoftWarps);
+          if (warp == 0) {
+            float M = __uint_as_float(lds32(red + lane * 4));
+#pragma unroll
+            for (int x = 1; x < kSoftWarps; ++x) M = fmaxf(M, __uint_as_float(lds32(red + (x * 32 + lane) * 4)));
+            const float was = __uint_as_float(lds32(ref + lane * 4));
+            const bool move = M > was + kRise;
+            sts32(ref + lane * 4, __float_as_uint(move ? M + kLift : was));
+            sts32(ref + kRows * 4 + lane * 4, __float_as_uint(move ? ex2(was - (M + kLift)) : 1.f));
+          }
+          named_bar_sync(1, 32 * kSoftWarps);
+          if (!dead) {
+            float al[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; r += 4) {
+              const float4 f = lds128f(ref + kRows * 4 + r * 4);
+              al[r] = f.x;
+              al[r + 1] = f.y;
+              al[r + 2] = f.z;
+              al[r + 3] = f.w;
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) l[r] *= al[r];
+            if (ib > 0) {
+              if (!warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
+              if (!dead) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int term = 0; term < 3; ++term) {
+                  uint32_t v[32];
+                  tmem_load(tl + kKeyColO + term * 32, v);
+#pragma unroll
+                  for (int r = 0; r < kRows; ++r) v[r] = __float_as_uint(__uint_as_float(v[r]) * al[r]);
+                  tmem_store(tl + kKeyColO + term * 32, v, Cols<32>{});
+                }
+                tmem_wait_store();
+              }
+            }
+            if (!dead) exponents(true);
+          }
+        }
+        // ---- probabilities, as three e4m3 terms ----
+        // the product that read this buffer two blocks ago is done
+        if (!dead && n >= 2 && !warp_wait(o_done(n & 1), ((n - 2) >> 1) & 1)) dead = true;
+        if (dead) continue;
+        const uint32_t to = pb + (n & 1) * 3 * kKeyPTerm + kl * 32;
+#pragma unroll
+        for (int h16 = 0; h16 < 2; ++h16) {
+          uint32_t t[3][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t part[3][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int r = 16 * h16 + 4 * q + 2 * x;
+              float p0 = ex2(y[r]), p1 = ex2(y[r + 1]);
+              const uint32_t h = pack2<true>(p0, p1);
+              fma2(p0, p1, inv_sv, 0.f);
+              add2(l[r], l[r + 1], p0, p1);
+              part[0][x] = f16x2_to_e4m3x2(h);
+              const uint32_t h1 = rest16(h, e4m3x2_to_f16x2((uint16_t)part[0][x]));
+              part[1][x] = f16x2_to_e4m3x2(h1);
+              part[2][x] = f16x2_to_e4m3x2(rest16(h1, e4m3x2_to_f16x2((uint16_t)part[1][x])));
+            }
+#pragma unroll
+            for (int x = 0; x < 3; ++x) t[x][q] = part[x][0] | (part[x][1] << 16);
+          }
+          // 32-byte rows; the 16-byte halves trade places every four keys
+          const uint32_t at = to + ((uint32_t)(h16 ^ ((kl >> 2) & 1)) << 4);
+#pragma unroll
+          for (int x = 0; x < 3; ++x) sts128(at + x * kKeyPTerm, t[x][0], t[x][1], t[x][2], t[x][3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(n & 1));
+      }
+
+      // ---- sums over the keys, then the output or this part's share ----
+#pragma unroll
+      for (int o = 16, cnt = 16; o; o >>= 1, cnt >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < cnt; ++k) {
+          const float give = up ? l[k] : l[k + cnt], keep = up ? l[k + cnt] : l[k];
+          l[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+      sts32(red + kl * 4, __float_as_uint(l[0]));
+      named_bar_sync(1, 32 * kSoftWarps);
+      const bool whole = w.blk == 0 && w.n_here == w.nb;
+      const size_t slot = (size_t)blockIdx.x * 2 + (w.u == part0 ? 0 : 1);
+      if (warp == 0) {
+        float lt = 0.f;
+#pragma unroll
+        for (int x = 0; x < kSoftWarps; ++x) lt += __uint_as_float(lds32(red + (x * 32 + lane) * 4));
+        // the output's factor per row, where the references' factors were
+        const float inv = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);    // NaN stays
+        sts32(ref + kRows * 4 + lane * 4, __float_as_uint(whole ? inv : 1.f));
+        if (!whole && lane < rows_here && !dead)
+          *reinterpret_cast<float2*>(A.part_ml + (slot * kRows + lane) * 2) =
+              make_float2(__uint_as_float(lds32(ref + lane * 4)), lt);
+      }
+      named_bar_sync(1, 32 * kSoftWarps);
+      if (!dead && !warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
+      tc_fence_after();
+      if (!dead) {
+        float o[kRows];
+        {
+          uint32_t v[32];
+          tmem_load(tl + kKeyColO, v);
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) o[r] = __uint_as_float(v[r]);
+          tmem_load(tl + kKeyColO + 32, v);
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) o[r] = fmaf(__uint_as_float(v[r]), 1.f / 16, o[r]);
+          tmem_load(tl + kKeyColO + 64, v);
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) o[r] = fmaf(__uint_as_float(v[r]), 1.f / 256, o[r]);
+        }
+        if (*odd) {
+          // NaN that were held back from the product (rare), for the rows that see them
+          for (int ib = 0; ib < w.n_here; ++ib) {
+            if (w.clean(ib)) continue;
+            const int jb = (w.first + w.blk + ib) * kBlk;
+            for (int k = 0; k < kBlk && jb + k < w.L; ++k) {
+              const uint8_t code =
+                  static_cast<const uint8_t*>(A.v)[(((size_t)w.b * A.Lmax + jb + k) * A.Hkv + w.h) * kD + kl];
+              if ((code & 0x7fu) != 0x7fu) continue;
+              const int a = jb + k - P0;
+              const int da = A.tree && a >= 0 ? (int)lds32(tree + 128 * 16 + a * 4) : a;
+#pragma unroll
+              for (int r = 0; r < kRows; ++r) {
+                const int dep = (int)lds32(t0 + 2 * kRows * 4 + r * 4), idx = (int)lds32(t0 + 3 * kRows * 4 + r * 4);
+                bool seen = A.window <= 0 || dep - da < A.window;
+                if (a >= 0)
+                  seen = seen && (A.tree ? ((lds32(tree + idx * 16 + (a >> 5) * 4) >> (a & 31)) & 1u) != 0 : a <= idx);
+                if (seen) o[r] = __uint_as_float(0x7fffffffu);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          if (r >= rows_here) break;
+          const float f = o[r] * __uint_as_float(lds32(ref + kRows * 4 + r * 4));
+          if (whole) {
+            const int i = pos0 + r / A.G;
+            A.out[(((size_t)w.b * A.n_new + i) * A.Hq + (size_t)w.h * A.G + r % A.G) * kD + kl] = __float2bfloat16(f);
+          } else {
+            A.part_o[(slot * kRows + r) * kD + kl] = f;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty(qs));
+      tc_fence_before();
+      named_bar_sync(1, 32 * kSoftWarps);    // the tables are free for the next tile
+    }
+  }
+  tc_fence_before();
+  __syncthreads();   // every role has left its loop
+  tc_fence_after();
+  if (warp == 6) tmem_dealloc(tmem, 256);
+  if (*abort && warp == 4 && lane == 0)
+    // A wait gave up: let every copy already issued land before the CTA exits.
+    for (int s = 0; s < kR; ++s) {
+      if (issued_k & (1u << s)) wait_drain(k_full(s), (phase_k >> s) & 1u);
+      if (issued_v & (1u << s)) wait_drain(v_full(s), (phase_v >> s) & 1u);
+    }
+}
+
+template <bool kExtra>
+cudaError_t launch_keys(const CacheAttnLaunch& A, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t stream) {
+  static std::atomic<int> smem_set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !smem_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(cache_attn_keys_kernel<kExtra>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeySmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
+  }
+  const long long tiles = (long long)A.B * A.Hkv * A.n_groups;
+  const long long most = tiles * ((A.Lmax + kKeyBlk - 1) / kKeyBlk + kTileCost);
+  const int grid = (int)(most < kCacheAttnMaxCtas ? most : kCacheAttnMaxCtas);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kKeyThreads);
+  cfg.dynamicSmemBytes = kKeySmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, cache_attn_keys_kernel<kExtra>, A, tk, tv);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)tiles, (A.group_pos * A.G + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<true, kKeyD, kKeyRows>, A, grid);
+}
+
+}  // namespace cache_attn
+}  // namespace specdec

@@ -189,7 +189,8 @@ int attn_smem_bytes(int n_mt, int n_stages);
 
 // Verify-step attention with caps, biases, windows and token trees, over a
 // bf16 or an e4m3 cache (cache_attention.cuh).
-constexpr int kCacheAttnCtas = 152;  // CTAs at most: one per SM
+constexpr int kCacheAttnCtas = 152;       // CTAs at most: one per SM of a 152-SM part,
+constexpr int kCacheAttnMaxCtas = 304;    // or two (cache_attention_keys.cuh)
 struct CacheAttnLaunch {
   int B, n_new, Hq, Hkv, G, Lmax;    // G = Hq / Hkv
   int n_groups, group_pos;           // the new positions in equal groups of at most 128 rows
@@ -206,8 +207,8 @@ struct CacheAttnLaunch {
   const float* slopes;               // [Hq] or null
   const int32_t* seq_lens;           // [B]
   __nv_bfloat16* out;                // [B, n_new, Hq, D]
-  float* part_o;                     // [2 kCacheAttnCtas, rows, D]
-  float* part_ml;                    // [2 kCacheAttnCtas, rows, 2]
+  float* part_o;                     // [2 CTAs, rows, D]
+  float* part_ml;                    // [2 CTAs, rows, 2]
   int* status;
   uint32_t anc[SPECDEC_MAX_TREE_NODES][4];   // bit a of row i: node i sees node a
   uint8_t depth[SPECDEC_MAX_TREE_NODES];
@@ -216,6 +217,8 @@ struct CacheAttnLaunch {
 constexpr int cache_attn_block(bool e4m3, int D) { return e4m3 && D != 256 ? 128 : 64; }
 // Lanes that a group of query rows takes: 32, 64 or 128.
 constexpr int cache_attn_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Whether the form with the cache on the M side takes the call.
+constexpr bool cache_attn_by_keys(bool e4m3, int D, int rows) { return e4m3 && D == 128 && rows <= 32; }
 // tmap_q: the queries as a bf16 tensor {D, Hq, n_new, B} with a box of 64
 // dims x G heads x group_pos positions, 128-byte swizzle (bf16 cache only).
 cudaError_t launch_cache_attention_kv8(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
