@@ -66,7 +66,8 @@ bool encode_cache(CUtensorMap* map, const void* base, bool e4m3, int B, int Lmax
   return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             panel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            panel == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The queries as a 4-D tensor {D, Hq, n_new, B}; box: 64 dims of a group's
@@ -132,6 +133,8 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.n_groups = pl.n_groups;
   A.group_pos = pl.group_pos;
   A.window = window;
+  // at least two parts per head: with more heads than that, a CTA takes them all in turn
+  A.head_lanes = 2 * Hkv <= kCacheAttnCtas ? Hkv : 1;
   A.n_scale = (Lmax + SPECDEC_KV8_BLOCK - 1) / SPECDEC_KV8_BLOCK;
   A.scale = scale > 0.f ? scale : 1.f / std::sqrt((float)D);
   A.cap = softcap;

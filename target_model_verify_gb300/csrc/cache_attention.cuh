@@ -14,12 +14,15 @@
 // Bound: HBM (each K and V row is read once per group of up to 128 query
 // rows).
 //
-// Schedule. The (sequence, KV head, row group) tiles, each a run of cache
-// blocks as long as its own sequence (or window), are laid end to end and
-// the run of blocks is cut into equal parts, one per CTA (one CTA per SM), on
-// the device from seq_lens, so ragged batches keep every SM busy to the end.
-// A tile that lies inside one part is finished by its CTA; the others leave
-// (maximum, sum, unnormalised output) partials that combine_kernel merges.
+// Schedule. A tile is a (sequence, KV head, row group), a run of cache blocks
+// as long as its own sequence (or window). A head's tiles are laid end to end
+// and cut into equal parts, on the device from seq_lens, so ragged batches
+// keep every SM busy to the end. Part p of head h goes to CTA p * Hkv + h:
+// the heads' CTAs go through the same cache rows at the same time, and since
+// a row of the cache holds all its heads side by side, DRAM pages are read
+// whole. A tile that lies inside one part is finished by its CTA; the others
+// leave (maximum, sum, unnormalised output) partials that combine_kernel
+// merges.
 //
 // CTA: warps 0-3 softmax, 4-7 auxiliary, 8 and 9 TMA producers (K with Q,
 // and V, whose slots free up at different times), 10 and 11 tcgen05 issuers (one per product: a thread takes 50 to 100 cycles for each MMA, as
@@ -366,15 +369,19 @@ __device__ __forceinline__ int part_begin(int total, int c, int n) {
   return total / n * c + (int)((unsigned)(total % n) * (unsigned)c / (unsigned)n);
 }
 
-// One warp: the batch's units, and where unit part_begin(c) lies: sequence b
-// (B when there is none) and offset inside it.
+// CTAs beside each other on one part: one per KV head, or, with too many heads
+// for that, one that takes all heads' tiles.
+__device__ __forceinline__ int heads_of(const CacheAttnLaunch& A) { return A.head_lanes > 1 ? 1 : A.Hkv; }
+
+// One warp: the units of a head lane, and where unit part_begin(c) lies:
+// sequence b (B when there is none) and offset inside it.
 struct Place {
   int total, u0, u1, b, off;
   bool any_bad;
 };
 template <int kBlk>
 __device__ __forceinline__ Place find_part(const CacheAttnLaunch& A, int lane, int c, int n) {
-  const int per = A.Hkv * A.n_groups;
+  const int per = heads_of(A) * A.n_groups;
   Place p;
   int first, units0 = 0, sum = 0;
   bool bad, bad_seen = false;
@@ -419,7 +426,7 @@ __device__ __forceinline__ Place find_part(const CacheAttnLaunch& A, int lane, i
 // Walks the tiles of a part: (b, h, group) and the block range inside each.
 template <int kBlk>
 struct Walk {
-  int b, h, g;        // tile
+  int b, h, g, h0;    // tile, the part's first head
   int blk, n_here;    // first block inside the tile, blocks of this part
   int nb, first, L;   // the tile's blocks, its first cache block, its length
   int clean_lo, clean_hi;   // the tile's blocks that every new position sees whole
@@ -447,7 +454,8 @@ struct Walk {
     const int units = tile_units(nb), t = off / units;
     tile0 = u - (off - t * units);
     g = t % A.n_groups;
-    h = t / A.n_groups;
+    h0 = A.head_lanes > 1 ? (int)blockIdx.x % A.head_lanes : 0;
+    h = h0 + t / A.n_groups;
     cut();
     if (n_here == 0) next(A);
   }
@@ -459,8 +467,8 @@ struct Walk {
       if (u >= end) return;
       if (++g == A.n_groups) {
         g = 0;
-        if (++h == A.Hkv) {
-          h = 0;
+        if (++h == h0 + heads_of(A)) {
+          h = h0;
           do {
             ++b;
             load(A);
@@ -570,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();          // the merge may get ready on idle SMs
   if (warp == 0) {
-    const Place pl = find_part<kBlk>(A, lane, blockIdx.x, gridDim.x);
+    const Place pl = find_part<kBlk>(A, lane, blockIdx.x / A.head_lanes, gridDim.x / A.head_lanes);
     if (lane == 0) {
       place[0] = pl.b;
       place[1] = pl.off;
@@ -1311,7 +1319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // zeroes the outputs of sequences without blocks. One warp per query row:
 // blockIdx.x = tile, blockIdx.y * 8 + warp = row of its group.
 template <bool kE4m3, int kD, int kRP>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CacheAttnLaunch A, int n_ctas) {
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CacheAttnLaunch A, int n_parts) {
   constexpr int kBlk = cache_attn_block(kE4m3, kD);
   __shared__ int sh_before[8], sh_total[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1345,13 +1353,33 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
     before += sh_before[x];
     total += sh_total[x];
   }
-  const int per = A.Hkv * A.n_groups;
+  const int per = heads_of(A) * A.n_groups;
   total *= per;
-  const int u0 = before * per + (h * A.n_groups + grp) * tile_units(nb);
+  const int u0 = before * per + ((A.head_lanes > 1 ? 0 : h) * A.n_groups + grp) * tile_units(nb);
   const int pos0 = grp * A.group_pos;
   const int r = blockIdx.y * 8 + warp;
+  const bool mine = r < min(A.group_pos, A.n_new - pos0) * A.G;
+  // Part c holds unit u iff part_begin(c) <= u < part_begin(c + 1); the tile's
+  // blocks are its units from u0 + kTileCost on.
+  int c0 = 0, c1 = -1;
+  if (nb > 0) {
+    auto owner = [&](int u) { return (int)(((unsigned long long)(u + 1) * n_parts - 1) / total); };
+    c0 = owner(u0 + kTileCost);
+    c1 = owner(u0 + kTileCost + nb - 1);
+  }
+  // A lane looks after every 32nd of those parts: which of its CTA's two
+  // partials (c0 may have begun before the tile: then the second). An empty
+  // part has none; it counts as c0's with weight 0.
+  auto slot_of = [&](int c, bool& none) {
+    const int pb = part_begin(total, c, n_parts);
+    none = c > c1 || pb == part_begin(total, c + 1, n_parts);
+    const int cta = (none ? c0 : c) * A.head_lanes + (A.head_lanes > 1 ? h : 0);
+    return 2 * cta + ((none || c == c0) && part_begin(total, c0, n_parts) < u0 ? 1 : 0);
+  };
+  bool none0 = true;
+  const int slot0 = nb > 0 ? slot_of(c0 + lane, none0) : 0;
   grid_dependency_wait();
-  if (r >= min(A.group_pos, A.n_new - pos0) * A.G) return;
+  if (!mine || (nb > 0 && c0 == c1)) return;     // no such row, or its CTA wrote the output
   constexpr int kPer = kD / 32;
   __nv_bfloat16* dst = A.out +
                        (((size_t)b * A.n_new + pos0 + r / A.G) * A.Hq + (size_t)h * A.G + r % A.G) * kD +
@@ -1359,42 +1387,44 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
   float acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  float inv = 0.f;
-  if (nb > 0) {
-    // CTA c owns unit u iff part_begin(c) <= u < part_begin(c + 1); the tile's
-    // blocks are its units from u0 + kTileCost on.
-    auto owner = [&](int u) { return (int)(((long long)(u + 1) * n_ctas - 1) / total); };
-    const int c0 = owner(u0 + kTileCost), c1 = owner(u0 + kTileCost + nb - 1);
-    if (c0 == c1) return;                        // its CTA wrote the output
-    // CTA c0's part may have begun before the tile: then it is its second partial
-    auto slot_of = [&](int c) { return (size_t)c * 2 + (c == c0 && part_begin(total, c, n_ctas) < u0 ? 1 : 0); };
-    auto empty = [&](int c) { return part_begin(total, c, n_ctas) == part_begin(total, c + 1, n_ctas); };
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32)
-      if (!empty(c)) M = fmaxf(M, A.part_ml[(slot_of(c) * kRP + r) * 2]);
-    M = warp_max(M);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      if (empty(c)) continue;
-      const size_t slot = slot_of(c);
-      const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + (slot * kRP + r) * 2);
-      const float wgt = ex2(ml.x - mu);
-      l += ml.y * wgt;
-      const float* po = A.part_o + (slot * kRP + r) * kD + lane * kPer;
+  float l = 0.f, M = -INFINITY;
+  for (int cb = c0; cb <= c1; cb += 32) {
+    bool none = none0;
+    const int slot = cb == c0 ? slot0 : slot_of(cb + lane, none);
+    const float2 ml = none ? make_float2(-INFINITY, 0.f)
+                           : *reinterpret_cast<const float2*>(A.part_ml + ((size_t)slot * kRP + r) * 2);
+    const float m_new = fmaxf(M, warp_max(ml.x));
+    const float mu = m_new == -INFINITY ? 0.f : m_new;
+    const float alpha = ex2(M - mu), wgt = none ? 0.f : ex2(ml.x - mu);
+    l = fmaf(l, alpha, warp_sum(none ? 0.f : ml.y * wgt));
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] *= alpha;
+    M = m_new;
+    const int here = min(32, c1 - cb + 1);
+#pragma unroll 8
+    for (int x = 0; x < here; ++x) {
+      const int s = __shfl_sync(0xffffffffu, slot, x);
+      const float f = __shfl_sync(0xffffffffu, wgt, x);
+      const float* po = A.part_o + ((size_t)s * kRP + r) * kD + lane * kPer;
 #pragma unroll
       for (int k = 0; k < kPer; k += 2) {
         const float2 v = *reinterpret_cast<const float2*>(po + k);
-        acc[k] = fmaf(v.x, wgt, acc[k]);
-        acc[k + 1] = fmaf(v.y, wgt, acc[k + 1]);
+        acc[k] = fmaf(v.x, f, acc[k]);
+        acc[k + 1] = fmaf(v.y, f, acc[k + 1]);
       }
     }
-    inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
   for (int k = 0; k < kPer; k += 2)
     *reinterpret_cast<uint32_t*>(dst + k) = pack2<false>(acc[k] * inv, acc[k + 1] * inv);
+}
+
+// Parts of the schedule: as many as the CTAs (or the work, `most` units in
+// all heads at the longest) allow.
+inline int cache_attn_parts(const CacheAttnLaunch& A, int ctas, long long most) {
+  const long long by_work = (most + A.head_lanes - 1) / A.head_lanes, by_ctas = ctas / A.head_lanes;
+  return (int)(by_work < by_ctas ? by_work : by_ctas);
 }
 
 template <bool kE4m3, int kD, int kRP, bool kExtra>
@@ -1413,9 +1443,9 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
   }
   const long long tiles = (long long)A.B * A.Hkv * A.n_groups;
   const long long most = tiles * ((A.Lmax + S::kBlk - 1) / S::kBlk + kTileCost);
-  const int grid = (int)(most < kCacheAttnCtas ? most : kCacheAttnCtas);
+  const int parts = cache_attn_parts(A, kCacheAttnCtas, most);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(parts * A.head_lanes);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
@@ -1429,7 +1459,7 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
   cfg.gridDim = dim3((unsigned)tiles, (A.group_pos * A.G + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<kE4m3, kD, kRP>, A, grid);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<kE4m3, kD, kRP>, A, parts);
 }
 
 template <bool kE4m3, int kD, int kRP>

@@ -19,9 +19,10 @@
 // barrier with a vote per block finds out; sums stay with the keys' threads
 // until the tile ends.
 //
-// Two CTAs per SM (256 tensor memory columns each). Warps 0-3 softmax, 4
-// producer, 5 and 6 issuers, 7 queries, row tables and the check of V blocks
-// that not every query sees whole.
+// Two CTAs per SM (256 tensor memory columns each) of six warps, so that a
+// thread may have 168 registers: 0-3 softmax, 4 loads (K and V blocks,
+// queries and row tables, the check of V blocks that not every query sees
+// whole), 5 issues both products.
 #pragma once
 
 #include "cache_attention.cuh"
@@ -29,7 +30,7 @@
 namespace specdec {
 namespace cache_attn {
 
-constexpr int kKeyThreads = 256;
+constexpr int kKeyThreads = 192;
 constexpr int kKeyD = 128, kKeyBlk = 128, kKeyRows = 32, kKeyRing = 2;
 constexpr int kKeySlot = kKeyBlk * kKeyD;
 constexpr int kKeyPTerm = kKeyBlk * kKeyRows;           // [keys][32 rows] codes of one term
@@ -39,7 +40,7 @@ constexpr float kRise = 4.f, kLift = 2.f, kBase = 4.f;  // log2: see above; p at
 // row tables per query buffer: score factor, slope, depth, index [32] each
 constexpr int kKeyTab = 4 * kKeyRows * 4;
 constexpr int kKeySmem = 1024 + 2 * kKeyRing * kKeySlot + 2 * 3 * kKeyPTerm + 2 * kKeyQBytes + 2 * kKeyTab +
-                         2 * kKeyRows * 4 + 4 * kKeyRows * 4 + 128 * 16 + 128 * 4 + 512;
+                         3 * kKeyRows * 4 + 4 * kKeyRows * 4 + 128 * 16 + 128 * 4 + 512;
 static_assert(2 * (kKeySmem + 1024) <= 228 * 1024, "two CTAs per SM");
 
 // MN-major operand of 32-byte rows (32 codes along N), 32-byte swizzle.
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
   const uint32_t qb = pb + 2 * 3 * kKeyPTerm;
   const uint32_t tab = qb + 2 * kKeyQBytes;
   const uint32_t ref = tab + 2 * kKeyTab;                  // references, then factors for what moved
-  const uint32_t red = ref + 2 * kRows * 4;                // [4 warps][32 rows]
+  const uint32_t zeros = ref + 2 * kRows * 4;              // [32]
+  const uint32_t red = zeros + kRows * 4;                  // [4 warps][32 rows]
   const uint32_t tree = red + 4 * kRows * 4;
   const uint32_t bars = tree + 128 * 16 + 128 * 4;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       mbar_init(k_full(s), 1);
       mbar_init(k_empty(s), 1);
       mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 2);          // the product and the checking warp
+      mbar_init(v_empty(s), 1);
       mbar_init(v_clean(s), 1);
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), kSoftWarps);
@@ -124,12 +126,13 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1 + kSoftWarps);
     }
-    mbar_init(drained, 2);
+    mbar_init(drained, 1);
     *abort = 0;
     *odd = 0;
     fence_mbar_init();
   }
-  if (warp == 6) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 256);
+  if (warp == 0) sts32(zeros + lane * 4, 0u);
+  if (warp == 5) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 256);
   if (A.tree) {
     for (int e = threadIdx.x; e < A.n_new; e += kKeyThreads) {
       sts128(tree + e * 16, A.anc[e][0], A.anc[e][1], A.anc[e][2], A.anc[e][3]);
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
   grid_dependency_wait();
   grid_launch_dependents();          // the merge may get ready on idle SMs
   if (warp == 0) {
-    const Place pl = find_part<kBlk>(A, lane, blockIdx.x, gridDim.x);
+    const Place pl = find_part<kBlk>(A, lane, blockIdx.x / A.head_lanes, gridDim.x / A.head_lanes);
     if (lane == 0) {
       place[0] = pl.b;
       place[1] = pl.off;
@@ -161,99 +164,18 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
   uint32_t issued_k = 0, issued_v = 0, phase_k = 0, phase_v = 0;   // producer: copies in flight
 
   if (warp == 4) {
-    // ---------------------------------------------------------- producer --
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_first();
-      uint32_t n = 0;
-      bool ok = true;
-      for (; ok && !w.done(); w.next(A))
-        for (int i = 0; i < w.n_here; ++i, ++n) {
-          const int s = n & 1, j0 = (w.first + w.blk + i) * kBlk;
-          const uint32_t ph = (n >> 1) & 1;
-          if (!(ok = mbar_wait(k_empty(s), ph ^ 1u, abort, A.status))) break;
-          mbar_arrive_expect_tx(k_full(s), kKeySlot);
-          tma_load_4d(ring_k + s * kKeySlot, &tmap_k, k_full(s), 0, w.h, j0, w.b, pol);
-          issued_k |= 1u << s;
-          phase_k = (phase_k & ~(1u << s)) | (ph << s);
-          if (!(ok = mbar_wait(v_empty(s), ph ^ 1u, abort, A.status))) break;
-          mbar_arrive_expect_tx(v_full(s), kKeySlot);
-          tma_load_4d(ring_v + s * kKeySlot, &tmap_v, v_full(s), 0, w.h, j0, w.b, pol);
-          issued_v |= 1u << s;
-          phase_v = (phase_v & ~(1u << s)) | (ph << s);
-        }
-    }
-  } else if (warp == 5) {
-    // ------------------------------------------------- issuer of K Q^T --
-    constexpr uint32_t id = instr_desc(0, false, 2 * kRows);
-    const uint64_t k_desc = operand_desc<128>(ring_k, 16), q_desc = operand_desc<128>(qb, 16);
+    // ------------------------------------------------------------- loads --
+    const uint64_t pol = policy_evict_first();
     uint32_t n = 0, nt = 0;
     bool ok = true;
-    for (; ok && !w.done(); w.next(A), ++nt) {
-      const uint32_t qs = nt & 1;
-      if (!(ok = warp_wait(q_full(qs), (nt >> 1) & 1))) break;
-      const uint64_t qd = q_desc + (uint64_t)(qs * (kKeyQBytes >> 4));
-      for (int i = 0; i < w.n_here; ++i, ++n) {
-        const uint32_t s = n & 1;
-        if (!(ok = warp_wait(k_full(s), (n >> 1) & 1))) break;
-        if (n >= 2 && !(ok = warp_wait(p_full(s), ((n - 2) >> 1) & 1))) break;   // scores two blocks ago are read
-        tc_fence_after();
-        const uint64_t kd = k_desc + (uint64_t)(s * (kKeySlot >> 4));
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kD / 32; ++k)
-            mma_ss<true>(tmem + kKeyColS + s * 64, kd + 2 * k, qd + 2 * k, id, k > 0);
-          tc_commit(s_full(s));
-          tc_commit(k_empty(s));
-          if (i + 1 == w.n_here) tc_commit(q_empty(qs));
-        }
-        __syncwarp();
-      }
-    }
-    if (elect_one()) tc_commit(drained);
-    wait_drain(drained, 0);
-  } else if (warp == 6) {
-    // ----------------------------------------------- issuer of V^T P^T --
-    constexpr uint32_t id = instr_desc(0, true, 3 * kRows) | (1u << 15);     // A (V^T) is M-major too
-    const uint64_t v_desc = operand_desc<128>(ring_v, 16), p_desc = operand_desc32(pb, kKeyPTerm);
-    uint32_t n = 0, clean_ph = 0;
-    bool ok = true;
-    for (; ok && !w.done(); w.next(A))
-      for (int i = 0; i < w.n_here; ++i, ++n) {
-        const uint32_t s = n & 1;
-        if (!(ok = warp_wait(v_full(s), (n >> 1) & 1))) break;
-        if (!w.clean(i)) {
-          if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) break;
-          clean_ph ^= 1u << s;
-        }
-        if (!(ok = warp_wait(p_full(s), (n >> 1) & 1))) break;
-        tc_fence_after();
-        const uint64_t vd = v_desc + (uint64_t)(s * (kKeySlot >> 4));
-        const uint64_t pd = p_desc + (uint64_t)(s * (3 * kKeyPTerm >> 4));
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kBlk / 32; ++k)
-            mma_ss<true>(tmem + kKeyColO, vd + k * (32 * 128 >> 4), pd + k * (32 * 32 >> 4), id, i > 0 || k > 0);
-          tc_commit(o_done(s));
-          tc_commit(v_empty(s));
-        }
-        __syncwarp();
-      }
-    // every product has to be done before the tensor memory is given back
-    if (elect_one()) tc_commit(drained);
-    wait_drain(drained, 0);
-  } else if (warp == 7) {
-    // ------------------------------ queries, row tables, odd values of V --
-    Walk<kBlk> wl = w;                   // the tile whose queries come next
-    uint32_t tl = 0, n = 0;
-    bool ok = true;
     auto load_queries = [&]() {
-      const uint32_t qs = tl & 1;
-      if (!warp_wait(q_empty(qs), ((tl >> 1) & 1) ^ 1u)) return false;
+      const uint32_t qs = nt & 1;
+      if (!warp_wait(q_empty(qs), ((nt >> 1) & 1) ^ 1u)) return false;
       // lane = row: two e4m3 terms of its 128 dims
-      const int pos0 = wl.g * A.group_pos, row = lane;
+      const int pos0 = w.g * A.group_pos, row = lane;
       const bool mine = row < min(A.group_pos, A.n_new - pos0) * A.G;
-      const int idx = mine ? pos0 + row / A.G : 0, head = wl.h * A.G + (mine ? row % A.G : 0);
-      const uint4* src = reinterpret_cast<const uint4*>(A.q + ((size_t)wl.b * A.n_new + idx) * A.q_stride +
+      const int idx = mine ? pos0 + row / A.G : 0, head = w.h * A.G + (mine ? row % A.G : 0);
+      const uint4* src = reinterpret_cast<const uint4*>(A.q + ((size_t)w.b * A.n_new + idx) * A.q_stride +
                                                         (size_t)head * kD);
       uint32_t wv[kD / 2];
 #pragma unroll
@@ -302,51 +224,132 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(qs));
-      ++tl;
-      wl.next(A);
       return true;
     };
-    for (int k = 0; k < 2; ++k)
-      if (ok && !wl.done()) ok = load_queries();
-    for (uint32_t nt = 0; ok && !w.done(); w.next(A), ++nt) {
+    // A block that not every query sees whole, before V^T P^T takes it.
+    int check_j0 = -1, check_L = 0;      // the last block loaded: its first row (-1: nothing to do), its sequence
+    auto check_values = [&](uint32_t nb) {
+      if (check_j0 < 0) return true;
+      const uint32_t s = nb & 1;
+      if (!warp_wait(v_full(s), (nb >> 1) & 1)) return false;
+      // Rows past the sequence hold anything, and a NaN in a row that not
+      // every query sees would pass a zero probability: neither stays in
+      // the product. The epilogue adds the NaN where seen.
+      for (int e = lane; e < kKeySlot / 16; e += 32) {
+        const uint32_t a = ring_v + s * kKeySlot + e * 16;
+        const uint4 v = lds128(a);
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        bool put = false;
+        if (check_j0 + (e >> 3) >= check_L) {
+          x[0] = x[1] = x[2] = x[3] = 0u;
+          put = true;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // bytes whose low seven bits are all ones
+          const uint32_t nan = __vcmpeq4(x[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          if (nan) {
+            x[k] &= ~nan;
+            put = true;
+            *odd = 1;
+          }
+        }
+        if (put) sts128(a, x[0], x[1], x[2], x[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_clean(s));
+      return true;
+    };
+    for (; ok && !w.done(); w.next(A), ++nt) {
+      if (!(ok = load_queries())) break;
       for (int i = 0; i < w.n_here; ++i, ++n) {
+        const uint32_t s = n & 1, ph = (n >> 1) & 1;
+        const int j0 = (w.first + w.blk + i) * kBlk;
+        if (!(ok = warp_wait(k_empty(s), ph ^ 1u))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(k_full(s), kKeySlot);
+          tma_load_4d(ring_k + s * kKeySlot, &tmap_k, k_full(s), 0, w.h, j0, w.b, pol);
+        }
+        __syncwarp();
+        issued_k |= 1u << s;
+        phase_k = (phase_k & ~(1u << s)) | (ph << s);
+        if (!(ok = warp_wait(v_empty(s), ph ^ 1u))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(v_full(s), kKeySlot);
+          tma_load_4d(ring_v + s * kKeySlot, &tmap_v, v_full(s), 0, w.h, j0, w.b, pol);
+        }
+        __syncwarp();
+        issued_v |= 1u << s;
+        phase_v = (phase_v & ~(1u << s)) | (ph << s);
+        // the check runs a block behind, when its values are likely there
+        if (!(ok = check_values(n - 1))) break;
+        check_j0 = w.clean(i) ? -1 : j0;
+        check_L = w.L;
+      }
+    }
+    if (ok) check_values(n - 1);
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ issuer --
+    // Scores run a block ahead of the values' product.
+    constexpr uint32_t id_s = instr_desc(0, false, 2 * kRows);
+    constexpr uint32_t id_o = instr_desc(0, true, 3 * kRows) | (1u << 15);     // A (V^T) is M-major too
+    const uint64_t k_desc = operand_desc<128>(ring_k, 16), q_desc = operand_desc<128>(qb, 16);
+    const uint64_t v_desc = operand_desc<128>(ring_v, 16), p_desc = operand_desc32(pb, kKeyPTerm);
+    Walk<kBlk> wq = w;
+    uint32_t nq = 0, tq = 0, n = 0, clean_ph = 0;
+    int iq = 0;
+    auto issue_scores = [&]() {
+      const uint32_t qs = tq & 1, s = nq & 1;
+      if (iq == 0 && !warp_wait(q_full(qs), (tq >> 1) & 1)) return false;
+      if (!warp_wait(k_full(s), (nq >> 1) & 1)) return false;
+      tc_fence_after();
+      const uint64_t kd = k_desc + (uint64_t)(s * (kKeySlot >> 4)), qd = q_desc + (uint64_t)(qs * (kKeyQBytes >> 4));
+      const bool last = iq + 1 == wq.n_here;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k) mma_ss<true>(tmem + kKeyColS + s * 64, kd + 2 * k, qd + 2 * k, id_s, k > 0);
+        tc_commit(s_full(s));
+        tc_commit(k_empty(s));
+        if (last) tc_commit(q_empty(qs));
+      }
+      __syncwarp();
+      ++nq;
+      ++iq;
+      if (last) {
+        iq = 0;
+        ++tq;
+        wq.next(A);
+      }
+      return true;
+    };
+    bool ok = w.done() || issue_scores();
+    for (; ok && !w.done(); w.next(A))
+      for (int i = 0; i < w.n_here; ++i, ++n) {
+        // the other buffer's scores were read before the last product was issued
+        if (!wq.done() && !(ok = issue_scores())) break;
         const uint32_t s = n & 1;
         if (!(ok = warp_wait(v_full(s), (n >> 1) & 1))) break;
         if (!w.clean(i)) {
-          // Rows past the sequence hold anything, and a NaN in a row that not
-          // every query sees would pass a zero probability: neither stays in
-          // the product. The epilogue adds the NaN where seen.
-          const int j0 = (w.first + w.blk + i) * kBlk;
-          for (int e = lane; e < kKeySlot / 16; e += 32) {
-            const uint32_t a = ring_v + s * kKeySlot + e * 16;
-            const uint4 v = lds128(a);
-            uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            bool put = false;
-            if (j0 + (e >> 3) >= w.L) {
-              x[0] = x[1] = x[2] = x[3] = 0u;
-              put = true;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // bytes whose low seven bits are all ones
-              const uint32_t nan = __vcmpeq4(x[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              if (nan) {
-                x[k] &= ~nan;
-                put = true;
-                *odd = 1;
-              }
-            }
-            if (put) sts128(a, x[0], x[1], x[2], x[3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v_clean(s));
+          if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) break;
+          clean_ph ^= 1u << s;
         }
-        if (lane == 0) mbar_arrive(v_empty(s));
-        // the next tile's queries, once the last tile's buffer is about free
-        if (i == 0 && nt > 0 && !wl.done() && !(ok = load_queries())) break;
+        if (!(ok = warp_wait(p_full(s), (n >> 1) & 1))) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + (uint64_t)(s * (kKeySlot >> 4));
+        const uint64_t pd = p_desc + (uint64_t)(s * (3 * kKeyPTerm >> 4));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kBlk / 32; ++k)
+            mma_ss<true>(tmem + kKeyColO, vd + k * (32 * 128 >> 4), pd + k * (32 * 32 >> 4), id_o, i > 0 || k > 0);
+          tc_commit(o_done(s));
+          tc_commit(v_empty(s));
+        }
+        __syncwarp();
       }
-    }
+    // every product has to be done before the tensor memory is given back
+    if (elect_one()) tc_commit(drained);
+    wait_drain(drained, 0);
   } else {
     // ----------------------------------------------------------- softmax --
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
@@ -381,9 +384,14 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
         if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
         tc_fence_after();
         float y[kRows];
-        // Exponents of this key for every row, less `base` minus the rows'
-        // references (with_ref) or as they are.
-        auto exponents = [&](bool with_ref) {
+        // The tile's first block begins with its rows' maxima, other blocks
+        // with exponents against the references; one of those too high
+        // brings in the maxima as well. (`from_ref` points at the references,
+        // or at zeros: one piece of code for both.)
+        bool maxima = ib == 0, settled = ib == 0;
+        for (;;) {
+          const uint32_t from_ref = maxima ? zeros : ref;
+          if (!dead) {
           const uint32_t from = tl + kKeyColS + (n & 1) * 64;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -406,8 +414,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
 #pragma unroll
           for (int r = 0; r < kRows; r += 4) {
             const float4 c = lds128f(t0 + r * 4);
-            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (with_ref) m = lds128f(ref + r * 4);
+            const float4 m = lds128f(from_ref + r * 4);
             const float cc[4] = {c.x, c.y, c.z, c.w};
             const float bb[4] = {lv + kBase - m.x, lv + kBase - m.y, lv + kBase - m.z, lv + kBase - m.w};
             if constexpr (kExtra) {
@@ -449,16 +456,19 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
               if (!seen) y[r] = -INFINITY;
             }
           }
-        };
-        if (!dead) exponents(true);
-        float top = -INFINITY;
-        if (!dead) {
+          }
+          if (!maxima) {
+            if (settled) break;
+            float top = -INFINITY;
+            if (!dead) {
 #pragma unroll
-          for (int r = 0; r < kRows; r += 4) top = max3(max3(top, y[r], y[r + 1]), y[r + 2], y[r + 3]);
-        }
-        if (bar_any(1, 32 * kSoftWarps, top > kBase + kRise)) {
-          // ---- some row's reference has to move: all rows' maxima ----
-          if (!dead) exponents(false);
+              for (int r = 0; r < kRows; r += 4) top = max3(max3(top, y[r], y[r + 1]), y[r + 2], y[r + 3]);
+            }
+            if (!bar_any(1, 32 * kSoftWarps, top > kBase + kRise)) break;
+            maxima = settled = true;
+            continue;
+          }
+          // ---- some row's reference has to move ----
           if (dead) {
 #pragma unroll
             for (int r = 0; r < kRows; ++r) y[r] = -INFINITY;
@@ -512,8 +522,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
                 tmem_wait_store();
               }
             }
-            if (!dead) exponents(true);
           }
+          maxima = false;
         }
         // ---- probabilities, as three e4m3 terms ----
         // the product that read this buffer two blocks ago is done
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
   tc_fence_before();
   __syncthreads();   // every role has left its loop
   tc_fence_after();
-  if (warp == 6) tmem_dealloc(tmem, 256);
+  if (warp == 5) tmem_dealloc(tmem, 256);
   if (*abort && warp == 4 && lane == 0)
     // A wait gave up: let every copy already issued land before the CTA exits.
     for (int s = 0; s < kR; ++s) {
@@ -660,9 +670,9 @@ cudaError_t launch_keys(const CacheAttnLaunch& A, const CUtensorMap& tk, const C
   }
   const long long tiles = (long long)A.B * A.Hkv * A.n_groups;
   const long long most = tiles * ((A.Lmax + kKeyBlk - 1) / kKeyBlk + kTileCost);
-  const int grid = (int)(most < kCacheAttnMaxCtas ? most : kCacheAttnMaxCtas);
+  const int parts = cache_attn_parts(A, kCacheAttnMaxCtas, most);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(parts * A.head_lanes);
   cfg.blockDim = dim3(kKeyThreads);
   cfg.dynamicSmemBytes = kKeySmem;
   cfg.stream = stream;
@@ -676,7 +686,7 @@ cudaError_t launch_keys(const CacheAttnLaunch& A, const CUtensorMap& tk, const C
   cfg.gridDim = dim3((unsigned)tiles, (A.group_pos * A.G + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<true, kKeyD, kKeyRows>, A, grid);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<true, kKeyD, kKeyRows>, A, parts);
 }
 
 }  // namespace cache_attn

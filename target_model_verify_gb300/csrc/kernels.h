@@ -198,6 +198,7 @@ struct CacheAttnLaunch {
   int tree;                          // 1: anc and depth describe the new positions
   int max_depth;                     // of the new positions (n_new - 1 for a chain)
   int n_scale;                       // scales per (sequence, KV head)
+  int head_lanes;                    // CTAs beside each other on a part: Hkv, or 1
   float scale, cap, cap_exp;         // cap_exp = 2 log2(e) / cap
   long long q_stride;                // elements from one position's queries to the next's
   const __nv_bfloat16* q;            // [B, n_new, Hq, D]
