@@ -228,14 +228,29 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 // Two fp32 operations in one instruction.
-__device__ __forceinline__ void fma2(float& a, float& b, float c, float d) {   // (a, b) * c + d
+__device__ __forceinline__ void fma2(float& a, float& b, float c, float d, float e, float f) {   // a c + e, b d + f
   asm("{\n\t.reg .b64 x, y, z;\n\t"
-      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmov.b64 z, {%4, %5};\n\t"
       "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d), "f"(e), "f"(f));
+}
+__device__ __forceinline__ void fma2(float& a, float& b, float c, float d) { fma2(a, b, c, c, d, d); }
+__device__ __forceinline__ void acc2(float& a, float& b, float c, float d, float e) {   // a += c e, b += d e
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmov.b64 z, {%4, %4};\n\t"
+      "fma.rn.f32x2 x, y, z, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d), "f"(e));
+}
+__device__ __forceinline__ void mul2(float& a, float& b, float c, float d) {   // a *= c, b *= d
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a), "+f"(b)
       : "f"(c), "f"(d));
 }
-__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {   // (a, b) + (c, d)
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {   // a += c, b += d
   asm("{\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
       "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
@@ -1400,18 +1415,28 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] *= alpha;
     M = m_new;
+    // eight partials' loads in flight at a time
     const int here = min(32, c1 - cb + 1);
-#pragma unroll 8
-    for (int x = 0; x < here; ++x) {
-      const int s = __shfl_sync(0xffffffffu, slot, x);
-      const float f = __shfl_sync(0xffffffffu, wgt, x);
-      const float* po = A.part_o + ((size_t)s * kRP + r) * kD + lane * kPer;
+    for (int x0 = 0; x0 < here; x0 += 8) {
+      float f[8];
+      float2 v[8][kPer / 2];
 #pragma unroll
-      for (int k = 0; k < kPer; k += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(po + k);
-        acc[k] = fmaf(v.x, f, acc[k]);
-        acc[k + 1] = fmaf(v.y, f, acc[k + 1]);
+      for (int x = 0; x < 8; ++x) {
+        const int from = min(x0 + x, here - 1);
+        const int s = __shfl_sync(0xffffffffu, slot, from);
+        f[x] = __shfl_sync(0xffffffffu, wgt, from);
+        if (x0 + x >= here) f[x] = 0.f;
+        const float2* po = reinterpret_cast<const float2*>(A.part_o + ((size_t)s * kRP + r) * kD + lane * kPer);
+#pragma unroll
+        for (int k = 0; k < kPer / 2; ++k) v[x][k] = __ldcg(po + k);
       }
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int k = 0; k < kPer / 2; ++k) {
+          acc[2 * k] = fmaf(v[x][k].x, f[x], acc[2 * k]);
+          acc[2 * k + 1] = fmaf(v[x][k].y, f[x], acc[2 * k + 1]);
+        }
     }
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);

@@ -37,8 +37,9 @@ constexpr int kKeyPTerm = kKeyBlk * kKeyRows;           // [keys][32 rows] codes
 constexpr int kKeyQBytes = 2 * kKeyRows * kKeyD;        // [hi rows, lo rows][dims]
 constexpr int kKeyColS = 0, kKeyColO = 128;
 constexpr float kRise = 4.f, kLift = 2.f, kBase = 4.f;  // log2: see above; p at the reference is 2^kBase
-// row tables per query buffer: score factor, slope, depth, index [32] each
-constexpr int kKeyTab = 4 * kKeyRows * 4;
+// tables per query buffer: of every row its score factor, slope, depth and
+// place in the output [32]; of every new position the rows that see it [128]
+constexpr int kKeyTab = 4 * kKeyRows * 4 + 128 * 4;
 constexpr int kKeySmem = 1024 + 2 * kKeyRing * kKeySlot + 2 * 3 * kKeyPTerm + 2 * kKeyQBytes + 2 * kKeyTab +
                          3 * kKeyRows * 4 + 4 * kKeyRows * 4 + 128 * 16 + 128 * 4 + 512;
 static_assert(2 * (kKeySmem + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -168,14 +169,14 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
     const uint64_t pol = policy_evict_first();
     uint32_t n = 0, nt = 0;
     bool ok = true;
-    auto load_queries = [&]() {
+    auto load_queries = [&](const Walk<kBlk>& t, uint32_t nt) {
       const uint32_t qs = nt & 1;
       if (!warp_wait(q_empty(qs), ((nt >> 1) & 1) ^ 1u)) return false;
       // lane = row: two e4m3 terms of its 128 dims
-      const int pos0 = w.g * A.group_pos, row = lane;
+      const int pos0 = t.g * A.group_pos, row = lane;
       const bool mine = row < min(A.group_pos, A.n_new - pos0) * A.G;
-      const int idx = mine ? pos0 + row / A.G : 0, head = w.h * A.G + (mine ? row % A.G : 0);
-      const uint4* src = reinterpret_cast<const uint4*>(A.q + ((size_t)w.b * A.n_new + idx) * A.q_stride +
+      const int idx = mine ? pos0 + row / A.G : 0, head = t.h * A.G + (mine ? row % A.G : 0);
+      const uint4* src = reinterpret_cast<const uint4*>(A.q + ((size_t)t.b * A.n_new + idx) * A.q_stride +
                                                         (size_t)head * kD);
       uint32_t wv[kD / 2];
 #pragma unroll
@@ -211,16 +212,35 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           hi[k] = ph[0] | (ph[1] << 16);
           lo[k] = pl[0] | (pl[1] << 16);
         }
-        const uint32_t at = (uint32_t)((c ^ (row & 7)) << 4);
-        sts128(hi_row + at, hi[0], hi[1], hi[2], hi[3]);
-        sts128(lo_row + at, lo[0], lo[1], lo[2], lo[3]);
+        const uint32_t to = (uint32_t)((c ^ (row & 7)) << 4);
+        sts128(hi_row + to, hi[0], hi[1], hi[2], hi[3]);
+        sts128(lo_row + to, lo[0], lo[1], lo[2], lo[3]);
       }
-      const uint32_t t = tab + qs * kKeyTab + row * 4;
+      const uint32_t at = tab + qs * kKeyTab + row * 4;
       const float q_scale = fine ? __uint_as_float((uint32_t)(127 + down) << 23) : __uint_as_float(0x7fffffffu);
-      sts32(t, __float_as_uint(A.scale * q_scale * (kExtra ? 1.f : kLog2e)));
-      sts32(t + kRows * 4, __float_as_uint(kExtra && A.slopes ? A.slopes[head] * kLog2e : 0.f));
-      sts32(t + 2 * kRows * 4, (uint32_t)(A.tree ? (int)lds32(tree + 128 * 16 + idx * 4) : idx));
-      sts32(t + 3 * kRows * 4, (uint32_t)idx);
+      sts32(at, __float_as_uint(A.scale * q_scale * (kExtra ? 1.f : kLog2e)));
+      sts32(at + kRows * 4, __float_as_uint(kExtra && A.slopes ? A.slopes[head] * kLog2e : 0.f));
+      const int dep = A.tree ? (int)lds32(tree + 128 * 16 + idx * 4) : idx;
+      sts32(at + 2 * kRows * 4, __float_as_uint((float)dep));
+      sts32(at + 3 * kRows * 4, (uint32_t)(idx * A.Hq + head));
+      for (int a0 = 0; a0 < A.n_new; a0 += 32) {
+        uint32_t sees = 0, of_mine = 0;          // new positions a0 .. a0 + 31 that this row sees
+        if (A.tree)
+          sees = lds32(tree + idx * 16 + (a0 >> 5) * 4);
+        else if (idx >= a0)
+          sees = idx - a0 >= 31 ? 0xffffffffu : (2u << (idx - a0)) - 1u;
+#pragma unroll
+        for (int a = 0; a < 32; ++a) {
+          bool see = (sees >> a) & 1u;
+          if (A.window > 0) {
+            const int da = A.tree ? (int)lds32(tree + 128 * 16 + (a0 + a) * 4) : a0 + a;
+            see = see && dep - da < A.window;
+          }
+          const uint32_t rows = __ballot_sync(0xffffffffu, see);
+          if (lane == a) of_mine = rows;
+        }
+        sts32(tab + qs * kKeyTab + 4 * kRows * 4 + (a0 + lane) * 4, of_mine);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(qs));
@@ -261,8 +281,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       if (lane == 0) mbar_arrive(v_clean(s));
       return true;
     };
+    if (!w.done()) ok = load_queries(w, 0);
     for (; ok && !w.done(); w.next(A), ++nt) {
-      if (!(ok = load_queries())) break;
       for (int i = 0; i < w.n_here; ++i, ++n) {
         const uint32_t s = n & 1, ph = (n >> 1) & 1;
         const int j0 = (w.first + w.blk + i) * kBlk;
@@ -286,6 +306,12 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
         if (!(ok = check_values(n - 1))) break;
         check_j0 = w.clean(i) ? -1 : j0;
         check_L = w.L;
+        if (i == w.n_here / 2) {
+          // halfway, when the last tile's buffer is free: the next one's queries
+          Walk<kBlk> then = w;
+          then.next(A);
+          if (!then.done() && !(ok = load_queries(then, nt + 1))) break;
+        }
       }
     }
     if (ok) check_values(n - 1);
@@ -370,39 +396,51 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
         sv_next = jw < w.L ? __ldg(vs + jw / SPECDEC_KV8_BLOCK) : 1.f;
       };
       load_scales(j - lane);
+      // The rows that see cache row jj: those that see its new position, or,
+      // before the new rows, those whose window reaches it.
+      auto seen_by = [&](int jj) {
+        const int a = jj - P0;
+        if (jj >= w.L) return 0u;
+        if (a >= 0) return lds32(t0 + 4 * kRows * 4 + a * 4);
+        if (A.window <= 0) return 0xffffffffu;
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < kRows; r += 4) {
+          const float4 d = lds128f(t0 + 2 * kRows * 4 + r * 4);
+          m |= ((int)d.x - a < A.window ? 1u : 0u) << r | ((int)d.y - a < A.window ? 2u : 0u) << r |
+               ((int)d.z - a < A.window ? 4u : 0u) << r | ((int)d.w - a < A.window ? 8u : 0u) << r;
+        }
+        return m;
+      };
       float l[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) l[r] = 0.f;
-      if (warp == 0) sts32(ref + lane * 4, __float_as_uint(-INFINITY));
+      if (warp == 0) sts32(ref + lane * 4, __float_as_uint(INFINITY));      // negated: none yet
       if (!dead && !warp_wait(q_full(qs), (nt >> 1) & 1)) dead = true;
       named_bar_sync(1, 32 * kSoftWarps);
 
       for (int ib = 0; ib < w.n_here; ++ib, ++n, j += kBlk) {
         const bool clean = w.clean(ib);
-        const float sk = sk_next, lv = __log2f(sv_next), inv_sv = rcp(sv_next);
+        const float sk = sk_next, lvb = __log2f(sv_next) + kBase, inv_sv = rcp(sv_next);
         if (ib + 1 < w.n_here) load_scales(j - lane + kBlk);
         if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
         tc_fence_after();
         float y[kRows];
         // The tile's first block begins with its rows' maxima, other blocks
         // with exponents against the references; one of those too high
-        // brings in the maxima as well. (`from_ref` points at the references,
-        // or at zeros: one piece of code for both.)
+        // brings in the maxima as well. (`from_ref` points at the negated
+        // references, or at zeros: one piece of code for both.)
         bool maxima = ib == 0, settled = ib == 0;
         for (;;) {
           const uint32_t from_ref = maxima ? zeros : ref;
           if (!dead) {
-          const uint32_t from = tl + kKeyColS + (n & 1) * 64;
+            uint32_t u[64];
+            tmem_load(tl + kKeyColS + (n & 1) * 64, u);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t a[16], b[16];
-            tmem_load(from + 16 * hf, a);
-            tmem_load(from + 32 + 16 * hf, b);
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              y[16 * hf + k] = __uint_as_float(a[k]);
-              y[16 * hf + k + 1] = __uint_as_float(a[k + 1]);
-              add2(y[16 * hf + k], y[16 * hf + k + 1], __uint_as_float(b[k]), __uint_as_float(b[k + 1]));
+            for (int r = 0; r < kRows; r += 2) {
+              y[r] = __uint_as_float(u[r]);
+              y[r + 1] = __uint_as_float(u[r + 1]);
+              add2(y[r], y[r + 1], __uint_as_float(u[32 + r]), __uint_as_float(u[33 + r]));
             }
           }
           float pj = 0.f;
@@ -414,17 +452,20 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
 #pragma unroll
           for (int r = 0; r < kRows; r += 4) {
             const float4 c = lds128f(t0 + r * 4);
-            const float4 m = lds128f(from_ref + r * 4);
-            const float cc[4] = {c.x, c.y, c.z, c.w};
-            const float bb[4] = {lv + kBase - m.x, lv + kBase - m.y, lv + kBase - m.z, lv + kBase - m.w};
+            float4 b = lds128f(from_ref + r * 4);
+            add2(b.x, b.y, lvb, lvb);
+            add2(b.z, b.w, lvb, lvb);
+            // The product with the row's factor is rounded before anything is
+            // added, so that exponents of any size agree with their reference.
+            mul2(y[r], y[r + 1], c.x, c.y);
+            mul2(y[r + 2], y[r + 3], c.z, c.w);
             if constexpr (kExtra) {
-              const float4 sl = lds128f(t0 + kRows * 4 + r * 4);
-              const uint4 dp = lds128(t0 + 2 * kRows * 4 + r * 4);
-              const float ss[4] = {sl.x, sl.y, sl.z, sl.w};
-              const float dd[4] = {(float)(int)dp.x, (float)(int)dp.y, (float)(int)dp.z, (float)(int)dp.w};
+              const float4 sl = lds128f(t0 + kRows * 4 + r * 4), dp = lds128f(t0 + 2 * kRows * 4 + r * 4);
+              const float bb[4] = {b.x, b.y, b.z, b.w}, ss[4] = {sl.x, sl.y, sl.z, sl.w},
+                          dd[4] = {dp.x, dp.y, dp.z, dp.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float z = y[r + k] * (cc[k] * sk);
+                const float z = y[r + k] * sk;
                 float e;
                 if (A.cap > 0.f)       // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
                   e = fmaf(-2.f * A.cap * kLog2e, rcp(1.f + ex2(z * A.cap_exp)), A.cap * kLog2e);
@@ -433,29 +474,14 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
                 y[r + k] = fmaf(ss[k], pj - dd[k], e) + bb[k];
               }
             } else {
-              // the product is rounded before the reference comes off, so that
-              // exponents of any size agree with it
-#pragma unroll
-              for (int k = 0; k < 4; ++k) y[r + k] = fmaf(y[r + k], cc[k] * sk, 0.f) + bb[k];
+              fma2(y[r], y[r + 1], sk, sk, b.x, b.y);
+              fma2(y[r + 2], y[r + 3], sk, sk, b.z, b.w);
             }
           }
           if (!clean) {
-            const int a = j - P0;
-            const int da = A.tree && a >= 0 ? (int)lds32(tree + 128 * 16 + min(a, A.n_new - 1) * 4) : a;
+            const uint32_t m = seen_by(j);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-              const int dep = (int)lds32(t0 + 2 * kRows * 4 + r * 4);
-              bool seen = j < w.L && (A.window <= 0 || dep - da < A.window);
-              if (a >= 0) {
-                const int idx = (int)lds32(t0 + 3 * kRows * 4 + r * 4);
-                if (A.tree)
-                  seen = seen && ((lds32(tree + idx * 16 + (min(a, 127) >> 5) * 4) >> (a & 31)) & 1u);
-                else
-                  seen = seen && a <= idx;
-              }
-              if (!seen) y[r] = -INFINITY;
-            }
-          }
+            for (int r = 0; r < kRows; ++r) y[r] = (m >> r) & 1u ? y[r] : -INFINITY;
           }
           if (!maxima) {
             if (settled) break;
@@ -489,9 +515,9 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
             float M = __uint_as_float(lds32(red + lane * 4));
 #pragma unroll
             for (int x = 1; x < kSoftWarps; ++x) M = fmaxf(M, __uint_as_float(lds32(red + (x * 32 + lane) * 4)));
-            const float was = __uint_as_float(lds32(ref + lane * 4));
+            const float was = -__uint_as_float(lds32(ref + lane * 4));
             const bool move = M > was + kRise;
-            sts32(ref + lane * 4, __float_as_uint(move ? M + kLift : was));
+            sts32(ref + lane * 4, __float_as_uint(-(move ? M + kLift : was)));
             sts32(ref + kRows * 4 + lane * 4, __float_as_uint(move ? ex2(was - (M + kLift)) : 1.f));
           }
           named_bar_sync(1, 32 * kSoftWarps);
@@ -526,8 +552,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           maxima = false;
         }
         // ---- probabilities, as three e4m3 terms ----
-        // the product that read this buffer two blocks ago is done
-        if (!dead && n >= 2 && !warp_wait(o_done(n & 1), ((n - 2) >> 1) & 1)) dead = true;
+        // (the product that read this buffer two blocks ago was issued before
+        // this block's scores, so it is done)
         if (dead) continue;
         const uint32_t to = pb + (n & 1) * 3 * kKeyPTerm + kl * 32;
 #pragma unroll
@@ -539,10 +565,9 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const int r = 16 * h16 + 4 * q + 2 * x;
-              float p0 = ex2(y[r]), p1 = ex2(y[r + 1]);
+              const float p0 = ex2(y[r]), p1 = ex2(y[r + 1]);
               const uint32_t h = pack2<true>(p0, p1);
-              fma2(p0, p1, inv_sv, 0.f);
-              add2(l[r], l[r + 1], p0, p1);
+              acc2(l[r], l[r + 1], p0, p1, inv_sv);
               part[0][x] = f16x2_to_e4m3x2(h);
               const uint32_t h1 = rest16(h, e4m3x2_to_f16x2((uint16_t)part[0][x]));
               part[1][x] = f16x2_to_e4m3x2(h1);
@@ -585,7 +610,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
         sts32(ref + kRows * 4 + lane * 4, __float_as_uint(whole ? inv : 1.f));
         if (!whole && lane < rows_here && !dead)
           *reinterpret_cast<float2*>(A.part_ml + (slot * kRows + lane) * 2) =
-              make_float2(__uint_as_float(lds32(ref + lane * 4)), lt);
+              make_float2(-__uint_as_float(lds32(ref + lane * 4)), lt);
       }
       named_bar_sync(1, 32 * kSoftWarps);
       if (!dead && !warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
@@ -613,28 +638,29 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
               const uint8_t code =
                   static_cast<const uint8_t*>(A.v)[(((size_t)w.b * A.Lmax + jb + k) * A.Hkv + w.h) * kD + kl];
               if ((code & 0x7fu) != 0x7fu) continue;
-              const int a = jb + k - P0;
-              const int da = A.tree && a >= 0 ? (int)lds32(tree + 128 * 16 + a * 4) : a;
+              const uint32_t m = seen_by(jb + k);
 #pragma unroll
-              for (int r = 0; r < kRows; ++r) {
-                const int dep = (int)lds32(t0 + 2 * kRows * 4 + r * 4), idx = (int)lds32(t0 + 3 * kRows * 4 + r * 4);
-                bool seen = A.window <= 0 || dep - da < A.window;
-                if (a >= 0)
-                  seen = seen && (A.tree ? ((lds32(tree + idx * 16 + (a >> 5) * 4) >> (a & 31)) & 1u) != 0 : a <= idx);
-                if (seen) o[r] = __uint_as_float(0x7fffffffu);
-              }
+              for (int r = 0; r < kRows; ++r)
+                if ((m >> r) & 1u) o[r] = __uint_as_float(0x7fffffffu);
             }
           }
         }
+        __nv_bfloat16* out = A.out + (size_t)w.b * A.n_new * A.Hq * kD + kl;
+        float* part = A.part_o + slot * kRows * kD + kl;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < kRows; r += 4) {
           if (r >= rows_here) break;
-          const float f = o[r] * __uint_as_float(lds32(ref + kRows * 4 + r * 4));
-          if (whole) {
-            const int i = pos0 + r / A.G;
-            A.out[(((size_t)w.b * A.n_new + i) * A.Hq + (size_t)w.h * A.G + r % A.G) * kD + kl] = __float2bfloat16(f);
-          } else {
-            A.part_o[(slot * kRows + r) * kD + kl] = f;
+          const float4 f = lds128f(ref + kRows * 4 + r * 4);
+          const uint4 at = lds128(t0 + 3 * kRows * 4 + r * 4);
+          const float ff[4] = {f.x, f.y, f.z, f.w};
+          const uint32_t to[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (r + k >= rows_here) break;
+            if (whole)
+              out[(size_t)to[k] * kD] = __float2bfloat16(o[r + k] * ff[k]);
+            else
+              part[(r + k) * kD] = o[r + k];
           }
         }
       }
