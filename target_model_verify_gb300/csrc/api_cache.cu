@@ -29,7 +29,7 @@ int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
 
 struct AttnPlan {
   int n_groups, group_pos;
-  size_t off_ml, off_o, total;
+  size_t off_notes, off_ml, off_o, total;
 };
 
 // The new positions in equal groups of at most 128 query rows per KV head;
@@ -44,6 +44,8 @@ AttnPlan make_plan(bool e4m3, int n_new, int G, int D) {
   size_t off = align_up(sizeof(WsHeader));
   const int ctas = cache_attn_by_keys(e4m3, D, p.group_pos * G) ? kCacheAttnMaxCtas : kCacheAttnCtas;
   const size_t rows = (size_t)2 * ctas * cache_attn_rows(p.group_pos * G);
+  p.off_notes = off;
+  off = align_up(off + ctas * sizeof(int4));
   p.off_ml = off;
   off = align_up(off + rows * 2 * sizeof(float));
   p.off_o = off;
@@ -149,6 +151,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.out = static_cast<__nv_bfloat16*>(out);
   A.part_ml = reinterpret_cast<float*>(ws + pl.off_ml);
   A.part_o = reinterpret_cast<float*>(ws + pl.off_o);
+  A.notes = reinterpret_cast<int4*>(ws + pl.off_notes);
   A.status = reinterpret_cast<int*>(ws);
   CUtensorMap tk, tv, tq;
   if (!encode_cache(&tk, k_cache, e4m3, B, Lmax, Hkv, D) || !encode_cache(&tv, v_cache, e4m3, B, Lmax, Hkv, D))

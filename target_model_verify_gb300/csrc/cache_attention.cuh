@@ -20,9 +20,12 @@
 // keep every SM busy to the end. Part p of head h goes to CTA p * Hkv + h:
 // the heads' CTAs go through the same cache rows at the same time, and since
 // a row of the cache holds all its heads side by side, DRAM pages are read
-// whole. A tile that lies inside one part is finished by its CTA; the others
-// leave (maximum, sum, unnormalised output) partials that combine_kernel
-// merges.
+// whole. A tile that lies inside one part is finished by its CTA; of the
+// others every CTA leaves a partial (maximum, sum, unnormalised output), and
+// the first one a note of who shares it, from which combine_kernel merges.
+// (The last CTA of a tile merging in place, counted in by an atomic, was
+// slower in every case measured, by 1 to 12 us a call: its four warps take
+// the rows one batch after another while the grid waits.)
 //
 // CTA: warps 0-3 softmax, 4-7 auxiliary, 8 and 9 TMA producers (K with Q,
 // and V, whose slots free up at different times), 10 and 11 tcgen05 issuers (one per product: a thread takes 50 to 100 cycles for each MMA, as
@@ -391,7 +394,7 @@ __device__ __forceinline__ int heads_of(const CacheAttnLaunch& A) { return A.hea
 // One warp: the units of a head lane, and where unit part_begin(c) lies:
 // sequence b (B when there is none) and offset inside it.
 struct Place {
-  int total, u0, u1, b, off;
+  int total, parts, u0, u1, b, off;      // parts: those with units, of n
   bool any_bad;
 };
 template <int kBlk>
@@ -410,11 +413,13 @@ __device__ __forceinline__ Place find_part(const CacheAttnLaunch& A, int lane, i
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   p.any_bad = __any_sync(0xffffffffu, bad_seen);
   p.total = sum;
-  p.u0 = part_begin(sum, c, n);
-  p.u1 = part_begin(sum, c + 1, n);
+  p.parts = min(n, sum);
+  p.u0 = p.u1 = 0;
   p.b = A.B;
   p.off = 0;
-  if (p.u0 >= p.u1) return p;
+  if (c >= p.parts) return p;
+  p.u0 = part_begin(sum, c, p.parts);
+  p.u1 = part_begin(sum, c + 1, p.parts);
   int before = 0;
   for (int b0 = 0; b0 < A.B; b0 += 32) {
     const int b = b0 + lane;
@@ -497,6 +502,159 @@ struct Walk {
     return blk + ib >= clean_lo && blk + ib < clean_hi;
   }
 };
+
+// What the CTA with a shared tile's first block notes for the merge: the
+// sequence (-1: no such tile), KV head and row group, the last part with
+// blocks of it, and which of its own two partials is the tile's.
+__device__ __forceinline__ void write_note(const CacheAttnLaunch& A, int b, int head_group, int last, int slot) {
+  A.notes[blockIdx.x] = make_int4(b, head_group, last, slot);
+}
+// The part that holds the walk's tile's last unit.
+template <int kBlk>
+__device__ __forceinline__ int last_part(const Walk<kBlk>& w, int total, int parts) {
+  // part c holds unit u iff part_begin(c) <= u < part_begin(c + 1)
+  return (int)(((unsigned long long)(w.tile0 + tile_units(w.nb)) * parts - 1) / total);
+}
+
+// Outputs of sequences without blocks are zero: the softmax warps of the grid
+// share them out.
+template <int kD, int kBlk>
+__device__ __forceinline__ void zero_empty(const CacheAttnLaunch& A) {
+  for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+    int first;
+    bool bad;
+    if (seq_blocks<kBlk>(A, A.seq_lens[b], first, bad) > 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(A.out + (size_t)b * A.n_new * A.Hq * kD);
+    for (int e = threadIdx.x; e < A.n_new * A.Hq * (kD / 8); e += 32 * kSoftWarps) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Merges the partials of the tiles that more than one CTA worked on.
+// blockIdx.x = the CTA with the tile's first block, blockIdx.y: rows. `wpr`
+// of the eight warps share the partials of kRows rows, which they take
+// together, so that eight loads are in flight either way.
+template <int kD, int kRP>
+struct MergeShape {
+  static constexpr int kRows = kRP / 32;                    // 1, 2 or 4
+  static constexpr int kParts = 8 / kRows;
+};
+template <int kD, int kRP>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CacheAttnLaunch A, int wpr) {
+  constexpr int kPer = kD / 32, kRows = MergeShape<kD, kRP>::kRows, kParts = MergeShape<kD, kRP>::kParts;
+  __shared__ float part[8][kRows][kD];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  const int4 note = __ldcg(A.notes + blockIdx.x);
+  if (note.x < 0) return;
+  const int b = note.x, grp = note.y % A.n_groups, h = note.y / A.n_groups;
+  const int pos0 = grp * A.group_pos, rows = min(A.group_pos, A.n_new - pos0) * A.G;
+  const int r0 = (blockIdx.y * (8 / wpr) + warp / wpr) * kRows, slice = warp % wpr;
+  const int first = blockIdx.x / A.head_lanes, head_lane = blockIdx.x % A.head_lanes;
+  float acc[kRows][kPer], l[kRows], M[kRows];
+#pragma unroll
+  for (int y = 0; y < kRows; ++y) {
+    l[y] = 0.f;
+    M[y] = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[y][k] = 0.f;
+  }
+  if (r0 < rows) {
+    // a lane looks after every 32nd part's statistics and kPer dims
+    for (int cb = first; cb <= note.z; cb += 32) {
+      const int c = min(cb + lane, note.z), here = min(32, note.z - cb + 1);
+      const bool none = cb + lane > note.z;
+      const int slot = 2 * (c * A.head_lanes + head_lane) + (c == first ? note.w : 0);
+      float2 ml[kRows];
+      float wgt[kRows];
+#pragma unroll
+      for (int y = 0; y < kRows; ++y)
+        ml[y] = __ldcg(reinterpret_cast<const float2*>(A.part_ml) + (size_t)slot * kRP + min(r0 + y, rows - 1));
+#pragma unroll
+      for (int y = 0; y < kRows; ++y) {
+        if (none) ml[y] = make_float2(-INFINITY, 0.f);
+        const float m_new = fmaxf(M[y], warp_max(ml[y].x));
+        const float mu = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = ex2(M[y] - mu);
+        wgt[y] = none ? 0.f : ex2(ml[y].x - mu);
+        l[y] = fmaf(l[y], alpha, warp_sum(none ? 0.f : ml[y].y * wgt[y]));
+        M[y] = m_new;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[y][k] *= alpha;
+      }
+      for (int x0 = slice; x0 < here; x0 += kParts * wpr) {
+        float2 v[kParts][kRows][kPer / 2];
+#pragma unroll
+        for (int x = 0; x < kParts; ++x) {
+          const int s = __shfl_sync(0xffffffffu, slot, min(x0 + x * wpr, here - 1));
+#pragma unroll
+          for (int y = 0; y < kRows; ++y) {
+            const float2* po = reinterpret_cast<const float2*>(
+                A.part_o + ((size_t)s * kRP + min(r0 + y, rows - 1)) * kD + lane * kPer);
+#pragma unroll
+            for (int k = 0; k < kPer / 2; ++k)
+              v[x][y][k] = x0 + x * wpr < here ? __ldcg(po + k) : make_float2(0.f, 0.f);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kParts; ++x)
+#pragma unroll
+          for (int y = 0; y < kRows; ++y) {
+            const float w = __shfl_sync(0xffffffffu, wgt[y], min(x0 + x * wpr, here - 1));
+            const float f = x0 + x * wpr < here ? w : 0.f;
+#pragma unroll
+            for (int k = 0; k < kPer / 2; ++k) {
+              acc[y][2 * k] = fmaf(v[x][y][k].x, f, acc[y][2 * k]);
+              acc[y][2 * k + 1] = fmaf(v[x][y][k].y, f, acc[y][2 * k + 1]);
+            }
+          }
+      }
+    }
+  }
+  if (wpr > 1) {
+#pragma unroll
+    for (int y = 0; y < kRows; ++y)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) part[warp][y][lane * kPer + k] = acc[y][k];
+    __syncthreads();
+    if (slice) return;
+    for (int x = 1; x < wpr; ++x)
+#pragma unroll
+      for (int y = 0; y < kRows; ++y)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[y][k] += part[warp + x][y][lane * kPer + k];
+  }
+#pragma unroll
+  for (int y = 0; y < kRows; ++y) {
+    const int r = r0 + y;
+    if (r >= rows) return;
+    const float inv = l[y] > 0.f ? 1.f / l[y] : (l[y] == 0.f ? 0.f : l[y]);       // NaN stays
+    uint32_t* dst = reinterpret_cast<uint32_t*>(
+        A.out + (((size_t)b * A.n_new + pos0 + r / A.G) * A.Hq + (size_t)h * A.G + r % A.G) * kD + lane * kPer);
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) dst[k] = pack2<false>(acc[y][2 * k] * inv, acc[y][2 * k + 1] * inv);
+  }
+}
+
+// Parts of the schedule: as many as the CTAs (or the work, `most` units in
+// all heads at the longest) allow.
+inline int cache_attn_parts(const CacheAttnLaunch& A, int ctas, long long most) {
+  const long long by_work = (most + A.head_lanes - 1) / A.head_lanes, by_ctas = ctas / A.head_lanes;
+  return (int)(by_work < by_ctas ? by_work : by_ctas);
+}
+
+// The merge, after the attention kernel on the same stream. Warps per row:
+// as many as a tile has parts when the parts are dealt out evenly, at most 8.
+template <int kD, int kRP>
+cudaError_t launch_combine(const CacheAttnLaunch& A, int parts, cudaLaunchConfig_t& cfg) {
+  const long long tiles = (long long)A.B * A.n_groups * (A.head_lanes > 1 ? 1 : A.Hkv);
+  const long long each = parts / tiles;
+  const int wpr = each >= 8 ? 8 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
+  const int per_cta = 8 / wpr * MergeShape<kD, kRP>::kRows;
+  cfg.gridDim = dim3(parts * A.head_lanes, (A.group_pos * A.G + per_cta - 1) / per_cta);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<kD, kRP>, A, wpr);
+}
 
 // The visible rows among 32 of the cache, for one query row: the cached
 // prefix (rows below P0, bounded below by the window) and the new rows' own
@@ -599,6 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       place[1] = pl.off;
       place[2] = pl.u0;
       place[3] = pl.u1;
+      place[4] = pl.total;
+      place[5] = pl.parts;
       if (blockIdx.x == 0) *A.status = pl.any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
     }
   }
@@ -1001,6 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kPiece = kKpl <= 64 ? kKpl : 32, kPieces = kKpl / kPiece;
     constexpr int kSubKeys = kKpl < 32 ? kKpl : 32, kSubs = kKpl / kSubKeys;   // runs with one scale
     bool dead = false;                   // a wait ran out: keep to the barriers, compute nothing
+    bool noted = false;
     uint32_t n = 0, nt = 0;
     if constexpr (S::kCopies > 1) {
       const uint32_t zero[32] = {};
@@ -1315,7 +1476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           __syncwarp();
       }
+      if (!whole && w.blk == 0 && threadIdx.x == 0) {
+        write_note(A, w.b, w.h * A.n_groups + w.g, last_part(w, place[4], place[5]), (int)(slot & 1));
+        noted = true;
+      }
     }
+    if (!noted && threadIdx.x == 0) write_note(A, -1, 0, 0, 0);
+    zero_empty<kD, kBlk>(A);
   }
   tc_fence_before();
   __syncthreads();   // every role has left its loop
@@ -1328,128 +1495,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_drain(warp == kProducerV ? v_full(s) : k_full(s), (issued_phase >> s) & 1u);
       if (issued_q & (1u << s)) wait_drain(q_full(s), (issued_q_phase >> s) & 1u);
     }
-}
-
-// Merges the partials of the tiles that more than one CTA worked on, and
-// zeroes the outputs of sequences without blocks. One warp per query row:
-// blockIdx.x = tile, blockIdx.y * 8 + warp = row of its group.
-template <bool kE4m3, int kD, int kRP>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CacheAttnLaunch A, int n_parts) {
-  constexpr int kBlk = cache_attn_block(kE4m3, kD);
-  __shared__ int sh_before[8], sh_total[8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = blockIdx.x;
-  const int grp = tile % A.n_groups;
-  const int h = tile / A.n_groups % A.Hkv;
-  const int b = tile / A.n_groups / A.Hkv;
-  // The schedule again (the lengths were there before the attention kernel
-  // let this one start), then its partials.
-  int before = 0, total = 0, first;
-  bool bad;
-  for (int x = threadIdx.x; x < A.B; x += 256) {
-    const int u = tile_units(seq_blocks<kBlk>(A, A.seq_lens[x], first, bad));
-    total += u;
-    if (x < b) before += u;
-  }
-  const int nb = seq_blocks<kBlk>(A, A.seq_lens[b], first, bad);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) {
-    sh_before[warp] = before;
-    sh_total[warp] = total;
-  }
-  __syncthreads();
-  before = total = 0;
-#pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    before += sh_before[x];
-    total += sh_total[x];
-  }
-  const int per = heads_of(A) * A.n_groups;
-  total *= per;
-  const int u0 = before * per + ((A.head_lanes > 1 ? 0 : h) * A.n_groups + grp) * tile_units(nb);
-  const int pos0 = grp * A.group_pos;
-  const int r = blockIdx.y * 8 + warp;
-  const bool mine = r < min(A.group_pos, A.n_new - pos0) * A.G;
-  // Part c holds unit u iff part_begin(c) <= u < part_begin(c + 1); the tile's
-  // blocks are its units from u0 + kTileCost on.
-  int c0 = 0, c1 = -1;
-  if (nb > 0) {
-    auto owner = [&](int u) { return (int)(((unsigned long long)(u + 1) * n_parts - 1) / total); };
-    c0 = owner(u0 + kTileCost);
-    c1 = owner(u0 + kTileCost + nb - 1);
-  }
-  // A lane looks after every 32nd of those parts: which of its CTA's two
-  // partials (c0 may have begun before the tile: then the second). An empty
-  // part has none; it counts as c0's with weight 0.
-  auto slot_of = [&](int c, bool& none) {
-    const int pb = part_begin(total, c, n_parts);
-    none = c > c1 || pb == part_begin(total, c + 1, n_parts);
-    const int cta = (none ? c0 : c) * A.head_lanes + (A.head_lanes > 1 ? h : 0);
-    return 2 * cta + ((none || c == c0) && part_begin(total, c0, n_parts) < u0 ? 1 : 0);
-  };
-  bool none0 = true;
-  const int slot0 = nb > 0 ? slot_of(c0 + lane, none0) : 0;
-  grid_dependency_wait();
-  if (!mine || (nb > 0 && c0 == c1)) return;     // no such row, or its CTA wrote the output
-  constexpr int kPer = kD / 32;
-  __nv_bfloat16* dst = A.out +
-                       (((size_t)b * A.n_new + pos0 + r / A.G) * A.Hq + (size_t)h * A.G + r % A.G) * kD +
-                       lane * kPer;
-  float acc[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  float l = 0.f, M = -INFINITY;
-  for (int cb = c0; cb <= c1; cb += 32) {
-    bool none = none0;
-    const int slot = cb == c0 ? slot0 : slot_of(cb + lane, none);
-    const float2 ml = none ? make_float2(-INFINITY, 0.f)
-                           : *reinterpret_cast<const float2*>(A.part_ml + ((size_t)slot * kRP + r) * 2);
-    const float m_new = fmaxf(M, warp_max(ml.x));
-    const float mu = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = ex2(M - mu), wgt = none ? 0.f : ex2(ml.x - mu);
-    l = fmaf(l, alpha, warp_sum(none ? 0.f : ml.y * wgt));
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] *= alpha;
-    M = m_new;
-    // eight partials' loads in flight at a time
-    const int here = min(32, c1 - cb + 1);
-    for (int x0 = 0; x0 < here; x0 += 8) {
-      float f[8];
-      float2 v[8][kPer / 2];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int from = min(x0 + x, here - 1);
-        const int s = __shfl_sync(0xffffffffu, slot, from);
-        f[x] = __shfl_sync(0xffffffffu, wgt, from);
-        if (x0 + x >= here) f[x] = 0.f;
-        const float2* po = reinterpret_cast<const float2*>(A.part_o + ((size_t)s * kRP + r) * kD + lane * kPer);
-#pragma unroll
-        for (int k = 0; k < kPer / 2; ++k) v[x][k] = __ldcg(po + k);
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-#pragma unroll
-        for (int k = 0; k < kPer / 2; ++k) {
-          acc[2 * k] = fmaf(v[x][k].x, f[x], acc[2 * k]);
-          acc[2 * k + 1] = fmaf(v[x][k].y, f[x], acc[2 * k + 1]);
-        }
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-  for (int k = 0; k < kPer; k += 2)
-    *reinterpret_cast<uint32_t*>(dst + k) = pack2<false>(acc[k] * inv, acc[k + 1] * inv);
-}
-
-// Parts of the schedule: as many as the CTAs (or the work, `most` units in
-// all heads at the longest) allow.
-inline int cache_attn_parts(const CacheAttnLaunch& A, int ctas, long long most) {
-  const long long by_work = (most + A.head_lanes - 1) / A.head_lanes, by_ctas = ctas / A.head_lanes;
-  return (int)(by_work < by_ctas ? by_work : by_ctas);
 }
 
 template <bool kE4m3, int kD, int kRP, bool kExtra>
@@ -1481,10 +1526,7 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<kE4m3, kD, kRP, kExtra>, A, tk, tv, tq);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)tiles, (A.group_pos * A.G + 7) / 8);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<kE4m3, kD, kRP>, A, parts);
+  return launch_combine<kD, kRP>(A, parts, cfg);
 }
 
 template <bool kE4m3, int kD, int kRP>

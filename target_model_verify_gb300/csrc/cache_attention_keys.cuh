@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       place[1] = pl.off;
       place[2] = pl.u0;
       place[3] = pl.u1;
+      place[4] = pl.total;
+      place[5] = pl.parts;
       if (blockIdx.x == 0) *A.status = pl.any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
     }
   }
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
     // ----------------------------------------------------------- softmax --
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
     const int kl = warp * 32 + lane;         // this thread's key of a block, and its dim of the output
-    bool dead = false;
+    bool dead = false, noted = false;
     uint32_t n = 0, nt = 0;
     for (; !w.done(); w.next(A), ++nt) {
       const int P0 = w.L - A.n_new, pos0 = w.g * A.group_pos;
@@ -668,7 +670,13 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       if (lane == 0) mbar_arrive(q_empty(qs));
       tc_fence_before();
       named_bar_sync(1, 32 * kSoftWarps);    // the tables are free for the next tile
+      if (!whole && w.blk == 0 && threadIdx.x == 0) {
+        write_note(A, w.b, w.h * A.n_groups + w.g, last_part(w, place[4], place[5]), (int)(slot & 1));
+        noted = true;
+      }
     }
+    if (!noted && threadIdx.x == 0) write_note(A, -1, 0, 0, 0);
+    zero_empty<kD, kBlk>(A);
   }
   tc_fence_before();
   __syncthreads();   // every role has left its loop
@@ -709,10 +717,7 @@ cudaError_t launch_keys(const CacheAttnLaunch& A, const CUtensorMap& tk, const C
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, cache_attn_keys_kernel<kExtra>, A, tk, tv);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)tiles, (A.group_pos * A.G + 7) / 8);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<true, kKeyD, kKeyRows>, A, parts);
+  return launch_combine<kKeyD, kKeyRows>(A, parts, cfg);
 }
 
 }  // namespace cache_attn

@@ -210,6 +210,7 @@ struct CacheAttnLaunch {
   __nv_bfloat16* out;                // [B, n_new, Hq, D]
   float* part_o;                     // [2 CTAs, rows, D]
   float* part_ml;                    // [2 CTAs, rows, 2]
+  int4* notes;                       // [CTAs] the shared tile whose first block a CTA has (write_note)
   int* status;
   uint32_t anc[SPECDEC_MAX_TREE_NODES][4];   // bit a of row i: node i sees node a
   uint8_t depth[SPECDEC_MAX_TREE_NODES];

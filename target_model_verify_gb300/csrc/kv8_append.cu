@@ -13,7 +13,8 @@
 // read, 2 x 1 written), latency for a step's few rows. One warp owns a
 // (block, KV head, K or V): the block's new rows stay in registers between
 // the maximum and the encoding, so they are read once, and no other warp
-// writes that block.
+// writes that block. Calls of up to kFew new rows keep registers for that
+// many only, so that all their warps are resident at once.
 #include <cuda_fp16.h>
 
 #include "kernels.h"
@@ -23,6 +24,7 @@ namespace {
 
 constexpr int kT = SPECDEC_KV8_BLOCK;
 constexpr int kWarps = 4;
+constexpr int kFew = 8;
 constexpr int kMinExp = -40, kMaxExp = 40;
 
 // e4m3 pair from two floats: nearest, ties to even, saturating; NaN stays.
@@ -49,7 +51,7 @@ __device__ __forceinline__ bool sequence_ok(const Kv8AppendLaunch& A, int start,
   return count <= A.n && start >= 0 && start <= A.Lmax - count;
 }
 
-template <int kD>
+template <int kD, int kMost>
 __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ Kv8AppendLaunch A,
                                                              long long items) {
   grid_dependency_wait();
@@ -86,8 +88,10 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
 
   constexpr int kLanes = kD / 8;                    // lanes per row, 8 values each
   constexpr int kRowsAtOnce = 32 / kLanes;
-  constexpr int kSteps = kT / kRowsAtOnce;
+  constexpr int kSteps = kMost / kRowsAtOnce;
   const int c = lane % kLanes, r0 = lane / kLanes;
+  const int base = max(first, start);               // the block's first new row
+  const int end = min(first + kT, start + count);   // at most kMost rows on
   float* scale_at = A.scale[kv] + ((size_t)b * A.Hkv + h) * A.n_scale + blk;
   const float was = first < start ? *scale_at : 0.f;
   uint4 x[kSteps];
@@ -95,9 +99,9 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   bool ok = true;
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    const int i = first + k * kRowsAtOnce + r0 - start;       // new row
+    const int i = base + k * kRowsAtOnce + r0 - start;        // new row
     x[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (i >= 0 && i < count) {
+    if (i < end - start) {
       int src = i;
       if (A.rows) {
         src = A.rows[(size_t)b * A.n + i];
@@ -144,8 +148,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   }
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    const int r = first + k * kRowsAtOnce + r0;
-    if (r < start || r >= start + count) continue;
+    const int r = base + k * kRowsAtOnce + r0;
+    if (r >= end) continue;
     const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
     uint32_t n[4];
 #pragma unroll
@@ -168,7 +172,8 @@ cudaError_t launch_dim(const Kv8AppendLaunch& A, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<kD>, A, items);
+  return A.n <= kFew ? cudaLaunchKernelEx(&cfg, append_kernel<kD, kFew>, A, items)
+                     : cudaLaunchKernelEx(&cfg, append_kernel<kD, kT>, A, items);
 }
 
 }  // namespace
