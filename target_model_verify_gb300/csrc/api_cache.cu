@@ -42,7 +42,7 @@ AttnPlan make_plan(bool e4m3, int n_new, int G, int D) {
   p.group_pos = (n_new + p.n_groups - 1) / p.n_groups;
   p.n_groups = (n_new + p.group_pos - 1) / p.group_pos;
   size_t off = align_up(sizeof(WsHeader));
-  const int ctas = cache_attn_by_keys(e4m3, D, p.group_pos * G) ? kCacheAttnMaxCtas : kCacheAttnCtas;
+  const int ctas = cache_attn_can_key(e4m3, D, p.group_pos * G) ? kCacheAttnMaxCtas : kCacheAttnCtas;
   const size_t rows = (size_t)2 * ctas * cache_attn_rows(p.group_pos * G);
   p.off_notes = off;
   off = align_up(off + ctas * sizeof(int4));

@@ -90,7 +90,7 @@ struct Shape {
   static constexpr int kPBufs = kQTmem ? 1 : 2;
   static constexpr int kV16Bytes = kE4m3 ? kBlk * kD * 2 : 0;   // widened V, two of them
   static constexpr int kStageBytes = 128 * kStagePitch;      // 32 output columns of every lane
-  static constexpr int kTabBytes = 128 * 4 + 128 * 8 + 128 * 16 + 128 * 4;  // q scales, (m, l), tree
+  static constexpr int kTabBytes = 128 * 4 + 128 * 8 + 128 * 4 + 128 * 16 + 128 * 4;  // q scales, (m, l), places, tree
   static constexpr int kFixed = 1024 + 2 * kV16Bytes + kQBufs * kQBytes + kStageBytes + kTabBytes + 512;
   static constexpr int kRingMax = (kSmemLimit - kFixed) / (2 * kSlotBytes);
   static constexpr int kRing = kRingMax < 6 ? kRingMax : 6;  // K blocks (and V blocks) in flight
@@ -696,7 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t stage = qb + kNq * S::kQBytes;
   const uint32_t q_tab = stage + S::kStageBytes;           // query row scales, by lane
   const uint32_t ml_tab = q_tab + 128 * 4;                 // (reference, sum) of every lane
-  const uint32_t tree = ml_tab + 128 * 8;                  // [128][4] ancestor words, then depth [128]
+  const uint32_t place_tab = ml_tab + 128 * 8;             // a row's place in the output, by lane
+  const uint32_t tree = place_tab + 128 * 4;               // [128][4] ancestor words, then depth [128]
   const uint32_t bars = tree + 128 * 16 + 128 * 4;
   auto k_full = [&](int s) { return bars + 8u * (uint32_t)s; };
   auto k_empty = [&](int s) { return bars + 8u * (uint32_t)(kR + s); };
@@ -1195,6 +1196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int a = 0; a < 32 && 32 * k + a < A.n_new; ++a)
             if (dep - (int)lds32(tree + 128 * 16 + (32 * k + a) * 4) >= A.window) sight.v[k] &= ~(1u << a);
       }
+      sts32(place_tab + lg * 4, (uint32_t)(idx * A.Hq + w.h * A.G + gq));
       const float slope = kExtra && A.slopes ? A.slopes[w.h * A.G + gq] * kLog2e : 0.f;
       const int key0 = copy * kKpl;                                // this copy's first key of a block
       const float* ks = nullptr;
@@ -1450,26 +1452,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         const int c4 = (lane & 7) * 4;
         constexpr int kRowStep = S::kCopies > 1 ? 16 : 4;        // rows written at a time by who shares them
-        const int r0 = S::kCopies > 1 ? warp * 4 : warp * 32;
-        const int r_end = min(rows_here, S::kCopies > 1 ? kRP : warp * 32 + 32);
-        for (int r = r0 + (lane >> 3); r < r_end; r += kRowStep) {
+        const int r0 = (S::kCopies > 1 ? warp * 4 : warp * 32) + (lane >> 3);
+        __nv_bfloat16* const out = A.out + (size_t)w.b * A.n_new * A.Hq * kD + c0 + c4;
+        float* const part = A.part_o + slot * kRP * kD + c0 + c4;
+#pragma unroll
+        for (int x = 0; x < (S::kCopies > 1 ? kRP : 32) / kRowStep; ++x) {
+          const int r = r0 + x * kRowStep;
           float4 v = lds128f(stage + r * kStagePitch + c4 * 4);
 #pragma unroll
           for (int c = 1; c < S::kCopies; ++c) {
             const float4 y = lds128f(stage + (c * kRP + r) * kStagePitch + c4 * 4);
-            v.x += y.x;
-            v.y += y.y;
-            v.z += y.z;
-            v.w += y.w;
+            add2(v.x, v.y, y.x, y.y);
+            add2(v.z, v.w, y.z, y.w);
           }
-          if (dead) continue;
-          if (whole) {
-            const int i = pos0 + r / A.G;
-            *reinterpret_cast<uint2*>(A.out + (((size_t)w.b * A.n_new + i) * A.Hq + (size_t)w.h * A.G + r % A.G) * kD +
-                                      c0 + c4) = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
-          } else {
-            *reinterpret_cast<float4*>(A.part_o + (slot * kRP + r) * kD + c0 + c4) = v;
-          }
+          if (dead || r >= rows_here) continue;
+          if (whole)
+            *reinterpret_cast<uint2*>(out + (size_t)lds32(place_tab + r * 4) * kD) =
+                make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+          else
+            *reinterpret_cast<float4*>(part + r * kD) = v;
         }
         if constexpr (S::kCopies > 1)
           named_bar_sync(1, 32 * kSoftWarps);

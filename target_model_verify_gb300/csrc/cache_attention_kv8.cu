@@ -6,7 +6,7 @@ namespace specdec {
 cudaError_t launch_cache_attention_kv8(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
                                        const CUtensorMap& tmap_v, const CUtensorMap& tmap_q,
                                        cudaStream_t stream) {
-  if (cache_attn_by_keys(true, D, A.group_pos * A.G))
+  if (cache_attn_by_keys(A, D))
     return A.cap > 0.f || A.slopes ? cache_attn::launch_keys<true>(A, tmap_k, tmap_v, stream)
                                    : cache_attn::launch_keys<false>(A, tmap_k, tmap_v, stream);
   switch (D) {

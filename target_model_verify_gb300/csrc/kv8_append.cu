@@ -14,7 +14,8 @@
 // (block, KV head, K or V): the block's new rows stay in registers between
 // the maximum and the encoding, so they are read once, and no other warp
 // writes that block. Calls of up to kFew new rows keep registers for that
-// many only, so that all their warps are resident at once.
+// many only, and in longer ones two warps share a block (16 rows each), so
+// that more warps are resident (4 x 4096 rows: 8.4 us with one warp).
 #include <cuda_fp16.h>
 
 #include "kernels.h"
@@ -51,9 +52,11 @@ __device__ __forceinline__ bool sequence_ok(const Kv8AppendLaunch& A, int start,
   return count <= A.n && start >= 0 && start <= A.Lmax - count;
 }
 
-template <int kD, int kMost>
+// kMost: rows a warp holds; kSharers: warps that share a block.
+template <int kD, int kMost, int kSharers>
 __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ Kv8AppendLaunch A,
                                                              long long items) {
+  grid_launch_dependents();          // the next kernel may get ready, and wait for this one's end
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == gridDim.x - 1) {
@@ -73,7 +76,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
     if (threadIdx.x == 0) *A.status = bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
     return;
   }
-  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, sharer = warp % kSharers;
+  const long long item = (long long)blockIdx.x * (kWarps / kSharers) + warp / kSharers;
   if (item >= items) return;
   const int kv = (int)(item & 1);
   const int h = (int)((item >> 1) % A.Hkv);
@@ -90,8 +94,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   constexpr int kRowsAtOnce = 32 / kLanes;
   constexpr int kSteps = kMost / kRowsAtOnce;
   const int c = lane % kLanes, r0 = lane / kLanes;
-  const int base = max(first, start);               // the block's first new row
-  const int end = min(first + kT, start + count);   // at most kMost rows on
+  const int base = max(first, start) + sharer * kMost;                     // this warp's first new row
+  const int end = min(min(first + kT, start + count), base + kMost);
   float* scale_at = A.scale[kv] + ((size_t)b * A.Hkv + h) * A.n_scale + blk;
   const float was = first < start ? *scale_at : 0.f;
   uint4 x[kSteps];
@@ -124,13 +128,27 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
       if (hi < INFINITY) amax = fmaxf(amax, hi);
     }
   }
-  if (!__all_sync(0xffffffffu, ok)) return;
+  ok = __all_sync(0xffffffffu, ok);
   amax = warp_max(amax);
+  if constexpr (kSharers > 1) {
+    // the sharers' maxima (and whether every row index was good)
+    __shared__ float shared_max[kWarps];
+    const int pair = warp / kSharers;
+    if (lane == 0) shared_max[warp] = ok ? amax : -1.f;
+    named_bar_sync(1 + pair, 32 * kSharers);
+#pragma unroll
+    for (int x = 0; x < kSharers; ++x) {
+      const float a = shared_max[pair * kSharers + x];
+      ok = ok && a >= 0.f;
+      amax = fmaxf(amax, a);
+    }
+  }
+  if (!ok) return;
   const float s = fmaxf(pow2(scale_exponent(amax)), was);
   const float inv = 1.f / s;
   uint8_t* out = A.cache[kv] + ((size_t)b * A.Lmax * A.Hkv + h) * kD + c * 8;
   const size_t pitch = (size_t)A.Hkv * kD;
-  if (first < start && s != was) {
+  if (sharer == 0 && first < start && s != was) {
     // the block's scale grows: its earlier rows are encoded again
     const float ratio = was * inv;
     for (int r = first + r0; r < start; r += kRowsAtOnce) {
@@ -157,14 +175,15 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
       n[q] = e4m3x2(__uint_as_float(w[q] << 16) * inv, __uint_as_float(w[q] & 0xffff0000u) * inv);
     *reinterpret_cast<uint2*>(out + (size_t)r * pitch) = make_uint2(n[0] | (n[1] << 16), n[2] | (n[3] << 16));
   }
-  if (lane == 0 && s != was) *scale_at = s;
+  if (sharer == 0 && lane == 0 && s != was) *scale_at = s;
 }
 
 template <int kD>
 cudaError_t launch_dim(const Kv8AppendLaunch& A, cudaStream_t stream) {
   const long long items = 2ll * A.B * A.max_blocks * A.Hkv;
+  const int per_cta = A.n <= kFew ? kWarps : kWarps / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((items + kWarps - 1) / kWarps + 1));
+  cfg.gridDim = dim3((unsigned)((items + per_cta - 1) / per_cta + 1));
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -172,8 +191,8 @@ cudaError_t launch_dim(const Kv8AppendLaunch& A, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return A.n <= kFew ? cudaLaunchKernelEx(&cfg, append_kernel<kD, kFew>, A, items)
-                     : cudaLaunchKernelEx(&cfg, append_kernel<kD, kT>, A, items);
+  return A.n <= kFew ? cudaLaunchKernelEx(&cfg, append_kernel<kD, kFew, 1>, A, items)
+                     : cudaLaunchKernelEx(&cfg, append_kernel<kD, kT / 2, 2>, A, items);
 }
 
 }  // namespace

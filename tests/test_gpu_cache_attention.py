@@ -5,8 +5,13 @@ bf16 cache (verify_attention_masked) on the GPU against the fp64 oracle
 Tolerance, from the arithmetic. With u = finfo.eps / 2 (bf16 2^-8, f16
 2^-11), V the largest visible |v| and o the output:
   - the output is rounded to bf16: 2^-8 |o|;
-  - the probabilities are rounded: to f16 over the 8-bit cache, which moves a
-    weighted mean of values by at most 2^-11 V; to bf16 over the bf16 cache,
+  - the probabilities are rounded. Over the 8-bit cache to f16, which moves a
+    weighted mean of values by at most 2^-11 V; the form for many tiles then
+    writes them as three e4m3 terms, exact but for the last term's half step,
+    2^-10 / 256, where a row's largest probability is at least 2^2: each of L
+    weights is off by at most 2^-20 of that one, the mean by 2^-20 L V (the
+    row form's f16 ends at 2^-25 / 2^7 of it, 2^-32 L V). Over the bf16 cache
+    to bf16,
     whose rounded weights are also what the sum counts, so the mean moves by
     at most 2^-8 * sum w |v - o| <= 2^-8 * 2 V;
   - scores: products are exact, their sum over D terms runs through D / 16
@@ -34,7 +39,7 @@ def _f(t):
 def _inputs(kind, seed, B, n, Hq, Hkv, D, Lmax, lens=None, spread=True):
     g = torch.Generator(device=DEV).manual_seed(seed)
     q = (torch.randn(B, n, Hq, D, generator=g, device=DEV) * 1.5).to(torch.bfloat16)
-    if kind == "kv8":
+    if kind != "masked":
         def one():
             c = (torch.randn(B, Lmax, Hkv, D, generator=g, device=DEV) * 60).to(torch.float8_e4m3fn)
             e = torch.randint(-7, -4, (B, Hkv, -(-Lmax // 32)), generator=g, device=DEV) if spread else \
@@ -59,6 +64,15 @@ def _values(cache):
 def _call(kind, q, cache, lens, workspace=None, **how):
     """The call; unless the caller brings a workspace, no device-side error is expected of it."""
     import target_model_verify_gb300 as tv
+    if kind == "kv8_keys":
+        B, more = q.shape[0], max(0, 256 // cache[0].shape[2] + 1 - q.shape[0])
+        pad = lambda t: torch.cat([t, t[:1].expand(more, *t.shape[1:])]) if t.element_size() > 1 else \
+            torch.cat([t.view(torch.uint8), t[:1].view(torch.uint8).expand(more, *t.shape[1:])]).view(t.dtype)  # noqa: E731
+        lens = torch.cat([lens, torch.zeros(more, dtype=torch.int32, device=DEV)])
+        out, how["out"] = how.get("out"), None
+        got = _call("kv8", pad(q), tuple(pad(t) for t in cache), lens, workspace=workspace, **how)
+        assert not got[B:].any()
+        return got[:B] if out is None else out.copy_(got[:B])
     fn = tv.verify_attention_kv8 if kind == "kv8" else tv.verify_attention_masked
     if workspace is not None or torch.cuda.is_current_stream_capturing() or "stream" in how:
         return fn(q, *cache, lens, workspace=workspace, **how)
@@ -93,13 +107,20 @@ def _check(kind, q, cache, lens, out, seqs=None, **how):
         if how.get("slopes") is not None:
             A += float(np.abs(how["slopes"]).max()) * L
         score = 2.0 ** -18 * A + 2 * 2.0 ** -22 * how.get("softcap", 0.0)
-        weight = 2.0 ** -11 if kind == "kv8" else 2 * 2.0 ** -8
+        weight = 2 * 2.0 ** -8 if kind == "masked" else 2.0 ** -11 + 2.0 ** -20 * int(L)
         tol = 2.0 ** -8 * np.abs(want[b]) + (weight + 2 * score) * V * (1 + 2.0 ** -8)
         err = np.abs(got[b] - want[b])
         assert (err <= tol).all(), (kind, b, L, float(err.max()), float((err - tol).max()))
 
 
-KINDS = ["kv8", "masked"]
+# kv8_keys: the 8-bit cache with unused batch slots added, so that the call goes
+# to the form of the kernel for many tiles (head dim 128, up to 32 query rows).
+KINDS = ["kv8", "kv8_keys", "masked"]
+
+
+def _skip_unless_it_applies(kind, D, rows):
+    if kind == "kv8_keys" and (D != 128 or rows > 32):
+        pytest.skip("the form for many tiles is for head dim 128 and up to 32 query rows")
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -114,6 +135,7 @@ KINDS = ["kv8", "masked"]
     (40, 2, 4, 2, 64, 129),       # more tiles than one CTA's share of each
 ])
 def test_chain_matches_oracle(kind, B, n, Hq, Hkv, D, Lmax):
+    _skip_unless_it_applies(kind, D, n * Hq // Hkv)
     q, cache, lens = _inputs(kind, B + Lmax, B, n, Hq, Hkv, D, Lmax)
     _check(kind, q, cache, lens, _call(kind, q, cache, lens))
 
@@ -128,6 +150,9 @@ def test_chain_matches_oracle(kind, B, n, Hq, Hkv, D, Lmax):
 def test_options_match_oracle(kind, D, how):
     n = 26 if "parent" in how else 4
     how = dict(how)
+    if kind == "kv8_keys" and n == 26:
+        how["parent"], n = TREE26[:16], 16
+    _skip_unless_it_applies(kind, D, 2 * n)
     if how.get("slopes"):
         how["slopes"] = torch.tensor([0.5, 0.25, 0.1, 0.01], device=DEV)
     q, cache, lens = _inputs(kind, D + n, 3, n, 4, 2, D, 310, lens=[310, n, 129])
@@ -142,21 +167,63 @@ def test_lengths_around_the_blocks(kind):
     _check(kind, q, cache, lens, _call(kind, q, cache, lens))
 
 
-@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("how", [{}, {"window": 2500}], ids=str)
-def test_long_ragged_batch(kind, how):
+def test_long_ragged_batch(kind, D, how):
     """Many blocks that every position sees between those with masks, several tiles per CTA."""
     import target_model_verify_gb300 as tv
     lens = [6000, 40, 5111, 3, 2600, 1, 0, 4097] * 4
-    q, cache, lens = _inputs(kind, 22, len(lens), 1, 16, 8, 64, 6000, lens=lens)
-    ws = torch.empty(tv.cache_attention_workspace_bytes(len(lens), 1, 16, 8, 64, 6000), dtype=torch.uint8,
+    q, cache, lens = _inputs(kind, 22, len(lens), 1, 16, 8, D, 6000, lens=lens)      # 256 tiles
+    ws = torch.empty(tv.cache_attention_workspace_bytes(len(lens), 1, 16, 8, D, 6000), dtype=torch.uint8,
                      device=DEV)
     out = _call(kind, q, cache, lens, workspace=ws, **how)
     assert tv.read_status(ws) == 0
     _check(kind, q, cache, lens, out, seqs=[0, 2, 3, 15, 28, 30, 31], **how)
 
 
-@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+@pytest.mark.parametrize("n,Hq,Hkv,D,L", [
+    (2, 4, 1, 128, 20000),        # one KV head: a tile shared by more CTAs than a warp has lanes
+    (2, 4, 2, 256, 9001),
+    (40, 1, 1, 64, 5000),         # 64 lanes of query rows
+    (9, 16, 2, 128, 4001),        # 72 query rows
+    (3, 8, 8, 128, 33001),        # the form for many blocks
+])
+def test_one_sequence_over_every_cta(kind, n, Hq, Hkv, D, L):
+    q, cache, lens = _inputs(kind, L, 1, n, Hq, Hkv, D, L, lens=[L])
+    _check(kind, q, cache, lens, _call(kind, q, cache, lens))
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+def test_many_kv_heads(kind):
+    """More KV heads than can have CTAs side by side."""
+    q, cache, lens = _inputs(kind, 23, 2, 2, 200, 100, 64, 300, lens=[300, 131])
+    _check(kind, q, cache, lens, _call(kind, q, cache, lens))
+
+
+def test_many_tiles_in_a_graph():
+    """The form for many tiles, captured and replayed on new lengths and queries; twice alike."""
+    import target_model_verify_gb300 as tv
+    B = 33
+    q, cache, lens = _inputs("kv8", 24, B, 4, 32, 8, 128, 333)
+    ws = torch.empty(tv.cache_attention_workspace_bytes(B, 4, 32, 8, 128, 333), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tv.verify_attention_kv8(q, *cache, lens, workspace=ws)
+    for step in range(2):
+        lens.copy_((lens + 97 * step) % 330 + 4)
+        q.copy_(q.flip(0))
+        graph.replay()
+        first = out.clone()
+        graph.replay()
+        assert tv.read_status(ws) == 0
+        assert torch.equal(out, first)
+        assert torch.equal(out, tv.verify_attention_kv8(q, *cache, lens))
+        _check("kv8", q, cache, lens, out, seqs=[0, 7, 32])
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
 def test_deepest_tree(kind):
     """128 nodes: a chain of 64 and leaves hung on it, 4 query heads per KV head (512 rows)."""
     parent = [-1] + list(range(63)) + [5 * i % 64 for i in range(64)]
@@ -170,10 +237,11 @@ def test_deepest_tree(kind):
 def test_unseen_rows_never_reach_the_output(kind, D):
     """NaN (and infinities) in rows past the length, in later positions' rows, in other branches
     and before the window change nothing; in a visible row they do, for the rows that see it."""
+    _skip_unless_it_applies(kind, D, 8)
     parent = (-1, 0, 0, 1)
     q, cache, lens = _inputs(kind, 13, 2, 4, 4, 2, D, 200, lens=[150, 190])
     base = _call(kind, q, cache, lens, parent=parent, window=90)
-    bad = float("nan") if kind == "kv8" else float("inf")
+    bad = float("inf") if kind == "masked" else float("nan")
     k, v = cache[0].float(), cache[1].float()
     for t in (k, v):
         t[0, 150:] = float("nan")
@@ -244,7 +312,7 @@ def test_queries_of_every_size():
         np.testing.assert_allclose(_f(out)[0, 4, h], v[0, best, h // 2], rtol=2.0 ** -8, atol=0)
 
 
-@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
 def test_streams_graphs_and_repeats(kind):
     """A fused projection's slice of queries; another stream; a captured call replayed on new
     lengths; equal results every time."""
