@@ -347,14 +347,21 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
  * 1/sqrt(D)), capped, then biased. Distance is the difference of positions:
  * row j before the new ones stands at j, new position i at seq_lens[b] - n_new
  * + i, or, in a tree, + the depth of node i. Rows that a position does not see
- * never reach its output, whatever they hold. Softmax and sums in fp32; the
- * probabilities enter the value product as f16 (kv8) or bf16 (masked).
+ * never reach its output, whatever they hold.
+ * A query row that holds an infinity or a NaN gives NaN (kv8). Softmax and
+ * sums in fp32; the probabilities enter the value product as f16, or as three
+ * e4m3 terms of it that keep 2^-20 of the row's largest (kv8), or as bf16
+ * (masked); the queries enter the score product as bf16 (masked) or as two
+ * e4m3 terms, exact to 2^-18 of the row's largest element (kv8).
  * Limits: D = 64, 128 or 256, 1 <= n_new <= SPECDEC_MAX_TREE_NODES, Hq % Hkv
- * == 0, Hq / Hkv <= 128, Hq <= 2^20, q_stride < 2^31, B * n_new * Hq < 2^31, n_new <= Lmax <= 2^30,
- * B * Lmax * Hkv * D < 2^40; q, caches and out 16-byte aligned. A length that is neither 0 nor within
- * [n_new, Lmax] sets SPECDEC_ERR_INVALID_ARG in the status word and that
- * sequence's output is 0. The workspace does not grow with B or Lmax.
- * Asynchronous.
+ * == 0, Hq / Hkv <= 128, Hq <= 2^20, q_stride < 2^31, B * n_new * Hq < 2^31,
+ * n_new <= Lmax <= 2^30, B * Lmax * Hkv * D < 2^40, B * Hkv * n_new * (Lmax /
+ * 64 + 8) < 2^31; scale and softcap, where positive, at least 1e-30, softcap
+ * at most 1e30; q, caches and out 16-byte aligned. A length that is neither 0
+ * nor within [n_new, Lmax] sets SPECDEC_ERR_INVALID_ARG in the status word and
+ * that sequence's output is 0; a device-side wait that ran out sets
+ * SPECDEC_ERR_TIMEOUT, and the output is not to be used. The workspace does
+ * not grow with B or Lmax. Asynchronous.
  */
 size_t specdec_verify_attention_kv8_workspace_size(int B, int n_new, int Hq, int Hkv, int D,
                                                    int Lmax);

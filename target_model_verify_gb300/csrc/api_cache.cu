@@ -104,6 +104,8 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   if (q_stride < (long long)Hq * D || q_stride % 8 != 0 || q_stride >= (1ll << 31)) return SPECDEC_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
     return SPECDEC_ERR_INVALID_ARG;
+  if (softcap > 0.f && (softcap < 1e-30f || softcap > 1e30f)) return SPECDEC_ERR_INVALID_ARG;   // its reciprocal is used
+  if (scale > 0.f && scale < 1e-30f) return SPECDEC_ERR_INVALID_ARG;
   CacheAttnLaunch A;
   A.tree = parent != nullptr;
   A.max_depth = n_new - 1;

@@ -525,7 +525,8 @@ __device__ __forceinline__ void zero_empty(const CacheAttnLaunch& A) {
     bool bad;
     if (seq_blocks<kBlk>(A, A.seq_lens[b], first, bad) > 0) continue;
     uint4* dst = reinterpret_cast<uint4*>(A.out + (size_t)b * A.n_new * A.Hq * kD);
-    for (int e = threadIdx.x; e < A.n_new * A.Hq * (kD / 8); e += 32 * kSoftWarps) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+    const long long chunks = (long long)A.n_new * A.Hq * (kD / 8);
+    for (long long e = threadIdx.x; e < chunks; e += 32 * kSoftWarps) dst[e] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
