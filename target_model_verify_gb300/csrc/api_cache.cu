@@ -20,9 +20,9 @@ int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
     return SPECDEC_ERR_UNSUPPORTED;
   if (Hq / Hkv > 128 || Hq > (1 << 20)) return SPECDEC_ERR_UNSUPPORTED;
   if ((__int128)B * Lmax * Hkv * D >= ((__int128)1 << 40)) return SPECDEC_ERR_UNSUPPORTED;
-  // (sequence, KV head, row group) tiles are a grid dimension
+  // (sequence, KV head, row group) tiles and their blocks of 64 keys or more
+  // are counted in 32 bits
   if ((long long)B * Hq * n_new >= (1ll << 31)) return SPECDEC_ERR_UNSUPPORTED;
-  // and their blocks of 64 keys or more are counted in 32 bits
   if ((__int128)B * Hkv * n_new * (Lmax / 64 + 8) >= ((__int128)1 << 31)) return SPECDEC_ERR_UNSUPPORTED;
   return SPECDEC_OK;
 }
@@ -236,7 +236,8 @@ int specdec_verify_attention_kv8(const void* q, long long q_stride, const void* 
 }
 
 size_t specdec_verify_attention_masked_workspace_size(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
-  return specdec_verify_attention_kv8_workspace_size(B, n_new, Hq, Hkv, D, Lmax);
+  if (check_shape(B, n_new, Hq, Hkv, D, Lmax) != SPECDEC_OK) return 0;
+  return make_plan(false, n_new, Hq / Hkv, D).total;
 }
 
 int specdec_verify_attention_masked(const void* q, long long q_stride, const void* k_cache,
