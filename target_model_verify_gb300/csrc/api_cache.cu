@@ -56,14 +56,14 @@ AttnPlan make_plan(bool e4m3, int n_new, int G, int D) {
 
 // The cache as a 4-D tensor {D, Hkv, Lmax, B}; box: up to 128 bytes of a row
 // x one head x one block of rows, swizzled.
-bool encode_cache(CUtensorMap* map, const void* base, bool e4m3, int B, int Lmax, int Hkv, int D) {
+bool encode_cache(CUtensorMap* map, const void* base, bool e4m3, int B, int Lmax, int Hkv, int D, int block) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t es = e4m3 ? 1 : 2, row = (cuuint64_t)D * es;
   const cuuint32_t panel = row < 128 ? (cuuint32_t)row : 128u;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)Lmax, (cuuint64_t)B};
   const cuuint64_t strides[3] = {row, row * Hkv, row * Hkv * Lmax};
-  const cuuint32_t box[4] = {panel / (cuuint32_t)es, 1, (cuuint32_t)cache_attn_block(e4m3, D), 1};
+  const cuuint32_t box[4] = {panel / (cuuint32_t)es, 1, (cuuint32_t)block, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -156,7 +156,9 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.notes = reinterpret_cast<int4*>(ws + pl.off_notes);
   A.status = reinterpret_cast<int*>(ws);
   CUtensorMap tk, tv, tq;
-  if (!encode_cache(&tk, k_cache, e4m3, B, Lmax, Hkv, D) || !encode_cache(&tv, v_cache, e4m3, B, Lmax, Hkv, D))
+  const int block = cache_attn_block(e4m3, D, cache_attn_rows(pl.group_pos * G));
+  if (!encode_cache(&tk, k_cache, e4m3, B, Lmax, Hkv, D, block) ||
+      !encode_cache(&tv, v_cache, e4m3, B, Lmax, Hkv, D, block))
     return SPECDEC_ERR_CUDA;
   if (e4m3)
     tq = tk;                                   // not read: the kernel converts the queries itself

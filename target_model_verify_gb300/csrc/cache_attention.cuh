@@ -72,7 +72,7 @@ constexpr int kTileCost = 3;                  // units of work that a tile costs
 template <bool kE4m3, int kD, int kRP>
 struct Shape {
   static constexpr int kElem = kE4m3 ? 1 : 2;
-  static constexpr int kBlk = cache_attn_block(kE4m3, kD);   // keys per block
+  static constexpr int kBlk = cache_attn_block(kE4m3, kD, kRP);   // keys per block
   static constexpr int kRowBytes = kD * kElem;
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;   // one TMA box row
   static constexpr int kPanels = kRowBytes / kPanelBytes;
@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kIssuerO) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
   if (A.tree) {
-    for (int e = threadIdx.x; e < A.n_new; e += kThreads) {
+    // not by warp 0, which looks for its part meanwhile
+    for (int e = (int)threadIdx.x - 32; e >= 0 && e < A.n_new; e += kThreads - 32) {
       sts128(tree + e * 16, A.anc[e][0], A.anc[e][1], A.anc[e][2], A.anc[e][3]);
       sts32(tree + 128 * 16 + e * 4, A.depth[e]);
     }

@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
   if (warp == 0) sts32(zeros + lane * 4, 0u);
   if (warp == 5) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 256);
   if (A.tree) {
-    for (int e = threadIdx.x; e < A.n_new; e += kKeyThreads) {
+    // not by warp 0, which looks for its part meanwhile
+    for (int e = (int)threadIdx.x - 32; e >= 0 && e < A.n_new; e += kKeyThreads - 32) {
       sts128(tree + e * 16, A.anc[e][0], A.anc[e][1], A.anc[e][2], A.anc[e][3]);
       sts32(tree + 128 * 16 + e * 4, A.depth[e]);
     }
