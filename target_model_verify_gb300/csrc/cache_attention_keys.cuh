@@ -31,7 +31,8 @@ namespace specdec {
 namespace cache_attn {
 
 constexpr int kKeyThreads = 192;
-constexpr int kKeyD = 128, kKeyBlk = 128, kKeyRows = 32, kKeyRing = 2;
+constexpr int kKeyD = 128, kKeyBlk = 128, kKeyRows = 32;
+constexpr int kKeyRingK = 2, kKeyRingV = 3;             // blocks of each in flight: V's are held longer
 constexpr int kKeySlot = kKeyBlk * kKeyD;
 constexpr int kKeyPTerm = kKeyBlk * kKeyRows;           // [keys][32 rows] codes of one term
 constexpr int kKeyQBytes = 2 * kKeyRows * kKeyD;        // [hi rows, lo rows][dims]
@@ -40,8 +41,8 @@ constexpr float kRise = 4.f, kLift = 2.f, kBase = 4.f;  // log2: see above; p at
 // tables per query buffer: of every row its score factor, slope, depth and
 // place in the output [32]; of every new position the rows that see it [128]
 constexpr int kKeyTab = 4 * kKeyRows * 4 + 128 * 4;
-constexpr int kKeySmem = 1024 + 2 * kKeyRing * kKeySlot + 2 * 3 * kKeyPTerm + 2 * kKeyQBytes + 2 * kKeyTab +
-                         3 * kKeyRows * 4 + 4 * kKeyRows * 4 + 128 * 16 + 128 * 4 + 512;
+constexpr int kKeySmem = 1024 + (kKeyRingK + kKeyRingV) * kKeySlot + 3 * kKeyPTerm + 2 * kKeyQBytes + 2 * kKeyTab +
+                         3 * kKeyRows * 4 + 4 * kKeyRows * 4 + 128 * 4 + 512;
 static_assert(2 * (kKeySmem + 1024) <= 228 * 1024, "two CTAs per SM");
 
 // MN-major operand of 32-byte rows (32 codes along N), 32-byte swizzle.
@@ -82,33 +83,33 @@ template <bool kExtra>
 __global__ void __launch_bounds__(kKeyThreads, 2)
     cache_attn_keys_kernel(const __grid_constant__ CacheAttnLaunch A, const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v) {
-  constexpr int kBlk = kKeyBlk, kD = kKeyD, kR = kKeyRing, kRows = kKeyRows;
+  constexpr int kBlk = kKeyBlk, kD = kKeyD, kRows = kKeyRows;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring_k = (raw + 1023u) & ~1023u;
-  const uint32_t ring_v = ring_k + kR * kKeySlot;
-  const uint32_t pb = ring_v + kR * kKeySlot;              // probabilities: [2][3 terms]
-  const uint32_t qb = pb + 2 * 3 * kKeyPTerm;
+  const uint32_t ring_v = ring_k + kKeyRingK * kKeySlot;
+  const uint32_t pb = ring_v + kKeyRingV * kKeySlot;       // probabilities: three terms
+  const uint32_t qb = pb + 3 * kKeyPTerm;
   const uint32_t tab = qb + 2 * kKeyQBytes;
   const uint32_t ref = tab + 2 * kKeyTab;                  // references, then factors for what moved
   const uint32_t zeros = ref + 2 * kRows * 4;              // [32]
   const uint32_t red = zeros + kRows * 4;                  // [4 warps][32 rows]
-  const uint32_t tree = red + 4 * kRows * 4;
-  const uint32_t bars = tree + 128 * 16 + 128 * 4;
+  const uint32_t depths = red + 4 * kRows * 4;             // of the tree's nodes [128]
+  const uint32_t bars = depths + 128 * 4;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   auto k_full = [&](int s) { return bar(s); };
   auto k_empty = [&](int s) { return bar(2 + s); };
-  auto v_full = [&](int s) { return bar(4 + s); };
-  auto v_empty = [&](int s) { return bar(6 + s); };
-  auto v_clean = [&](int s) { return bar(8 + s); };
-  auto s_full = [&](int s) { return bar(10 + s); };
-  auto p_full = [&](int s) { return bar(12 + s); };
-  auto o_done = [&](int s) { return bar(14 + s); };
-  auto q_full = [&](int s) { return bar(16 + s); };
-  auto q_empty = [&](int s) { return bar(18 + s); };
-  const uint32_t drained = bar(20);
-  uint8_t* const words = smem_raw + (bar(22) - raw);
+  auto s_full = [&](int s) { return bar(4 + s); };
+  auto p_full = [&](int s) { return bar(6 + s); };
+  auto o_done = [&](int s) { return bar(8 + s); };
+  auto q_full = [&](int s) { return bar(10 + s); };
+  auto q_empty = [&](int s) { return bar(12 + s); };
+  auto v_full = [&](int s) { return bar(14 + s); };
+  auto v_empty = [&](int s) { return bar(17 + s); };
+  auto v_clean = [&](int s) { return bar(20 + s); };
+  const uint32_t drained = bar(23);
+  uint8_t* const words = smem_raw + (bar(24) - raw);
   volatile int* const abort = reinterpret_cast<volatile int*>(words);
   volatile int* const odd = abort + 1;
   volatile uint32_t* const tmem_slot = reinterpret_cast<volatile uint32_t*>(words) + 2;
@@ -118,14 +119,16 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
     for (int s = 0; s < 2; ++s) {
       mbar_init(k_full(s), 1);
       mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
-      mbar_init(v_clean(s), 1);
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), kSoftWarps);
       mbar_init(o_done(s), 1);
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1 + kSoftWarps);
+    }
+    for (int s = 0; s < kKeyRingV; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+      mbar_init(v_clean(s), 1);
     }
     mbar_init(drained, 1);
     *abort = 0;
@@ -134,13 +137,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
   }
   if (warp == 0) sts32(zeros + lane * 4, 0u);
   if (warp == 5) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 256);
-  if (A.tree) {
-    // not by warp 0, which looks for its part meanwhile
-    for (int e = (int)threadIdx.x - 32; e >= 0 && e < A.n_new; e += kKeyThreads - 32) {
-      sts128(tree + e * 16, A.anc[e][0], A.anc[e][1], A.anc[e][2], A.anc[e][3]);
-      sts32(tree + 128 * 16 + e * 4, A.depth[e]);
-    }
-  }
+  if (A.tree)                        // not by warp 0, which looks for its part meanwhile
+    for (int e = (int)threadIdx.x - 32; e >= 0 && e < A.n_new; e += kKeyThreads - 32) sts32(depths + e * 4, A.depth[e]);
   grid_dependency_wait();
   grid_launch_dependents();          // the merge may get ready on idle SMs
   if (warp == 0) {
@@ -223,20 +221,20 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       const float q_scale = fine ? __uint_as_float((uint32_t)(127 + down) << 23) : __uint_as_float(0x7fffffffu);
       sts32(at, __float_as_uint(A.scale * q_scale * (kExtra ? 1.f : kLog2e)));
       sts32(at + kRows * 4, __float_as_uint(kExtra && A.slopes ? A.slopes[head] * kLog2e : 0.f));
-      const int dep = A.tree ? (int)lds32(tree + 128 * 16 + idx * 4) : idx;
+      const int dep = A.tree ? (int)lds32(depths + idx * 4) : idx;
       sts32(at + 2 * kRows * 4, __float_as_uint((float)dep));
       sts32(at + 3 * kRows * 4, (uint32_t)(idx * A.Hq + head));
       for (int a0 = 0; a0 < A.n_new; a0 += 32) {
         uint32_t sees = 0, of_mine = 0;          // new positions a0 .. a0 + 31 that this row sees
         if (A.tree)
-          sees = lds32(tree + idx * 16 + (a0 >> 5) * 4);
+          sees = A.anc[idx][a0 >> 5];
         else if (idx >= a0)
           sees = idx - a0 >= 31 ? 0xffffffffu : (2u << (idx - a0)) - 1u;
 #pragma unroll
         for (int a = 0; a < 32; ++a) {
           bool see = (sees >> a) & 1u;
           if (A.window > 0) {
-            const int da = A.tree ? (int)lds32(tree + 128 * 16 + (a0 + a) * 4) : a0 + a;
+            const int da = A.tree ? (int)lds32(depths + (a0 + a) * 4) : a0 + a;
             see = see && dep - da < A.window;
           }
           const uint32_t rows = __ballot_sync(0xffffffffu, see);
@@ -253,8 +251,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
     int check_j0 = -1, check_L = 0;      // the last block loaded: its first row (-1: nothing to do), its sequence
     auto check_values = [&](uint32_t nb) {
       if (check_j0 < 0) return true;
-      const uint32_t s = nb & 1;
-      if (!warp_wait(v_full(s), (nb >> 1) & 1)) return false;
+      const uint32_t s = nb % kKeyRingV;
+      if (!warp_wait(v_full(s), (nb / kKeyRingV) & 1)) return false;
       // Rows past the sequence hold anything, and a NaN in a row that not
       // every query sees would pass a zero probability: neither stays in
       // the product. The epilogue adds the NaN where seen.
@@ -297,14 +295,15 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
         __syncwarp();
         issued_k |= 1u << s;
         phase_k = (phase_k & ~(1u << s)) | (ph << s);
-        if (!(ok = warp_wait(v_empty(s), ph ^ 1u))) break;
+        const uint32_t sv = n % kKeyRingV, phv = (n / kKeyRingV) & 1;
+        if (!(ok = warp_wait(v_empty(sv), phv ^ 1u))) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(v_full(s), kKeySlot);
-          tma_load_4d(ring_v + s * kKeySlot, &tmap_v, v_full(s), 0, w.h, j0, w.b, pol);
+          mbar_arrive_expect_tx(v_full(sv), kKeySlot);
+          tma_load_4d(ring_v + sv * kKeySlot, &tmap_v, v_full(sv), 0, w.h, j0, w.b, pol);
         }
         __syncwarp();
-        issued_v |= 1u << s;
-        phase_v = (phase_v & ~(1u << s)) | (ph << s);
+        issued_v |= 1u << sv;
+        phase_v = (phase_v & ~(1u << sv)) | (phv << sv);
         // the check runs a block behind, when its values are likely there
         if (!(ok = check_values(n - 1))) break;
         check_j0 = w.clean(i) ? -1 : j0;
@@ -357,22 +356,21 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       for (int i = 0; i < w.n_here; ++i, ++n) {
         // the other buffer's scores were read before the last product was issued
         if (!wq.done() && !(ok = issue_scores())) break;
-        const uint32_t s = n & 1;
-        if (!(ok = warp_wait(v_full(s), (n >> 1) & 1))) break;
+        const uint32_t s = n & 1, sv = n % kKeyRingV;
+        if (!(ok = warp_wait(v_full(sv), (n / kKeyRingV) & 1))) break;
         if (!w.clean(i)) {
-          if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) break;
-          clean_ph ^= 1u << s;
+          if (!(ok = warp_wait(v_clean(sv), (clean_ph >> sv) & 1))) break;
+          clean_ph ^= 1u << sv;
         }
         if (!(ok = warp_wait(p_full(s), (n >> 1) & 1))) break;
         tc_fence_after();
-        const uint64_t vd = v_desc + (uint64_t)(s * (kKeySlot >> 4));
-        const uint64_t pd = p_desc + (uint64_t)(s * (3 * kKeyPTerm >> 4));
+        const uint64_t vd = v_desc + (uint64_t)(sv * (kKeySlot >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBlk / 32; ++k)
-            mma_ss<true>(tmem + kKeyColO, vd + k * (32 * 128 >> 4), pd + k * (32 * 32 >> 4), id_o, i > 0 || k > 0);
+            mma_ss<true>(tmem + kKeyColO, vd + k * (32 * 128 >> 4), p_desc + k * (32 * 32 >> 4), id_o, i > 0 || k > 0);
           tc_commit(o_done(s));
-          tc_commit(v_empty(s));
+          tc_commit(v_empty(sv));
         }
         __syncwarp();
       }
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           float pj = 0.f;
           if (kExtra && A.slopes) {
             int p = j - P0;                            // position from the first new one's
-            if (A.tree && p >= 0) p = (int)lds32(tree + 128 * 16 + min(p, A.n_new - 1) * 4);
+            if (A.tree && p >= 0) p = (int)lds32(depths + min(p, A.n_new - 1) * 4);
             pj = (float)p;
           }
 #pragma unroll
@@ -555,10 +553,10 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           maxima = false;
         }
         // ---- probabilities, as three e4m3 terms ----
-        // (the product that read this buffer two blocks ago was issued before
-        // this block's scores, so it is done)
+        // the last block's product has read its own
+        if (!dead && n > 0 && !warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
         if (dead) continue;
-        const uint32_t to = pb + (n & 1) * 3 * kKeyPTerm + kl * 32;
+        const uint32_t to = pb + kl * 32;
 #pragma unroll
         for (int h16 = 0; h16 < 2; ++h16) {
           uint32_t t[3][4];
@@ -685,7 +683,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
   if (warp == 5) tmem_dealloc(tmem, 256);
   if (*abort && warp == 4 && lane == 0)
     // A wait gave up: let every copy already issued land before the CTA exits.
-    for (int s = 0; s < kR; ++s) {
+    for (int s = 0; s < kKeyRingV; ++s) {
       if (issued_k & (1u << s)) wait_drain(k_full(s), (phase_k >> s) & 1u);
       if (issued_v & (1u << s)) wait_drain(v_full(s), (phase_v >> s) & 1u);
     }
