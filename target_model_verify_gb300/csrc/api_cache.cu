@@ -156,7 +156,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.notes = reinterpret_cast<int4*>(ws + pl.off_notes);
   A.status = reinterpret_cast<int*>(ws);
   CUtensorMap tk, tv, tq;
-  const int block = cache_attn_block(e4m3, D, cache_attn_rows(pl.group_pos * G));
+  const int block = cache_attn_block(D, cache_attn_rows(pl.group_pos * G));
   if (!encode_cache(&tk, k_cache, e4m3, B, Lmax, Hkv, D, block) ||
       !encode_cache(&tv, v_cache, e4m3, B, Lmax, Hkv, D, block))
     return SPECDEC_ERR_CUDA;

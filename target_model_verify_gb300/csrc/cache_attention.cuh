@@ -72,7 +72,7 @@ constexpr int kTileCost = 3;                  // units of work that a tile costs
 template <bool kE4m3, int kD, int kRP>
 struct Shape {
   static constexpr int kElem = kE4m3 ? 1 : 2;
-  static constexpr int kBlk = cache_attn_block(kE4m3, kD, kRP);   // keys per block
+  static constexpr int kBlk = cache_attn_block(kD, kRP);   // keys per block
   static constexpr int kRowBytes = kD * kElem;
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;   // one TMA box row
   static constexpr int kPanels = kRowBytes / kPanelBytes;
@@ -450,6 +450,7 @@ struct Walk {
   int blk, n_here;    // first block inside the tile, blocks of this part
   int nb, first, L;   // the tile's blocks, its first cache block, its length
   int clean_lo, clean_hi;   // the tile's blocks that every new position sees whole
+  bool backward;            // the order of the blocks: see at()
   int u, end, tile0;  // this part's first unit in the tile, the part's end, the tile's first unit
 
   __device__ __forceinline__ void load(const CacheAttnLaunch& A) {
@@ -469,6 +470,7 @@ struct Walk {
     u = u0;
     end = u1;
     b = b0;
+    backward = A.slopes != nullptr;
     if (u >= end) return;
     load(A);
     const int units = tile_units(nb), t = off / units;
@@ -498,9 +500,13 @@ struct Walk {
       cut();
     } while (n_here == 0);
   }
-  __device__ __forceinline__ bool clean(int ib) const {
-    return blk + ib >= clean_lo && blk + ib < clean_hi;
-  }
+  // This part's block i, in the order in which they are taken: from the
+  // sequence's start, but from its end with a bias by distance, which makes
+  // the last rows' exponents the largest: the references then move at the
+  // tile's first block only (in the other order, at almost every block).
+  __device__ __forceinline__ int at(int i) const { return blk + (backward ? n_here - 1 - i : i); }
+  __device__ __forceinline__ int row(int i) const { return (first + at(i)) * kBlk; }
+  __device__ __forceinline__ bool clean(int i) const { return at(i) >= clean_lo && at(i) < clean_hi; }
 };
 
 // What the CTA with a shared tile's first block notes for the merge: the
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           issued_q_phase = (issued_q_phase & ~(1u << qs)) | (qph << qs);
         }
         for (int i = 0; i < w.n_here; ++i) {
-          const int j0 = (w.first + w.blk + i) * kBlk;
+          const int j0 = w.row(i);
           const uint32_t full = is_v ? v_full(s) : k_full(s);
           if (!(ok = mbar_wait(is_v ? v_empty(s) : k_empty(s), ph ^ 1u, abort, A.status))) break;
           mbar_arrive_expect_tx(full, (uint32_t)S::kSlotBytes);
@@ -1038,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && !w.done(); w.next(A)) {
         for (int i = 0; i < w.n_here; ++i, ++n) {
           const bool clean = w.clean(i);
-          const int j0 = (w.first + w.blk + i) * kBlk;
+          const int j0 = w.row(i);
           if (!(ok = warp_wait(v_full(s), ph))) break;
           if (!(ok = warp_wait(v16_empty(n & 1), ((n >> 1) & 1) ^ 1u))) break;
           // A warp takes 8 keys x 4 chunks of 16 codes at a time: rows p and
@@ -1118,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // ring never part by more than the ring's length
           if (!(ok = warp_wait(v_full(s), ph))) break;
           if (!w.clean(i)) {
-            const int j0 = (w.first + w.blk + i) * kBlk;
+            const int j0 = w.row(i);
             for (int e = at; e < S::kSlotBytes / 16; e += 32 * kAuxWarps) {
               const int j = (e >> 3) % kBlk;
               const uint32_t a = ring_v + s * S::kSlotBytes + e * 16;
@@ -1219,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t so = ((size_t)w.b * A.Hkv + w.h) * A.n_scale;
         ks = A.k_scale + so;
         vs = A.v_scale + so;
-        load_scales((w.first + w.blk) * kBlk + key0);
+        load_scales(w.row(0) + key0);
         if (!dead && !warp_wait(q_full(0), nt & 1)) dead = true;
         ck *= __uint_as_float(lds32(q_tab + lg * 4));
         __syncwarp();
@@ -1228,8 +1234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!kExtra) ck *= kLog2e;
 
       float m_ref = -INFINITY, l = 0.f;
-      int j0 = (w.first + w.blk) * kBlk + key0;
-      for (int ib = 0; ib < w.n_here; ++ib, ++n, j0 += kBlk) {
+      for (int ib = 0; ib < w.n_here; ++ib, ++n) {
+        const int j0 = w.row(ib) + key0;
         const bool clean = w.clean(ib);
         float cs[kSubs], lv[kSubs], inv_sv[kSubs];                 // per run: score factor, log2 s_v, 1 / s_v
 #pragma unroll
@@ -1244,7 +1250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             inv_sv[x] = rcp(sv_next[x]);
           }
         }
-        if (kE4m3 && ib + 1 < w.n_here) load_scales(j0 + kBlk);
+        if (kE4m3 && ib + 1 < w.n_here) load_scales(w.row(ib + 1) + key0);
         if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
         if (dead) continue;
         tc_fence_after();
@@ -1263,28 +1269,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* const y = x.f + sub * kSubKeys;
             const int xs = pc * (kPiece / kSubKeys) + sub, js = j0 + xs * kSubKeys;
             if constexpr (kExtra) {
+              // bias slope * (pos_j - pos_i): rows before the new ones stand at
+              // their index, so do a chain's; tree nodes stand at their depth
+              const bool linear = A.slopes && (!A.tree || js + kSubKeys <= P0);
+              const float at0 = lv[xs] + (linear ? slope * (float)(js - P0 - dep) : 0.f);
               if (A.cap > 0.f) {
                 // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
-                const float in = cs[xs] * A.cap_exp, out = -2.f * A.cap * kLog2e, add = A.cap * kLog2e + lv[xs];
+                const float in = cs[xs] * A.cap_exp, out = -2.f * A.cap * kLog2e, add = A.cap * kLog2e;
 #pragma unroll
-                for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(out, rcp(1.f + ex2(y[k] * in)), add);
+                for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(out, rcp(1.f + ex2(y[k] * in)), add) + at0;
               } else {
 #pragma unroll
-                for (int k = 0; k < kSubKeys; k += 2) fma2(y[k], y[k + 1], cs[xs] * kLog2e, lv[xs]);
+                for (int k = 0; k < kSubKeys; k += 2) fma2(y[k], y[k + 1], cs[xs] * kLog2e, at0);
               }
-              if (A.slopes) {
-                // bias slope * (pos_j - pos_i); tree nodes stand at their depth
-                if (!A.tree || js + kSubKeys <= P0) {
-                  const float base = (float)(js - P0 - dep);
+              if (linear) {
 #pragma unroll
-                  for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(slope, base + (float)k, y[k]);
-                } else {
+                for (int k = 0; k < kSubKeys; k += 2) acc2(y[k], y[k + 1], (float)k, (float)(k + 1), slope);
+              } else if (A.slopes) {
 #pragma unroll
-                  for (int k = 0; k < kSubKeys; ++k) {
-                    int pj = js + k - P0;
-                    if (pj >= 0) pj = (int)lds32(tree + 128 * 16 + min(pj, A.n_new - 1) * 4);
-                    y[k] = fmaf(slope, (float)(pj - dep), y[k]);
-                  }
+                for (int k = 0; k < kSubKeys; ++k) {
+                  int pj = js + k - P0;
+                  if (pj >= 0) pj = (int)lds32(tree + 128 * 16 + min(pj, A.n_new - 1) * 4);
+                  y[k] = fmaf(slope, (float)(pj - dep), y[k]);
                 }
               }
             }
@@ -1420,7 +1426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // for the rows that see them.
             for (int ib = 0; ib < w.n_here; ++ib) {
               if (w.clean(ib)) continue;
-              const int jb = (w.first + w.blk + ib) * kBlk + key0;
+              const int jb = w.row(ib) + key0;
               for (int k = 0; k < kKpl && jb + k < w.L; ++k) {
                 const bool seen = mine && (sight.mask(jb + k) & 1u);
                 const size_t at = (((size_t)w.b * A.Lmax + jb + k) * A.Hkv + w.h) * kD + c0;

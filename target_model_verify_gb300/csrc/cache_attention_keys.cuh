@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
     for (; ok && !w.done(); w.next(A), ++nt) {
       for (int i = 0; i < w.n_here; ++i, ++n) {
         const uint32_t s = n & 1, ph = (n >> 1) & 1;
-        const int j0 = (w.first + w.blk + i) * kBlk;
+        const int j0 = w.row(i);
         if (!(ok = warp_wait(k_empty(s), ph ^ 1u))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(k_full(s), kKeySlot);
@@ -390,13 +390,12 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       const size_t so = ((size_t)w.b * A.Hkv + w.h) * A.n_scale;
       const float* ks = A.k_scale + so;
       const float* vs = A.v_scale + so;
-      int j = (w.first + w.blk) * kBlk + kl;           // this thread's cache row
       float sk_next, sv_next;
       auto load_scales = [&](int jw) {
         sk_next = jw < w.L ? __ldg(ks + jw / SPECDEC_KV8_BLOCK) : 1.f;
         sv_next = jw < w.L ? __ldg(vs + jw / SPECDEC_KV8_BLOCK) : 1.f;
       };
-      load_scales(j - lane);
+      load_scales(w.row(0) + warp * 32);
       // The rows that see cache row jj: those that see its new position, or,
       // before the new rows, those whose window reaches it.
       auto seen_by = [&](int jj) {
@@ -420,10 +419,11 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       if (!dead && !warp_wait(q_full(qs), (nt >> 1) & 1)) dead = true;
       named_bar_sync(1, 32 * kSoftWarps);
 
-      for (int ib = 0; ib < w.n_here; ++ib, ++n, j += kBlk) {
+      for (int ib = 0; ib < w.n_here; ++ib, ++n) {
+        const int j = w.row(ib) + kl;                  // this thread's cache row
         const bool clean = w.clean(ib);
         const float sk = sk_next, lvb = __log2f(sv_next) + kBase, inv_sv = rcp(sv_next);
-        if (ib + 1 < w.n_here) load_scales(j - lane + kBlk);
+        if (ib + 1 < w.n_here) load_scales(w.row(ib + 1) + warp * 32);
         if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
         tc_fence_after();
         float y[kRows];
@@ -462,18 +462,24 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
             mul2(y[r + 2], y[r + 3], c.z, c.w);
             if constexpr (kExtra) {
               const float4 sl = lds128f(t0 + kRows * 4 + r * 4), dp = lds128f(t0 + 2 * kRows * 4 + r * 4);
-              const float bb[4] = {b.x, b.y, b.z, b.w}, ss[4] = {sl.x, sl.y, sl.z, sl.w},
-                          dd[4] = {dp.x, dp.y, dp.z, dp.w};
+              mul2(y[r], y[r + 1], sk, sk);
+              mul2(y[r + 2], y[r + 3], sk, sk);
+              if (A.cap > 0.f) {       // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float z = y[r + k] * sk;
-                float e;
-                if (A.cap > 0.f)       // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
-                  e = fmaf(-2.f * A.cap * kLog2e, rcp(1.f + ex2(z * A.cap_exp)), A.cap * kLog2e);
-                else
-                  e = z * kLog2e;
-                y[r + k] = fmaf(ss[k], pj - dd[k], e) + bb[k];
+                for (int k = 0; k < 4; ++k)
+                  y[r + k] = fmaf(-2.f * A.cap * kLog2e, rcp(1.f + ex2(y[r + k] * A.cap_exp)), A.cap * kLog2e);
+              } else {
+                mul2(y[r], y[r + 1], kLog2e, kLog2e);
+                mul2(y[r + 2], y[r + 3], kLog2e, kLog2e);
               }
+              // bias slope * (pos_j - pos_i)
+              float4 away = make_float4(-dp.x, -dp.y, -dp.z, -dp.w);
+              add2(away.x, away.y, pj, pj);
+              add2(away.z, away.w, pj, pj);
+              fma2(away.x, away.y, sl.x, sl.y, b.x, b.y);
+              fma2(away.z, away.w, sl.z, sl.w, b.z, b.w);
+              add2(y[r], y[r + 1], away.x, away.y);
+              add2(y[r + 2], y[r + 3], away.z, away.w);
             } else {
               fma2(y[r], y[r + 1], sk, sk, b.x, b.y);
               fma2(y[r + 2], y[r + 3], sk, sk, b.z, b.w);
@@ -634,7 +640,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           // NaN that were held back from the product (rare), for the rows that see them
           for (int ib = 0; ib < w.n_here; ++ib) {
             if (w.clean(ib)) continue;
-            const int jb = (w.first + w.blk + ib) * kBlk;
+            const int jb = w.row(ib);
             for (int k = 0; k < kBlk && jb + k < w.L; ++k) {
               const uint8_t code =
                   static_cast<const uint8_t*>(A.v)[(((size_t)w.b * A.Lmax + jb + k) * A.Hkv + w.h) * kD + kl];

@@ -218,12 +218,11 @@ struct CacheAttnLaunch {
 // Lanes that a group of query rows takes: 32, 64 or 128.
 constexpr int cache_attn_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 // Keys per block (and TMA box): 128, but 64 at 256 dims (shared memory) and
-// for 128 query rows over a bf16 cache, where a lane holds a score of every
-// key (64 against 128 keys: 38.3 / 40.9 us on the 26-node tree over 8 x 4096
-// rows; 20 query rows over 16 ragged sequences with a window: 30.2 / 27.6).
-constexpr int cache_attn_block(bool e4m3, int D, int lanes) {
-  return D == 256 || (!e4m3 && lanes == 128) ? 64 : 128;
-}
+// for 128 lanes of query rows, where a lane holds a score of every key. 64
+// against 128 keys there: 38.3 / 40.9 us on a 26-node tree over 8 x 4096 bf16
+// rows, 127 / 139 over 32 x 4096 e4m3 rows. With fewer lanes 128 pay: 30.2 /
+// 27.6 us for 20 query rows on 16 ragged bf16 sequences with a window.
+constexpr int cache_attn_block(int D, int lanes) { return D == 256 || lanes == 128 ? 64 : 128; }
 // The form with the cache on the M side (cache_attention_keys.cuh) can take a
 // call with up to 32 query rows per KV head, and does from 256 tiles or 2048
 // blocks of cache on. Measured, keys against rows form, us a call: 64 x 4096
