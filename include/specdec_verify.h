@@ -309,8 +309,9 @@ int specdec_verify_attention(const void* q, const void* k_cache, const void* v_c
  * A start or count outside the cache, or a count above n, sets
  * SPECDEC_ERR_INVALID_ARG in the status word and skips that sequence; a rows
  * entry outside [0, n) does the same for the block of 32 cache rows it would
- * go to. Limits: D = 64, 128 or 256; Lmax <= 2^30; B * Lmax * Hkv * D < 2^40;
- * B * Hkv * (n / 32 + 2) < 2^31; bf16 and code pointers 16-byte aligned. The sources and the caches must not overlap. Asynchronous; the
+ * go to. Limits: n >= 1; D = 64, 128 or 256; Lmax <= 2^30; B * Lmax * Hkv * D
+ * < 2^40; B * Hkv * (n / 32 + 2) < 2^31; bf16 and code pointers 16-byte
+ * aligned. The sources and the caches must not overlap. Asynchronous; the
  * workspace holds the status word only.
  */
 #define SPECDEC_KV8_BLOCK 32
@@ -348,7 +349,8 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
  * row j before the new ones stands at j, new position i at seq_lens[b] - n_new
  * + i, or, in a tree, + the depth of node i. Rows that a position does not see
  * never reach its output, whatever they hold.
- * A query row that holds an infinity or a NaN gives NaN (kv8). Softmax and
+ * An infinity or a NaN in a value row makes that column infinite or NaN for
+ * the positions that see the row; a query row that holds one gives NaN (kv8). Softmax and
  * sums in fp32; the probabilities enter the value product as f16, or as three
  * e4m3 terms of it that keep 2^-20 of the row's largest (kv8), or as bf16
  * (masked); the queries enter the score product as bf16 (masked) or as two
@@ -357,7 +359,7 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
  * == 0, Hq / Hkv <= 128, Hq <= 2^20, q_stride < 2^31, B * n_new * Hq < 2^31,
  * n_new <= Lmax <= 2^30, B * Lmax * Hkv * D < 2^40, B * Hkv * n_new * (Lmax /
  * 64 + 8) < 2^31; scale and softcap, where positive, at least 1e-30, softcap
- * at most 1e30; q, caches and out 16-byte aligned. A length that is neither 0
+ * at most 1000; q, caches and out 16-byte aligned. A length that is neither 0
  * nor within [n_new, Lmax] sets SPECDEC_ERR_INVALID_ARG in the status word and
  * that sequence's output is 0; a device-side wait that ran out sets
  * SPECDEC_ERR_TIMEOUT, and the output is not to be used. The workspace does

@@ -208,6 +208,13 @@ def verify_attention(q, k_cache, v_cache, seq_lens, scale=0.0, out=None, workspa
 KV8_BLOCK = _b.SPECDEC_KV8_BLOCK
 
 
+def _on(stream, t):
+    """The stream as the current one, for a call on t's device."""
+    if t.is_cuda and t.device != stream.device:
+        raise ValueError("stream must be of the tensors' device")
+    return torch.cuda.stream(stream)
+
+
 def alloc_kv8_cache(B, Lmax, Hkv, D, device=None):
     """(k_cache, v_cache, k_scale, v_scale) of an empty 8-bit cache: float8_e4m3fn codes
     [B, Lmax, Hkv, D] and float32 scales [B, Hkv, ceil(Lmax / KV8_BLOCK)]."""
@@ -231,7 +238,7 @@ def append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts=N
     (k_cache, v_cache, k_scale, v_scale).
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, k_new):
             return append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts, rows, workspace)
     rc = _b.native().append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts, rows, workspace)
     if rc != 0:
@@ -255,7 +262,7 @@ def verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale=
     makes the new positions a token tree. Returns out [B, n_new, Hq, D] bf16.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
                                         slopes, parent, out, workspace)
     rc, out = _b.native().cache_attention(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
@@ -269,7 +276,7 @@ def verify_attention_masked(q, k_cache, v_cache, seq_lens, scale=0.0, softcap=0.
                             parent=None, out=None, workspace=None, stream=None):
     """verify_attention_kv8() over a bf16 cache k_cache, v_cache [B, Lmax, Hkv, D]."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return verify_attention_masked(q, k_cache, v_cache, seq_lens, scale, softcap, window, slopes, parent,
                                            out, workspace)
     rc, out = _b.native().cache_attention(q, k_cache, v_cache, None, None, seq_lens, scale, softcap, window, slopes,

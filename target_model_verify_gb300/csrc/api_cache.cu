@@ -104,7 +104,8 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   if (q_stride < (long long)Hq * D || q_stride % 8 != 0 || q_stride >= (1ll << 31)) return SPECDEC_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
     return SPECDEC_ERR_INVALID_ARG;
-  if (softcap > 0.f && (softcap < 1e-30f || softcap > 1e30f)) return SPECDEC_ERR_INVALID_ARG;   // its reciprocal is used
+  // its reciprocal is used, and the tanh rounds to 2^-22 of it
+  if (softcap > 0.f && (softcap < 1e-30f || softcap > 1000.f)) return SPECDEC_ERR_INVALID_ARG;
   if (scale > 0.f && scale < 1e-30f) return SPECDEC_ERR_INVALID_ARG;
   CacheAttnLaunch A;
   A.tree = parent != nullptr;
@@ -184,7 +185,7 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
     return SPECDEC_ERR_UNSUPPORTED;
   if ((__int128)B * Lmax * Hkv * D >= ((__int128)1 << 40)) return SPECDEC_ERR_UNSUPPORTED;
   const long long max_blocks = ((long long)n + SPECDEC_KV8_BLOCK - 2) / SPECDEC_KV8_BLOCK + 1;
-  if ((__int128)B * max_blocks * Hkv >= ((__int128)1 << 31)) return SPECDEC_ERR_UNSUPPORTED;
+  if ((__int128)B * Hkv * (n / SPECDEC_KV8_BLOCK + 2) >= ((__int128)1 << 31)) return SPECDEC_ERR_UNSUPPORTED;
   if (B == 0) return SPECDEC_OK;
   if (!k_new || !v_new || !start || !k_cache || !v_cache || !k_scale || !v_scale)
     return SPECDEC_ERR_INVALID_ARG;

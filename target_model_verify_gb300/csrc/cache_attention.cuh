@@ -28,8 +28,11 @@
 // the rows one batch after another while the grid waits.)
 //
 // CTA: warps 0-3 softmax, 4-7 auxiliary, 8 and 9 TMA producers (K with Q,
-// and V, whose slots free up at different times), 10 and 11 tcgen05 issuers (one per product: a thread takes 50 to 100 cycles for each MMA, as
-// long as the MMA itself, and more for each wait).
+// and V, whose slots free up at different times), 10 and 11 tcgen05 issuers
+// (one per product: a thread takes 50 to 100 cycles for each MMA, as long as
+// the MMA itself, and more for each wait). What an earlier kernel may have
+// written (queries, scales) is not read with ld.global.nc: this kernel can
+// begin before that one ends.
 //   S = Q K^T: tcgen05.mma, M = 128 query rows, N = a block of keys, into one
 //     of two tensor-memory buffers, a block ahead of the softmax. bf16:
 //     kind::f16. e4m3: kind::f8f6f4 on the codes as they lie; the query row,
@@ -87,7 +90,8 @@ struct Shape {
   static constexpr int kQTerm = 128 * kRowBytes;
   static constexpr int kQBytes = kQTmem ? 0 : kTerms * kQTerm;
   static constexpr int kQBufs = !kE4m3 && kD <= 128 ? 2 : 1;
-  static constexpr int kPBufs = kQTmem ? 1 : 2;
+  // two P buffers where tensor memory has room for them
+  static constexpr int kPBufs = 3 * kBlk + kD + (kQTmem ? kTerms * (kD / 4) : 0) <= 512 ? 2 : 1;
   static constexpr int kV16Bytes = kE4m3 ? kBlk * kD * 2 : 0;   // widened V, two of them
   static constexpr int kStageBytes = 128 * kStagePitch;      // 32 output columns of every lane
   static constexpr int kTabBytes = 128 * 4 + 128 * 8 + 128 * 4 + 128 * 16 + 128 * 4;  // q scales, (m, l), places, tree
@@ -132,6 +136,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+// log2(e) cap tanh(z / cap), cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap))),
+// from 2 log2(e) z / cap. Off by about 2^-22 cap, less than the probabilities'
+// rounding for the caps allowed (up to 1000).
+__device__ __forceinline__ float capped(float z_cap_exp, float cap_log2e, float plus) {   // plus = the cap + a bias
+  return fmaf(-2.f * cap_log2e, rcp(1.f + ex2(z_cap_exp)), plus);
+}
 // Two e4m3 codes (16 bits) to two f16 values; every e4m3 value is an f16 value.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
   uint32_t h;
@@ -160,6 +170,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tma
       ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
       "l"((uint64_t)tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
       : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -265,34 +286,43 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
   return m;
 }
+template <int kN>
+__device__ __forceinline__ float largest(const float* y) {      // kN = 16 or 32
+  float a = max3(y[0], y[1], y[2]), b = max3(y[3], y[4], y[5]);
+#pragma unroll
+  for (int k = 6; k + 3 < kN; k += 4) {
+    a = max3(a, y[k], y[k + 1]);
+    b = max3(b, y[k + 2], y[k + 3]);
+  }
+  return fmaxf(max3(a, y[kN - 2], y[kN - 1]), b);
+}
 __device__ __forceinline__ float4 lds128f(uint32_t a) {
   const uint4 v = lds128(a);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
 // Tensor memory: each thread of a warp reads or writes consecutive 32-bit
-// columns of its lane. Loads return with the values there.
+// columns of its lane. Loads return with the values there,
+// but tmem_load_begin's only after tmem_load_end.
 template <int kN>
 struct Cols {};
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[16]) {
+__device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
-      "}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "}, [%16];"
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
         "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
         "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
       : "r"(taddr + 0)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[32]) {
+__device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
-      "}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "}, [%32];"
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
         "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
         "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
@@ -302,7 +332,7 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[32]) {
       : "r"(taddr + 0)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[64]) {
+__device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -311,8 +341,7 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[64]) {
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
       "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
-      "}, [%65];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "}, [%65];"
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
         "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
         "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
@@ -326,6 +355,17 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[64]) {
         "=r"(x[60]), "=r"(x[61]), "=r"(x[62]), "=r"(x[63])
       : "r"(taddr + 0), "r"(taddr + 32)
       : "memory");
+}
+template <int kN>
+__device__ __forceinline__ void tmem_load_end(uint32_t (&x)[kN]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < kN; ++k) asm volatile("" : "+r"(x[k]));
+}
+template <int kN>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[kN]) {
+  tmem_load_begin(taddr, x);
+  tmem_load_end(x);
 }
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Cols<8>) {
   asm volatile(
@@ -503,7 +543,9 @@ struct Walk {
   // This part's block i, in the order in which they are taken: from the
   // sequence's start, but from its end with a bias by distance, which makes
   // the last rows' exponents the largest: the references then move at the
-  // tile's first block only (in the other order, at almost every block).
+  // tile's first block only. 23.7 against 24.5 us in this order for a tree of
+  // 26 over 8 ragged sequences of up to 3001 rows (e4m3, 64 dims), 10.1 against
+  // 10.5 for a chain of 3 over 3 of 1003 (bf16).
   __device__ __forceinline__ int at(int i) const { return blk + (backward ? n_here - 1 - i : i); }
   __device__ __forceinline__ int row(int i) const { return (first + at(i)) * kBlk; }
   __device__ __forceinline__ bool clean(int i) const { return at(i) >= clean_lo && at(i) < clean_hi; }
@@ -720,8 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v16_empty = [&](int s) { return bars2 + 8u * (uint32_t)(10 + s); };
   // One per block parity: the softmax takes note of every phase of each.
   auto o_done = [&](int s) { return bars2 + 8u * (uint32_t)(12 + s); };
-  const uint32_t drained = bars2 + 8u * 14;
-  uint8_t* const words = smem_raw + (bars2 + 8u * 16 - raw);
+  auto s_empty = [&](int s) { return bars2 + 8u * (uint32_t)(14 + s); };
+  const uint32_t drained = bars2 + 8u * 16;
+  uint8_t* const words = smem_raw + (bars2 + 8u * 18 - raw);
   volatile int* const abort = reinterpret_cast<volatile int*>(words);
   volatile int* const odd = abort + 1;                     // a value that is no number was held back
   volatile uint32_t* const tmem_slot = reinterpret_cast<volatile uint32_t*>(words) + 2;
@@ -737,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
+      mbar_init(s_empty(s), kSoftWarps);
       mbar_init(o_done(s), 1);
       mbar_init(p_full(s), kSoftWarps);
       mbar_init(q_full(s), kE4m3 ? kAuxWarps : 1);
@@ -842,8 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qd = q_desc + (uint64_t)((uint32_t)(qs * S::kQBytes) >> 4);
       for (int i = 0; i < w.n_here; ++i, ++n) {
         if (!(ok = warp_wait(k_full(s), ph))) break;
-        // the buffer's previous scores have been read
-        if (n >= 2 && !(ok = warp_wait(p_full(n & 1), ((n - 2) >> 1) & 1))) break;
+        // the buffer's previous scores are in the softmax's registers
+        if (n >= 2 && !(ok = warp_wait(s_empty(n & 1), ((n - 2) >> 1) & 1))) break;
         tc_fence_after();
         const uint64_t kd = k_desc + (uint64_t)((uint32_t)(s * S::kSlotBytes) >> 4);
         const uint32_t d = tmem + S::kColS + (n & 1) * kBlk;
@@ -934,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t wv[kD / 2];
 #pragma unroll
           for (int c = 0; c < kD / 8; ++c) {
-            const uint4 v = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 v = mine ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
             wv[4 * c] = v.x;
             wv[4 * c + 1] = v.y;
             wv[4 * c + 2] = v.z;
@@ -981,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = e / kCh, c = e % kCh;
             uint4 val = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows)
-              val = __ldg(reinterpret_cast<const uint4*>(
+              val = __ldcg(reinterpret_cast<const uint4*>(
                   A.q + ((size_t)t.b * A.n_new + pos0 + r / A.G) * A.q_stride +
                   (size_t)(t.h * A.G + r % A.G) * kD + c * 8));
             const uint32_t wv[4] = {val.x, val.y, val.z, val.w};
@@ -1031,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int copy = 0; copy < S::kCopies; ++copy)
                 sts32(q_tab + (copy * kRP + r) * 4, fine ? (uint32_t)(127 + down) << 23 : 0x7fffffffu);
           }
-  fence_proxy_async_smem();
+          fence_proxy_async_smem();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full(0));
@@ -1165,13 +1209,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------- softmax --
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);      // this warp's lanes
     const int lg = warp * 32 + lane, row = lg % kRP, copy = warp * 32 / kRP;
-    // A lane's keys of a block: at once up to 64, in pieces of 32 above (a
-    // piece's scores are read twice then, rather than held).
-    constexpr int kPiece = kKpl <= 64 ? kKpl : 32, kPieces = kKpl / kPiece;
+    static_assert(kKpl >= 16 && kKpl <= 64, "a lane's scores of a block stay in registers");
     constexpr int kSubKeys = kKpl < 32 ? kKpl : 32, kSubs = kKpl / kSubKeys;   // runs with one scale
+    constexpr int kRun = 16, kRuns = kExtra ? kKpl / kRun : 1;                 // runs with one bias start
     bool dead = false;                   // a wait ran out: keep to the barriers, compute nothing
     bool noted = false;
     uint32_t n = 0, nt = 0;
+    // A test of a barrier ahead of its wait, which costs 200 cycles even when
+    // it has nothing to wait for.
+    bool s_ready = false;                // of block n's scores
+    bool p_stored = false;               // block n - 1's probabilities are on their way
+    auto send_p = [&]() {
+      if (!p_stored) return;
+      tmem_wait_store();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full((n - 1) & 1));
+      p_stored = false;
+    };
     if constexpr (S::kCopies > 1) {
       const uint32_t zero[32] = {};
 #pragma unroll
@@ -1205,7 +1260,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (dep - (int)lds32(tree + 128 * 16 + (32 * k + a) * 4) >= A.window) sight.v[k] &= ~(1u << a);
       }
       sts32(place_tab + lg * 4, (uint32_t)(idx * A.Hq + w.h * A.G + gq));
+      // Cap and bias: key k of a run adds kb[k], the run's start adds to all.
       const float slope = kExtra && A.slopes ? A.slopes[w.h * A.G + gq] * kLog2e : 0.f;
+      const float cap_log2e = A.cap * kLog2e;
+      float kb[kExtra ? kRun : 1];
+      if constexpr (kExtra) {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) kb[k] = fmaf(slope, (float)k, cap_log2e);
+      }
       const int key0 = copy * kKpl;                                // this copy's first key of a block
       const float* ks = nullptr;
       const float* vs = nullptr;
@@ -1215,8 +1277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < kSubs; ++x) {
             const int jj = j + x * kSubKeys;
-            sk_next[x] = jj < w.L ? __ldg(ks + jj / SPECDEC_KV8_BLOCK) : 1.f;
-            sv_next[x] = jj < w.L ? __ldg(vs + jj / SPECDEC_KV8_BLOCK) : 1.f;
+            sk_next[x] = jj < w.L ? __ldcg(ks + jj / SPECDEC_KV8_BLOCK) : 1.f;
+            sv_next[x] = jj < w.L ? __ldcg(vs + jj / SPECDEC_KV8_BLOCK) : 1.f;
           }
         }
       };
@@ -1251,70 +1313,73 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (kE4m3 && ib + 1 < w.n_here) load_scales(w.row(ib + 1) + key0);
-        if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
+        // The last block's probabilities are announced while this one's
+        // scores come in, or before a wait for them.
+        if (__builtin_expect(!__all_sync(0xffffffffu, s_ready), 0)) {
+          send_p();
+          if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
+        }
         if (dead) continue;
         tc_fence_after();
-        const uint32_t from = tl + S::kColS + (n & 1) * kBlk + key0;
         union {
-          uint32_t u[kPiece];
-          float f[kPiece];
+          uint32_t u[kKpl];
+          float f[kKpl];
         } x;
+        tmem_load_begin(tl + S::kColS + (n & 1) * kBlk + key0, x.u);
+        send_p();
+        tmem_load_end(x.u);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty(n & 1));
         // ---- masks, cap and bias; the lane's largest exponent ----
-        float top = -INFINITY;
+        float top = -INFINITY, at[kRuns];
+        if constexpr (kExtra) {
+          if (A.cap > 0.f) {
 #pragma unroll
-        for (int pc = 0; pc < kPieces; ++pc) {
-          tmem_load(from + pc * kPiece, x.u);
+            for (int k = 0; k < kKpl; ++k)
+              x.f[k] = capped(x.f[k] * (cs[k / kSubKeys] * A.cap_exp), cap_log2e, kb[k % kRun]);
+          } else {
 #pragma unroll
-          for (int sub = 0; sub < kPiece / kSubKeys; ++sub) {
-            float* const y = x.f + sub * kSubKeys;
-            const int xs = pc * (kPiece / kSubKeys) + sub, js = j0 + xs * kSubKeys;
-            if constexpr (kExtra) {
-              // bias slope * (pos_j - pos_i): rows before the new ones stand at
-              // their index, so do a chain's; tree nodes stand at their depth
-              const bool linear = A.slopes && (!A.tree || js + kSubKeys <= P0);
-              const float at0 = lv[xs] + (linear ? slope * (float)(js - P0 - dep) : 0.f);
-              if (A.cap > 0.f) {
-                // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
-                const float in = cs[xs] * A.cap_exp, out = -2.f * A.cap * kLog2e, add = A.cap * kLog2e;
-#pragma unroll
-                for (int k = 0; k < kSubKeys; ++k) y[k] = fmaf(out, rcp(1.f + ex2(y[k] * in)), add) + at0;
-              } else {
-#pragma unroll
-                for (int k = 0; k < kSubKeys; k += 2) fma2(y[k], y[k + 1], cs[xs] * kLog2e, at0);
-              }
-              if (linear) {
-#pragma unroll
-                for (int k = 0; k < kSubKeys; k += 2) acc2(y[k], y[k + 1], (float)k, (float)(k + 1), slope);
-              } else if (A.slopes) {
-#pragma unroll
-                for (int k = 0; k < kSubKeys; ++k) {
-                  int pj = js + k - P0;
-                  if (pj >= 0) pj = (int)lds32(tree + 128 * 16 + min(pj, A.n_new - 1) * 4);
-                  y[k] = fmaf(slope, (float)(pj - dep), y[k]);
-                }
-              }
+            for (int k = 0; k < kKpl; k += 2) {
+              const float c = cs[k / kSubKeys] * kLog2e;
+              fma2(x.f[k], x.f[k + 1], c, c, kb[k % kRun], kb[k % kRun + 1]);
             }
-            if (!clean) {
-              const uint32_t m = sight.mask(js);
-#pragma unroll
-              for (int k = 0; k < kSubKeys; ++k) y[k] = (m >> k) & 1u ? y[k] : -INFINITY;
-            }
-            float t0 = max3(y[0], y[1], y[2]), t1 = max3(y[3], y[4], y[5]);
-#pragma unroll
-            for (int k = 6; k + 3 < kSubKeys; k += 4) {
-              t0 = max3(t0, y[k], y[k + 1]);
-              t1 = max3(t1, y[k + 2], y[k + 3]);
-            }
-            t0 = max3(t0, y[kSubKeys - 2], y[kSubKeys - 1]);
-            t0 = fmaxf(t0, t1);
-            top = fmaxf(top, kExtra ? t0 : fmaf(t0, cs[xs], lv[xs]));
           }
-          if (kPieces > 1 && (kExtra || !clean)) tmem_store(from + pc * kPiece, x.u, Cols<kPiece>{});
+          // bias slope * (pos_j - pos_i), with rows at their index
+#pragma unroll
+          for (int run = 0; run < kRuns; ++run)
+            at[run] = fmaf(slope, (float)(j0 + run * kRun - P0 - dep), lv[run * kRun / kSubKeys]);
         }
-        if (kPieces > 1 && (kExtra || !clean)) tmem_wait_store();
+        if (__builtin_expect(!clean, 0)) {
+          if (kExtra && A.tree && A.slopes) {
+            // a tree's nodes stand at their depth instead
+#pragma unroll
+            for (int k = 0; k < kKpl; ++k) {
+              const int jn = j0 + k - P0;
+              if (jn >= 0 && jn < A.n_new)
+                x.f[k] = fmaf(slope, (float)((int)lds32(tree + 128 * 16 + jn * 4) - jn), x.f[k]);
+            }
+          }
+#pragma unroll
+          for (int sub = 0; sub < kSubs; ++sub) {
+            const uint32_t m = sight.mask(j0 + sub * kSubKeys);
+#pragma unroll
+            for (int k = 0; k < kSubKeys; ++k)
+              x.f[sub * kSubKeys + k] = (m >> k) & 1u ? x.f[sub * kSubKeys + k] : -INFINITY;
+          }
+        }
+        if constexpr (!kExtra) {
+#pragma unroll
+          for (int sub = 0; sub < kSubs; ++sub)
+            top = fmaxf(top, fmaf(largest<kSubKeys>(x.f + sub * kSubKeys), cs[sub], lv[sub]));
+        }
+        if constexpr (kExtra) {
+#pragma unroll
+          for (int run = 0; run < kRuns; ++run) top = fmaxf(top, largest<kRun>(x.f + run * kRun) + at[run]);
+        }
         // ---- the reference follows the maximum when it has to ----
         const bool need = mine && top > m_ref + kHeadroom;
-        if (__any_sync(0xffffffffu, need)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
           const float to = need ? top : m_ref;
           const float alpha = need ? ex2(m_ref - to) : 1.f;
           l *= alpha;
@@ -1342,51 +1407,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - (kE4m3 ? 7.f : 0.f);
         // Exponents of 2^20 and more are rounded before the subtraction, as the
         // reference was: a fused one would bring out the reference's rounding.
-        const bool large = !kExtra && __any_sync(0xffffffffu, fabsf(mu) >= 1048576.f);
+        float af[kSubs], bf[kRuns > kSubs ? kRuns : kSubs];    // exponent - reference = score * af + bf
 #pragma unroll
-        for (int pc = 0; pc < kPieces; ++pc) {
-          if (kPieces > 1) tmem_load(from + pc * kPiece, x.u);
-          uint32_t pk[kPiece / 2];
+        for (int sub = 0; sub < kSubs; ++sub) af[sub] = kExtra ? 1.f : cs[sub];
 #pragma unroll
-          for (int sub = 0; sub < kPiece / kSubKeys; ++sub) {
-            float* const y = x.f + sub * kSubKeys;
-            const int xs = pc * (kPiece / kSubKeys) + sub;
-            float s0 = 0.f, s1 = 0.f;
+        for (int run = 0; run < (kExtra ? kRuns : kSubs); ++run) bf[run] = (kExtra ? at[run] : lv[run]) - mu;
+        if (__builtin_expect(__any_sync(0xffffffffu, fabsf(mu) >= 1048576.f), 0)) {
 #pragma unroll
-            for (int k = 0; k < kSubKeys; k += 2) {
-              if (!kExtra && !large) {
-                fma2(y[k], y[k + 1], cs[xs], lv[xs] - mu);
-              } else {
-                if (!kExtra) fma2(y[k], y[k + 1], cs[xs], lv[xs]);
-                add2(y[k], y[k + 1], -mu, -mu);
-              }
-              const float p0 = ex2(y[k]), p1 = ex2(y[k + 1]);
-              const uint32_t u = pack2<kE4m3>(p0, p1);
-              pk[(sub * kSubKeys + k) / 2] = u;
-              // The sum takes bf16 weights as rounded: their error then moves
-              // the output by w (v - o) only. The f16 rounding is left out of it.
-              if constexpr (kE4m3)
-                add2(s0, s1, p0, p1);
-              else
-                add2(s0, s1, __uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-            }
-            l = kE4m3 ? fmaf(s0 + s1, inv_sv[xs], l) : l + (s0 + s1);
+          for (int k = 0; k < kKpl; k += 2) {
+            const float b = kExtra ? at[k / kRun % kRuns] : lv[k / kSubKeys];
+            fma2(x.f[k], x.f[k + 1], af[k / kSubKeys], af[k / kSubKeys], b, b);
+            add2(x.f[k], x.f[k + 1], -mu, -mu);
           }
-          // the product that last read this P buffer is done
-          if (pc == 0 && n >= S::kPBufs &&
-              !warp_wait(o_done((n - S::kPBufs) & 1), ((n - S::kPBufs) >> 1) & 1)) {
-            dead = true;
-            break;
-          }
-          tmem_store(tl + S::kColP + (S::kPBufs == 2 ? (n & 1) * (kBlk / 2) : 0) + (key0 + pc * kPiece) / 2, pk,
-                     Cols<kPiece / 2>{});
+#pragma unroll
+          for (int sub = 0; sub < kSubs; ++sub) af[sub] = 1.f;
+#pragma unroll
+          for (int run = 0; run < (kExtra ? kRuns : kSubs); ++run) bf[run] = 0.f;
         }
+        uint32_t pk[kKpl / 2];
+        bool p_free = n < S::kPBufs;         // the product that last read this P buffer is done
+        s_ready = false;
+#pragma unroll
+        for (int xs = 0; xs < kSubs; ++xs) {
+          float* const y = x.f + xs * kSubKeys;
+          if (xs == 0) {
+            if (ib + 1 < w.n_here) s_ready = mbar_test(s_full((n + 1) & 1), ((n + 1) >> 1) & 1);
+            if (!p_free) p_free = mbar_test(o_done((n - S::kPBufs) & 1), ((n - S::kPBufs) >> 1) & 1);
+          }
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int k = 0; k < kSubKeys; k += 2) {
+            if constexpr (kExtra) {
+              const float b = bf[(xs * kSubKeys + k) / kRun % kRuns];
+              add2(y[k], y[k + 1], b, b);
+            } else {
+              fma2(y[k], y[k + 1], af[xs], af[xs], bf[xs], bf[xs]);
+            }
+            const float p0 = ex2(y[k]), p1 = ex2(y[k + 1]);
+            const uint32_t u = pack2<kE4m3>(p0, p1);
+            pk[(xs * kSubKeys + k) / 2] = u;
+            // The sum takes bf16 weights as rounded: their error then moves
+            // the output by w (v - o) only. The f16 rounding is left out of it.
+            if constexpr (kE4m3)
+              add2(s0, s1, p0, p1);
+            else
+              add2(s0, s1, __uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+          }
+          l = kE4m3 ? fmaf(s0 + s1, inv_sv[xs], l) : l + (s0 + s1);
+        }
+        if (__builtin_expect(!__all_sync(0xffffffffu, p_free), 0) &&
+            !warp_wait(o_done((n - S::kPBufs) & 1), ((n - S::kPBufs) >> 1) & 1))
+          dead = true;
         if (dead) continue;
-        tmem_wait_store();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(n & 1));
+        tmem_store(tl + S::kColP + (S::kPBufs == 2 ? (n & 1) * (kBlk / 2) : 0) + key0 / 2, pk, Cols<kKpl / 2>{});
+        p_stored = true;
       }
+      send_p();
 
       // ---- the tile's output, or this part's share of it ----
       const bool whole = w.blk == 0 && w.n_here == w.nb;
@@ -1463,22 +1539,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r0 = (S::kCopies > 1 ? warp * 4 : warp * 32) + (lane >> 3);
         __nv_bfloat16* const out = A.out + (size_t)w.b * A.n_new * A.Hq * kD + c0 + c4;
         float* const part = A.part_o + slot * kRP * kD + c0 + c4;
+        constexpr int kWrites = (S::kCopies > 1 ? kRP : 32) / kRowStep;
+        float4 v[kWrites];
+        uint32_t at[kWrites];
 #pragma unroll
-        for (int x = 0; x < (S::kCopies > 1 ? kRP : 32) / kRowStep; ++x) {
-          const int r = r0 + x * kRowStep;
-          float4 v = lds128f(stage + r * kStagePitch + c4 * 4);
+        for (int x = 0; x < kWrites; ++x) {
+          v[x] = lds128f(stage + (r0 + x * kRowStep) * kStagePitch + c4 * 4);
+          at[x] = lds32(place_tab + (r0 + x * kRowStep) * 4);
+        }
 #pragma unroll
-          for (int c = 1; c < S::kCopies; ++c) {
-            const float4 y = lds128f(stage + (c * kRP + r) * kStagePitch + c4 * 4);
-            add2(v.x, v.y, y.x, y.y);
-            add2(v.z, v.w, y.z, y.w);
+        for (int c = 1; c < S::kCopies; ++c)
+#pragma unroll
+          for (int x = 0; x < kWrites; ++x) {
+            const float4 y = lds128f(stage + (c * kRP + r0 + x * kRowStep) * kStagePitch + c4 * 4);
+            add2(v[x].x, v[x].y, y.x, y.y);
+            add2(v[x].z, v[x].w, y.z, y.w);
           }
+#pragma unroll
+        for (int x = 0; x < kWrites; ++x) {
+          const int r = r0 + x * kRowStep;
           if (dead || r >= rows_here) continue;
           if (whole)
-            *reinterpret_cast<uint2*>(out + (size_t)lds32(place_tab + r * 4) * kD) =
-                make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+            *reinterpret_cast<uint2*>(out + (size_t)at[x] * kD) =
+                make_uint2(pack2<false>(v[x].x, v[x].y), pack2<false>(v[x].z, v[x].w));
           else
-            *reinterpret_cast<float4*>(part + r * kD) = v;
+            *reinterpret_cast<float4*>(part + r * kD) = v[x];
         }
         if constexpr (S::kCopies > 1)
           named_bar_sync(1, 32 * kSoftWarps);

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       uint32_t wv[kD / 2];
 #pragma unroll
       for (int c = 0; c < kD / 8; ++c) {
-        const uint4 v = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = mine ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
         wv[4 * c] = v.x;
         wv[4 * c + 1] = v.y;
         wv[4 * c + 2] = v.z;
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       const float* vs = A.v_scale + so;
       float sk_next, sv_next;
       auto load_scales = [&](int jw) {
-        sk_next = jw < w.L ? __ldg(ks + jw / SPECDEC_KV8_BLOCK) : 1.f;
-        sv_next = jw < w.L ? __ldg(vs + jw / SPECDEC_KV8_BLOCK) : 1.f;
+        sk_next = jw < w.L ? __ldcg(ks + jw / SPECDEC_KV8_BLOCK) : 1.f;
+        sv_next = jw < w.L ? __ldcg(vs + jw / SPECDEC_KV8_BLOCK) : 1.f;
       };
       load_scales(w.row(0) + warp * 32);
       // The rows that see cache row jj: those that see its new position, or,
@@ -464,10 +464,9 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
               const float4 sl = lds128f(t0 + kRows * 4 + r * 4), dp = lds128f(t0 + 2 * kRows * 4 + r * 4);
               mul2(y[r], y[r + 1], sk, sk);
               mul2(y[r + 2], y[r + 3], sk, sk);
-              if (A.cap > 0.f) {       // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap)))
+              if (A.cap > 0.f) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  y[r + k] = fmaf(-2.f * A.cap * kLog2e, rcp(1.f + ex2(y[r + k] * A.cap_exp)), A.cap * kLog2e);
+                for (int k = 0; k < 4; ++k) y[r + k] = capped(y[r + k] * A.cap_exp, A.cap * kLog2e, A.cap * kLog2e);
               } else {
                 mul2(y[r], y[r + 1], kLog2e, kLog2e);
                 mul2(y[r + 2], y[r + 3], kLog2e, kLog2e);

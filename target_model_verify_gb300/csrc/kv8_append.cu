@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
           src = 0;
         }
       }
-      x[k] = __ldg(reinterpret_cast<const uint4*>(A.src[kv] + ((size_t)b * A.n + src) * A.stride[kv] +
+      x[k] = __ldcg(reinterpret_cast<const uint4*>(A.src[kv] + ((size_t)b * A.n + src) * A.stride[kv] +
                                                   (size_t)h * kD + c * 8));
     }
   }

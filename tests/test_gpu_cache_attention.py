@@ -11,8 +11,7 @@ Tolerance, from the arithmetic. With u = finfo.eps / 2 (bf16 2^-8, f16
     2^-10 / 256, where a row's largest probability is at least 2^2: each of L
     weights is off by at most 2^-20 of that one, the mean by 2^-20 L V (the
     row form's f16 ends at 2^-25 / 2^7 of it, 2^-32 L V). Over the bf16 cache
-    to bf16,
-    whose rounded weights are also what the sum counts, so the mean moves by
+    to bf16, whose rounded weights are also what the sum counts, so the mean moves by
     at most 2^-8 * sum w |v - o| <= 2^-8 * 2 V;
   - scores: products are exact, their sum over D terms runs through D / 16
     tensor-core steps, and the scale, cap, bias and exponent are a few fp32
@@ -157,6 +156,14 @@ def test_options_match_oracle(kind, D, how):
         how["slopes"] = torch.tensor([0.5, 0.25, 0.1, 0.01], device=DEV)
     q, cache, lens = _inputs(kind, D + n, 3, n, 4, 2, D, 310, lens=[310, n, 129])
     _check(kind, q, cache, lens, _call(kind, q, cache, lens, **how), **how)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 1000.0])
+def test_narrow_and_wide_caps(kind, cap):
+    """A cap far below the scores leaves their signs, one far above the scores themselves."""
+    q, cache, lens = _inputs(kind, 21, 2, 3, 4, 2, 128, 290, lens=[290, 100])
+    _check(kind, q, cache, lens, _call(kind, q, cache, lens, softcap=cap), softcap=cap)
 
 
 @pytest.mark.parametrize("kind", KINDS)
