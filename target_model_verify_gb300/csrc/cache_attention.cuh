@@ -1211,6 +1211,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lg = warp * 32 + lane, row = lg % kRP, copy = warp * 32 / kRP;
     static_assert(kKpl >= 16 && kKpl <= 64, "a lane's scores of a block stay in registers");
     constexpr int kSubKeys = kKpl < 32 ? kKpl : 32, kSubs = kKpl / kSubKeys;   // runs with one scale
+    // A block's probabilities are announced while the next one's scores come in
+    // (or before a wait for them) where the softmax is what bounds: 109 against
+    // 120 us for a tree of 26 over 32 x 4096 e4m3 rows. Elsewhere at once, since
+    // V's slot waits for the product: 146 / 152 us for 48 query rows on 64 x
+    // 4096 e4m3 rows, 37.6 / 39.7 for the tree over 8 x 4096 bf16 rows.
+    constexpr bool kDefer = kE4m3 && kRP == 128;
     constexpr int kRun = 16, kRuns = kExtra ? kKpl / kRun : 1;                 // runs with one bias start
     bool dead = false;                   // a wait ran out: keep to the barriers, compute nothing
     bool noted = false;
@@ -1313,10 +1319,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (kE4m3 && ib + 1 < w.n_here) load_scales(w.row(ib + 1) + key0);
-        // e4m3: the last block's probabilities are announced while this one's
-        // scores come in, or before a wait for them. (bf16 values hold their
-        // slots until the product, so there they are announced at once: 37.6
-        // against 39.7 us on the tree of 26 over 8 x 4096 rows.)
         if (__builtin_expect(!__all_sync(0xffffffffu, s_ready), 0)) {
           send_p(n - 1);
           if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
@@ -1463,7 +1465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (dead) continue;
         tmem_store(tl + S::kColP + (S::kPBufs == 2 ? (n & 1) * (kBlk / 2) : 0) + key0 / 2, pk, Cols<kKpl / 2>{});
         p_stored = true;
-        if (!kE4m3) send_p(n);
+        if (!kDefer) send_p(n);
       }
       send_p(n - 1);
 

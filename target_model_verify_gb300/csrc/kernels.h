@@ -224,16 +224,17 @@ constexpr int cache_attn_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 
 // 27.6 us for 20 query rows on 16 ragged bf16 sequences with a window.
 constexpr int cache_attn_block(int D, int lanes) { return D == 256 || lanes == 128 ? 64 : 128; }
 // The form with the cache on the M side (cache_attention_keys.cuh) can take a
-// call with up to 32 query rows per KV head, and does from 256 tiles or 2048
+// call with up to 32 query rows per KV head, and does from 256 tiles or 4096
 // blocks of cache on. Measured, keys against rows form, us a call: 64 x 4096
-// rows 103 / 121, 256 x 128 70 / 100, 64 x 200 29 / 37, 32 x 256 17 / 23;
-// below, its longer way to a tile's first block shows: 1 x 517 14.4 / 12.4,
-// 1 x 8192 21.7 / 18.4, 8 x 512 19.2 / 16.2 (8 KV heads, 20 query rows each).
+// rows 103 / 123, 1 x 131072 57.9 / 61.4, 256 x 128 71 / 98, 64 x 200 28 / 37,
+// 32 x 256 17 / 23; below, its longer way to a tile's first block shows:
+// 1 x 517 13.9 / 12.6, 1 x 32768 29.0 / 27.4, 8 x 4096 30.9 / 28.9, 16 x 2048
+// 32.4 / 30.3 (8 KV heads, 20 query rows each).
 constexpr bool cache_attn_can_key(bool e4m3, int D, int rows) { return e4m3 && D == 128 && rows <= 32; }
 inline bool cache_attn_by_keys(const CacheAttnLaunch& A, int D) {
   const long long tiles = (long long)A.B * A.Hkv * A.n_groups;
   return cache_attn_can_key(true, D, A.group_pos * A.G) &&
-         (tiles >= 256 || tiles * ((A.Lmax + 127) / 128) >= 2048);
+         (tiles >= 256 || tiles * ((A.Lmax + 127) / 128) >= 4096);
 }
 // tmap_q: the queries as a bf16 tensor {D, Hq, n_new, B} with a box of 64
 // dims x G heads x group_pos positions, 128-byte swizzle (bf16 cache only).
