@@ -12,7 +12,12 @@
 // running maximum of y, so weights of every block share one range.
 //
 // Bound: HBM (each K and V row is read once per group of up to 128 query
-// rows).
+// rows). Measured on a GB300 (graph replays; copy peak 6771 GB/s): 64 x 4096
+// bf16 rows, 5 positions, 32 query / 8 KV heads of 128: 161 us for 1074 MB,
+// 0.98 of the copy peak (16 positions: 163 us); a tree of 26 over 8 x 4096:
+// 38 us for 136 MB, where starting, the softmax of 128 lanes and the merge
+// show; the tree over 32 x 4096 e4m3 rows: 109 us for 268 MB, bound by the
+// softmax (one warp per scheduler takes 0.9 us for a lane's 64 scores).
 //
 // Schedule. A tile is a (sequence, KV head, row group), a run of cache blocks
 // as long as its own sequence (or window). A head's tiles are laid end to end

@@ -23,6 +23,12 @@
 // thread may have 168 registers: 0-3 softmax, 4 loads (K and V blocks,
 // queries and row tables, the check of V blocks that not every query sees
 // whole), 5 issues both products.
+//
+// Measured (64 x 4096 rows, 5 positions, 32 query / 8 KV heads): 103 us for
+// 541 MB, 5260 GB/s or 0.78 of the copy peak (the other form: 123 us); DRAM
+// reads are the algorithmic bytes. What is left is the start (6 us until the
+// first block's products), the first block's pass for its references, the
+// SMs' unequal ends and the merge (4 us).
 #pragma once
 
 #include "cache_attention.cuh"

@@ -15,7 +15,11 @@
 // the maximum and the encoding, so they are read once, and no other warp
 // writes that block. Calls of up to kFew new rows keep registers for that
 // many only, and in longer ones two warps share a block (16 rows each), so
-// that more warps are resident (4 x 4096 rows: 8.4 us with one warp).
+// that more warps are resident. Measured (8 KV heads of 128): 2.3 us for one
+// sequence's 5 rows (a launch's latency), 5.1 us for 256 sequences' (7.9 MB),
+// 8.3 us for four ragged prompts of 3206 rows in all (19.7 MB, 2370 GB/s; 8.4
+// us with one warp per block): one wave of short warps, each a chain of three
+// dependent trips to memory.
 #include <cuda_fp16.h>
 
 #include "kernels.h"
