@@ -140,6 +140,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.window = window;
   // at least two parts per head: with more heads than that, a CTA takes them all in turn
   A.head_lanes = 2 * Hkv <= kCacheAttnCtas ? Hkv : 1;
+  A.note_tiles = 0;                          // the launch decides
   A.n_scale = (Lmax + SPECDEC_KV8_BLOCK - 1) / SPECDEC_KV8_BLOCK;
   A.scale = scale > 0.f ? scale : 1.f / std::sqrt((float)D);
   A.cap = softcap;

@@ -27,7 +27,8 @@
 // a row of the cache holds all its heads side by side, DRAM pages are read
 // whole. A tile that lies inside one part is finished by its CTA; of the
 // others every CTA leaves a partial (maximum, sum, unnormalised output), and
-// the first one a note of who shares it, from which combine_kernel merges.
+// the one with its first block a note of who shares it, from which
+// combine_kernel merges.
 // (The last CTA of a tile merging in place, counted in by an atomic, was
 // slower in every case measured, by 1 to 12 us a call: its four warps take
 // the rows one batch after another while the grid waits.)
@@ -556,11 +557,15 @@ struct Walk {
   __device__ __forceinline__ bool clean(int i) const { return at(i) >= clean_lo && at(i) < clean_hi; }
 };
 
-// What the CTA with a shared tile's first block notes for the merge: the
-// sequence (-1: no such tile), KV head and row group, the last part with
-// blocks of it, and which of its own two partials is the tile's.
-__device__ __forceinline__ void write_note(const CacheAttnLaunch& A, int b, int head_group, int last, int slot) {
-  A.notes[blockIdx.x] = make_int4(b, head_group, last, slot);
+// What the CTA with a tile's first block notes for the merge: the sequence
+// (-1: nothing to merge), KV head and row group, the last part with blocks of
+// it, its own part and which of its two partials is the tile's. True if noted.
+__device__ __forceinline__ bool write_note(const CacheAttnLaunch& A, int b, int h, int g, bool whole, int last,
+                                           int slot) {
+  if (whole && !A.note_tiles) return false;
+  A.notes[A.note_tiles ? (b * A.Hkv + h) * A.n_groups + g : blockIdx.x] =
+      make_int4(whole ? -1 : b, h * A.n_groups + g, last, (int)(blockIdx.x / A.head_lanes) * 2 + slot);
+  return true;
 }
 // The part that holds the walk's tile's last unit.
 template <int kBlk>
@@ -577,6 +582,9 @@ __device__ __forceinline__ void zero_empty(const CacheAttnLaunch& A) {
     int first;
     bool bad;
     if (seq_blocks<kBlk>(A, A.seq_lens[b], first, bad) > 0) continue;
+    if (A.note_tiles)
+      for (int e = threadIdx.x; e < A.Hkv * A.n_groups; e += 32 * kSoftWarps)
+        A.notes[b * A.Hkv * A.n_groups + e].x = -1;
     uint4* dst = reinterpret_cast<uint4*>(A.out + (size_t)b * A.n_new * A.Hq * kD);
     const long long chunks = (long long)A.n_new * A.Hq * (kD / 8);
     for (long long e = threadIdx.x; e < chunks; e += 32 * kSoftWarps) dst[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -584,7 +592,7 @@ __device__ __forceinline__ void zero_empty(const CacheAttnLaunch& A) {
 }
 
 // Merges the partials of the tiles that more than one CTA worked on.
-// blockIdx.x = the CTA with the tile's first block, blockIdx.y: rows. `wpr`
+// blockIdx.x = the note, blockIdx.y: rows. `wpr`
 // of the eight warps share the partials of kRows rows, which they take
 // together, so that eight loads are in flight either way.
 template <int kD, int kRP>
@@ -603,7 +611,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
   const int b = note.x, grp = note.y % A.n_groups, h = note.y / A.n_groups;
   const int pos0 = grp * A.group_pos, rows = min(A.group_pos, A.n_new - pos0) * A.G;
   const int r0 = (blockIdx.y * (8 / wpr) + warp / wpr) * kRows, slice = warp % wpr;
-  const int first = blockIdx.x / A.head_lanes, head_lane = blockIdx.x % A.head_lanes;
+  const int first = note.w >> 1, head_lane = A.head_lanes > 1 ? h : 0;
   float acc[kRows][kPer], l[kRows], M[kRows];
 #pragma unroll
   for (int y = 0; y < kRows; ++y) {
@@ -617,7 +625,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
     for (int cb = first; cb <= note.z; cb += 32) {
       const int c = min(cb + lane, note.z), here = min(32, note.z - cb + 1);
       const bool none = cb + lane > note.z;
-      const int slot = 2 * (c * A.head_lanes + head_lane) + (c == first ? note.w : 0);
+      const int slot = 2 * (c * A.head_lanes + head_lane) + (c == first ? note.w & 1 : 0);
       float2 ml[kRows];
       float wgt[kRows];
 #pragma unroll
@@ -696,6 +704,13 @@ inline int cache_attn_parts(const CacheAttnLaunch& A, int ctas, long long most) 
   return (int)(by_work < by_ctas ? by_work : by_ctas);
 }
 
+// A note per tile where there are no more tiles than CTAs (the merge then has
+// fewer CTAs that find nothing to do), else a note per CTA.
+inline int note_tiles(const CacheAttnLaunch& A, int parts) {
+  const long long tiles = (long long)A.B * A.Hkv * A.n_groups;
+  return tiles <= (long long)parts * A.head_lanes ? (int)tiles : 0;
+}
+
 // The merge, after the attention kernel on the same stream. Warps per row:
 // as many as a tile has parts when the parts are dealt out evenly, at most 8.
 template <int kD, int kRP>
@@ -704,7 +719,7 @@ cudaError_t launch_combine(const CacheAttnLaunch& A, int parts, cudaLaunchConfig
   const long long each = parts / tiles;
   const int wpr = each >= 8 ? 8 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
   const int per_cta = 8 / wpr * MergeShape<kD, kRP>::kRows;
-  cfg.gridDim = dim3(parts * A.head_lanes, (A.group_pos * A.G + per_cta - 1) / per_cta);
+  cfg.gridDim = dim3(A.note_tiles ? A.note_tiles : parts * A.head_lanes, (A.group_pos * A.G + per_cta - 1) / per_cta);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, combine_kernel<kD, kRP>, A, wpr);
@@ -1507,7 +1522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!dead) {
           uint32_t u[32];
           tmem_load(tl + S::kColO + c0, u);
-          if (has_odd) {
+          if (__builtin_expect(has_odd, 0)) {
             // Infinities and NaN that were held back from the product (rare),
             // for the rows that see them.
             for (int ib = 0; ib < w.n_here; ++ib) {
@@ -1565,27 +1580,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             add2(v[x].x, v[x].y, y.x, y.y);
             add2(v[x].z, v[x].w, y.z, y.w);
           }
+        if (!dead && whole) {
 #pragma unroll
-        for (int x = 0; x < kWrites; ++x) {
-          const int r = r0 + x * kRowStep;
-          if (dead || r >= rows_here) continue;
-          if (whole)
-            *reinterpret_cast<uint2*>(out + (size_t)at[x] * kD) =
-                make_uint2(pack2<false>(v[x].x, v[x].y), pack2<false>(v[x].z, v[x].w));
-          else
-            *reinterpret_cast<float4*>(part + r * kD) = v[x];
+          for (int x = 0; x < kWrites; ++x)
+            if (r0 + x * kRowStep < rows_here)
+              *reinterpret_cast<uint2*>(out + (size_t)at[x] * kD) =
+                  make_uint2(pack2<false>(v[x].x, v[x].y), pack2<false>(v[x].z, v[x].w));
+        } else if (!dead) {
+#pragma unroll
+          for (int x = 0; x < kWrites; ++x)
+            if (r0 + x * kRowStep < rows_here) *reinterpret_cast<float4*>(part + (r0 + x * kRowStep) * kD) = v[x];
         }
         if constexpr (S::kCopies > 1)
           named_bar_sync(1, 32 * kSoftWarps);
         else
           __syncwarp();
       }
-      if (!whole && w.blk == 0 && threadIdx.x == 0) {
-        write_note(A, w.b, w.h * A.n_groups + w.g, last_part(w, place[4], place[5]), (int)(slot & 1));
-        noted = true;
-      }
+      if (w.blk == 0 && threadIdx.x == 0)
+        noted |= write_note(A, w.b, w.h, w.g, whole, last_part(w, place[4], place[5]), (int)(slot & 1));
     }
-    if (!noted && threadIdx.x == 0) write_note(A, -1, 0, 0, 0);
+    if (!noted && !A.note_tiles && threadIdx.x == 0) A.notes[blockIdx.x].x = -1;
     zero_empty<kD, kBlk>(A);
   }
   tc_fence_before();
@@ -1628,9 +1642,11 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<kE4m3, kD, kRP, kExtra>, A, tk, tv, tq);
+  CacheAttnLaunch L = A;
+  L.note_tiles = note_tiles(A, parts);
+  e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<kE4m3, kD, kRP, kExtra>, L, tk, tv, tq);
   if (e != cudaSuccess) return e;
-  return launch_combine<kD, kRP>(A, parts, cfg);
+  return launch_combine<kD, kRP>(L, parts, cfg);
 }
 
 template <bool kE4m3, int kD, int kRP>

@@ -680,12 +680,10 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       if (lane == 0) mbar_arrive(q_empty(qs));
       tc_fence_before();
       named_bar_sync(1, 32 * kSoftWarps);    // the tables are free for the next tile
-      if (!whole && w.blk == 0 && threadIdx.x == 0) {
-        write_note(A, w.b, w.h * A.n_groups + w.g, last_part(w, place[4], place[5]), (int)(slot & 1));
-        noted = true;
-      }
+      if (w.blk == 0 && threadIdx.x == 0)
+        noted |= write_note(A, w.b, w.h, w.g, whole, last_part(w, place[4], place[5]), (int)(slot & 1));
     }
-    if (!noted && threadIdx.x == 0) write_note(A, -1, 0, 0, 0);
+    if (!noted && !A.note_tiles && threadIdx.x == 0) A.notes[blockIdx.x].x = -1;
     zero_empty<kD, kBlk>(A);
   }
   tc_fence_before();
@@ -725,9 +723,11 @@ cudaError_t launch_keys(const CacheAttnLaunch& A, const CUtensorMap& tk, const C
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cache_attn_keys_kernel<kExtra>, A, tk, tv);
+  CacheAttnLaunch L = A;
+  L.note_tiles = note_tiles(A, parts);
+  e = cudaLaunchKernelEx(&cfg, cache_attn_keys_kernel<kExtra>, L, tk, tv);
   if (e != cudaSuccess) return e;
-  return launch_combine<kKeyD, kKeyRows>(A, parts, cfg);
+  return launch_combine<kKeyD, kKeyRows>(L, parts, cfg);
 }
 
 }  // namespace cache_attn

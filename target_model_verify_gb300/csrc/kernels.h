@@ -199,6 +199,7 @@ struct CacheAttnLaunch {
   int max_depth;                     // of the new positions (n_new - 1 for a chain)
   int n_scale;                       // scales per (sequence, KV head)
   int head_lanes;                    // CTAs beside each other on a part: Hkv, or 1
+  int note_tiles;                    // a note per tile (this many), or 0: per CTA
   float scale, cap, cap_exp;         // cap_exp = 2 log2(e) / cap
   long long q_stride;                // elements from one position's queries to the next's
   const __nv_bfloat16* q;            // [B, n_new, Hq, D]
@@ -210,7 +211,7 @@ struct CacheAttnLaunch {
   __nv_bfloat16* out;                // [B, n_new, Hq, D]
   float* part_o;                     // [2 CTAs, rows, D]
   float* part_ml;                    // [2 CTAs, rows, 2]
-  int4* notes;                       // [CTAs] the shared tile whose first block a CTA has (write_note)
+  int4* notes;                       // [tiles or CTAs] who shares a tile (write_note)
   int* status;
   uint32_t anc[SPECDEC_MAX_TREE_NODES][4];   // bit a of row i: node i sees node a
   uint8_t depth[SPECDEC_MAX_TREE_NODES];
