@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       tc_fence_before();
       named_bar_sync(1, 32 * kSoftWarps);    // the tables are free for the next tile
       if (w.blk == 0 && threadIdx.x == 0)
-        noted |= write_note(A, w.b, w.h, w.g, whole, last_part(w, place[4], place[5]), (int)(slot & 1));
+        noted |= write_note(A, w.b, w.h, w.g, whole, whole ? 0 : last_part(w, place[4], place[5]), (int)(slot & 1));
     }
     if (!noted && !A.note_tiles && threadIdx.x == 0) A.notes[blockIdx.x].x = -1;
     zero_empty<kD, kBlk>(A);
