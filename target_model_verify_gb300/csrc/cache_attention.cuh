@@ -308,27 +308,28 @@ __device__ __forceinline__ float4 lds128f(uint32_t a) {
 }
 
 // Tensor memory: each thread of a warp reads or writes consecutive 32-bit
-// columns of its lane. Loads return with the values there,
-// but tmem_load_begin's only after tmem_load_end.
+// columns of its lane. Loads return with the values there.
 template <int kN>
 struct Cols {};
-__device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[16]) {
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
-      "}, [%16];"
+      "}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
         "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
         "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
       : "r"(taddr + 0)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[32]) {
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
-      "}, [%32];"
+      "}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
         "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
         "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
@@ -338,7 +339,7 @@ __device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[32
       : "r"(taddr + 0)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[64]) {
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -347,7 +348,8 @@ __device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[64
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
       "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
-      "}, [%65];"
+      "}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
         "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
         "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
@@ -361,17 +363,6 @@ __device__ __forceinline__ void tmem_load_begin(uint32_t taddr, uint32_t (&x)[64
         "=r"(x[60]), "=r"(x[61]), "=r"(x[62]), "=r"(x[63])
       : "r"(taddr + 0), "r"(taddr + 32)
       : "memory");
-}
-template <int kN>
-__device__ __forceinline__ void tmem_load_end(uint32_t (&x)[kN]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int k = 0; k < kN; ++k) asm volatile("" : "+r"(x[k]));
-}
-template <int kN>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[kN]) {
-  tmem_load_begin(taddr, x);
-  tmem_load_end(x);
 }
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Cols<8>) {
   asm volatile(
@@ -1238,12 +1229,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lg = warp * 32 + lane, row = lg % kRP, copy = warp * 32 / kRP;
     static_assert(kKpl >= 16 && kKpl <= 64, "a lane's scores of a block stay in registers");
     constexpr int kSubKeys = kKpl < 32 ? kKpl : 32, kSubs = kKpl / kSubKeys;   // runs with one scale
-    // A block's probabilities are announced while the next one's scores come in
-    // (or before a wait for them) where the softmax is what bounds: 109 against
-    // 120 us for a tree of 26 over 32 x 4096 e4m3 rows. Elsewhere at once, since
-    // V's slot waits for the product: 146 / 152 us for 48 query rows on 64 x
-    // 4096 e4m3 rows, 37.6 / 39.7 for the tree over 8 x 4096 bf16 rows.
-    constexpr bool kDefer = kE4m3 && kRP == 128;
     constexpr int kRun = 16, kRuns = kExtra ? kKpl / kRun : 1;                 // runs with one bias start
     bool dead = false;                   // a wait ran out: keep to the barriers, compute nothing
     bool noted = false;
@@ -1251,15 +1236,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A test of a barrier ahead of its wait, which costs 200 cycles even when
     // it has nothing to wait for.
     bool s_ready = false;                // of block n's scores
-    bool p_stored = false;               // the last block's probabilities are on their way
-    auto send_p = [&](uint32_t of) {
-      if (!p_stored) return;
-      tmem_wait_store();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(of & 1));
-      p_stored = false;
-    };
     if constexpr (S::kCopies > 1) {
       const uint32_t zero[32] = {};
 #pragma unroll
@@ -1346,19 +1322,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (kE4m3 && ib + 1 < w.n_here) load_scales(w.row(ib + 1) + key0);
-        if (__builtin_expect(!__all_sync(0xffffffffu, s_ready), 0)) {
-          send_p(n - 1);
-          if (!dead && !warp_wait(s_full(n & 1), (n >> 1) & 1)) dead = true;
-        }
+        if (__builtin_expect(!__all_sync(0xffffffffu, s_ready), 0) && !dead &&
+            !warp_wait(s_full(n & 1), (n >> 1) & 1))
+          dead = true;
         if (dead) continue;
         tc_fence_after();
         union {
           uint32_t u[kKpl];
           float f[kKpl];
         } x;
-        tmem_load_begin(tl + S::kColS + (n & 1) * kBlk + key0, x.u);
-        send_p(n - 1);
-        tmem_load_end(x.u);
+        tmem_load(tl + S::kColS + (n & 1) * kBlk + key0, x.u);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty(n & 1));
@@ -1491,10 +1464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           dead = true;
         if (dead) continue;
         tmem_store(tl + S::kColP + (S::kPBufs == 2 ? (n & 1) * (kBlk / 2) : 0) + key0 / 2, pk, Cols<kKpl / 2>{});
-        p_stored = true;
-        if (!kDefer) send_p(n);
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(n & 1));
       }
-      send_p(n - 1);
 
       // ---- the tile's output, or this part's share of it ----
       const bool whole = w.blk == 0 && w.n_here == w.nb;
