@@ -15,9 +15,10 @@
 // rows). Measured on a GB300 (graph replays; copy peak 6771 GB/s): 64 x 4096
 // bf16 rows, 5 positions, 32 query / 8 KV heads of 128: 161 us for 1074 MB,
 // 0.98 of the copy peak (16 positions: 163 us); a tree of 26 over 8 x 4096:
-// 38 us for 136 MB, where starting, the softmax of 128 lanes and the merge
-// show; the tree over 32 x 4096 e4m3 rows: 109 us for 268 MB, bound by the
-// softmax (one warp per scheduler takes 0.9 us for a lane's 64 scores).
+// 37 us for 136 MB, where starting, the softmax of 128 lanes and the merge
+// show; the tree over 32 x 4096 e4m3 rows: 110 us for 268 MB (130 with a
+// bias), bound by the softmax (one warp per scheduler takes 0.9 us for a
+// lane's 64 scores).
 //
 // Schedule. A tile is a (sequence, KV head, row group), a run of cache blocks
 // as long as its own sequence (or window). A head's tiles are laid end to end
@@ -52,7 +53,10 @@
 //     columns stay zero, so the copies are independent online softmaxes,
 //     merged once per tile. The reference M moves only when a row's maximum
 //     passes it by 2^8 (the exponents have that headroom), so the output in
-//     tensor memory is rarely rescaled.
+//     tensor memory is rarely rescaled. Code for rare blocks (masks, moving
+//     references, huge exponents) stands outside the loop's line: the loop is
+//     longer than the nearest instruction cache, and jumps over unrolled code
+//     cost 500 cycles a block with a bias.
 //   O += P V: P from tensor memory, V the MN-major operand, kind::f16. e4m3
 //     values are widened to f16 (exact) by the auxiliary warps into a second
 //     shared-memory tile, since P needs f16's 11 bits and both operands share
@@ -550,13 +554,11 @@ struct Walk {
 
 // What the CTA with a tile's first block notes for the merge: the sequence
 // (-1: nothing to merge), KV head and row group, the last part with blocks of
-// it, its own part and which of its two partials is the tile's. True if noted.
-__device__ __forceinline__ bool write_note(const CacheAttnLaunch& A, int b, int h, int g, bool whole, int last,
+// it, its own part and which of its two partials is the tile's.
+__device__ __forceinline__ void write_note(const CacheAttnLaunch& A, int b, int h, int g, bool whole, int last,
                                            int slot) {
-  if (whole && !A.note_tiles) return false;
   A.notes[A.note_tiles ? (b * A.Hkv + h) * A.n_groups + g : blockIdx.x] =
       make_int4(whole ? -1 : b, h * A.n_groups + g, last, (int)(blockIdx.x / A.head_lanes) * 2 + slot);
-  return true;
 }
 // The part that holds the walk's tile's last unit.
 template <int kBlk>
@@ -1577,8 +1579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           __syncwarp();
       }
-      if (w.blk == 0 && threadIdx.x == 0)
-        noted |= write_note(A, w.b, w.h, w.g, whole, whole ? 0 : last_part(w, place[4], place[5]), (int)(slot & 1));
+      if (w.blk == 0 && (!whole || A.note_tiles) && threadIdx.x == 0) {
+        write_note(A, w.b, w.h, w.g, whole, last_part(w, place[4], place[5]), (int)(slot & 1));
+        noted = true;
+      }
     }
     if (!noted && !A.note_tiles && threadIdx.x == 0) A.notes[blockIdx.x].x = -1;
     zero_empty<kD, kBlk>(A);

@@ -24,8 +24,8 @@
 // queries and row tables, the check of V blocks that not every query sees
 // whole), 5 issues both products.
 //
-// Measured (64 x 4096 rows, 5 positions, 32 query / 8 KV heads): 103 us for
-// 541 MB, 5260 GB/s or 0.78 of the copy peak (the other form: 123 us); DRAM
+// Measured (64 x 4096 rows, 5 positions, 32 query / 8 KV heads): 104 us for
+// 543 MB, 5220 GB/s or 0.77 of the copy peak (the other form: 122 us); DRAM
 // reads are the algorithmic bytes. What is left is the start (6 us until the
 // first block's products), the first block's pass for its references, the
 // SMs' unequal ends and the merge (4 us).
@@ -680,8 +680,10 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       if (lane == 0) mbar_arrive(q_empty(qs));
       tc_fence_before();
       named_bar_sync(1, 32 * kSoftWarps);    // the tables are free for the next tile
-      if (w.blk == 0 && threadIdx.x == 0)
-        noted |= write_note(A, w.b, w.h, w.g, whole, whole ? 0 : last_part(w, place[4], place[5]), (int)(slot & 1));
+      if (w.blk == 0 && (!whole || A.note_tiles) && threadIdx.x == 0) {
+        write_note(A, w.b, w.h, w.g, whole, last_part(w, place[4], place[5]), (int)(slot & 1));
+        noted = true;
+      }
     }
     if (!noted && !A.note_tiles && threadIdx.x == 0) A.notes[blockIdx.x].x = -1;
     zero_empty<kD, kBlk>(A);

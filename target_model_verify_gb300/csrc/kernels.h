@@ -220,17 +220,18 @@ struct CacheAttnLaunch {
 constexpr int cache_attn_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 // Keys per block (and TMA box): 128, but 64 at 256 dims (shared memory) and
 // for 128 lanes of query rows, where a lane holds a score of every key. 64
-// against 128 keys there: 38.3 / 40.9 us on a 26-node tree over 8 x 4096 bf16
-// rows, 127 / 139 over 32 x 4096 e4m3 rows. With fewer lanes 128 pay: 30.2 /
+// against 128 keys there (when both were built, before scores were released
+// early): 38.3 / 40.9 us on a 26-node tree over 8 x 4096 bf16 rows, 127 / 139
+// over 32 x 4096 e4m3 rows. With fewer lanes 128 pay: 30.2 /
 // 27.6 us for 20 query rows on 16 ragged bf16 sequences with a window.
 constexpr int cache_attn_block(int D, int lanes) { return D == 256 || lanes == 128 ? 64 : 128; }
 // The form with the cache on the M side (cache_attention_keys.cuh) can take a
 // call with up to 32 query rows per KV head, and does from 256 tiles or 4096
 // blocks of cache on. Measured, keys against rows form, us a call: 64 x 4096
-// rows 103 / 123, 1 x 131072 57.9 / 61.4, 256 x 128 71 / 98, 64 x 200 28 / 37,
+// rows 104 / 122, 1 x 131072 55.8 / 59.8, 256 x 128 72 / 99, 64 x 200 29 / 37,
 // 32 x 256 17 / 23; below, its longer way to a tile's first block shows:
-// 1 x 517 13.9 / 12.6, 1 x 32768 29.0 / 27.4, 8 x 4096 30.9 / 28.9, 16 x 2048
-// 32.4 / 30.3 (8 KV heads, 20 query rows each).
+// 1 x 517 13.7 / 11.6, 1 x 32768 26.5 / 26.0, 8 x 4096 30.7 / 28.5, 16 x 2048
+// 32.2 / 30.4 (8 KV heads, 20 query rows each).
 constexpr bool cache_attn_can_key(bool e4m3, int D, int rows) { return e4m3 && D == 128 && rows <= 32; }
 inline bool cache_attn_by_keys(const CacheAttnLaunch& A, int D) {
   const long long tiles = (long long)A.B * A.Hkv * A.n_groups;

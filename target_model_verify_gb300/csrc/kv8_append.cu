@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == gridDim.x - 1) {
-    // the last CTA alone judges the call's tables and writes the status word
+    // the last CTA alone checks the tables of the call and writes the status word
     int bad = 0;
     for (long long e = threadIdx.x; e < A.B; e += 32 * kWarps) {
       const int count = A.counts ? A.counts[e] : A.n;

@@ -62,7 +62,8 @@ def test_attention_argument_errors(name):
         assert size(*shape.values()) == 0, bad
     for bad in ({"q": 0}, {"kc": 0}, {"vc": 0}, {"lens": 0}, {"out": 0}, {"q": P + 8}, {"out": P + 2},
                 {"lens": P + 2}, {"slopes": P + 1}, {"qs": 4095}, {"qs": 4088}, {"qs": 4100}, {"qs": 1 << 31},
-                {"scale": float("nan")}, {"scale": 1e-35}, {"cap": -1.0}, {"cap": 1e-35}, {"cap": 1e35}, {"cap": float("inf")}, {"window": -1},
+                {"scale": float("nan")}, {"scale": 1e-35}, {"cap": -1.0}, {"cap": 1e-35}, {"cap": 1001.0},
+                {"cap": float("inf")}, {"window": -1},
                 {"parent": (0, 0, 0, 0, 0)}, {"parent": (-1, 1, 0, 0, 0)}, {"parent": (-1, 0, 0, 3, 0)},
                 {"parent": (-1, 0, -1, 0, 0)}):
         assert _attend(fn, **bad) == b.SPECDEC_ERR_INVALID_ARG, bad

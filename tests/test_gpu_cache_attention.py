@@ -421,6 +421,30 @@ def test_verify_layer_step():
             assert (np.abs(a - w) <= 4 * 2.0 ** -4 * np.abs(w) + 4 * 2.0 ** -10 * step).all()
 
 
+@pytest.mark.parametrize("kind,B,n,Hq,Hkv,D,Lmax,lens", [
+    ("kv8", 3, 5, 32, 8, 128, 300, [300, 0, 129]),        # fewer tiles than CTAs, an unused slot
+    ("kv8", 40, 3, 32, 8, 128, 200, None),                # the form for many tiles
+    ("kv8", 1, 26, 32, 8, 64, 5000, [5000]),              # 128 lanes, one sequence over every CTA
+    ("masked", 2, 40, 16, 2, 256, 150, [150, 40]),        # several row groups
+    ("masked", 5, 2, 200, 100, 64, 90, None),             # more heads than CTAs side by side
+])
+def test_margins_are_left(kind, B, n, Hq, Hkv, D, Lmax, lens):
+    """Workspace and output lie between margins of 4 KB; a call writes neither."""
+    import target_model_verify_gb300 as tv
+    q, cache, lens = _inputs(kind, 30, B, n, Hq, Hkv, D, Lmax, lens=lens)
+    sizes = {"workspace": tv.cache_attention_workspace_bytes(B, n, Hq, Hkv, D, Lmax), "out": q.numel() * 2}
+    if kind == "masked":
+        sizes["workspace"] = tv._b.specdec_verify_attention_masked_workspace_size(B, n, Hq, Hkv, D, Lmax)
+    whole = {k: torch.full((v + 8192,), 0xA5, dtype=torch.uint8, device=DEV) for k, v in sizes.items()}
+    inner = {k: whole[k][4096:4096 + v] for k, v in sizes.items()}
+    inner["out"] = inner["out"].view(torch.bfloat16).view(q.shape)
+    out = _call(kind, q, cache, lens, **inner)
+    for k, v in sizes.items():
+        assert (whole[k][:4096] == 0xA5).all() and (whole[k][4096 + v:] == 0xA5).all(), k
+    assert tv.read_status(inner["workspace"]) == 0
+    _check(kind, q, cache, lens, out)
+
+
 def test_refusals():
     import target_model_verify_gb300 as tv
     q, cache, lens = _inputs("kv8", 21, 2, 3, 4, 2, 128, 64)
