@@ -3,6 +3,7 @@
 // of interpreter time on a Grace core for a dozen tensors, against 3 to 10 us
 // of GPU time for a small batch's step; here about 3 us).
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -77,15 +78,17 @@ constexpr const char* kCodes = "the caches must be contiguous float8_e4m3fn CUDA
 
 int narrow(int64_t x) { return (int)std::min<int64_t>(x, INT32_MAX); }   // the C call refuses what it cannot hold
 
-void* workspace_of(const OptTensor& given, size_t bytes, const Tensor& like, Tensor& own, size_t& have) {
+// The caller's workspace, or one for this call from the current stream's pool
+// (straight from the allocator, without a tensor around it).
+void* workspace_of(const OptTensor& given, size_t bytes, c10::DataPtr& own, size_t& have) {
   if (given) {
     check_type(given->is_contiguous() && given->is_cuda(), "workspace must be a contiguous CUDA tensor");
     have = given->nbytes();
     return given->data_ptr();
   }
-  own = at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
+  own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
   have = bytes;
-  return own.data_ptr();
+  return own.get();
 }
 
 int append_kv8(const Tensor& k_new, const Tensor& v_new, const Tensor& k_cache, const Tensor& v_cache,
@@ -108,9 +111,9 @@ int append_kv8(const Tensor& k_new, const Tensor& v_new, const Tensor& k_cache, 
   same_device(k_new, workspace);
   const long long ks = B ? row_stride(k_new) : Hkv * D, vs = B ? row_stride(v_new) : Hkv * D;
   const c10::cuda::CUDAGuard guard(k_new.device());
-  Tensor own;
+  c10::DataPtr own;
   size_t have;
-  void* ws = workspace_of(workspace, specdec_kv8_append_workspace_size(), k_new, own, have);
+  void* ws = workspace_of(workspace, specdec_kv8_append_workspace_size(), own, have);
   return specdec_kv8_append(k_new.data_ptr(), ks, v_new.data_ptr(), vs, ptr<int32_t>(start), ptr<int32_t>(counts),
                             ptr<int32_t>(rows), narrow(B), narrow(n), narrow(Hkv), narrow(D), narrow(Lmax),
                             k_cache.data_ptr(), v_cache.data_ptr(), ptr<float>(k_scale), ptr<float>(v_scale), ws,
@@ -171,9 +174,9 @@ std::pair<int, Tensor> cache_attention(const Tensor& q, const Tensor& k_cache, c
                                                         narrow(Lmax));
     if (bytes == 0) return {SPECDEC_ERR_UNSUPPORTED, out};
   }
-  Tensor own;
+  c10::DataPtr own;
   size_t have;
-  void* ws = workspace_of(workspace, bytes, q, own, have);
+  void* ws = workspace_of(workspace, bytes, own, have);
   void* stream = c10::cuda::getCurrentCUDAStream(q.device().index()).stream();
   const int32_t* pp = par.empty() ? nullptr : par.data();
   // a window beyond any distance is none; a negative one is the C call's to refuse
