@@ -585,9 +585,9 @@ __device__ __forceinline__ void zero_empty(const CacheAttnLaunch& A) {
 }
 
 // Merges the partials of the tiles that more than one CTA worked on.
-// blockIdx.x = the note, blockIdx.y: rows. `wpr`
-// of the eight warps share the partials of kRows rows, which they take
-// together, so that eight loads are in flight either way.
+// blockIdx.x = the note, blockIdx.y: rows. `wpr` of the eight warps share the
+// partials of kRows rows, which they take together, so that eight loads are in
+// flight either way.
 template <int kD, int kRP>
 struct MergeShape {
   static constexpr int kRows = kRP / 32;                    // 1, 2 or 4
@@ -1235,9 +1235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool dead = false;                   // a wait ran out: keep to the barriers, compute nothing
     bool noted = false;
     uint32_t n = 0, nt = 0;
-    // A test of a barrier ahead of its wait, which costs 200 cycles even when
-    // it has nothing to wait for.
-    bool s_ready = false;                // of block n's scores
+    bool s_ready = false;                // block n's scores were seen ready
     if constexpr (S::kCopies > 1) {
       const uint32_t zero[32] = {};
 #pragma unroll
@@ -1432,14 +1430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t pk[kKpl / 2];
         bool p_free = n < S::kPBufs;         // the product that last read this P buffer is done
-        s_ready = false;
+        // Tests ahead of waits, which cost 200 cycles even with nothing to wait for.
+        s_ready = ib + 1 < w.n_here && mbar_test(s_full((n + 1) & 1), ((n + 1) >> 1) & 1);
+        if (!p_free) p_free = mbar_test(o_done((n - S::kPBufs) & 1), ((n - S::kPBufs) >> 1) & 1);
 #pragma unroll
         for (int xs = 0; xs < kSubs; ++xs) {
           float* const y = x.f + xs * kSubKeys;
-          if (xs == 0) {
-            if (ib + 1 < w.n_here) s_ready = mbar_test(s_full((n + 1) & 1), ((n + 1) >> 1) & 1);
-            if (!p_free) p_free = mbar_test(o_done((n - S::kPBufs) & 1), ((n - S::kPBufs) >> 1) & 1);
-          }
           float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int k = 0; k < kSubKeys; k += 2) {
