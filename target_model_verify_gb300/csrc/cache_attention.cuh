@@ -990,6 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_queries = [&](const Walk<kBlk>& t) {
         if (!warp_wait(q_empty(0), (nt & 1) ^ 1u)) return false;
         if constexpr (S::kQTmem) {
+          tc_fence_after();                    // the last tile's products have read their terms
           const int row = at % kRP, pos0 = t.g * A.group_pos;
           const bool mine = row < min(A.group_pos, A.n_new - pos0) * A.G;
           const uint4* src = reinterpret_cast<const uint4*>(
@@ -1461,6 +1462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             !warp_wait(o_done((n - S::kPBufs) & 1), ((n - S::kPBufs) >> 1) & 1))
           dead = true;
         if (dead) continue;
+        tc_fence_after();                    // the product has read what is overwritten now
         tmem_store(tl + S::kColP + (S::kPBufs == 2 ? (n & 1) * (kBlk / 2) : 0) + key0 / 2, pk, Cols<kKpl / 2>{});
         tmem_wait_store();
         tc_fence_before();
