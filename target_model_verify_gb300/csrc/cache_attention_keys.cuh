@@ -1,34 +1,45 @@
 // The cache attention (cache_attention.cuh) over an e4m3 cache of head dim
-// 128 for up to 32 query rows per KV head, with the cache on the M side of
+// 128 for up to 24 query rows per KV head, with the cache on the M side of
 // both products.
 //
 // With few query rows the row-per-lane form pays for 128 of them: its products
 // and their operand reads, and widening V to f16, take as long as the cache
 // takes to arrive. Here
-//   S^T = K Q^T:   M = 128 keys, N = 64: the rows' two e4m3 query terms side
+//   S^T = K Q^T:   M = 128 keys, N = 48: the rows' two e4m3 query terms side
 //                  by side (K is read from shared memory once; the terms'
 //                  scores are added in registers);
-//   O^T += V^T P^T: M = 128 dims, N = 96: the rows' probabilities as three
-//                  e4m3 terms, p = hi + mid / 16 + lo / 256, with an
-//                  accumulator each. The terms are those of p rounded to f16,
-//                  exact down to 2^-20 of a row's largest weight, and V is
-//                  multiplied as it lies in the cache.
+//   O^T += V^T P^T: M = 128 dims, N = 96: the rows' probabilities as four
+//                  e5m2 terms, p = t0 + t1 / 8 + t2 / 64 + t3 / 512, with an
+//                  accumulator each, and V is multiplied as it lies in the
+//                  cache. A term has three significant bits and f16's exponents,
+//                  so the four are p rounded to f16, exactly, at every size.
+//                  (Three e4m3 terms hold as many bits but end 2^28 below
+//                  their top: the small weights beside one dominant key
+//                  vanished from outputs whose sum counted them.)
 // Lane = key in the softmax, so a row's statistics run over lanes and warps.
-// Only its reference does not follow every maximum: it is set 2^2 above the
-// row's first and moved when an exponent passes it by 2^4, which one
-// barrier with a vote per block finds out; sums stay with the keys' threads
-// until the tile ends.
+// Only its reference (the exponent of p = 2^15, the most of which a term can
+// hold eight times the rest) does not follow every maximum: it is set 2^6
+// above one, and moved when a block's largest p would pass 2^15 or stay below
+// 2^-14, where f16's normal numbers end. So a weight is off by at most 2^-11
+// of itself, or below those by half of f16's last step, 2^-25: 2^-34 of the
+// row's largest and 2^-11 of the largest among its own 128 rows. (A key that
+// takes nearly all of a row's weight, as the first one does in many models,
+// leaves the small ones their precision.) References go down at most 2^24
+// below their highest, which keeps sums and outputs finite. One barrier per
+// block, with votes, finds out whether one has to move; sums stay with the
+// keys' threads until the tile ends.
 //
 // Two CTAs per SM (256 tensor memory columns each) of six warps, so that a
 // thread may have 168 registers: 0-3 softmax, 4 loads (K and V blocks,
 // queries and row tables, the check of V blocks that not every query sees
 // whole), 5 issues both products.
 //
-// Measured (64 x 4096 rows, 5 positions, 32 query / 8 KV heads): 104 us for
-// 543 MB, 5220 GB/s or 0.77 of the copy peak (the other form: 122 us); DRAM
-// reads are the algorithmic bytes. What is left is the start (6 us until the
-// first block's products), the first block's pass for its references, the
-// SMs' unequal ends and the merge (4 us).
+// Measured (64 x 4096 rows, 5 positions, 32 query / 8 KV heads): 105 us for
+// 543 MB, 5170 GB/s or 0.76 of the copy peak (the other form: 121 us); scores
+// of twice and four times the spread 107 and 140 us, where references move and
+// are looked at more often. What is left is the start (6 us until the first
+// block's products), the first block's pass for its references, the SMs'
+// unequal ends and the merge (4 us).
 #pragma once
 
 #include "cache_attention.cuh"
@@ -37,18 +48,23 @@ namespace specdec {
 namespace cache_attn {
 
 constexpr int kKeyThreads = 192;
-constexpr int kKeyD = 128, kKeyBlk = 128, kKeyRows = 32;
+constexpr int kKeyD = 128, kKeyBlk = 128;
+constexpr int kKeyRows = kCacheAttnKeyRows, kKeyLanes = 32;     // query rows, and their tables' and partials' pitch
+constexpr int kKeyTerms = 4;
 constexpr int kKeyRingK = 2, kKeyRingV = 3;             // blocks of each in flight: V's are held longer
 constexpr int kKeySlot = kKeyBlk * kKeyD;
-constexpr int kKeyPTerm = kKeyBlk * kKeyRows;           // [keys][32 rows] codes of one term
+constexpr int kKeyPanel = kKeyBlk * 32, kKeyPanels = kKeyRows / 8;      // [keys][4 terms][8 rows] codes
+static_assert(kKeyRows % 8 == 0 && kKeyTerms == 4 && kKeyRows <= kKeyLanes, "eight rows' terms to a panel");
 constexpr int kKeyQBytes = 2 * kKeyRows * kKeyD;        // [hi rows, lo rows][dims]
 constexpr int kKeyColS = 0, kKeyColO = 128;
-constexpr float kRise = 4.f, kLift = 2.f, kBase = 4.f;  // log2: see above; p at the reference is 2^kBase
+// log2: p at the reference; how far above a row's maximum that is set; how far
+// below it a block's maximum may lie; how far below its highest it may go
+constexpr float kBase = 15.f, kLift = 6.f, kFall = 29.f, kDeep = 24.f;
 // tables per query buffer: of every row its score factor, slope, depth and
 // place in the output [32]; of every new position the rows that see it [128]
-constexpr int kKeyTab = 4 * kKeyRows * 4 + 128 * 4;
-constexpr int kKeySmem = 1024 + (kKeyRingK + kKeyRingV) * kKeySlot + 3 * kKeyPTerm + 2 * kKeyQBytes + 2 * kKeyTab +
-                         3 * kKeyRows * 4 + 4 * kKeyRows * 4 + 128 * 4 + 512;
+constexpr int kKeyTab = 4 * kKeyLanes * 4 + 128 * 4;
+constexpr int kKeySmem = 1024 + (kKeyRingK + kKeyRingV) * kKeySlot + kKeyPanels * kKeyPanel + 2 * kKeyQBytes +
+                         2 * kKeyTab + 8 * kKeyLanes * 4 + 128 * 4 + 64 + 256;
 static_assert(2 * (kKeySmem + 1024) <= 228 * 1024, "two CTAs per SM");
 
 // MN-major operand of 32-byte rows (32 codes along N), 32-byte swizzle.
@@ -61,48 +77,101 @@ __device__ __forceinline__ uint64_t operand_desc32(uint32_t saddr, uint32_t lead
   d |= (uint64_t)6 << 61;
   return d;
 }
-__device__ __forceinline__ bool bar_any(int id, int nthreads, bool x) {
+// A barrier that counts the threads with x.
+__device__ __forceinline__ int bar_count(int id, int nthreads, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.popc.u32 %0, %2, %3, p;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)x), "r"(id), "r"(nthreads)
       : "memory");
-  return r != 0;
+  return (int)r;
 }
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t h) {
   uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
   return c;
 }
-// (h - back) * 16, elementwise; exact for back the e4m3 rounding of h.
-__device__ __forceinline__ uint32_t rest16(uint32_t h, uint32_t back) {
-  const __half2 s = __float2half2_rn(16.f);
-  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&back)), s);
+// (h - code) * 8, elementwise; exact for code the e5m2 rounding of h (whose
+// bytes are the upper ones of f16 values), and at most 2^15 for h up to that.
+__device__ __forceinline__ uint32_t rest8(uint32_t h, uint32_t code) {
+  const uint32_t back = __byte_perm(code, 0, 0x1404);
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&back)),
+                            __float2half2_rn(8.f));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[48]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47"
+      "}, [%49];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
+        "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
+        "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
+        "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
+        "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]),
+        "=r"(x[30]), "=r"(x[31]), "=r"(x[32]), "=r"(x[33]), "=r"(x[34]), "=r"(x[35]),
+        "=r"(x[36]), "=r"(x[37]), "=r"(x[38]), "=r"(x[39]), "=r"(x[40]), "=r"(x[41]),
+        "=r"(x[42]), "=r"(x[43]), "=r"(x[44]), "=r"(x[45]), "=r"(x[46]), "=r"(x[47])
+      : "r"(taddr + 0), "r"(taddr + 32)
+      : "memory");
+}
+// Halves the rows a lane carries five times: lane r returns the warp's
+// join of row r (rows past the last: `none`).
+template <typename Join>
+__device__ __forceinline__ float rows_to_lanes(const float (&x)[kKeyRows], int lane, float none, Join join) {
+  float y[kKeyLanes];
+#pragma unroll
+  for (int r = 0; r < kKeyLanes; ++r) y[r] = r < kKeyRows ? x[r] : none;
+#pragma unroll
+  for (int o = 16, cnt = 16; o; o >>= 1, cnt >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < cnt; ++k) {
+      const float give = up ? y[k] : y[k + cnt], keep = up ? y[k + cnt] : y[k];
+      y[k] = join(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  return y[0];
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float m;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
 }
 
 template <bool kExtra>
 __global__ void __launch_bounds__(kKeyThreads, 2)
     cache_attn_keys_kernel(const __grid_constant__ CacheAttnLaunch A, const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v) {
-  constexpr int kBlk = kKeyBlk, kD = kKeyD, kRows = kKeyRows;
+  constexpr int kBlk = kKeyBlk, kD = kKeyD, kRows = kKeyRows, kLanes = kKeyLanes;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring_k = (raw + 1023u) & ~1023u;
   const uint32_t ring_v = ring_k + kKeyRingK * kKeySlot;
-  const uint32_t pb = ring_v + kKeyRingV * kKeySlot;       // probabilities: three terms
-  const uint32_t qb = pb + 3 * kKeyPTerm;
+  const uint32_t pb = ring_v + kKeyRingV * kKeySlot;       // probabilities: all terms
+  const uint32_t qb = pb + kKeyPanels * kKeyPanel;
   const uint32_t tab = qb + 2 * kKeyQBytes;
   const uint32_t ref = tab + 2 * kKeyTab;                  // references, then factors for what moved
-  const uint32_t zeros = ref + 2 * kRows * 4;              // [32]
-  const uint32_t red = zeros + kRows * 4;                  // [4 warps][32 rows]
-  const uint32_t depths = red + 4 * kRows * 4;             // of the tree's nodes [128]
-  const uint32_t bars = depths + 128 * 4;
+  const uint32_t zeros = ref + 2 * kLanes * 4;             // [32]
+  const uint32_t red = zeros + kLanes * 4;                 // [4 warps][32 rows]
+  const uint32_t depths = red + 4 * kLanes * 4;            // of the tree's nodes [128]
+  const uint32_t marks = depths + 128 * 4;                 // [2 blocks][4 warps][2] rows, see below
+  const uint32_t peaks = marks + 64;                       // the rows' highest references
+  const uint32_t bars = peaks + kLanes * 4;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   auto k_full = [&](int s) { return bar(s); };
   auto k_empty = [&](int s) { return bar(2 + s); };
@@ -220,16 +289,18 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           lo[k] = pl[0] | (pl[1] << 16);
         }
         const uint32_t to = (uint32_t)((c ^ (row & 7)) << 4);
-        sts128(hi_row + to, hi[0], hi[1], hi[2], hi[3]);
-        sts128(lo_row + to, lo[0], lo[1], lo[2], lo[3]);
+        if (row < kRows) {
+          sts128(hi_row + to, hi[0], hi[1], hi[2], hi[3]);
+          sts128(lo_row + to, lo[0], lo[1], lo[2], lo[3]);
+        }
       }
       const uint32_t at = tab + qs * kKeyTab + row * 4;
       const float q_scale = fine ? __uint_as_float((uint32_t)(127 + down) << 23) : __uint_as_float(0x7fffffffu);
       sts32(at, __float_as_uint(A.scale * q_scale * (kExtra ? 1.f : kLog2e)));
-      sts32(at + kRows * 4, __float_as_uint(kExtra && A.slopes ? A.slopes[head] * kLog2e : 0.f));
+      sts32(at + kLanes * 4, __float_as_uint(kExtra && A.slopes ? A.slopes[head] * kLog2e : 0.f));
       const int dep = A.tree ? (int)lds32(depths + idx * 4) : idx;
-      sts32(at + 2 * kRows * 4, __float_as_uint((float)dep));
-      sts32(at + 3 * kRows * 4, (uint32_t)(idx * A.Hq + head));
+      sts32(at + 2 * kLanes * 4, __float_as_uint((float)dep));
+      sts32(at + 3 * kLanes * 4, (uint32_t)(idx * A.Hq + head));
       for (int a0 = 0; a0 < A.n_new; a0 += 32) {
         uint32_t sees = 0, of_mine = 0;          // new positions a0 .. a0 + 31 that this row sees
         if (A.tree)
@@ -246,7 +317,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           const uint32_t rows = __ballot_sync(0xffffffffu, see);
           if (lane == a) of_mine = rows;
         }
-        sts32(tab + qs * kKeyTab + 4 * kRows * 4 + (a0 + lane) * 4, of_mine);
+        sts32(tab + qs * kKeyTab + 4 * kLanes * 4 + (a0 + lane) * 4, of_mine);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -327,9 +398,10 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
     // ------------------------------------------------------------ issuer --
     // Scores run a block ahead of the values' product.
     constexpr uint32_t id_s = instr_desc(0, false, 2 * kRows);
-    constexpr uint32_t id_o = instr_desc(0, true, 3 * kRows) | (1u << 15);     // A (V^T) is M-major too
+    constexpr uint32_t id_o = instr_desc(0, true, kKeyTerms * kRows) | (1u << 15)     // A (V^T) is M-major too,
+                              | (1u << 10);                                         // B is e5m2
     const uint64_t k_desc = operand_desc<128>(ring_k, 16), q_desc = operand_desc<128>(qb, 16);
-    const uint64_t v_desc = operand_desc<128>(ring_v, 16), p_desc = operand_desc32(pb, kKeyPTerm);
+    const uint64_t v_desc = operand_desc<128>(ring_v, 16), p_desc = operand_desc32(pb, kKeyPanel);
     Walk<kBlk> wq = w;
     uint32_t nq = 0, tq = 0, n = 0, clean_ph = 0;
     int iq = 0;
@@ -407,12 +479,12 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       auto seen_by = [&](int jj) {
         const int a = jj - P0;
         if (jj >= w.L) return 0u;
-        if (a >= 0) return lds32(t0 + 4 * kRows * 4 + a * 4);
+        if (a >= 0) return lds32(t0 + 4 * kLanes * 4 + a * 4);
         if (A.window <= 0) return 0xffffffffu;
         uint32_t m = 0;
 #pragma unroll
         for (int r = 0; r < kRows; r += 4) {
-          const float4 d = lds128f(t0 + 2 * kRows * 4 + r * 4);
+          const float4 d = lds128f(t0 + 2 * kLanes * 4 + r * 4);
           m |= ((int)d.x - a < A.window ? 1u : 0u) << r | ((int)d.y - a < A.window ? 2u : 0u) << r |
                ((int)d.z - a < A.window ? 4u : 0u) << r | ((int)d.w - a < A.window ? 8u : 0u) << r;
         }
@@ -421,7 +493,10 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       float l[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) l[r] = 0.f;
-      if (warp == 0) sts32(ref + lane * 4, __float_as_uint(INFINITY));      // negated: none yet
+      if (warp == 0) {
+        sts32(ref + lane * 4, __float_as_uint(INFINITY));      // negated: none yet
+        sts32(peaks + lane * 4, __float_as_uint(-INFINITY));
+      }
       if (!dead && !warp_wait(q_full(qs), (nt >> 1) & 1)) dead = true;
       named_bar_sync(1, 32 * kSoftWarps);
 
@@ -434,20 +509,21 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
         tc_fence_after();
         float y[kRows];
         // The tile's first block begins with its rows' maxima, other blocks
-        // with exponents against the references; one of those too high
-        // brings in the maxima as well. (`from_ref` points at the negated
-        // references, or at zeros: one piece of code for both.)
+        // with exponents against the references; one of those too high, or
+        // a row without one high enough, brings in the maxima as well.
+        // (`from_ref` points at the negated references, or at zeros: one piece
+        // of code for both.)
         bool maxima = ib == 0, settled = ib == 0;
         for (;;) {
           const uint32_t from_ref = maxima ? zeros : ref;
           if (!dead) {
-            uint32_t u[64];
+            uint32_t u[2 * kRows];
             tmem_load(tl + kKeyColS + (n & 1) * 64, u);
 #pragma unroll
             for (int r = 0; r < kRows; r += 2) {
               y[r] = __uint_as_float(u[r]);
               y[r + 1] = __uint_as_float(u[r + 1]);
-              add2(y[r], y[r + 1], __uint_as_float(u[32 + r]), __uint_as_float(u[33 + r]));
+              add2(y[r], y[r + 1], __uint_as_float(u[kRows + r]), __uint_as_float(u[kRows + 1 + r]));
             }
           }
           float pj = 0.f;
@@ -467,7 +543,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
             mul2(y[r], y[r + 1], c.x, c.y);
             mul2(y[r + 2], y[r + 3], c.z, c.w);
             if constexpr (kExtra) {
-              const float4 sl = lds128f(t0 + kRows * 4 + r * 4), dp = lds128f(t0 + 2 * kRows * 4 + r * 4);
+              const float4 sl = lds128f(t0 + kLanes * 4 + r * 4), dp = lds128f(t0 + 2 * kLanes * 4 + r * 4);
               mul2(y[r], y[r + 1], sk, sk);
               mul2(y[r + 2], y[r + 3], sk, sk);
               if (A.cap > 0.f) {
@@ -496,13 +572,51 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
             for (int r = 0; r < kRows; ++r) y[r] = (m >> r) & 1u ? y[r] : -INFINITY;
           }
           if (!maxima) {
-            if (settled) break;
-            float top = -INFINITY;
+            if (settled) {
+              // exponents of 2^24 and more are whole steps from their reference
+#pragma unroll
+              for (int r = 0; r < kRows; ++r) y[r] = min_or_nan(y[r], kBase);
+              break;
+            }
+            float top = -INFINITY, bot = INFINITY;
             if (!dead) {
 #pragma unroll
-              for (int r = 0; r < kRows; r += 4) top = max3(max3(top, y[r], y[r + 1]), y[r + 2], y[r + 3]);
+              for (int r = 0; r < kRows; r += 4) {
+                top = max3(max3(top, y[r], y[r + 1]), y[r + 2], y[r + 3]);
+                bot = min3(min3(bot, y[r], y[r + 1]), y[r + 2], y[r + 3]);
+              }
             }
-            if (!bar_any(1, 32 * kSoftWarps, top > kBase + kRise)) break;
+            // Votes: 16 for a warp with an exponent too high, 1 for one with a
+            // key that every row holds high enough, which settles it in most blocks.
+            const bool high = __any_sync(0xffffffffu, top > kBase), even = __any_sync(0xffffffffu, bot > kBase - kFall);
+            const int votes = bar_count(1, 32 * kSoftWarps, lane < 16 ? high : lane == 16 && even);
+            if (__builtin_expect((votes & 15) && votes < 16, 1)) break;
+            if (votes < 16) {
+              // The rows with a key high enough, over the block's keys, and those
+              // with one that a lower reference would serve. (Two blocks' marks: a
+              // warp may still read the last one's.)
+              uint32_t loud = 0, worth = 0;
+#pragma unroll
+              for (int r = 0; r < kRows; r += 4) {
+                const float4 p = lds128f(peaks + r * 4), m = lds128f(ref + r * 4);
+                const float least[4] = {p.x + m.x, p.y + m.y, p.z + m.z, p.w + m.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  loud |= (y[r + k] > kBase - kFall ? 1u : 0u) << (r + k);
+                  worth |= (y[r + k] - (kBase - kDeep - kLift) > least[k] ? 1u : 0u) << (r + k);
+                }
+              }
+              loud = __reduce_or_sync(0xffffffffu, loud);
+              worth = __reduce_or_sync(0xffffffffu, worth);
+              const uint32_t mark = marks + (n & 1) * 32;
+              if (lane == 0) sts64(mark + warp * 8, dead ? 0u : loud, dead ? 0u : worth);
+              named_bar_sync(1, 32 * kSoftWarps);
+              const uint4 a = lds128(mark), b = lds128(mark + 16);
+              loud = a.x | a.z | b.x | b.z;
+              worth = a.y | a.w | b.y | b.w;
+              // rows of padding have no say
+              if ((worth & ~loud & (0xffffffffu >> (32 - rows_here))) == 0) break;
+            }
             maxima = settled = true;
             continue;
           }
@@ -511,51 +625,42 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
 #pragma unroll
             for (int r = 0; r < kRows; ++r) y[r] = -INFINITY;
           }
-          // halve the rows a lane carries five times: lane r ends up with row r
-#pragma unroll
-          for (int o = 16, cnt = 16; o; o >>= 1, cnt >>= 1) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int k = 0; k < cnt; ++k) {
-              const float give = up ? y[k] : y[k + cnt], keep = up ? y[k + cnt] : y[k];
-              y[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
-            }
-          }
-          sts32(red + kl * 4, __float_as_uint(y[0] - kBase));
+          const float mine = rows_to_lanes(y, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+          sts32(red + kl * 4, __float_as_uint(mine - kBase));
           named_bar_sync(1, 32 * kSoftWarps);
           if (warp == 0) {
             float M = __uint_as_float(lds32(red + lane * 4));
 #pragma unroll
             for (int x = 1; x < kSoftWarps; ++x) M = fmaxf(M, __uint_as_float(lds32(red + (x * 32 + lane) * 4)));
-            const float was = -__uint_as_float(lds32(ref + lane * 4));
-            const bool move = M > was + kRise;
-            sts32(ref + lane * 4, __float_as_uint(-(move ? M + kLift : was)));
-            sts32(ref + kRows * 4 + lane * 4, __float_as_uint(move ? ex2(was - (M + kLift)) : 1.f));
+            const float was = -__uint_as_float(lds32(ref + lane * 4)), to = M + kLift;
+            const float peak = __uint_as_float(lds32(peaks + lane * 4));
+            const bool move = M > was || (M < was - kFall && to > peak - kDeep);
+            if (move) sts32(peaks + lane * 4, __float_as_uint(fmaxf(peak, to)));
+            sts32(ref + lane * 4, __float_as_uint(-(move ? to : was)));
+            sts32(ref + kLanes * 4 + lane * 4, __float_as_uint(move ? ex2(was - to) : 1.f));
           }
           named_bar_sync(1, 32 * kSoftWarps);
           if (!dead) {
-            float al[kRows];
+            const uint32_t al = ref + kLanes * 4;
 #pragma unroll
             for (int r = 0; r < kRows; r += 4) {
-              const float4 f = lds128f(ref + kRows * 4 + r * 4);
-              al[r] = f.x;
-              al[r + 1] = f.y;
-              al[r + 2] = f.z;
-              al[r + 3] = f.w;
+              const float4 f = lds128f(al + r * 4);
+              mul2(l[r], l[r + 1], f.x, f.y);
+              mul2(l[r + 2], l[r + 3], f.z, f.w);
             }
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) l[r] *= al[r];
             if (ib > 0) {
               if (!warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
               if (!dead) {
                 tc_fence_after();
 #pragma unroll 1
-                for (int term = 0; term < 3; ++term) {
+                for (int g = 0; g < kKeyPanels; ++g) {
+                  const float4 lo = lds128f(al + g * 32), hi = lds128f(al + g * 32 + 16);
+                  const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                   uint32_t v[32];
-                  tmem_load(tl + kKeyColO + term * 32, v);
+                  tmem_load(tl + kKeyColO + 32 * g, v);
 #pragma unroll
-                  for (int r = 0; r < kRows; ++r) v[r] = __float_as_uint(__uint_as_float(v[r]) * al[r]);
-                  tmem_store(tl + kKeyColO + term * 32, v, Cols<32>{});
+                  for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f[k % 8]);
+                  tmem_store(tl + kKeyColO + 32 * g, v, Cols<32>{});
                 }
                 tmem_wait_store();
               }
@@ -563,35 +668,34 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           }
           maxima = false;
         }
-        // ---- probabilities, as three e4m3 terms ----
+        // ---- probabilities, as four e5m2 terms ----
         // the last block's product has read its own
         if (!dead && n > 0 && !warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) dead = true;
         if (dead) continue;
-        const uint32_t to = pb + kl * 32;
+        const uint32_t to = pb + kl * 32, half = ((uint32_t)kl >> 2 & 1) << 4;   // halves trade places every four keys
 #pragma unroll
-        for (int h16 = 0; h16 < 2; ++h16) {
-          uint32_t t[3][4];
+        for (int g = 0; g < kKeyPanels; ++g) {
+          uint32_t code[kKeyTerms][2];                 // [term][rows 4x .. 4x + 3 of the panel's]
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t part[3][2];
+          for (int x = 0; x < 2; ++x) {
+            uint32_t part[kKeyTerms][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int r = 16 * h16 + 4 * q + 2 * x;
+            for (int z = 0; z < 2; ++z) {
+              const int r = 8 * g + 4 * x + 2 * z;
               const float p0 = ex2(y[r]), p1 = ex2(y[r + 1]);
-              const uint32_t h = pack2<true>(p0, p1);
+              uint32_t h = pack2<true>(p0, p1);
               acc2(l[r], l[r + 1], p0, p1, inv_sv);
-              part[0][x] = f16x2_to_e4m3x2(h);
-              const uint32_t h1 = rest16(h, e4m3x2_to_f16x2((uint16_t)part[0][x]));
-              part[1][x] = f16x2_to_e4m3x2(h1);
-              part[2][x] = f16x2_to_e4m3x2(rest16(h1, e4m3x2_to_f16x2((uint16_t)part[1][x])));
+#pragma unroll
+              for (int t = 0; t < kKeyTerms; ++t) {
+                part[t][z] = f16x2_to_e5m2x2(h);
+                if (t + 1 < kKeyTerms) h = rest8(h, part[t][z]);
+              }
             }
 #pragma unroll
-            for (int x = 0; x < 3; ++x) t[x][q] = part[x][0] | (part[x][1] << 16);
+            for (int t = 0; t < kKeyTerms; ++t) code[t][x] = part[t][0] | (part[t][1] << 16);
           }
-          // 32-byte rows; the 16-byte halves trade places every four keys
-          const uint32_t at = to + ((uint32_t)(h16 ^ ((kl >> 2) & 1)) << 4);
-#pragma unroll
-          for (int x = 0; x < 3; ++x) sts128(at + x * kKeyPTerm, t[x][0], t[x][1], t[x][2], t[x][3]);
+          sts128(to + g * kKeyPanel + half, code[0][0], code[0][1], code[1][0], code[1][1]);
+          sts128(to + g * kKeyPanel + (half ^ 16), code[2][0], code[2][1], code[3][0], code[3][1]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -600,16 +704,8 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       }
 
       // ---- sums over the keys, then the output or this part's share ----
-#pragma unroll
-      for (int o = 16, cnt = 16; o; o >>= 1, cnt >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int k = 0; k < cnt; ++k) {
-          const float give = up ? l[k] : l[k + cnt], keep = up ? l[k + cnt] : l[k];
-          l[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-        }
-      }
-      sts32(red + kl * 4, __float_as_uint(l[0]));
+      const float sum = rows_to_lanes(l, lane, 0.f, [](float a, float b) { return a + b; });
+      sts32(red + kl * 4, __float_as_uint(sum));
       named_bar_sync(1, 32 * kSoftWarps);
       const bool whole = w.blk == 0 && w.n_here == w.nb;
       const size_t slot = (size_t)blockIdx.x * 2 + (w.u == part0 ? 0 : 1);
@@ -619,9 +715,9 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
         for (int x = 0; x < kSoftWarps; ++x) lt += __uint_as_float(lds32(red + (x * 32 + lane) * 4));
         // the output's factor per row, where the references' factors were
         const float inv = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);    // NaN stays
-        sts32(ref + kRows * 4 + lane * 4, __float_as_uint(whole ? inv : 1.f));
+        sts32(ref + kLanes * 4 + lane * 4, __float_as_uint(whole ? inv : 1.f));
         if (!whole && lane < rows_here && !dead)
-          *reinterpret_cast<float2*>(A.part_ml + (slot * kRows + lane) * 2) =
+          *reinterpret_cast<float2*>(A.part_ml + (slot * kLanes + lane) * 2) =
               make_float2(-__uint_as_float(lds32(ref + lane * 4)), lt);
       }
       named_bar_sync(1, 32 * kSoftWarps);
@@ -629,17 +725,15 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       tc_fence_after();
       if (!dead) {
         float o[kRows];
-        {
+#pragma unroll
+        for (int g = 0; g < kKeyPanels; ++g) {
           uint32_t v[32];
-          tmem_load(tl + kKeyColO, v);
+          tmem_load(tl + kKeyColO + 32 * g, v);
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) o[r] = __uint_as_float(v[r]);
-          tmem_load(tl + kKeyColO + 32, v);
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) o[r] = fmaf(__uint_as_float(v[r]), 1.f / 16, o[r]);
-          tmem_load(tl + kKeyColO + 64, v);
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) o[r] = fmaf(__uint_as_float(v[r]), 1.f / 256, o[r]);
+          for (int k = 0; k < 8; ++k) {
+            auto term = [&](int t) { return __uint_as_float(v[8 * t + k]); };
+            o[8 * g + k] = fmaf(term(3), 1.f / 512, fmaf(term(2), 1.f / 64, fmaf(term(1), 1.f / 8, term(0))));
+          }
         }
         if (*odd) {
           // NaN that were held back from the product (rare), for the rows that see them
@@ -658,12 +752,12 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
           }
         }
         __nv_bfloat16* out = A.out + (size_t)w.b * A.n_new * A.Hq * kD + kl;
-        float* part = A.part_o + slot * kRows * kD + kl;
+        float* part = A.part_o + slot * kLanes * kD + kl;
 #pragma unroll
         for (int r = 0; r < kRows; r += 4) {
           if (r >= rows_here) break;
-          const float4 f = lds128f(ref + kRows * 4 + r * 4);
-          const uint4 at = lds128(t0 + 3 * kRows * 4 + r * 4);
+          const float4 f = lds128f(ref + kLanes * 4 + r * 4);
+          const uint4 at = lds128(t0 + 3 * kLanes * 4 + r * 4);
           const float ff[4] = {f.x, f.y, f.z, f.w};
           const uint32_t to[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
@@ -729,7 +823,7 @@ cudaError_t launch_keys(const CacheAttnLaunch& A, const CUtensorMap& tk, const C
   L.note_tiles = note_tiles(A, parts);
   e = cudaLaunchKernelEx(&cfg, cache_attn_keys_kernel<kExtra>, L, tk, tv);
   if (e != cudaSuccess) return e;
-  return launch_combine<kKeyD, kKeyRows>(L, parts, cfg);
+  return launch_combine<kKeyD, kKeyLanes>(L, parts, cfg);
 }
 
 }  // namespace cache_attn

@@ -226,17 +226,25 @@ constexpr int cache_attn_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 
 // 27.6 us for 20 query rows on 16 ragged bf16 sequences with a window.
 constexpr int cache_attn_block(int D, int lanes) { return D == 256 || lanes == 128 ? 64 : 128; }
 // The form with the cache on the M side (cache_attention_keys.cuh) can take a
-// call with up to 32 query rows per KV head, and does from 256 tiles or 4096
+// call with up to 24 query rows per KV head, and does from 256 tiles or 4096
 // blocks of cache on. Measured, keys against rows form, us a call: 64 x 4096
-// rows 104 / 122, 1 x 131072 55.8 / 59.8, 256 x 128 72 / 99, 64 x 200 29 / 37,
-// 32 x 256 17 / 23; below, its longer way to a tile's first block shows:
-// 1 x 517 13.7 / 11.6, 1 x 32768 26.5 / 26.0, 8 x 4096 30.7 / 28.5, 16 x 2048
-// 32.2 / 30.4 (8 KV heads, 20 query rows each).
-constexpr bool cache_attn_can_key(bool e4m3, int D, int rows) { return e4m3 && D == 128 && rows <= 32; }
+// rows 105 / 121, 1 x 131072 53.5 / 58.5, 1 x 65536 36.6 / 37.9, 256 x 128 71 /
+// 99, 64 x 200 28 / 38, 32 x 256 17.2 / 23.3; below, its longer way to a tile's
+// first block shows: 1 x 517 13.5 / 12.0, 8 x 4096 29.7 / 28.3, 16 x 2048 31.2 /
+// 30.1, and between 2048 and 4096 blocks the two are within 4 % of each other,
+// either way: 1 x 32768 25.4 / 25.9, 10 x 4096 31.4 / 31.3, 12 x 4096 34.0 / 35.3,
+// 14 x 4096 38.6 / 38.3 (8 KV heads, 20 query rows each). The lengths are on the
+// device, so the cache's capacity stands for them: one sequence of 517 rows in a
+// cache of 131072 takes 14.3 us here and would take 13.4 in the other form.
+// With a distance bias steep heads leave whole blocks without weights, and each
+// costs this form a look at its references: 64 x 384 38.5 / 42.1, but 64 x 512
+// 46.4 / 45.5, 64 x 4096 150 / 130.
+constexpr int kCacheAttnKeyRows = 24;
+constexpr bool cache_attn_can_key(bool e4m3, int D, int rows) { return e4m3 && D == 128 && rows <= kCacheAttnKeyRows; }
 inline bool cache_attn_by_keys(const CacheAttnLaunch& A, int D) {
   const long long tiles = (long long)A.B * A.Hkv * A.n_groups;
   return cache_attn_can_key(true, D, A.group_pos * A.G) &&
-         (tiles >= 256 || tiles * ((A.Lmax + 127) / 128) >= 4096);
+         (tiles >= 256 || tiles * ((A.Lmax + 127) / 128) >= 4096) && (!A.slopes || A.Lmax < 512);
 }
 // tmap_q: the queries as a bf16 tensor {D, Hq, n_new, B} with a box of 64
 // dims x G heads x group_pos positions, 128-byte swizzle (bf16 cache only).

@@ -1,0 +1,25 @@
+"""What the bounds of the cache attention (tests/cache_bounds.py) rest on, without a GPU."""
+import numpy as np
+import torch
+
+
+def _e5m2(x):
+    return x.to(torch.float8_e5m2)
+
+
+def test_four_e5m2_terms_hold_every_f16_weight():
+    """p = t0 + t1 / 8 + t2 / 64 + t3 / 512 for every f16 value up to 2^15, the terms e5m2 roundings
+    of what the ones before leave, times 8; no term passes 2^15."""
+    h = torch.arange(0x7801, dtype=torch.int32).to(torch.int16).view(torch.float16)
+    assert h[-1] == 2.0 ** 15
+    rest, total = h.clone(), torch.zeros(len(h), dtype=torch.float64)
+    for t in range(4):
+        term = _e5m2(rest)
+        assert term.double().abs().max() <= 2.0 ** 15
+        total += term.double() / 8.0 ** t
+        rest = (rest - term.to(torch.float16)) * 8
+    assert torch.equal(total, h.double())
+    # an e5m2 code is the upper byte of that f16 value
+    term = _e5m2(h)
+    np.testing.assert_array_equal(term.view(torch.uint8).numpy().astype(np.int64) << 8,
+                                  term.to(torch.float16).view(torch.int16).numpy())

@@ -1,0 +1,107 @@
+"""The cache attention's weights and merges on the GPU, against bounds that do not grow with the
+length (tests/cache_bounds.py): a key that takes nearly all of a row's weight, long sequences in which
+every run of rows shows in the output."""
+import numpy as np
+import pytest
+import torch
+
+from tests import cache_bounds as cb
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _quantised(x):
+    """(codes, scales [Hkv, blocks]) of x [L, Hkv, D], scales as the cache's."""
+    L, H, D = x.shape
+    nb = -(-L // 32)
+    pad = np.concatenate([x, np.zeros((nb * 32 - L, H, D))]).reshape(nb, 32, H, D)
+    amax = np.abs(pad).max((1, 3))                                       # [nb, H]
+    s = np.exp2(np.ceil(np.log2(np.maximum(amax, 1e-30) / 448.0)).clip(-40, 40))
+    codes = torch.from_numpy((pad / s[:, None, :, None]).reshape(-1, H, D)[:L]).float().to(torch.float8_e4m3fn)
+    return codes, torch.from_numpy(s.T.copy()).float()
+
+
+def _run(kind, seqs, B, **how):
+    """[(q, k, v)] of one length repeated to a batch of B; the outputs of the first len(seqs), and the bounds'
+    inputs as the kernel sees them."""
+    import target_model_verify_gb300 as tv
+    L, Hkv, D = seqs[0][1].shape
+    n, Hq = seqs[0][0].shape[:2]
+    picked = [seqs[b % len(seqs)] for b in range(len(seqs))]
+    q = torch.stack([torch.from_numpy(s[0]).to(torch.bfloat16) for s in picked])
+    seen = []
+    many = lambda t: torch.cat([t.to(DEV)] * -(-B // len(seqs)))[:B].contiguous()  # noqa: E731
+    byte = lambda t: t.view(torch.uint8)                                          # noqa: E731
+    if kind == "masked":
+        k, v = (torch.stack([torch.from_numpy(s[x]).to(torch.bfloat16) for s in picked]) for x in (1, 2))
+        for b in range(len(seqs)):
+            seen.append((q[b].double().numpy(), k[b].double().numpy(), v[b].double().numpy(), None))
+        cache = (many(k), many(v))
+    else:
+        ks, vs = [_quantised(s[1]) for s in picked], [_quantised(s[2]) for s in picked]
+        for b in range(len(seqs)):
+            at = np.arange(L) // 32
+            sk, sv = ks[b][1].double().numpy().T[at], vs[b][1].double().numpy().T[at]      # [L, Hkv]
+            seen.append((q[b].double().numpy(), ks[b][0].double().numpy() * sk[..., None],
+                         vs[b][0].double().numpy() * sv[..., None], sv))
+        codes = [many(byte(torch.stack([x[0] for x in t]))).view(torch.float8_e4m3fn) for t in (ks, vs)]
+        cache = (*codes, *(many(torch.stack([x[1] for x in t])) for t in (ks, vs)))
+    lens = torch.full((B,), L, dtype=torch.int32, device=DEV)
+    if how.get("slopes") is not None:
+        how = dict(how, slopes=torch.tensor(how["slopes"], dtype=torch.float32, device=DEV))
+    ws = torch.empty(tv.cache_attention_workspace_bytes(B, n, Hq, Hkv, D, L), dtype=torch.uint8, device=DEV)
+    fn = tv.verify_attention_masked if kind == "masked" else tv.verify_attention_kv8
+    out = fn(many(q), *cache, lens, workspace=ws, **how)
+    again = fn(many(q), *cache, lens, workspace=ws, **how)
+    assert tv.read_status(ws) == 0
+    assert torch.equal(out, again)
+    for b in range(len(seqs), B):
+        if b >= B - len(seqs):                                           # the batch's far end, of equal inputs
+            # its parts are cut elsewhere: other partial sums, the same bounds
+            seen.append(seen[b % len(seqs)])
+    got = out[list(range(len(seqs))) + list(range(max(len(seqs), B - len(seqs)), B))].double().cpu().numpy()
+    return got, seen
+
+
+def _compare(kind, seqs, B, **how):
+    got, seen = _run(kind, seqs, B, **how)
+    for g, (q, k, v, sv) in zip(got, seen):
+        want, tol = cb.outputs_and_bounds(kind, q, k, v, sv, **how)
+        err = np.abs(g - want)
+        assert (err <= tol).all(), (kind, float((err / tol).max()), float(err.max()), float(np.abs(want).max()))
+
+
+@pytest.mark.parametrize("weight", [0.9, 0.98, 1 - 2.0 ** -10])
+@pytest.mark.parametrize("kind,B,n,Hq,Hkv,D,L", [
+    ("kv8", 32, 2, 16, 8, 128, 32768),         # many tiles: the cache on the M side
+    ("kv8", 40, 2, 16, 8, 128, 4096),
+    ("kv8", 3, 2, 16, 8, 128, 2000),           # few tiles: copies of the query rows
+    ("kv8", 2, 10, 8, 2, 128, 9000),           # 40 query rows
+    ("kv8", 2, 26, 8, 2, 64, 9000),            # 104 query rows, a lane each
+    ("kv8", 2, 2, 8, 2, 256, 9000),
+    ("masked", 8, 2, 16, 8, 128, 32768),
+    ("masked", 2, 26, 8, 2, 64, 9000),
+])
+def test_one_key_with_nearly_all_the_weight(kind, B, n, Hq, Hkv, D, L, weight):
+    """The first key takes `weight` of every row and has value 0: the output is what the other keys'
+    small weights say."""
+    rng = np.random.default_rng([B, D, L])
+    _compare(kind, [cb.with_sink(rng, n, Hq, Hkv, D, L, weight) for _ in range(2)], B)
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+def test_sharp_scores_and_a_sink(kind):
+    """Scores of three times the spread: the references move both ways."""
+    rng = np.random.default_rng(5)
+    _compare(kind, [cb.with_sink(rng, 2, 16, 8, 128, 4096, 0.98, sigma=3.0) for _ in range(2)], 40)
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,L", [(1, 2, 16, 8, 128, 40000), (40, 2, 16, 8, 128, 3000),
+                                            (40, 2, 16, 8, 128, 500), (2, 4, 8, 2, 128, 3000)])
+def test_sink_under_a_distance_bias(kind, B, n, Hq, Hkv, D, L):
+    """Biases from flat to steep: references go down block by block, as far as they may."""
+    rng = np.random.default_rng([B, L])
+    slopes = np.exp2(-np.arange(Hq) * 0.75).astype(np.float32)
+    _compare(kind, [cb.with_sink(rng, n, Hq, Hkv, D, L, 0.9) for _ in range(min(B, 2))], B, slopes=slopes)
