@@ -53,7 +53,11 @@
 //     columns stay zero, so the copies are independent online softmaxes,
 //     merged once per tile. The reference M moves only when a row's maximum
 //     passes it by 2^8 (the exponents have that headroom), so the output in
-//     tensor memory is rarely rescaled. Code for rare blocks (masks, moving
+//     tensor memory is rarely rescaled. f16 probabilities (e4m3 caches) have
+//     normal numbers down to 2^-21 of M: a block that stays below that moves M
+//     to 2^24 below its highest, so that the many small weights beside a
+//     dominant one keep their precision, down to 2^-45 of it; no further, so
+//     that sums and outputs stay finite. bf16 ones have fp32's exponents. Code for rare blocks (masks, moving
 //     references, huge exponents) stands outside the loop's line: the loop is
 //     longer than the nearest instruction cache, and jumps over unrolled code
 //     cost 500 cycles a block with a bias.
@@ -78,7 +82,11 @@ constexpr int kProducer = 8, kProducerV = 9, kIssuerS = 10, kIssuerO = 11;   // 
 constexpr int kThreads = 384;
 constexpr unsigned long long kDrainNs = 1000000000ull;
 constexpr int kStagePitch = 36 * 4;           // bytes: 32 floats, 16-byte accesses free of bank conflicts
-constexpr float kHeadroom = 8.f;              // log2 by which a maximum may pass its reference
+constexpr float kHeadroom = 8.f;              // log2 by which a maximum may pass its reference,
+constexpr float kBelow = 21.f;                // and stay below it (f16 probabilities)
+constexpr float kNear = 17.f;                 // (this far, when its warp rescales anyway)
+constexpr float kDeep = 24.f;                 // log2 by which a reference goes below its highest,
+constexpr float kReach = 45.f;                // for blocks no further below that than this
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kTileCost = 3;                  // units of work that a tile costs besides its blocks
 
@@ -1305,7 +1313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!kExtra) ck *= kLog2e;
 
-      float m_ref = -INFINITY, l = 0.f;
+      // m_low: what a block's maximum has to pass for its reference to go down
+      float m_ref = -INFINITY, m_peak = -INFINITY, m_low = INFINITY, l = 0.f;
       for (int ib = 0; ib < w.n_here; ++ib, ++n) {
         const int j0 = w.row(ib) + key0;
         const bool clean = w.clean(ib);
@@ -1383,12 +1392,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int run = 0; run < kRuns; ++run) top = fmaxf(top, largest<kRun>(x.f + run * kRun) + at[run]);
         }
         // ---- the reference follows the maximum when it has to ----
-        const bool need = mine && top > m_ref + kHeadroom;
-        if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
-          const float to = need ? top : m_ref;
-          const float alpha = need ? ex2(m_ref - to) : 1.f;
+        const bool up = mine && top > m_ref + kHeadroom, down = kE4m3 && top < m_ref - kBelow && top > m_low;
+        if (__builtin_expect(__any_sync(0xffffffffu, up || down), 0)) {
+          const float to = up ? top : kE4m3 && top < m_ref - kNear && top > m_low ? m_peak - kDeep : m_ref;
+          const float alpha = to != m_ref ? ex2(m_ref - to) : 1.f;
           l *= alpha;
           m_ref = to;
+          if constexpr (kE4m3) {
+            m_peak = fmaxf(m_peak, to);
+            m_low = to > m_peak - kDeep ? m_peak - kReach : INFINITY;
+          }
           if (ib > 0) {
             if (!warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1)) {
               dead = true;

@@ -19,13 +19,13 @@
 // Lane = key in the softmax, so a row's statistics run over lanes and warps.
 // Only its reference (the exponent of p = 2^15, the most of which a term can
 // hold eight times the rest) does not follow every maximum: it is set 2^6
-// above one, and moved when a block's largest p would pass 2^15 or stay below
-// 2^-14, where f16's normal numbers end. So a weight is off by at most 2^-11
+// above one when a block's largest p would pass 2^15, and to 2^24 below its
+// highest when that would stay below 2^-14, where f16's normal numbers end. So a weight is off by at most 2^-11
 // of itself, or below those by half of f16's last step, 2^-25: 2^-34 of the
 // row's largest and 2^-11 of the largest among its own 128 rows. (A key that
 // takes nearly all of a row's weight, as the first one does in many models,
-// leaves the small ones their precision.) References go down at most 2^24
-// below their highest, which keeps sums and outputs finite. One barrier per
+// leaves the small ones their precision, down to 2^-45 of it.) They go no
+// further down, so that sums and outputs stay finite. One barrier per
 // block, with votes, finds out whether one has to move; sums stay with the
 // keys' threads until the tile ends.
 //
@@ -58,8 +58,8 @@ static_assert(kKeyRows % 8 == 0 && kKeyTerms == 4 && kKeyRows <= kKeyLanes, "eig
 constexpr int kKeyQBytes = 2 * kKeyRows * kKeyD;        // [hi rows, lo rows][dims]
 constexpr int kKeyColS = 0, kKeyColO = 128;
 // log2: p at the reference; how far above a row's maximum that is set; how far
-// below it a block's maximum may lie; how far below its highest it may go
-constexpr float kBase = 15.f, kLift = 6.f, kFall = 29.f, kDeep = 24.f;
+// below it a block's maximum may lie (kDeep and kReach as in the other form)
+constexpr float kBase = 15.f, kLift = 6.f, kFall = 29.f;
 // tables per query buffer: of every row its score factor, slope, depth and
 // place in the output [32]; of every new position the rows that see it [128]
 constexpr int kKeyTab = 4 * kKeyLanes * 4 + 128 * 4;
@@ -598,12 +598,13 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
               uint32_t loud = 0, worth = 0;
 #pragma unroll
               for (int r = 0; r < kRows; r += 4) {
+                // how far each reference is below its highest: one at its end is not moved
                 const float4 p = lds128f(peaks + r * 4), m = lds128f(ref + r * 4);
-                const float least[4] = {p.x + m.x, p.y + m.y, p.z + m.z, p.w + m.w};
+                const float down[4] = {p.x + m.x, p.y + m.y, p.z + m.z, p.w + m.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   loud |= (y[r + k] > kBase - kFall ? 1u : 0u) << (r + k);
-                  worth |= (y[r + k] - (kBase - kDeep - kLift) > least[k] ? 1u : 0u) << (r + k);
+                  worth |= (down[k] < kDeep && y[r + k] > down[k] + (kBase - kLift - kReach) ? 1u : 0u) << (r + k);
                 }
               }
               loud = __reduce_or_sync(0xffffffffu, loud);
@@ -632,9 +633,11 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
             float M = __uint_as_float(lds32(red + lane * 4));
 #pragma unroll
             for (int x = 1; x < kSoftWarps; ++x) M = fmaxf(M, __uint_as_float(lds32(red + (x * 32 + lane) * 4)));
-            const float was = -__uint_as_float(lds32(ref + lane * 4)), to = M + kLift;
+            const float was = -__uint_as_float(lds32(ref + lane * 4));
             const float peak = __uint_as_float(lds32(peaks + lane * 4));
-            const bool move = M > was || (M < was - kFall && to > peak - kDeep);
+            const bool down = M < was - kFall && M > peak - kLift - kReach && was > peak - kDeep;
+            const bool move = M > was || down;
+            const float to = down ? peak - kDeep : M + kLift;
             if (move) sts32(peaks + lane * 4, __float_as_uint(fmaxf(peak, to)));
             sts32(ref + lane * 4, __float_as_uint(-(move ? to : was)));
             sts32(ref + kLanes * 4 + lane * 4, __float_as_uint(move ? ex2(was - to) : 1.f));

@@ -7,9 +7,11 @@ the scale of value row j (1 over a bf16 cache) and c_j = v_j / s_j:
   - masked: a weight is rounded to bf16, and the sum takes it as rounded, so o
     moves by at most 2^-8 sum_j w_j |v_j - o|;
   - kv8: a weight is rounded to f16, 2^-11 of it, and below f16's normal numbers
-    to a fixed step, half of which is at most 2^-32 of the largest w_j s_j. The
-    sum is not rounded. Together
-    2^-11 sum_j w_j |v_j| + 2^-32 max(w s) sum_j |c_j|;
+    to a fixed step, half of which is at most 2^-32 of the largest w_j s_j, and
+    at most 2^-11 of the largest among the cache rows that share a reference in
+    one block, no more than 128 (or those are below 2^-45 of the largest of
+    all). The sum is not rounded. Together 2^-11 sum_j w_j |v_j| +
+    sum_j max(min(2^-11 max_block(w s), 2^-32 max(w s)), 2^-45 max(w s)) |c_j|;
   - an error of at most e in every score moves o by at most
     e sum_j w_j |v_j - o| (to first order; e^2 of that is left to the slack).
     e: the product's sum over D terms runs through D / 16 tensor-core steps,
@@ -26,6 +28,8 @@ Nothing of this grows with the length.
 import math
 
 import numpy as np
+
+BLOCK = 128
 
 
 def sight(n, L, window=0, parent=None):
@@ -62,6 +66,7 @@ def outputs_and_bounds(kind, q, k, v, sv=None, scale=0.0, softcap=0.0, window=0,
     see, away = sight(n, L, window, parent)
     sv = np.ones((L, Hkv)) if sv is None else sv
     out, tol = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    edges = np.arange(0, L, BLOCK)
     for h in range(Hq):
         kk, vv, ss = k[:, h // G], v[:, h // G], sv[:, h // G]
         s = scale * (q[:, h] @ kk.T)
@@ -84,8 +89,9 @@ def outputs_and_bounds(kind, q, k, v, sv=None, scale=0.0, softcap=0.0, window=0,
             if kind == "masked":
                 t = t + 2.0 ** -8 * spread
             else:
-                seen = np.abs(vv / ss[:, None]) * see[i][:, None]
-                t = t + 2.0 ** -11 * (w[i] @ np.abs(vv)) + 2.0 ** -32 * (w[i] * ss).max() * seen.sum(0)
+                top = np.repeat(np.maximum.reduceat(w[i] * ss, edges), BLOCK)[:L]
+                step = np.maximum(np.minimum(2.0 ** -11 * top, 2.0 ** -32 * top.max()), 2.0 ** -45 * top.max())
+                t = t + 2.0 ** -11 * (w[i] @ np.abs(vv)) + (step * see[i] / ss) @ np.abs(vv)
             tol[i, h] = t * (1 + 2.0 ** -7)          # products of the above, and of them with the bf16 rounding
         if drop is not None:
             w = np.where(drop[None, :], 0.0, w)

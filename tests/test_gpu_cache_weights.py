@@ -90,6 +90,17 @@ def test_one_key_with_nearly_all_the_weight(kind, B, n, Hq, Hkv, D, L, weight):
     _compare(kind, [cb.with_sink(rng, n, Hq, Hkv, D, L, weight) for _ in range(2)], B)
 
 
+@pytest.mark.parametrize("weight", [0.999, 1 - 2.0 ** -14, 1 - 2.0 ** -20])
+@pytest.mark.parametrize("kind,B,n,Hq,Hkv,D,L", [
+    ("kv8", 40, 2, 16, 8, 128, 20000), ("kv8", 2, 2, 16, 8, 128, 9000), ("kv8", 2, 10, 8, 2, 128, 9000),
+    ("kv8", 2, 26, 8, 2, 64, 20000), ("kv8", 2, 2, 8, 2, 256, 9000), ("masked", 2, 2, 16, 8, 128, 9000),
+])
+def test_equal_weights_beside_a_dominant_one(kind, B, n, Hq, Hkv, D, L, weight):
+    """All other scores are equal, so that a rounding of their weights is the same for all and shows."""
+    rng = np.random.default_rng([B, D, L, 1])
+    _compare(kind, [cb.with_sink(rng, n, Hq, Hkv, D, L, weight, sigma=0.0) for _ in range(2)], B)
+
+
 @pytest.mark.parametrize("kind", ["kv8", "masked"])
 def test_sharp_scores_and_a_sink(kind):
     """Scores of three times the spread: the references move both ways."""
