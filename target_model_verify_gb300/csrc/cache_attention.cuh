@@ -1422,9 +1422,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- probabilities ----
         // f16 ones are kept 2^7 high: the headroom's 2^8 above that still fits,
         // and small weights stay normal numbers down to 2^-21.
-        const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - (kE4m3 ? 7.f : 0.f);
+        constexpr float kHigh = kE4m3 ? 7.f : 0.f;
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref, mu = ref - kHigh;
         // Exponents of 2^20 and more are rounded before the subtraction, as the
         // reference was: a fused one would bring out the reference's rounding.
+        // The 2^7 come last: from 2^24 on, less than a step, they would be lost
+        // or doubled in the reference, and 2^8 above it no f16 any more.
         float af[kSubs], bf[kRuns > kSubs ? kRuns : kSubs];    // exponent - reference = score * af + bf
 #pragma unroll
         for (int sub = 0; sub < kSubs; ++sub) af[sub] = kExtra ? 1.f : cs[sub];
@@ -1435,12 +1438,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kKpl; k += 2) {
             const float b = kExtra ? at[k / kRun % kRuns] : lv[k / kSubKeys];
             fma2(x.f[k], x.f[k + 1], af[k / kSubKeys], af[k / kSubKeys], b, b);
-            add2(x.f[k], x.f[k + 1], -mu, -mu);
+            add2(x.f[k], x.f[k + 1], -ref, -ref);
           }
 #pragma unroll
           for (int sub = 0; sub < kSubs; ++sub) af[sub] = 1.f;
 #pragma unroll
-          for (int run = 0; run < (kExtra ? kRuns : kSubs); ++run) bf[run] = 0.f;
+          for (int run = 0; run < (kExtra ? kRuns : kSubs); ++run) bf[run] = kHigh;
         }
         uint32_t pk[kKpl / 2];
         bool p_free = n < S::kPBufs;         // the product that last read this P buffer is done

@@ -116,3 +116,36 @@ def test_sink_under_a_distance_bias(kind, B, n, Hq, Hkv, D, L):
     rng = np.random.default_rng([B, L])
     slopes = np.exp2(-np.arange(Hq) * 0.75).astype(np.float32)
     _compare(kind, [cb.with_sink(rng, n, Hq, Hkv, D, L, 0.9) for _ in range(min(B, 2))], B, slopes=slopes)
+
+
+@pytest.mark.parametrize("cap", [0.0, 1000.0])
+@pytest.mark.parametrize("kind,B,D", [("kv8", 48, 64), ("kv8", 260, 128), ("masked", 48, 64)])
+def test_exponents_of_millions(kind, B, D, cap):
+    """Exponents of 2^24 and more, where fp32 has no fractions left: two equal scores, the second value
+    under a scale of up to 2^8 times the first's. Outputs stay between the two values."""
+    import target_model_verify_gb300 as tv
+    L, lead = 160, 20
+    q = torch.zeros(B, 1, 1, D)
+    q[..., 0] = 128.0
+    k = torch.zeros(B, L, 1, D)
+    k[..., 0] = -448.0
+    # odd sequences: all scores are negative
+    big = torch.tensor([448.0, 416.0, 384.0, 352.0, 320.0, 288.0])[torch.arange(B) // 2 % 6]
+    k[:, lead, 0, 0] = k[:, 128 + lead, 0, 0] = big * torch.tensor([1.0, -0.25])[torch.arange(B) % 2]
+    up = torch.tensor([2.0 ** 8, 2.0 ** 7, 2.0 ** 6, 2.0 ** 3])[torch.arange(B) // 12 % 4]
+    v = torch.zeros(B, L, 1, D)
+    v[:, lead] = 1.0
+    v[:, 128 + lead] = 2.0 if kind == "masked" else (2.0 / up)[:, None, None]
+    sk, sv = torch.ones(B, 1, 5), torch.ones(B, 1, 5)
+    sv[:, 0, 4] = up
+    lens = torch.full((B,), L, dtype=torch.int32, device=DEV)
+    q, k, v, sk, sv = (t.to(DEV) for t in (q, k, v, sk, sv))
+    for scale in (2.0 ** 6, 2.0 ** 8, 2.0 ** 9, 2.0 ** 10, 2.0 ** 12):
+        how = {"scale": scale, "softcap": cap}
+        if kind == "masked":
+            out = tv.verify_attention_masked(*(t.to(torch.bfloat16) for t in (q, k, v)), lens, **how)
+        else:
+            k8, v8 = (t.to(torch.float8_e4m3fn) for t in (k, v))
+            out = tv.verify_attention_kv8(q.to(torch.bfloat16), k8, v8, sk, sv, lens, **how)
+        assert out.isfinite().all(), (scale, out.isfinite().logical_not().nonzero()[:3])
+        assert ((out >= (0 if cap else 1)) & (out <= 2)).all(), scale
