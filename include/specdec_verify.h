@@ -361,7 +361,7 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
  * at most 1000; q, caches and out 16-byte aligned. A length that is neither 0
  * nor within [n_new, Lmax] sets SPECDEC_ERR_INVALID_ARG in the status word and
  * that sequence's output is 0; a device-side wait that ran out sets
- * SPECDEC_ERR_TIMEOUT, and the output is not to be used. The workspace does
+ * SPECDEC_ERR_TIMEOUT instead of that, and no output is to be used. The workspace does
  * not grow with B or Lmax. Asynchronous.
  */
 size_t specdec_verify_attention_kv8_workspace_size(int B, int n_new, int Hq, int Hkv, int D,
@@ -493,7 +493,8 @@ int specdec_read_status(const void* workspace, void* stream, int32_t* status);
  * MMA stage finds a barrier that nothing will ever arm. The wait gives up
  * after its bound (about 1 s), the kernel frees what it holds and returns,
  * and *status receives the status word it left: SPECDEC_ERR_TIMEOUT when the
- * detection works. Nothing faults, traps or hangs, and the CUDA context stays
+ * detection works (in place of the SPECDEC_ERR_INVALID_ARG that the kernel
+ * began with, as after a bad length: a timeout outranks the other codes). Nothing faults, traps or hangs, and the CUDA context stays
  * usable. Synchronises `stream`. workspace: at least
  * specdec_verify_workspace_size(1, 4, 64, 256, SPECDEC_BF16, SPECDEC_GREEDY)
  * bytes, 256-byte aligned; its contents are overwritten.

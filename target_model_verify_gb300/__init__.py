@@ -235,7 +235,8 @@ def append_kv8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, start, counts=N
     int32: rows to write (default n); rows [B, n] int32: which rows of k_new and v_new (default in
     order), so that append_kv8(..., start=root + 1, counts=n_accepted, rows=out_nodes) replaces a
     verified tree's rows by its accepted path's. Writes the cache in place and returns
-    (k_cache, v_cache, k_scale, v_scale).
+    (k_cache, v_cache, k_scale, v_scale). Entries that do not fit are found on the device: they are
+    skipped, and only read_status() of a workspace that the caller brought (256 bytes) tells.
     """
     if stream is not None:
         with _on(stream, k_new):
@@ -259,7 +260,9 @@ def verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale=
     alloc_kv8_cache() makes it and append_kv8() fills it, seq_lens [B] int32 with the new positions
     counted (0: unused slot, output 0). softcap > 0 caps the scores by a tanh, window > 0 limits
     the distance, slopes [Hq] float32 bias by distance, and parent (n_new ints as in verify_tree)
-    makes the new positions a token tree. Returns out [B, n_new, Hq, D] bf16.
+    makes the new positions a token tree. Returns out [B, n_new, Hq, D] bf16. A length that does not
+    fit the cache (its outputs are 0) and a device-side timeout (no output is to be used) are seen
+    only in read_status() of a workspace that the caller brought.
     """
     if stream is not None:
         with _on(stream, q):
