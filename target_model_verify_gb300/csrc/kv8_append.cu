@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
     }
     if (A.rows)
       for (long long e = threadIdx.x; e < (long long)A.B * A.n; e += 32 * kWarps) {
-        const int count = A.counts ? A.counts[e / A.n] : A.n;
-        const int i = (int)(e % A.n), src = A.rows[e];
-        if (i < count && (src < 0 || src >= A.n)) bad = 1;
+        // (a sequence's entries past its count are not read)
+        const int count = A.counts ? A.counts[e / A.n] : A.n, i = (int)(e % A.n);
+        if (i < count && (unsigned)A.rows[e] >= (unsigned)A.n) bad = 1;
       }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *A.status = bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
