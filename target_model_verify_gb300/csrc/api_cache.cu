@@ -137,7 +137,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.Lmax = Lmax;
   A.n_groups = pl.n_groups;
   A.group_pos = pl.group_pos;
-  A.window = window;
+  A.window = window < Lmax ? window : 0;      // no distance reaches Lmax, and the kernels' differences stay in 32 bits
   // at least two parts per head: with more heads than that, a CTA takes them all in turn
   A.head_lanes = 2 * Hkv <= kCacheAttnCtas ? Hkv : 1;
   A.note_tiles = 0;                          // the launch decides

@@ -52,3 +52,37 @@ def test_rows_table_may_end_with_the_last_count(n, counts):
     for x in (0, 1):
         np.testing.assert_array_equal(_f(cache[2 + x]), want[x][1])
         np.testing.assert_array_equal(_f(cache[x]), want[x][0])
+
+
+@pytest.mark.parametrize("B,D", [(3, 64), (130, 128)])
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+@pytest.mark.parametrize("parent", [None, (-1, 0, 0, 1, 3)], ids=str)
+def test_windows_to_the_end_of_32_bits(kind, B, D, parent):
+    """A window that no distance reaches is none, whatever its size; one that leaves out the first row
+    of the longest sequence alone does that."""
+    import target_model_verify_gb300 as tv
+    g = torch.Generator(device=DEV).manual_seed(2)
+    n, Hq, Hkv, Lmax = 5, 4, 2, 200
+    q = torch.randn(B, n, Hq, D, generator=g, device=DEV).to(torch.bfloat16)
+    k, v = (torch.randn(B, Lmax, Hkv, D, generator=g, device=DEV) for _ in range(2))
+    lens = torch.full((B,), Lmax, dtype=torch.int32, device=DEV)
+    lens[1] = 77
+    if kind == "masked":
+        cache = [k.to(torch.bfloat16), v.to(torch.bfloat16)]
+        call = lambda **how: tv.verify_attention_masked(q, *cache, lens, parent=parent, **how)      # noqa: E731
+        val = [_f(t[:2]) for t in cache]
+    else:
+        one = torch.ones(B, Hkv, 7, device=DEV)
+        cache = [k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)]
+        call = lambda **how: tv.verify_attention_kv8(q, *cache, one, one, lens, parent=parent, **how)   # noqa: E731
+        val = [_f(t[:2]) for t in cache]
+    base = call()
+    for window in (Lmax, Lmax + 1, 2 ** 31 - 200, 2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31, 2 ** 40):
+        assert torch.equal(call(window=window), base), window
+    top = Lmax - 1 if parent is None else Lmax - n + 3       # the deepest position's
+    got = _f(call(window=top)[:2])
+    want = oc.masked_attention(_f(q[:2]), *val, lens[:2].cpu().numpy(), window=top, parent=parent)
+    free = oc.masked_attention(_f(q[:2]), *val, lens[:2].cpu().numpy(), parent=parent)
+    assert np.abs(want[0, -1] - free[0, -1]).max() > 1e-4 and np.abs(want[1] - free[1]).max() == 0
+    # 2^-8 of the output and of the largest value (the weights), twice over for the scores
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 4 * 2.0 ** -8 * np.abs(val[1]).max()).all()
