@@ -170,8 +170,8 @@ std::pair<int, Tensor> cache_attention(const Tensor& q, const Tensor& k_cache, c
   }
   size_t bytes = 0;
   if (!workspace) {
-    bytes = specdec_verify_attention_kv8_workspace_size(narrow(B), narrow(n), narrow(Hq), narrow(Hkv), narrow(D),
-                                                        narrow(Lmax));
+    bytes = (e4m3 ? specdec_verify_attention_kv8_workspace_size : specdec_verify_attention_masked_workspace_size)(
+        narrow(B), narrow(n), narrow(Hq), narrow(Hkv), narrow(D), narrow(Lmax));
     if (bytes == 0) return {SPECDEC_ERR_UNSUPPORTED, out};
   }
   c10::DataPtr own;

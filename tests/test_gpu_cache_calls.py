@@ -86,3 +86,30 @@ def test_windows_to_the_end_of_32_bits(kind, B, D, parent):
     assert np.abs(want[0, -1] - free[0, -1]).max() > 1e-4 and np.abs(want[1] - free[1]).max() == 0
     # 2^-8 of the output and of the largest value (the weights), twice over for the scores
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 4 * 2.0 ** -8 * np.abs(val[1]).max()).all()
+
+
+def test_own_workspace_is_of_the_calls_own_size():
+    """A call without a workspace takes what its own size function says, and gives it back."""
+    import target_model_verify_gb300 as tv
+    shape = (4, 5, 32, 8, 128, 300)
+    B, n, Hq, Hkv, D, L = shape
+    b = tv._b
+    sizes = {"kv8": b.specdec_verify_attention_kv8_workspace_size(*shape),
+             "masked": b.specdec_verify_attention_masked_workspace_size(*shape)}
+    assert sizes["masked"] <= 0.75 * sizes["kv8"]               # else this shape shows nothing
+    q = torch.zeros(B, n, Hq, D, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    lens = torch.full((B,), L, dtype=torch.int32, device=DEV)
+    k8 = torch.zeros(B, L, Hkv, D, device=DEV).to(torch.float8_e4m3fn)
+    one = torch.ones(B, Hkv, -(-L // 32), device=DEV)
+    k16 = torch.zeros(B, L, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    for kind, call in (("kv8", lambda: tv.verify_attention_kv8(q, k8, k8, one, one, lens, out=out)),
+                       ("masked", lambda: tv.verify_attention_masked(q, k16, k16, lens, out=out))):
+        call()
+        torch.cuda.synchronize()
+        held = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        call()
+        assert torch.cuda.memory_allocated() == held
+        took = torch.cuda.max_memory_allocated() - held
+        assert sizes[kind] <= took <= sizes[kind] + 512, (kind, took, sizes)
