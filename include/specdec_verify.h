@@ -357,8 +357,8 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
  * Limits: D = 64, 128 or 256, 1 <= n_new <= SPECDEC_MAX_TREE_NODES, Hq % Hkv
  * == 0, Hq / Hkv <= 128, Hq <= 2^20, q_stride < 2^31, B * n_new * Hq < 2^31,
  * n_new <= Lmax <= 2^30, B * Lmax * Hkv * D < 2^40, B * Hkv * n_new * (Lmax /
- * 64 + 8) < 2^31; scale and softcap, where positive, at least 1e-30, softcap
- * at most 1000; q, caches and out 16-byte aligned. A length that is neither 0
+ * 64 + 8) < 2^31; scale and softcap, where positive, at least 1e-30, scale
+ * at most 1e30, softcap at most 1000; q, caches and out 16-byte aligned. A length that is neither 0
  * nor within [n_new, Lmax] sets SPECDEC_ERR_INVALID_ARG in the status word and
  * that sequence's output is 0; a device-side wait that ran out sets
  * SPECDEC_ERR_TIMEOUT instead of that, and no output is to be used. The workspace does

@@ -106,7 +106,8 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
     return SPECDEC_ERR_INVALID_ARG;
   // its reciprocal is used, and the tanh rounds to 2^-22 of it
   if (softcap > 0.f && (softcap < 1e-30f || softcap > 1000.f)) return SPECDEC_ERR_INVALID_ARG;
-  if (scale > 0.f && scale < 1e-30f) return SPECDEC_ERR_INVALID_ARG;
+  // factors of the scores stay normal numbers, and a score of 0 stays 0
+  if (scale > 0.f && (scale < 1e-30f || scale > 1e30f)) return SPECDEC_ERR_INVALID_ARG;
   CacheAttnLaunch A;
   A.tree = parent != nullptr;
   A.max_depth = n_new - 1;

@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <limits>
 #include <string>
 
 #include "specdec_verify.h"
@@ -75,6 +76,9 @@ void check_scales(const Tensor& k, const Tensor& ks, const Tensor& vs) {
   }
 }
 constexpr const char* kCodes = "the caches must be contiguous float8_e4m3fn CUDA tensors [B, Lmax, Hkv, D]";
+
+// Positive numbers too small for fp32 stay positive: 0 would mean the default.
+float to_float(double x) { return x > 0 && (float)x == 0.f ? std::numeric_limits<float>::denorm_min() : (float)x; }
 
 int narrow(int64_t x) { return (int)std::min<int64_t>(x, INT32_MAX); }   // the C call refuses what it cannot hold
 
@@ -185,12 +189,12 @@ std::pair<int, Tensor> cache_attention(const Tensor& q, const Tensor& k_cache, c
       e4m3 ? specdec_verify_attention_kv8(q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(),
                                           ptr<float>(k_scale), ptr<float>(v_scale), ptr<int32_t>(seq_lens), pp,
                                           ptr<float>(slopes), narrow(B), narrow(n), narrow(Hq), narrow(Hkv),
-                                          narrow(D), narrow(Lmax), (float)scale, (float)softcap, win,
+                                          narrow(D), narrow(Lmax), to_float(scale), to_float(softcap), win,
                                           out.data_ptr(), ws, have, stream)
            : specdec_verify_attention_masked(q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(),
                                              ptr<int32_t>(seq_lens), pp, ptr<float>(slopes), narrow(B), narrow(n),
-                                             narrow(Hq), narrow(Hkv), narrow(D), narrow(Lmax), (float)scale,
-                                             (float)softcap, win, out.data_ptr(), ws, have, stream);
+                                             narrow(Hq), narrow(Hkv), narrow(D), narrow(Lmax), to_float(scale),
+                                             to_float(softcap), win, out.data_ptr(), ws, have, stream);
   return {rc, out};
 }
 

@@ -113,3 +113,18 @@ def test_own_workspace_is_of_the_calls_own_size():
         assert torch.cuda.memory_allocated() == held
         took = torch.cuda.max_memory_allocated() - held
         assert sizes[kind] <= took <= sizes[kind] + 512, (kind, took, sizes)
+
+
+def test_numbers_too_small_for_fp32_are_refused():
+    """As fp32 they would be 0, which selects the default scale, or no cap."""
+    import target_model_verify_gb300 as tv
+    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    k8 = torch.zeros(1, 40, 2, 64, device=DEV).to(torch.float8_e4m3fn)
+    one = torch.ones(1, 2, 2, device=DEV)
+    lens = _i([40])
+    for how in ({"scale": 1e-50}, {"softcap": 1e-50}, {"scale": 1e-38}, {"scale": 1e31}, {"scale": float("inf")},
+                {"softcap": float("nan")}, {"scale": float("nan")}):
+        with pytest.raises(tv.SpecdecError):
+            tv.verify_attention_kv8(q, k8, k8, one, one, lens, **how)
+        with pytest.raises(tv.SpecdecError):
+            tv.verify_attention_masked(q, k8.to(torch.bfloat16), k8.to(torch.bfloat16), lens, **how)
