@@ -120,7 +120,8 @@ def native():
         path = os.path.join(os.path.dirname(LIB_PATH), "_native.so")
         if not os.path.exists(path):
             raise ImportError(
-                f"{path} is missing: build it with `python -m target_model_verify_gb300.build`")
+                f"{path} is missing: build it with `python -m target_model_verify_gb300.build` "
+                "(g++, PyTorch's headers)")
         import importlib.util
         spec = importlib.util.spec_from_file_location("_native", path)
         module = importlib.util.module_from_spec(spec)
