@@ -8,7 +8,8 @@ the CUDA runtime linked statically. csrc/native.cpp (argument marshalling
 against PyTorch's headers) compiles alongside with the host compiler into
 _lib/_native.so; where that fails (no PyTorch, none of its headers), the
 library is built all the same and only the operators that need the module
-raise. Each is rebuilt only when one of its sources or headers is newer.
+raise. Each is rebuilt only when one of its sources or headers is newer, the
+module also for another PyTorch or Python.
 """
 from __future__ import annotations
 
@@ -60,8 +61,25 @@ def _library_up_to_date() -> bool:
     return _newer_than(LIB_PATH, _sources() + _headers() + [__file__])
 
 
+def _torch_id() -> str:
+    """What the module is built against: the Python, and PyTorch's version and place."""
+    import importlib.metadata
+    import importlib.util
+    try:
+        spec, version = importlib.util.find_spec("torch"), importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        spec, version = None, "none"
+    return f"{sys.implementation.cache_tag} torch {version} {spec.origin if spec else ''}\n"
+
+
 def _native_up_to_date() -> bool:
-    return _newer_than(NATIVE_PATH, glob.glob(os.path.join(INCLUDE, "*.h")) + [NATIVE_SRC, __file__])
+    if not _newer_than(NATIVE_PATH, glob.glob(os.path.join(INCLUDE, "*.h")) + [NATIVE_SRC, __file__]):
+        return False
+    try:
+        with open(os.path.join(BUILD_DIR, "native.for"), encoding="utf-8") as f:
+            return f.read() == _torch_id()
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
@@ -109,6 +127,8 @@ def _link_native(obj: str) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"linking _native.so failed:\n{res.stderr}")
+    with open(os.path.join(BUILD_DIR, "native.for"), "w", encoding="utf-8") as f:
+        f.write(_torch_id())
     os.replace(tmp, NATIVE_PATH)
 
 

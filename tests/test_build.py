@@ -63,3 +63,21 @@ def test_a_failing_kernel_fails_the_build(sandbox):
     fail.add("nvcc")
     with pytest.raises(RuntimeError):
         libbuild.build()
+
+
+def test_another_pytorch_makes_the_module_stale(sandbox, monkeypatch):
+    ran, _ = sandbox
+    libbuild.build()
+    assert libbuild.up_to_date()
+    monkeypatch.setattr(libbuild, "_torch_id", lambda: "cpython-399 torch 9.9 elsewhere\n", raising=False)
+    assert not libbuild.up_to_date()
+    del ran[:]
+    libbuild.build()
+    assert {name for name, _ in ran} == {"g++"}                     # the module alone
+    assert libbuild.up_to_date()
+
+
+def test_the_module_names_the_pytorch_it_is_for():
+    import torch
+    assert torch.__version__.split("+")[0] in libbuild._torch_id()
+    assert os.path.dirname(torch.__file__) in libbuild._torch_id()
