@@ -406,10 +406,6 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Co
         "r"(x[30]), "r"(x[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* x, Cols<64>) {
-  tmem_store(taddr, x, Cols<32>{});
-  tmem_store(taddr + 32, x + 32, Cols<32>{});
-}
 __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -1047,6 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_store();
           tc_fence_before();
         } else {
+          static_assert(S::kPanelBytes == 128, "256 dims");
           constexpr int kCh = kD / 8;                    // lanes per row, 8 dims each
           const int pos0 = t.g * A.group_pos;
           const int rows = min(A.group_pos, A.n_new - pos0) * A.G;
@@ -1089,13 +1086,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               hi[k] = ph[0] | (ph[1] << 16);
               lo[k] = pl[0] | (pl[1] << 16);
             }
-            const int d0 = c * 8, p = d0 / S::kPanelBytes, cc = (d0 % S::kPanelBytes) / 16;
+            const int d0 = c * 8, p = d0 / 128, cc = (d0 % 128) / 16;
 #pragma unroll
             for (int copy = 0; copy < S::kCopies; ++copy) {
               const int rr = copy * kRP + r;
-              const int x = S::kPanelBytes == 128 ? (rr & 7) : ((rr >> 1) & 3);
-              const uint32_t dst = qb + p * 128 * S::kPanelBytes + rr * S::kPanelBytes +
-                                   ((cc ^ x) << 4) + (d0 & 8);
+              const uint32_t dst = qb + p * 128 * 128 + rr * 128 + ((cc ^ (rr & 7)) << 4) + (d0 & 8);
               sts64(dst, hi[0], hi[1]);
               sts64(dst + S::kQTerm, lo[0], lo[1]);
             }
