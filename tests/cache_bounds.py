@@ -53,11 +53,11 @@ def sight(n, L, window=0, parent=None):
 
 
 def outputs_and_bounds(kind, q, k, v, sv=None, scale=0.0, softcap=0.0, window=0, slopes=None, parent=None,
-                       drop=None):
+                       without=0):
     """(o, bound), each [n, Hq, D], of one sequence: q [n, Hq, D], k and v [L, Hkv, D], sv [L, Hkv].
 
-    drop: rows [L] whose weights are left out of o (what a lost partial would do); the bound is the
-    whole sequence's either way.
+    without: also [blocks]: for every run of that many rows, how many times its bound some output
+    moves when the run is left out (what a lost partial would do).
     """
     n, Hq, D = q.shape
     L, Hkv, _ = k.shape
@@ -67,6 +67,7 @@ def outputs_and_bounds(kind, q, k, v, sv=None, scale=0.0, softcap=0.0, window=0,
     sv = np.ones((L, Hkv)) if sv is None else sv
     out, tol = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
     edges = np.arange(0, L, BLOCK)
+    shows = np.zeros(-(-L // without)) if without else None
     for h in range(Hq):
         kk, vv, ss = k[:, h // G], v[:, h // G], sv[:, h // G]
         s = scale * (q[:, h] @ kk.T)
@@ -93,12 +94,14 @@ def outputs_and_bounds(kind, q, k, v, sv=None, scale=0.0, softcap=0.0, window=0,
                 step = np.maximum(np.minimum(2.0 ** -11 * top, 2.0 ** -32 * top.max()), 2.0 ** -45 * top.max())
                 t = t + 2.0 ** -11 * (w[i] @ np.abs(vv)) + (step * see[i] / ss) @ np.abs(vv)
             tol[i, h] = t * (1 + 2.0 ** -7)          # products of the above, and of them with the bf16 rounding
-        if drop is not None:
-            w = np.where(drop[None, :], 0.0, w)
-            with np.errstate(invalid="ignore", divide="ignore"):
-                o = w @ vv / w.sum(1, keepdims=True)
+            if without:
+                runs = np.arange(0, L, without)
+                lost = np.add.reduceat(w[i][:, None] * vv, runs)                   # [blocks, D]
+                share = np.add.reduceat(w[i], runs)[:, None]
+                moved = np.abs((o[i] - lost) / np.maximum(1 - share, 1e-30) - o[i])
+                shows = np.maximum(shows, (moved / tol[i, h]).max(1))
         out[:, h] = o
-    return out, tol
+    return (out, tol, shows) if without else (out, tol)
 
 
 # ------------------------------------------------------------------ inputs --

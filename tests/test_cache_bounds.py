@@ -1,6 +1,9 @@
 """What the bounds of the cache attention (tests/cache_bounds.py) rest on, without a GPU."""
 import numpy as np
+import pytest
 import torch
+
+from tests import cache_bounds as cb
 
 
 def _e5m2(x):
@@ -23,3 +26,18 @@ def test_four_e5m2_terms_hold_every_f16_weight():
     term = _e5m2(h)
     np.testing.assert_array_equal(term.view(torch.uint8).numpy().astype(np.int64) << 8,
                                   term.to(torch.float16).view(torch.int16).numpy())
+
+
+# The shapes of one sequence whose tiles are shared by many CTAs; 64 rows are the smallest block.
+SHARED = [(2, 4, 1, 128, 20000), (2, 4, 2, 256, 9001), (40, 1, 1, 64, 5000), (9, 16, 2, 128, 4001), (3, 8, 8, 128, 33001)]
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+@pytest.mark.parametrize("n,Hq,Hkv,D,L", SHARED)
+def test_no_run_of_rows_can_be_lost_unnoticed(kind, n, Hq, Hkv, D, L):
+    """Leaving out any 64 rows (a partial that the merge drops holds more) moves some output by more
+    than three times its bound."""
+    q, k, v = cb.with_marks(np.random.default_rng([n, L]), n, Hq, Hkv, D, L)
+    _, _, shows = cb.outputs_and_bounds(kind, q[:, :1], k[:, :1], v[:, :1], without=64)
+    shows = shows[:(L - n) // 64]                # the rest is not seen by every position
+    assert shows.min() > 3, (shows.min(), shows.argmin())

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import cache as oc
+from tests.test_gpu_cache_attention import _call, _check, _inputs
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -128,3 +129,20 @@ def test_numbers_too_small_for_fp32_are_refused():
             tv.verify_attention_kv8(q, k8, k8, one, one, lens, **how)
         with pytest.raises(tv.SpecdecError):
             tv.verify_attention_masked(q, k8.to(torch.bfloat16), k8.to(torch.bfloat16), lens, **how)
+
+
+@pytest.mark.parametrize("kind", ["kv8", "kv8_keys", "masked"])
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,Lmax,how", [
+    (2, 3, 16, 1, 128, 200, {}),                   # 16 query heads per KV head: 48 rows
+    (1, 5, 128, 1, 64, 150, {"window": 33}),       # 128: a group of rows per position
+    (2, 2, 192, 2, 256, 140, {"softcap": 9.0}),    # 96
+    (2, 4, 14, 2, 128, 260, {"window": 100}),      # 7
+    (1, 26, 40, 8, 64, 300, {}),                   # 5, 130 rows: two groups of 13 positions
+    (2, 6, 8, 2, 128, 300, {}),                    # 24 rows: the most that the form by keys takes
+    (2, 3, 16, 2, 128, 300, {"softcap": 9.0}),     # 24
+    (2, 25, 2, 2, 128, 300, {}),                   # 25: one more
+    (2, 8, 8, 2, 128, 300, {"window": 150}),       # 32
+])
+def test_query_heads_per_kv_head(kind, B, n, Hq, Hkv, D, Lmax, how):
+    q, cache, lens = _inputs(kind, B + Hq, B, n, Hq, Hkv, D, Lmax)
+    _check(kind, q, cache, lens, _call(kind, q, cache, lens, **how), **how)

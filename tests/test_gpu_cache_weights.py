@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests import cache_bounds as cb
+from tests.test_cache_bounds import SHARED
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -149,3 +150,21 @@ def test_exponents_of_millions(kind, B, D, cap):
             out = tv.verify_attention_kv8(q.to(torch.bfloat16), k8, v8, sk, sv, lens, **how)
         assert out.isfinite().all(), (scale, out.isfinite().logical_not().nonzero()[:3])
         assert ((out >= (0 if cap else 1)) & (out <= 2)).all(), scale
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,L", [(1, *s) for s in SHARED] + [
+    (3, 2, 8, 2, 128, 5000),        # three sequences over every CTA
+    (40, 2, 16, 8, 128, 3000),      # more tiles than CTAs, cut anywhere
+    (2, 4, 100, 100, 64, 1500),     # more heads than CTAs side by side
+])
+def test_every_part_of_a_shared_tile_reaches_the_output(kind, B, n, Hq, Hkv, D, L):
+    """Values in which every 64 rows show (test_no_run_of_rows_can_be_lost_unnoticed)."""
+    _compare(kind, [cb.with_marks(np.random.default_rng([n, L, b]), n, Hq, Hkv, D, L) for b in range(min(B, 2))], B)
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+@pytest.mark.parametrize("how", [{"window": 4000}, {"softcap": 20.0}, {"parent": (-1, 0, 0, 1), "window": 7001},
+                                 {"scale": 0.03}], ids=str)
+def test_shared_tiles_with_options(kind, how):
+    _compare(kind, [cb.with_marks(np.random.default_rng(9), 4, 8, 2, 128, 9001)], 1, **how)
