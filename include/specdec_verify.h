@@ -353,7 +353,7 @@ int specdec_kv8_append(const void* k_new, long long k_stride, const void* v_new,
  * the positions that see the row; a query row that holds one gives NaN (kv8). Softmax and
  * sums in fp32; the probabilities enter the value product as f16, held to 2^-32
  * of the row's largest or better (kv8), or as bf16 (masked); the queries enter the score product as bf16 (masked) or as two
- * e4m3 terms, exact to 2^-18 of the row's largest element (kv8).
+ * e4m3 terms, off by at most 2^-17 of the row's largest element (kv8).
  * Limits: D = 64, 128 or 256, 1 <= n_new <= SPECDEC_MAX_TREE_NODES, Hq % Hkv
  * == 0, Hq / Hkv <= 128, Hq <= 2^20, q_stride < 2^31, B * n_new * Hq < 2^31,
  * n_new <= Lmax <= 2^30, B * Lmax * Hkv * D < 2^40, B * Hkv * n_new * (Lmax /

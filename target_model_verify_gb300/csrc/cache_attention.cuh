@@ -44,8 +44,8 @@
 //     of two tensor-memory buffers, a block ahead of the softmax. bf16:
 //     kind::f16. e4m3: kind::f8f6f4 on the codes as they lie; the query row,
 //     scaled by a power of two to below 256, is the sum of two e4m3 terms
-//     (4 + 4 significant bits hold a bf16 value exactly down to 2^-10 of the
-//     row's largest, and to 2^-18 of it below), so two products accumulate.
+//     (4 + 4 significant bits hold a bf16 value exactly down to 2^-9 of the
+//     row's largest, and to within 2^-17 of it below), so two products accumulate.
 //   softmax: lane = query row, so maxima and sums need no exchange. With
 //     R <= 64 query rows the 128 lanes hold 128 / RP copies of the rows (RP =
 //     32 or 64) and each copy takes its own share of every block's keys; its

@@ -41,3 +41,18 @@ def test_no_run_of_rows_can_be_lost_unnoticed(kind, n, Hq, Hkv, D, L):
     _, _, shows = cb.outputs_and_bounds(kind, q[:, :1], k[:, :1], v[:, :1], without=64)
     shows = shows[:(L - n) // 64]                # the rest is not seen by every position
     assert shows.min() > 3, (shows.min(), shows.argmin())
+
+
+def test_two_e4m3_terms_of_a_query_row():
+    """Every bf16 value under every largest element in [2^7, 2^8): exact from 2^-9 of that on, else off
+    by at most 2^-17 of it, which occurs."""
+    x = torch.arange(0x4380, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).double()    # 0 .. 2^8
+    x = x[x < 256]
+    e4m3 = lambda t: t.float().to(torch.float8_e4m3fn).double()                              # noqa: E731
+    hi = e4m3(x)
+    off = (x - hi - e4m3(x - hi)).abs()
+    for largest in x[x >= 128].tolist():
+        here = x <= largest
+        assert not off[here & (x >= largest * 2.0 ** -9)].any()
+        assert (off[here] <= 2.0 ** -17 * largest).all()
+    assert off.max() == 2.0 ** -17 * 128 and float(x[off.argmax()]) < 1
