@@ -146,3 +146,10 @@ def test_numbers_too_small_for_fp32_are_refused():
 def test_query_heads_per_kv_head(kind, B, n, Hq, Hkv, D, Lmax, how):
     q, cache, lens = _inputs(kind, B + Hq, B, n, Hq, Hkv, D, Lmax)
     _check(kind, q, cache, lens, _call(kind, q, cache, lens, **how), **how)
+
+
+@pytest.mark.parametrize("kind,B,D", [("kv8", 3, 128), ("kv8", 1, 256), ("masked", 2, 256)])
+def test_many_kv_heads_in_every_form(kind, B, D):
+    """More KV heads than can have CTAs side by side; the first in the form for many tiles."""
+    q, cache, lens = _inputs(kind, 31, B, 2, 200, 100, D, 300, lens=[300, 131, 2][:B])
+    _check(kind, q, cache, lens, _call(kind, q, cache, lens))
