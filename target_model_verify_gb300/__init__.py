@@ -277,7 +277,8 @@ def verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale=
 
 def verify_attention_masked(q, k_cache, v_cache, seq_lens, scale=0.0, softcap=0.0, window=0, slopes=None,
                             parent=None, out=None, workspace=None, stream=None):
-    """verify_attention_kv8() over a bf16 cache k_cache, v_cache [B, Lmax, Hkv, D]."""
+    """verify_attention_kv8() over a bf16 cache k_cache, v_cache [B, Lmax, Hkv, D] (out bf16, where
+    verify_attention()'s is float32)."""
     if stream is not None:
         with _on(stream, q):
             return verify_attention_masked(q, k_cache, v_cache, seq_lens, scale, softcap, window, slopes, parent,

@@ -13,10 +13,10 @@
 //
 // Bound: HBM (each K and V row is read once per group of up to 128 query
 // rows). Measured on a GB300 (graph replays; copy peak 6771 GB/s): 64 x 4096
-// bf16 rows, 5 positions, 32 query / 8 KV heads of 128: 161 us for 1074 MB,
-// 0.98 of the copy peak (16 positions: 163 us); a tree of 26 over 8 x 4096:
-// 37 us for 136 MB, where starting, the softmax of 128 lanes and the merge
-// show; the tree over 32 x 4096 e4m3 rows: 110 us for 268 MB (130 with a
+// bf16 rows, 5 positions, 32 query / 8 KV heads of 128: 160 us for 1074 MB,
+// 0.99 of the copy peak (16 positions: 160 us); a tree of 26 over 8 x 4096:
+// 35 us for 136 MB, where starting, the softmax of 128 lanes and the merge
+// show; the tree over 32 x 4096 e4m3 rows: 103 us for 268 MB (131 with a
 // bias), bound by the softmax (one warp per scheduler takes 0.9 us for a
 // lane's 64 scores).
 //
@@ -64,7 +64,8 @@
 //   O += P V: P from tensor memory, V the MN-major operand, kind::f16. e4m3
 //     values are widened to f16 (exact) by the auxiliary warps into a second
 //     shared-memory tile, since P needs f16's 11 bits and both operands share
-//     a type; bf16 values are used as they land.
+//     a type; bf16 values are used as they land, and P is bf16 for the same
+//     reason (the sum takes it as rounded, see below).
 #pragma once
 
 #include <cuda_fp16.h>

@@ -18,8 +18,13 @@
 // that more warps are resident. Measured (8 KV heads of 128): 2.3 us for one
 // sequence's 5 rows (a launch's latency), 5.1 us for 256 sequences' (7.9 MB),
 // 8.3 us for four ragged prompts of 3206 rows in all (19.7 MB, 2370 GB/s; 8.4
-// us with one warp per block): one wave of short warps, each a chain of three
-// dependent trips to memory.
+// us with one warp per block). A warp is a chain of two dependent trips to
+// memory (its sequence's start and count, then rows and scale side by side;
+// with a table of rows three) and the write. The grid has room for n rows of
+// every sequence, so most of the prompts' 4129 CTAs (five per SM, more than
+// five waves) find nothing to do. The tables are checked by one CTA: tree
+// commits of 26 nodes take 3.1 us for 16 sequences, 6.8 for 64, 23.2 for 256
+// (10.5 without the table of rows).
 #include <cuda_fp16.h>
 
 #include "kernels.h"
