@@ -153,3 +153,64 @@ def test_many_kv_heads_in_every_form(kind, B, D):
     """More KV heads than can have CTAs side by side; the first in the form for many tiles."""
     q, cache, lens = _inputs(kind, 31, B, 2, 200, 100, D, 300, lens=[300, 131, 2][:B])
     _check(kind, q, cache, lens, _call(kind, q, cache, lens))
+
+
+def _layer(seed, B, n, Hq, Hkv, D, Lmax):
+    """One layer's step as a program holds it, and the call that runs it: append, then both attentions."""
+    import target_model_verify_gb300 as tv
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)     # noqa: E731
+    cache = tv.alloc_kv8_cache(B, Lmax, Hkv, D, device=DEV)
+    tv.append_kv8(rnd(B, Lmax, Hkv, D), rnd(B, Lmax, Hkv, D), *cache, torch.zeros(B, dtype=torch.int32, device=DEV))
+    q, k, v = rnd(B, n, Hq, D), rnd(B, n, Hkv, D), rnd(B, n, Hkv, D)
+    kb, vb = rnd(B, Lmax, Hkv, D), rnd(B, Lmax, Hkv, D)
+    lens = torch.randint(n + 40, Lmax + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    start = lens - n
+
+    def step():
+        tv.append_kv8(k, v, *cache, start)
+        a = tv.verify_attention_kv8(q, *cache, lens)
+        tv.append_kv8(v, k, *cache, start)                     # over the same rows: the next call sees these
+        b = tv.verify_attention_kv8(q, *cache, lens, softcap=20.0, window=50)
+        c = tv.verify_attention_masked(q, kb, vb, lens, window=90)
+        tv.append_kv8(k, v, *cache, start)
+        return a, b, c
+    return step
+
+
+def test_steps_on_two_streams_and_in_graphs():
+    """Steps of two layers, each a chain of calls that begin before the last one ends: run alone, side by
+    side on two streams, and captured and replayed side by side, they give the same bits."""
+    layers = [_layer(1, 40, 5, 16, 8, 128, 700), _layer(2, 3, 26, 16, 4, 128, 900), _layer(3, 5, 4, 8, 2, 256, 300)]
+    layers = [(layers[0], layers[1]), (layers[0], layers[2]), (layers[1], layers[2])]
+    for pair in layers:
+        alone = []
+        for step in pair:
+            step()
+            torch.cuda.synchronize()
+            alone.append([t.clone() for t in step()])
+            torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in pair]
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        got = [[], []]
+        for _ in range(6):
+            for x, (step, s) in enumerate(zip(pair, streams)):
+                with torch.cuda.stream(s):
+                    got[x].append(step())
+        torch.cuda.synchronize()
+        graphs, outs = [], []
+        for step, s in zip(pair, streams):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                outs.append([step() for _ in range(3)])
+            graphs.append(graph)
+        for _ in range(4):
+            for graph, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for x in (0, 1):
+            for one in got[x] + outs[x]:
+                for a, b in zip(one, alone[x]):
+                    assert torch.equal(a, b)
