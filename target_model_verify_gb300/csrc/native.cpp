@@ -9,7 +9,7 @@
 #include <torch/csrc/utils/pybind.h>
 
 #include <limits>
-#include <string>
+#include <vector>
 
 #include "specdec_verify.h"
 
@@ -154,7 +154,11 @@ std::pair<int, Tensor> cache_attention(const Tensor& q, const Tensor& k_cache, c
   }
   std::vector<int32_t> par;
   if (!parent.is_none()) {
-    par = parent.cast<std::vector<int32_t>>();
+    try {
+      for (const py::handle x : parent) par.push_back(x.cast<int32_t>());
+    } catch (const py::cast_error&) {
+      throw py::type_error("parent must hold 32-bit integers");
+    }
     check_value((int64_t)par.size() == n, "parent must have one entry per new position");
   }
   for (const Tensor* t : {&k_cache, &v_cache, &seq_lens}) same_device(q, *t);

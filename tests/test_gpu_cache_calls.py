@@ -214,3 +214,21 @@ def test_steps_on_two_streams_and_in_graphs():
             for one in got[x] + outs[x]:
                 for a, b in zip(one, alone[x]):
                     assert torch.equal(a, b)
+
+
+def test_parent_in_every_form_that_verify_tree_takes():
+    """Lists, tuples, arrays, tensors and iterators of ints; nothing else."""
+    import target_model_verify_gb300 as tv
+    q, cache, lens = _inputs("kv8", 40, 2, 5, 4, 2, 64, 90, lens=[90, 40])
+    tree = [-1, 0, 0, 1, 3]
+    base = _call("kv8", q, cache, lens, parent=tree)
+    _check("kv8", q, cache, lens, base, parent=tree)
+    for parent in (tuple(tree), np.array(tree), np.array(tree, dtype=np.int32), torch.tensor(tree), iter(tree),
+                   (p for p in tree), map(int, tree)):
+        assert torch.equal(tv.verify_attention_kv8(q, *cache, lens, parent=parent), base), type(parent)
+    for parent in ([-1, 0, 0, 1, 2 ** 40], [-1, 0, 0, 1, 1.5], [-1, 0, 0, 1, None], "abcde", 5, [[-1], [0], [0], [1], [3]]):
+        with pytest.raises(TypeError):
+            tv.verify_attention_kv8(q, *cache, lens, parent=parent)
+    for parent in ([], tree[:4], iter(tree[:2])):
+        with pytest.raises(ValueError):
+            tv.verify_attention_kv8(q, *cache, lens, parent=parent)
