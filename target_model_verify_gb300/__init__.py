@@ -215,6 +215,14 @@ def _on(stream, t):
     return torch.cuda.stream(stream)
 
 
+def _handed_over(got, given):
+    """An output that a call on a stream of its own allocated there: its memory is not given to that
+    stream again while the caller's still uses it."""
+    if given is None:
+        got.record_stream(torch.cuda.current_stream(got.device))
+    return got
+
+
 def alloc_kv8_cache(B, Lmax, Hkv, D, device=None):
     """(k_cache, v_cache, k_scale, v_scale) of an empty 8-bit cache: float8_e4m3fn codes
     [B, Lmax, Hkv, D] and float32 scales [B, Hkv, ceil(Lmax / KV8_BLOCK)]."""
@@ -266,8 +274,9 @@ def verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale=
     """
     if stream is not None:
         with _on(stream, q):
-            return verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
-                                        slopes, parent, out, workspace)
+            got = verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
+                                       slopes, parent, out, workspace)
+        return _handed_over(got, out)
     rc, out = _b.native().cache_attention(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
                                           slopes, parent, out, workspace)
     if rc != 0:
@@ -281,8 +290,9 @@ def verify_attention_masked(q, k_cache, v_cache, seq_lens, scale=0.0, softcap=0.
     verify_attention()'s is float32)."""
     if stream is not None:
         with _on(stream, q):
-            return verify_attention_masked(q, k_cache, v_cache, seq_lens, scale, softcap, window, slopes, parent,
-                                           out, workspace)
+            got = verify_attention_masked(q, k_cache, v_cache, seq_lens, scale, softcap, window, slopes, parent,
+                                          out, workspace)
+        return _handed_over(got, out)
     rc, out = _b.native().cache_attention(q, k_cache, v_cache, None, None, seq_lens, scale, softcap, window, slopes,
                                           parent, out, workspace)
     if rc != 0:

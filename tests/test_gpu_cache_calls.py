@@ -232,3 +232,26 @@ def test_parent_in_every_form_that_verify_tree_takes():
     for parent in ([], tree[:4], iter(tree[:2])):
         with pytest.raises(ValueError):
             tv.verify_attention_kv8(q, *cache, lens, parent=parent)
+
+
+@pytest.mark.parametrize("kind", ["kv8", "masked"])
+def test_an_output_from_another_stream_outlives_its_readers(kind):
+    """A result of a call on a side stream, read on the current one and dropped there: the side stream
+    does not get its memory while the reader still runs."""
+    q, cache, lens = _inputs(kind, 41, 3, 4, 8, 2, 128, 150)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = _call(kind, q, cache, lens, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(200_000_000)                     # about 0.1 s
+    kept = out.clone()
+    at, size = out.data_ptr(), out.numel() * 2
+    del out
+    with torch.cuda.stream(side):
+        held = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        for t in held:
+            t.fill_(0xFF)
+    assert not torch.cuda.current_stream().query(), "the reader was to be running still"
+    assert at not in [t.data_ptr() for t in held]
+    torch.cuda.synchronize()
+    assert torch.equal(kept, _call(kind, q, cache, lens))
