@@ -493,8 +493,7 @@ int specdec_read_status(const void* workspace, void* stream, int32_t* status);
  * MMA stage finds a barrier that nothing will ever arm. The wait gives up
  * after its bound (about 1 s), the kernel frees what it holds and returns,
  * and *status receives the status word it left: SPECDEC_ERR_TIMEOUT when the
- * detection works (in place of the SPECDEC_ERR_INVALID_ARG that the kernel
- * began with, as after a bad length: a timeout outranks the other codes). Nothing faults, traps or hangs, and the CUDA context stays
+ * detection works. Nothing faults, traps or hangs, and the CUDA context stays
  * usable. Synchronises `stream`. workspace: at least
  * specdec_verify_workspace_size(1, 4, 64, 256, SPECDEC_BF16, SPECDEC_GREEDY)
  * bytes, 256-byte aligned; its contents are overwritten.

@@ -605,6 +605,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_wait();
   const int4 note = __ldcg(A.notes + blockIdx.x);
+  // A bad length's code comes now, when a wait that ran out has left its own,
+  // which spoils every output and stays.
+  const int bad_lens = blockIdx.x == 0 && blockIdx.y == 0 ? __ldcg(A.status + 1) : 0;
+  if (bad_lens && threadIdx.x == 0) set_status(A.status, SPECDEC_ERR_INVALID_ARG);
   if (note.x < 0) return;
   const int b = note.x, grp = note.y % A.n_groups, h = note.y / A.n_groups;
   const int pos0 = grp * A.group_pos, rows = min(A.group_pos, A.n_new - pos0) * A.G;
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       place[3] = pl.u1;
       place[4] = pl.total;
       place[5] = pl.parts;
-      if (blockIdx.x == 0) *A.status = pl.any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
+      if (blockIdx.x == 0) *reinterpret_cast<int2*>(A.status) = make_int2(SPECDEC_OK, pl.any_bad);
     }
   }
   tc_fence_before();

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kKeyThreads, 2)
       place[3] = pl.u1;
       place[4] = pl.total;
       place[5] = pl.parts;
-      if (blockIdx.x == 0) *A.status = pl.any_bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
+      if (blockIdx.x == 0) *reinterpret_cast<int2*>(A.status) = make_int2(SPECDEC_OK, pl.any_bad);
     }
   }
   tc_fence_before();

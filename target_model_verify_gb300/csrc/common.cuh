@@ -72,9 +72,6 @@ __device__ __forceinline__ unsigned long long call_tag(unsigned long long epoch,
 __device__ __forceinline__ void set_status(int* st, int code) {
   atomicCAS(st, 0, code);
 }
-// A wait that ran out spoils every output of the call: it replaces a code that
-// spoils some of them.
-__device__ __forceinline__ void set_timeout(int* st) { atomicExch(st, SPECDEC_ERR_TIMEOUT); }
 
 // ------------------------------------------------------------- Philox --
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC'11): returns output word 0
@@ -229,7 +226,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
       if (*abort) return false;
       if (globaltimer() - t0 > kWaitLimitNs) {
         *abort = 1;
-        set_timeout(status);
+        set_status(status, SPECDEC_ERR_TIMEOUT);
         return false;
       }
     }
@@ -362,7 +359,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
       if (*abort) return false;
       if (globaltimer() - t0 > kWaitLimitNs) {
         *abort = 1;
-        set_timeout(status);
+        set_status(status, SPECDEC_ERR_TIMEOUT);
         return false;
       }
     }

@@ -212,7 +212,7 @@ struct CacheAttnLaunch {
   float* part_o;                     // [2 CTAs, rows, D]
   float* part_ml;                    // [2 CTAs, rows, 2]
   int4* notes;                       // [tiles or CTAs] who shares a tile (write_note)
-  int* status;
+  int* status;                       // the status word, and whether a length was bad, for the merge
   uint32_t anc[SPECDEC_MAX_TREE_NODES][4];   // bit a of row i: node i sees node a
   uint8_t depth[SPECDEC_MAX_TREE_NODES];
 };

@@ -255,3 +255,48 @@ def test_an_output_from_another_stream_outlives_its_readers(kind):
     assert at not in [t.data_ptr() for t in held]
     torch.cuda.synchronize()
     assert torch.equal(kept, _call(kind, q, cache, lens))
+
+
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_a_timeout_outranks_a_bad_length(Hq):
+    """What a wait that runs out does to the status word (its code where the word is 0), done by copies on
+    another stream while a call of a millisecond or more with one bad length runs: the timeout's code
+    stays. (One query row per KV head goes to the form by keys, 104 to the other.)"""
+    import target_model_verify_gb300 as tv
+    B, n, Hkv, D, L = 32, 1 if Hq == 8 else 26, 8, 128, 1 << 17
+    q = torch.zeros(B, n, Hq, D, dtype=torch.bfloat16, device=DEV)
+    cache = tv.alloc_kv8_cache(B, L, Hkv, D, device=DEV)
+    for t in cache[:2]:
+        t.view(torch.uint8).fill_(0x30)
+    for t in cache[2:]:
+        t.fill_(2.0 ** -6)
+    lens = torch.full((B,), L, dtype=torch.int32, device=DEV)
+    lens[3] = L + 1
+    ws = torch.empty(tv.cache_attention_workspace_bytes(B, n, Hq, Hkv, D, L), dtype=torch.uint8, device=DEV)
+    word, out = ws[:4].view(torch.int32), torch.empty_like(q)
+    call = lambda: tv.verify_attention_kv8(q, *cache, lens, out=out, workspace=ws)   # noqa: E731
+    call()
+    assert tv.read_status(ws) == tv._b.SPECDEC_ERR_INVALID_ARG
+    seen = torch.zeros(1, dtype=torch.int32).pin_memory()
+    timeout = torch.full((1,), tv._b.SPECDEC_ERR_TIMEOUT, dtype=torch.int32).pin_memory()
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    word.fill_(77)                                       # until the call begins
+    torch.cuda.synchronize()
+    call()
+    done.record()
+    with torch.cuda.stream(side):
+        for _ in range(1000):
+            seen.copy_(word, non_blocking=True)
+            side.synchronize()
+            if seen.item() != 77:
+                break
+        if seen.item() == 0:
+            word.copy_(timeout, non_blocking=True)
+            side.synchronize()
+    assert not done.query(), "the call was to be running still"
+    assert tv.read_status(ws) == tv._b.SPECDEC_ERR_TIMEOUT
+    call()
+    assert tv.read_status(ws) == tv._b.SPECDEC_ERR_INVALID_ARG
+    lens[3] = L
+    call()
+    assert tv.read_status(ws) == 0
