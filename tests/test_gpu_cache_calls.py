@@ -280,20 +280,24 @@ def test_a_timeout_outranks_a_bad_length(Hq):
     seen = torch.zeros(1, dtype=torch.int32).pin_memory()
     timeout = torch.full((1,), tv._b.SPECDEC_ERR_TIMEOUT, dtype=torch.int32).pin_memory()
     side, done = torch.cuda.Stream(), torch.cuda.Event()
-    word.fill_(77)                                       # until the call begins
-    torch.cuda.synchronize()
-    call()
-    done.record()
-    with torch.cuda.stream(side):
-        for _ in range(1000):
-            seen.copy_(word, non_blocking=True)
-            side.synchronize()
-            if seen.item() != 77:
-                break
-        if seen.item() == 0:
-            word.copy_(timeout, non_blocking=True)
-            side.synchronize()
-    assert not done.query(), "the call was to be running still"
+    for _ in range(20):
+        word.fill_(77)                                   # until the call begins
+        torch.cuda.synchronize()
+        call()
+        done.record()
+        with torch.cuda.stream(side):
+            for _ in range(1000):
+                seen.copy_(word, non_blocking=True)
+                side.synchronize()
+                if seen.item() != 77:
+                    break
+            if seen.item() == 0:
+                word.copy_(timeout, non_blocking=True)
+                side.synchronize()
+        if not done.query():                             # the copies came in time
+            break
+    else:
+        pytest.fail("the call never ran long enough")
     assert tv.read_status(ws) == tv._b.SPECDEC_ERR_TIMEOUT
     call()
     assert tv.read_status(ws) == tv._b.SPECDEC_ERR_INVALID_ARG

@@ -24,29 +24,30 @@ def _quantised(x):
 
 
 def _run(kind, seqs, B, **how):
-    """[(q, k, v)] of one length repeated to a batch of B; the outputs of the first len(seqs), and the bounds'
-    inputs as the kernel sees them."""
+    """A batch of B of the sequences (q, k, v) in turn. Returns the outputs of the first and the last of
+    them (whose tiles are cut elsewhere), and for each what the kernel saw: q, k, v, value scales."""
     import target_model_verify_gb300 as tv
     L, Hkv, D = seqs[0][1].shape
     n, Hq = seqs[0][0].shape[:2]
-    picked = [seqs[b % len(seqs)] for b in range(len(seqs))]
-    q = torch.stack([torch.from_numpy(s[0]).to(torch.bfloat16) for s in picked])
-    seen = []
-    many = lambda t: torch.cat([t.to(DEV)] * -(-B // len(seqs)))[:B].contiguous()  # noqa: E731
-    byte = lambda t: t.view(torch.uint8)                                          # noqa: E731
+    m = len(seqs)
+
+    def many(t):
+        return torch.cat([t.to(DEV)] * -(-B // m))[:B].contiguous()
+
+    q = torch.stack([torch.from_numpy(s[0]).to(torch.bfloat16) for s in seqs])
     if kind == "masked":
-        k, v = (torch.stack([torch.from_numpy(s[x]).to(torch.bfloat16) for s in picked]) for x in (1, 2))
-        for b in range(len(seqs)):
-            seen.append((q[b].double().numpy(), k[b].double().numpy(), v[b].double().numpy(), None))
+        k, v = (torch.stack([torch.from_numpy(s[x]).to(torch.bfloat16) for s in seqs]) for x in (1, 2))
+        seen = [(q[b].double().numpy(), k[b].double().numpy(), v[b].double().numpy(), None) for b in range(m)]
         cache = (many(k), many(v))
     else:
-        ks, vs = [_quantised(s[1]) for s in picked], [_quantised(s[2]) for s in picked]
-        for b in range(len(seqs)):
-            at = np.arange(L) // 32
+        ks, vs = [_quantised(s[1]) for s in seqs], [_quantised(s[2]) for s in seqs]
+        at = np.arange(L) // 32
+        seen = []
+        for b in range(m):
             sk, sv = ks[b][1].double().numpy().T[at], vs[b][1].double().numpy().T[at]      # [L, Hkv]
             seen.append((q[b].double().numpy(), ks[b][0].double().numpy() * sk[..., None],
                          vs[b][0].double().numpy() * sv[..., None], sv))
-        codes = [many(byte(torch.stack([x[0] for x in t]))).view(torch.float8_e4m3fn) for t in (ks, vs)]
+        codes = [many(torch.stack([x[0].view(torch.uint8) for x in t])).view(torch.float8_e4m3fn) for t in (ks, vs)]
         cache = (*codes, *(many(torch.stack([x[1] for x in t])) for t in (ks, vs)))
     lens = torch.full((B,), L, dtype=torch.int32, device=DEV)
     if how.get("slopes") is not None:
@@ -57,12 +58,8 @@ def _run(kind, seqs, B, **how):
     again = fn(many(q), *cache, lens, workspace=ws, **how)
     assert tv.read_status(ws) == 0
     assert torch.equal(out, again)
-    for b in range(len(seqs), B):
-        if b >= B - len(seqs):                                           # the batch's far end, of equal inputs
-            # its parts are cut elsewhere: other partial sums, the same bounds
-            seen.append(seen[b % len(seqs)])
-    got = out[list(range(len(seqs))) + list(range(max(len(seqs), B - len(seqs)), B))].double().cpu().numpy()
-    return got, seen
+    rows = list(range(m)) + list(range(max(m, B - m), B))
+    return out[rows].double().cpu().numpy(), [seen[b % m] for b in rows]
 
 
 def _compare(kind, seqs, B, **how):
