@@ -76,6 +76,7 @@ extern "C" {
 #define SPECDEC_ERR_CUDA (-4)          /* a CUDA runtime/driver call failed */
 #define SPECDEC_ERR_TIMEOUT (-5)       /* a device-side wait ran out (status word) */
 #define SPECDEC_ERR_TOKEN_RANGE (-6)   /* a draft token outside [0, V) (status word) */
+#define SPECDEC_ERR_NO_PAGES    (-7)   /* fewer free pages than a plan needs (status word) */
 
 /*
  * Bytes of device workspace specdec_verify() needs for this shape. The
@@ -382,6 +383,107 @@ int specdec_verify_attention_masked(const void* q, long long q_stride, const voi
                                     void* stream);
 
 /*
+ * A paged key/value cache: a pool of n_pages pages of `page` rows each, shared
+ * by all sequences. A cache tensor (one for K, one for V) is [n_pages, page,
+ * Hkv, D] bf16; slot s of it is row s % page of page s / page. Row j of
+ * sequence b lies in page table[b][j / page], at row j % page.
+ *
+ * specdec_plan_pages() brings the tables from one state of the batch to the
+ * next on the GPU, and maps the new rows to slots:
+ *   table      [B, max_pages] int32   (device, in and out) pages of every
+ *                                     sequence; entries past held[b] are -1
+ *                                     or whatever the caller left there
+ *   held       [B]            int32   (device, in and out) pages that it holds
+ *   free_pages [n_pages]      int32   (device, in and out) a stack: the first
+ *                                     n_free[0] entries are the free pages
+ *   n_free     [1]            int32   (device, in and out)
+ *   start, counts [B]         int32   (device) sequence b is to have rows
+ *                                     0 .. start + count - 1, of which the
+ *                                     last `count` are new
+ *   cu_rows    [B + 1]        int32   (device) or NULL: the new rows of
+ *                                     sequence b stand at cu_rows[b] .. of the
+ *                                     map (packed); NULL: at b * n ..
+ *   slots      [n_slots]      int32   (device) or NULL: the map, the slot of
+ *                                     every new row; -1 where there is none.
+ *                                     n_slots = B * n without cu_rows
+ * Afterwards held[b] = ceil((start + count) / page). Pages no longer held are
+ * pushed on the stack, sequence by sequence in ascending order of their
+ * entries, which become -1; then pages are taken off its top in the same
+ * order. So a step asks for room for its drafts (start = committed rows,
+ * counts = n_new), and after the verification a call with counts = what was
+ * kept gives the rest back; start = counts = 0 gives back all.
+ * A plan that needs more pages than there are changes nothing, sets
+ * SPECDEC_ERR_NO_PAGES in the status word and makes the map -1 throughout. A
+ * sequence whose start, count, held or place in the map is impossible
+ * (negative, past max_pages * page, more rows than the map has room for) is
+ * left as it is, its rows of the map are -1, and the status word gets
+ * SPECDEC_ERR_INVALID_ARG; so does a row of the map whose table entry is not
+ * a page (-1 there). A cu_rows that is not ascending within 0 .. n_slots, or a
+ * stack that could not hold what is given back, sets it too: nothing changes
+ * then, and the map is -1 throughout. Limits: page = 16, 32, 64, 128 or 256; max_pages * page
+ * and n_pages * page <= 2^30; n_slots < 2^31 - 4. B = 0 with a map fills it
+ * with -1. The tensors must not overlap. Asynchronous; the workspace holds
+ * the status word only.
+ */
+size_t specdec_plan_pages_workspace_size(void);
+int specdec_plan_pages(int32_t* table, int32_t* held, int32_t* free_pages, int32_t* n_free,
+                       const int32_t* start, const int32_t* counts, const int32_t* cu_rows, int B,
+                       int max_pages, int n_pages, int page, int n, long long n_slots,
+                       int32_t* slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Writes new positions' keys and values into a paged cache:
+ *   k_new, v_new [B, n, Hkv, D]  bf16   row i of sequence b at element
+ *                                       (b * n + i) * stride (the strides are
+ *                                       multiples of 8, at least Hkv * D, below
+ *                                       2^31); packed rows: B = 1
+ *   slots        [B, n] int32 (device)  where each row goes; -1: nowhere
+ *   rows         [B, n] int32 (device)  which row of its sequence goes to each
+ *                                       slot, or NULL: 0, 1, 2, ... With the
+ *                                       slots of specdec_plan_pages() for
+ *                                       start one past the root's row and
+ *                                       counts = n_accepted, and rows =
+ *                                       out_nodes of specdec_verify_tree(),
+ *                                       the accepted path's rows replace the
+ *                                       tree's. Not read where the slot is -1.
+ *   k_pages, v_pages                    as above
+ * A slot that is neither -1 nor in the pool, or an entry of rows outside
+ * [0, n), sets SPECDEC_ERR_INVALID_ARG in the status word and that row is
+ * skipped. Of a slot named twice, either row's values may remain, element by
+ * element. Limits: D = 64, 128 or 256; Hkv <= 2^20; page and n_pages as
+ * above; n_pages * page * Hkv * D < 2^40; B * n < 2^31; bf16 pointers 16-byte
+ * aligned. The sources and the caches must not overlap. Asynchronous; the
+ * workspace holds the status word only.
+ */
+size_t specdec_paged_append_workspace_size(void);
+int specdec_paged_append(const void* k_new, long long k_stride, const void* v_new,
+                         long long v_stride, const int32_t* slots, const int32_t* rows, int B,
+                         int n, int Hkv, int D, int n_pages, int page, void* k_pages,
+                         void* v_pages, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * specdec_verify_attention_masked() over a paged cache: a drafter's one new
+ * token (n_new = 1) or a verify step's, a tree's too. Arguments as there, and
+ *   k_pages, v_pages [n_pages, page, Hkv, D] bf16
+ *   table    [B, max_pages] int32 (device)  only entries of pages with rows
+ *                                  that some new position sees are read
+ * seq_lens [B] is 0 or within [n_new, max_pages * page]. An entry that is not
+ * a page sets SPECDEC_ERR_INVALID_ARG in the status word, and its rows count
+ * as zeros. Limits as there, with max_pages * page for Lmax and n_pages * page
+ * * Hkv * D < 2^40 for the cache; page as above, max_pages * page and n_pages
+ * * page <= 2^30; table 4-byte aligned.
+ */
+size_t specdec_verify_attention_paged_workspace_size(int B, int n_new, int Hq, int Hkv, int D,
+                                                     int n_pages, int page, int max_pages);
+int specdec_verify_attention_paged(const void* q, long long q_stride, const void* k_pages,
+                                   const void* v_pages, const int32_t* table,
+                                   const int32_t* seq_lens, const int32_t* parent,
+                                   const float* slopes, int B, int n_new, int Hq, int Hkv, int D,
+                                   int n_pages, int page, int max_pages, float scale,
+                                   float softcap, int window, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
  * The drafter's clustered LM head ("多詞元預測視覺化指南", section 高效嵌入器):
  * cluster logits y = h E^T, the top_k clusters of every row (largest y, ties
  * to the lower index), token logits z = h . W_r for the kept clusters'
@@ -481,8 +583,8 @@ int specdec_shard_draw(const float* all_shard_sums, int n_shards, int shard,
 /*
  * Reads the device status word of a workspace after synchronising `stream`:
  * SPECDEC_OK, SPECDEC_ERR_TIMEOUT, SPECDEC_ERR_TOKEN_RANGE (verify and tree
- * steps) or SPECDEC_ERR_INVALID_ARG (attention lengths, clustered-head
- * tables) of the last call that used it. *status receives the value; the
+ * steps), SPECDEC_ERR_NO_PAGES (plan_pages) or SPECDEC_ERR_INVALID_ARG
+ * (attention lengths, clustered-head and page tables) of the last call that used it. *status receives the value; the
  * return code reports the read itself.
  */
 int specdec_read_status(const void* workspace, void* stream, int32_t* status);

@@ -277,8 +277,8 @@ def verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale=
             got = verify_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
                                        slopes, parent, out, workspace)
         return _handed_over(got, out)
-    rc, out = _b.native().cache_attention(q, k_cache, v_cache, k_scale, v_scale, seq_lens, scale, softcap, window,
-                                          slopes, parent, out, workspace)
+    rc, out = _b.native().cache_attention(q, k_cache, v_cache, k_scale, v_scale, None, seq_lens, scale, softcap,
+                                          window, slopes, parent, out, workspace)
     if rc != 0:
         _b._check(rc, "specdec_verify_attention_kv8")
     return out
@@ -293,10 +293,97 @@ def verify_attention_masked(q, k_cache, v_cache, seq_lens, scale=0.0, softcap=0.
             got = verify_attention_masked(q, k_cache, v_cache, seq_lens, scale, softcap, window, slopes, parent,
                                           out, workspace)
         return _handed_over(got, out)
-    rc, out = _b.native().cache_attention(q, k_cache, v_cache, None, None, seq_lens, scale, softcap, window, slopes,
-                                          parent, out, workspace)
+    rc, out = _b.native().cache_attention(q, k_cache, v_cache, None, None, None, seq_lens, scale, softcap, window,
+                                          slopes, parent, out, workspace)
     if rc != 0:
         _b._check(rc, "specdec_verify_attention_masked")
+    return out
+
+
+def alloc_paged_cache(n_pages, page, Hkv, D, device=None):
+    """(k_pages, v_pages) of a paged cache: bfloat16 [n_pages, page, Hkv, D], page 16 to 256 rows (a
+    power of two)."""
+    return tuple(torch.empty(n_pages, page, Hkv, D, dtype=torch.bfloat16, device=device or "cuda")
+                 for _ in range(2))
+
+
+def alloc_page_tables(B, max_pages, n_pages, device=None):
+    """(table, held, free, n_free) of a batch without pages over a pool whose n_pages are all free:
+    int32 [B, max_pages], [B], [n_pages], [1], as plan_pages() keeps them."""
+    dev = device or "cuda"
+    return (torch.full((B, max_pages), -1, dtype=torch.int32, device=dev),
+            torch.zeros(B, dtype=torch.int32, device=dev),
+            torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=dev),
+            torch.full((1,), n_pages, dtype=torch.int32, device=dev))
+
+
+def plan_pages(table, held, free, n_free, start, counts, page, n=None, slots=None, cu_rows=None,
+               workspace=None, stream=None):
+    """Bring a batch's page tables to new lengths on the GPU and map the new rows to slots
+    (include/specdec_verify.h, specdec_plan_pages).
+
+    The tables are as alloc_page_tables() makes them, start and counts [B] int32: sequence b is to
+    have start + counts rows, the last counts of them new. Pages that it no longer needs go back to
+    the free ones, pages that it lacks are taken from them; the tables change in place. For a map of
+    the new rows bring `slots` [B, n] int32 to fill, or n for a new one; with cu_rows [B + 1] int32
+    (packed rows: sequence b's from cu_rows[b] on) slots is [rows], and n counts all rows. Returns
+    the map (None without one). A step asks for room for its drafts with start = committed rows,
+    counts = n_new; after the verification counts = what was kept gives the rest back, and start =
+    counts = 0 gives back all. Too few free pages (nothing changes, the map is -1) and impossible
+    entries are found on the device: only read_status() of a workspace that the caller brought
+    (256 bytes) tells.
+    """
+    if stream is not None:
+        with _on(stream, table):
+            got = plan_pages(table, held, free, n_free, start, counts, page, n, slots, cu_rows, workspace)
+        return got if got is None else _handed_over(got, slots)
+    rc, slots = _b.native().plan_pages(table, held, free, n_free, start, counts, page, n, slots, cu_rows, workspace)
+    if rc != 0:
+        _b._check(rc, "specdec_plan_pages")
+    return slots
+
+
+def append_paged(k_new, v_new, k_pages, v_pages, slots, rows=None, workspace=None, stream=None):
+    """Write new positions' keys and values into a paged cache (include/specdec_verify.h,
+    specdec_paged_append).
+
+    k_new, v_new [B, n, Hkv, D] or packed [rows, Hkv, D] bf16 (slices of a fused projection are
+    taken as they are), the cache as alloc_paged_cache() makes it, slots [B, n] or [rows] int32 as
+    plan_pages() gives them: -1 leaves a row out. rows (of the same shape, int32): which row of its
+    sequence each slot takes (default in order), so that the slots of a plan with start = root + 1 and
+    counts = n_accepted, and rows = out_nodes, replace a verified tree's rows by its accepted path's.
+    Writes the cache in place and returns (k_pages, v_pages). Entries that do not fit are skipped,
+    and only read_status() of a workspace that the caller brought (256 bytes) tells.
+    """
+    if stream is not None:
+        with _on(stream, k_new):
+            return append_paged(k_new, v_new, k_pages, v_pages, slots, rows, workspace)
+    rc = _b.native().append_paged(k_new, v_new, k_pages, v_pages, slots, rows, workspace)
+    if rc != 0:
+        _b._check(rc, "specdec_paged_append")
+    return k_pages, v_pages
+
+
+def paged_attention_workspace_bytes(B, n_new, Hq, Hkv, D, n_pages, page, max_pages) -> int:
+    """Workspace of verify_attention_paged."""
+    return _b.specdec_verify_attention_paged_workspace_size(B, n_new, Hq, Hkv, D, n_pages, page, max_pages)
+
+
+def verify_attention_paged(q, k_pages, v_pages, table, seq_lens, scale=0.0, softcap=0.0, window=0, slopes=None,
+                           parent=None, out=None, workspace=None, stream=None):
+    """verify_attention_masked() over a paged cache: k_pages, v_pages [n_pages, page, Hkv, D] as
+    alloc_paged_cache() makes them, table [B, max_pages] int32 the pages of every sequence. For a
+    drafter's one token (n_new = 1) as for a verify step's; out bf16. A length or a page that does
+    not fit shows in read_status() of a workspace that the caller brought."""
+    if stream is not None:
+        with _on(stream, q):
+            got = verify_attention_paged(q, k_pages, v_pages, table, seq_lens, scale, softcap, window, slopes,
+                                         parent, out, workspace)
+        return _handed_over(got, out)
+    rc, out = _b.native().cache_attention(q, k_pages, v_pages, None, None, table, seq_lens, scale, softcap, window,
+                                          slopes, parent, out, workspace)
+    if rc != 0:
+        _b._check(rc, "specdec_verify_attention_paged")
     return out
 
 

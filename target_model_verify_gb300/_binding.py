@@ -31,6 +31,7 @@ SPECDEC_ERR_WORKSPACE = -3
 SPECDEC_ERR_CUDA = -4
 SPECDEC_ERR_TIMEOUT = -5
 SPECDEC_ERR_TOKEN_RANGE = -6
+SPECDEC_ERR_NO_PAGES = -7
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -70,6 +71,13 @@ _SIGNATURES = {
     "specdec_verify_attention_masked_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "specdec_verify_attention_masked": (_i, [_vp, _ll] + [_vp] * 5 + [_i] * 6 + [_f, _f, _i, _vp, _vp,
                                                                                  _sz, _vp]),
+    "specdec_plan_pages_workspace_size": (_sz, []),
+    "specdec_plan_pages": (_i, [_vp] * 7 + [_i] * 5 + [_ll, _vp, _vp, _sz, _vp]),
+    "specdec_paged_append_workspace_size": (_sz, []),
+    "specdec_paged_append": (_i, [_vp, _ll, _vp, _ll, _vp, _vp] + [_i] * 6 + [_vp, _vp, _vp, _sz, _vp]),
+    "specdec_verify_attention_paged_workspace_size": (_sz, [_i] * 8),
+    "specdec_verify_attention_paged": (_i, [_vp, _ll] + [_vp] * 6 + [_i] * 8 + [_f, _f, _i, _vp, _vp,
+                                                                                _sz, _vp]),
     "specdec_shard_record_bytes": (_sz, [_i, _i]),
     "specdec_shard_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "specdec_shard_score": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp,
@@ -223,6 +231,31 @@ def specdec_verify_attention_masked_workspace_size(B, n_new, Hq, Hkv, D, Lmax) -
 def specdec_verify_attention_masked(*args) -> int:
     """Masked attention over a bf16 cache (the parent array is a host int32 array)."""
     return int(lib().specdec_verify_attention_masked(*args))
+
+
+def specdec_plan_pages_workspace_size() -> int:
+    return int(lib().specdec_plan_pages_workspace_size())
+
+
+def specdec_plan_pages(*args) -> int:
+    return int(lib().specdec_plan_pages(*args))
+
+
+def specdec_paged_append_workspace_size() -> int:
+    return int(lib().specdec_paged_append_workspace_size())
+
+
+def specdec_paged_append(*args) -> int:
+    return int(lib().specdec_paged_append(*args))
+
+
+def specdec_verify_attention_paged_workspace_size(B, n_new, Hq, Hkv, D, n_pages, page, max_pages) -> int:
+    return int(lib().specdec_verify_attention_paged_workspace_size(B, n_new, Hq, Hkv, D, n_pages, page, max_pages))
+
+
+def specdec_verify_attention_paged(*args) -> int:
+    """Attention over a paged cache (the parent array is a host int32 array)."""
+    return int(lib().specdec_verify_attention_paged(*args))
 
 
 def specdec_cluster_head_workspace_size(M, n_c, top_k, max_cluster) -> int:

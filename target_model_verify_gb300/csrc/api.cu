@@ -1175,6 +1175,7 @@ const char* specdec_status_string(int status) {
     case SPECDEC_ERR_CUDA: return "CUDA error";
     case SPECDEC_ERR_TIMEOUT: return "device-side wait timed out";
     case SPECDEC_ERR_TOKEN_RANGE: return "draft token outside [0, V)";
+    case SPECDEC_ERR_NO_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }

@@ -14,12 +14,12 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 
-int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
+// What both layouts of the cache ask for; Lmax rows of a sequence at most.
+int check_heads(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
   if (B < 0 || n_new < 1 || n_new > SPECDEC_MAX_TREE_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
       !head_dim_ok(D) || Lmax < n_new || Lmax > (1 << 30))
     return SPECDEC_ERR_UNSUPPORTED;
   if (Hq / Hkv > 128 || Hq > (1 << 20)) return SPECDEC_ERR_UNSUPPORTED;
-  if ((__int128)B * Lmax * Hkv * D >= ((__int128)1 << 40)) return SPECDEC_ERR_UNSUPPORTED;
   // (sequence, KV head, row group) tiles and their blocks of 64 keys or more
   // are counted in 32 bits
   if ((long long)B * Hq * n_new >= (1ll << 31)) return SPECDEC_ERR_UNSUPPORTED;
@@ -27,15 +27,35 @@ int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
   return SPECDEC_OK;
 }
 
+int check_shape(int B, int n_new, int Hq, int Hkv, int D, int Lmax) {
+  const int rc = check_heads(B, n_new, Hq, Hkv, D, Lmax);
+  if (rc != SPECDEC_OK) return rc;
+  return (__int128)B * Lmax * Hkv * D >= ((__int128)1 << 40) ? SPECDEC_ERR_UNSUPPORTED : SPECDEC_OK;
+}
+
+int check_pages(int B, int n_new, int Hq, int Hkv, int D, int n_pages, int page, int max_pages) {
+  if (page_log2(page) < 0 || n_pages < 1 || max_pages < 1 || (long long)n_pages * page > (1 << 30) ||
+      (long long)max_pages * page > (1 << 30))
+    return SPECDEC_ERR_UNSUPPORTED;
+  const int rc = check_heads(B, n_new, Hq, Hkv, D, max_pages * page);
+  if (rc != SPECDEC_OK) return rc;
+  return (__int128)n_pages * page * Hkv * D >= ((__int128)1 << 40) ? SPECDEC_ERR_UNSUPPORTED : SPECDEC_OK;
+}
+
 struct AttnPlan {
   int n_groups, group_pos;
-  size_t off_notes, off_ml, off_o, total;
+  size_t off_notes, off_ml, off_o, off_flags, total;
+};
+
+struct Pages {
+  const int32_t* table;
+  int n_pages, page, max_pages;
 };
 
 // The new positions in equal groups of at most 128 query rows per KV head;
 // the partials of the tiles that the CTAs share, two per CTA, whatever the
 // batch and the lengths.
-AttnPlan make_plan(bool e4m3, int n_new, int G, int D) {
+AttnPlan make_plan(bool e4m3, int n_new, int G, int D, bool paged = false) {
   AttnPlan p;
   const int most = 128 / G;
   p.n_groups = (n_new + most - 1) / most;
@@ -50,12 +70,13 @@ AttnPlan make_plan(bool e4m3, int n_new, int G, int D) {
   off = align_up(off + rows * 2 * sizeof(float));
   p.off_o = off;
   off = align_up(off + rows * D * sizeof(float));
-  p.total = off;
+  p.off_flags = off;                       // paged caches only
+  p.total = paged ? align_up(off + 2 * ctas * sizeof(int)) : off;
   return p;
 }
 
-// The cache as a 4-D tensor {D, Hkv, Lmax, B}; box: up to 128 bytes of a row
-// x one head x one block of rows, swizzled.
+// The cache as a 4-D tensor {D, Hkv, Lmax, B} (pages: one sequence of all the
+// pool's rows); box: up to 128 bytes of a row x one head x `block` rows, swizzled.
 bool encode_cache(CUtensorMap* map, const void* base, bool e4m3, int B, int Lmax, int Hkv, int D, int block) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
@@ -87,14 +108,19 @@ bool encode_queries(CUtensorMap* map, const void* q, long long q_stride, int B, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+int attention(bool e4m3, const Pages* pages, const void* q, long long q_stride, const void* k_cache, const void* v_cache,
               const float* k_scale, const float* v_scale, const int32_t* seq_lens, const int32_t* parent,
               const float* slopes, int B, int n_new, int Hq, int Hkv, int D, int Lmax, float scale,
               float softcap, int window, void* out, void* workspace, size_t workspace_bytes,
               void* stream_ptr) {
-  int rc = check_shape(B, n_new, Hq, Hkv, D, Lmax);
+  int rc = pages ? check_pages(B, n_new, Hq, Hkv, D, pages->n_pages, pages->page, pages->max_pages)
+                 : check_shape(B, n_new, Hq, Hkv, D, Lmax);
   if (rc != SPECDEC_OK) return rc;
   if (B == 0) return SPECDEC_OK;
+  if (pages) {
+    Lmax = pages->max_pages * pages->page;
+    if (!pages->table || ((uintptr_t)pages->table & 3u) != 0) return SPECDEC_ERR_INVALID_ARG;
+  }
   if (!q || !k_cache || !v_cache || !seq_lens || !out) return SPECDEC_ERR_INVALID_ARG;
   if (e4m3 && (!k_scale || !v_scale)) return SPECDEC_ERR_INVALID_ARG;
   if ((((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out) & 15u) != 0)
@@ -126,7 +152,7 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
     }
   }
   const int G = Hq / Hkv;
-  const AttnPlan pl = make_plan(e4m3, n_new, G, D);
+  const AttnPlan pl = make_plan(e4m3, n_new, G, D, pages != nullptr);
   if (!workspace || ((uintptr_t)workspace % kAlign) != 0 || workspace_bytes < pl.total)
     return SPECDEC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
@@ -158,18 +184,30 @@ int attention(bool e4m3, const void* q, long long q_stride, const void* k_cache,
   A.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   A.notes = reinterpret_cast<int4*>(ws + pl.off_notes);
   A.status = reinterpret_cast<int*>(ws);
+  A.table = pages ? pages->table : nullptr;
+  A.max_pages = pages ? pages->max_pages : 0;
+  A.page_log2 = pages ? page_log2(pages->page) : 0;
+  A.n_pages = pages ? pages->n_pages : 0;
+  A.flags = pages ? reinterpret_cast<int*>(ws + pl.off_flags) : nullptr;
+  A.n_flags = 0;                             // the launch knows
   CUtensorMap tk, tv, tq;
-  const int block = cache_attn_block(D, cache_attn_rows(pl.group_pos * G));
-  if (!encode_cache(&tk, k_cache, e4m3, B, Lmax, Hkv, D, block) ||
-      !encode_cache(&tv, v_cache, e4m3, B, Lmax, Hkv, D, block))
+  int block = cache_attn_block(D, cache_attn_rows(pl.group_pos * G)), seqs = B, rows = Lmax;
+  if (pages) {
+    block = pages->page < block ? pages->page : block;
+    seqs = 1;
+    rows = pages->n_pages * pages->page;
+  }
+  if (!encode_cache(&tk, k_cache, e4m3, seqs, rows, Hkv, D, block) ||
+      !encode_cache(&tv, v_cache, e4m3, seqs, rows, Hkv, D, block))
     return SPECDEC_ERR_CUDA;
   if (e4m3)
     tq = tk;                                   // not read: the kernel converts the queries itself
   else if (!encode_queries(&tq, q, q_stride, B, n_new, Hq, G, D, pl.group_pos))
     return SPECDEC_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  const cudaError_t e = e4m3 ? launch_cache_attention_kv8(A, D, tk, tv, tq, stream)
-                             : launch_cache_attention_bf16(A, D, tk, tv, tq, stream);
+  const cudaError_t e = pages ? launch_cache_attention_paged(A, D, tk, tv, tq, stream)
+                        : e4m3 ? launch_cache_attention_kv8(A, D, tk, tv, tq, stream)
+                               : launch_cache_attention_bf16(A, D, tk, tv, tq, stream);
   return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
@@ -236,7 +274,7 @@ int specdec_verify_attention_kv8(const void* q, long long q_stride, const void* 
                                  const int32_t* parent, const float* slopes, int B, int n_new, int Hq,
                                  int Hkv, int D, int Lmax, float scale, float softcap, int window, void* out,
                                  void* workspace, size_t workspace_bytes, void* stream) {
-  return attention(true, q, q_stride, k_cache, v_cache, k_scale, v_scale, seq_lens, parent, slopes, B, n_new,
+  return attention(true, nullptr, q, q_stride, k_cache, v_cache, k_scale, v_scale, seq_lens, parent, slopes, B, n_new,
                    Hq, Hkv, D, Lmax, scale, softcap, window, out, workspace, workspace_bytes, stream);
 }
 
@@ -250,8 +288,24 @@ int specdec_verify_attention_masked(const void* q, long long q_stride, const voi
                                     const float* slopes, int B, int n_new, int Hq, int Hkv, int D, int Lmax,
                                     float scale, float softcap, int window, void* out, void* workspace,
                                     size_t workspace_bytes, void* stream) {
-  return attention(false, q, q_stride, k_cache, v_cache, nullptr, nullptr, seq_lens, parent, slopes, B, n_new,
+  return attention(false, nullptr, q, q_stride, k_cache, v_cache, nullptr, nullptr, seq_lens, parent, slopes, B, n_new,
                    Hq, Hkv, D, Lmax, scale, softcap, window, out, workspace, workspace_bytes, stream);
+}
+
+size_t specdec_verify_attention_paged_workspace_size(int B, int n_new, int Hq, int Hkv, int D, int n_pages,
+                                                     int page, int max_pages) {
+  if (check_pages(B, n_new, Hq, Hkv, D, n_pages, page, max_pages) != SPECDEC_OK) return 0;
+  return make_plan(false, n_new, Hq / Hkv, D, true).total;
+}
+
+int specdec_verify_attention_paged(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
+                                   const int32_t* table, const int32_t* seq_lens, const int32_t* parent,
+                                   const float* slopes, int B, int n_new, int Hq, int Hkv, int D, int n_pages,
+                                   int page, int max_pages, float scale, float softcap, int window, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  const Pages pages = {table, n_pages, page, max_pages};
+  return attention(false, &pages, q, q_stride, k_pages, v_pages, nullptr, nullptr, seq_lens, parent, slopes, B,
+                   n_new, Hq, Hkv, D, 0, scale, softcap, window, out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -607,8 +607,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ca
   const int4 note = __ldcg(A.notes + blockIdx.x);
   // A bad length's code comes now, when a wait that ran out has left its own,
   // which spoils every output and stays.
-  const int bad_lens = blockIdx.x == 0 && blockIdx.y == 0 ? __ldcg(A.status + 1) : 0;
-  if (bad_lens && threadIdx.x == 0) set_status(A.status, SPECDEC_ERR_INVALID_ARG);
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int bad = __ldcg(A.status + 1);
+    if (A.flags) {
+      for (int i = threadIdx.x; i < 2 * A.n_flags; i += 256) bad |= __ldcg(A.flags + i);
+      bad = __syncthreads_or(bad);
+    }
+    if (bad && threadIdx.x == 0) set_status(A.status, SPECDEC_ERR_INVALID_ARG);
+  }
   if (note.x < 0) return;
   const int b = note.x, grp = note.y % A.n_groups, h = note.y / A.n_groups;
   const int pos0 = grp * A.group_pos, rows = min(A.group_pos, A.n_new - pos0) * A.G;
@@ -758,7 +764,7 @@ struct Sight {
   }
 };
 
-template <bool kE4m3, int kD, int kRP, bool kExtra>
+template <bool kE4m3, int kD, int kRP, bool kExtra, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnLaunch A, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_q) {
@@ -857,7 +863,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   uint32_t issued = 0, issued_phase = 0, issued_q = 0, issued_q_phase = 0;   // producers: copies in flight
 
-  if (warp == kProducer || warp == kProducerV) {
+  // The tile's query rows, once per copy (bf16).
+  auto load_query_boxes = [&](const Walk<kBlk>& t, int qs) {
+    const uint32_t box = (uint32_t)(A.group_pos * A.G) * 128u;
+    mbar_arrive_expect_tx(q_full(qs), box * (kD / 64) * S::kCopies);
+    for (int c = 0; c < S::kCopies; ++c)
+      for (int p = 0; p < kD / 64; ++p)
+        tma_load_4d(qb + qs * S::kQBytes + p * 128 * 128 + c * kRP * 128, &tmap_q, q_full(qs), p * 64,
+                    t.h * A.G, t.g * A.group_pos, t.b, policy_evict_normal());
+  };
+
+  if (kPaged && (warp == kProducer || warp == kProducerV)) {
+    // ------------------------- producers over a paged cache: K and Q; V --
+    // A block is up to eight boxes of 16 rows or more, one page's each: lane x
+    // looks up and loads box x, its page a block ahead. What no position of
+    // the sequence sees is not looked up (its page may be gone): such a box,
+    // and one of a page outside the pool, lies behind the pool's last row,
+    // which reads as zeros and moves nothing.
+    const bool is_v = warp == kProducerV;
+    const uint64_t pol = policy_evict_first();
+    const CUtensorMap* const map = is_v ? &tmap_v : &tmap_k;
+    const uint32_t ring = is_v ? ring_v : ring_k;
+    const int page = 1 << A.page_log2, box = min(page, kBlk), none = A.n_pages << A.page_log2;
+    int s = 0;
+    uint32_t ph = 0, nt = 0;
+    bool ok = true, bad = false;
+    auto box_row = [&](const Walk<kBlk>& t, int j0) {
+      const int j = j0 + lane * box, low = A.window > 0 ? t.L - A.n_new - A.window + 1 : 0;
+      if (lane * box >= kBlk || j >= t.L || j + box <= low) return none;
+      const int id = __ldcg(A.table + (size_t)t.b * A.max_pages + (j >> A.page_log2));
+      if ((unsigned)id >= (unsigned)A.n_pages) {
+        bad = true;
+        return none;
+      }
+      return (id << A.page_log2) + (j & (page - 1));
+    };
+    int next_row = w.done() ? none : box_row(w, w.row(0));
+    while (ok && !w.done()) {
+      if (!is_v) {
+        const int qs = nt % kNq;
+        const uint32_t qph = (nt / kNq) & 1;
+        if (!(ok = warp_wait(q_empty(qs), qph ^ 1u))) break;
+        if (lane == 0) load_query_boxes(w, qs);
+        issued_q |= 1u << qs;
+        issued_q_phase = (issued_q_phase & ~(1u << qs)) | (qph << qs);
+      }
+      Walk<kBlk> then = w;
+      then.next(A);
+      for (int i = 0; i < w.n_here; ++i) {
+        const int row = next_row;
+        if (i + 1 < w.n_here)
+          next_row = box_row(w, w.row(i + 1));
+        else if (!then.done())
+          next_row = box_row(then, then.row(0));
+        const uint32_t full = is_v ? v_full(s) : k_full(s);
+        if (!(ok = warp_wait(is_v ? v_empty(s) : k_empty(s), ph ^ 1u))) break;
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)S::kSlotBytes);
+        __syncwarp();
+        if (lane * box < kBlk)
+#pragma unroll
+          for (int p = 0; p < S::kPanels; ++p)
+            tma_load_4d(ring + s * S::kSlotBytes + (p * kBlk + lane * box) * S::kPanelBytes, map, full,
+                        p * (S::kPanelBytes / S::kElem), w.h, row, 0, pol);
+        issued |= 1u << s;
+        issued_phase = (issued_phase & ~(1u << s)) | (ph << s);
+        if (++s == kR) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      w = then;
+      ++nt;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) A.flags[2 * blockIdx.x + is_v] = bad;
+  } else if (warp == kProducer || warp == kProducerV) {
     // --------------------------------------- producers: K and Q; V --
     if (lane == 0) {
       const bool is_v = warp == kProducerV;
@@ -869,16 +949,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (; ok && !w.done(); w.next(A), ++nt) {
         if (!kE4m3 && !is_v) {
-          // the tile's query rows, once per copy
           const int qs = nt % kNq;
           const uint32_t qph = (nt / kNq) & 1;
           if (!(ok = mbar_wait(q_empty(qs), qph ^ 1u, abort, A.status))) break;
-          const uint32_t box = (uint32_t)(A.group_pos * A.G) * 128u;
-          mbar_arrive_expect_tx(q_full(qs), box * (kD / 64) * S::kCopies);
-          for (int c = 0; c < S::kCopies; ++c)
-            for (int p = 0; p < kD / 64; ++p)
-              tma_load_4d(qb + qs * S::kQBytes + p * 128 * 128 + c * kRP * 128, &tmap_q, q_full(qs), p * 64,
-                          w.h * A.G, w.g * A.group_pos, w.b, policy_evict_normal());
+          load_query_boxes(w, qs);
           issued_q |= 1u << qs;
           issued_q_phase = (issued_q_phase & ~(1u << qs)) | (qph << qs);
         }
@@ -1527,7 +1601,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int jb = w.row(ib) + key0;
               for (int k = 0; k < kKpl && jb + k < w.L; ++k) {
                 const bool seen = mine && (sight.mask(jb + k) & 1u);
-                const size_t at = (((size_t)w.b * A.Lmax + jb + k) * A.Hkv + w.h) * kD + c0;
+                size_t cache_row = (size_t)w.b * A.Lmax + jb + k;
+                if constexpr (kPaged) {
+                  // (a page outside the pool holds zeros)
+                  const int id = __ldcg(A.table + (size_t)w.b * A.max_pages + ((jb + k) >> A.page_log2));
+                  if ((unsigned)id >= (unsigned)A.n_pages) continue;
+                  cache_row = ((size_t)id << A.page_log2) + ((jb + k) & ((1 << A.page_log2) - 1));
+                }
+                const size_t at = (cache_row * A.Hkv + w.h) * kD + c0;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                   uint32_t bits;
@@ -1614,7 +1695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool kE4m3, int kD, int kRP, bool kExtra>
+template <bool kE4m3, int kD, int kRP, bool kExtra, bool kPaged>
 cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tq, cudaStream_t stream) {
   using S = Shape<kE4m3, kD, kRP>;
@@ -1623,7 +1704,7 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !smem_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(cache_attn_kernel<kE4m3, kD, kRP, kExtra>,
+    e = cudaFuncSetAttribute(cache_attn_kernel<kE4m3, kD, kRP, kExtra, kPaged>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
@@ -1643,26 +1724,27 @@ cudaError_t launch_one(const CacheAttnLaunch& A, const CUtensorMap& tk, const CU
   cfg.numAttrs = 1;
   CacheAttnLaunch L = A;
   L.note_tiles = note_tiles(A, parts);
-  e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<kE4m3, kD, kRP, kExtra>, L, tk, tv, tq);
+  L.n_flags = parts * A.head_lanes;
+  e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<kE4m3, kD, kRP, kExtra, kPaged>, L, tk, tv, tq);
   if (e != cudaSuccess) return e;
   return launch_combine<kD, kRP>(L, parts, cfg);
 }
 
-template <bool kE4m3, int kD, int kRP>
+template <bool kE4m3, int kD, int kRP, bool kPaged>
 cudaError_t launch_extra(const CacheAttnLaunch& A, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tq, cudaStream_t stream) {
-  return A.cap > 0.f || A.slopes ? launch_one<kE4m3, kD, kRP, true>(A, tk, tv, tq, stream)
-                                 : launch_one<kE4m3, kD, kRP, false>(A, tk, tv, tq, stream);
+  return A.cap > 0.f || A.slopes ? launch_one<kE4m3, kD, kRP, true, kPaged>(A, tk, tv, tq, stream)
+                                 : launch_one<kE4m3, kD, kRP, false, kPaged>(A, tk, tv, tq, stream);
 }
 
 // Rows per copy: the fewest of 32, 64 and 128 lanes that hold a group.
-template <bool kE4m3, int kD>
+template <bool kE4m3, int kD, bool kPaged = false>
 cudaError_t launch_rows(const CacheAttnLaunch& A, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& tq, cudaStream_t stream) {
   switch (cache_attn_rows(A.group_pos * A.G)) {
-    case 32: return launch_extra<kE4m3, kD, 32>(A, tk, tv, tq, stream);
-    case 64: return launch_extra<kE4m3, kD, 64>(A, tk, tv, tq, stream);
-    default: return launch_extra<kE4m3, kD, 128>(A, tk, tv, tq, stream);
+    case 32: return launch_extra<kE4m3, kD, 32, kPaged>(A, tk, tv, tq, stream);
+    case 64: return launch_extra<kE4m3, kD, 64, kPaged>(A, tk, tv, tq, stream);
+    default: return launch_extra<kE4m3, kD, 128, kPaged>(A, tk, tv, tq, stream);
   }
 }
 

@@ -213,6 +213,10 @@ struct CacheAttnLaunch {
   float* part_ml;                    // [2 CTAs, rows, 2]
   int4* notes;                       // [tiles or CTAs] who shares a tile (write_note)
   int* status;                       // the status word, and whether a length was bad, for the merge
+  const int32_t* table;              // paged cache: [B, max_pages] page of every (1 << page_log2) rows, or null
+  int max_pages, page_log2, n_pages;
+  int* flags;                        // [2 n_flags] by CTA and cache: a page outside the pool was named
+  int n_flags;
   uint32_t anc[SPECDEC_MAX_TREE_NODES][4];   // bit a of row i: node i sees node a
   uint8_t depth[SPECDEC_MAX_TREE_NODES];
 };
@@ -254,6 +258,10 @@ cudaError_t launch_cache_attention_kv8(const CacheAttnLaunch& A, int D, const CU
 cudaError_t launch_cache_attention_bf16(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
                                         const CUtensorMap& tmap_v, const CUtensorMap& tmap_q,
                                         cudaStream_t stream);
+// The same over a paged cache: boxes of up to a page's rows, A.table set.
+cudaError_t launch_cache_attention_paged(const CacheAttnLaunch& A, int D, const CUtensorMap& tmap_k,
+                                         const CUtensorMap& tmap_v, const CUtensorMap& tmap_q,
+                                         cudaStream_t stream);
 
 // Quantise new positions' keys and values into an e4m3 cache.
 struct Kv8AppendLaunch {
@@ -268,6 +276,42 @@ struct Kv8AppendLaunch {
   int* status;
 };
 cudaError_t launch_kv8_append(const Kv8AppendLaunch& A, cudaStream_t stream);
+
+// log2 of a page's rows; -1 for sizes that are not offered.
+inline int page_log2(int page) {
+  return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : page == 256 ? 8 : -1;
+}
+
+// Block tables and slot maps from the requests' lengths (paged_plan.cu).
+struct PagePlanLaunch {
+  int B, max_pages, n_pages, page_log2;
+  int n;                             // rows of a sequence in the map (without cu_rows)
+  long long n_slots;
+  int32_t* table;                    // [B, max_pages]
+  int32_t* held;                     // [B]
+  int32_t* free_pages;               // [n_pages], the first *n_free of them a stack
+  int32_t* n_free;
+  const int32_t* start;              // [B]
+  const int32_t* counts;             // [B]
+  const int32_t* cu_rows;            // [B + 1] or null
+  int32_t* slots;                    // [n_slots] or null
+  int* status;
+};
+cudaError_t launch_page_plan(const PagePlanLaunch& A, cudaStream_t stream);
+
+// New positions' keys and values into the pages (paged_append.cu).
+struct PagedAppendLaunch {
+  long long rows_total;              // B * n
+  int n, row_chunks;                 // rows of a sequence; 16-byte chunks of a row: Hkv * D / 8
+  long long pool_rows;               // n_pages * page
+  const uint4* src[2];               // k_new, v_new
+  long long stride[2];               // 16-byte chunks from one row to the next
+  uint4* pages[2];                   // [pool_rows, row_chunks]
+  const int32_t* slots;              // [rows_total]
+  const int32_t* rows;               // [rows_total] or null
+  int* status;
+};
+cudaError_t launch_paged_append(const PagedAppendLaunch& A, cudaStream_t stream);
 
 // The driver's tensor-map encoder (null when the driver lacks it).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();

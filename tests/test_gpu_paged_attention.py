@@ -1,0 +1,181 @@
+"""Attention over a paged bf16 cache (verify_attention_paged) on the GPU: against the fp64 oracle with the
+tolerances of tests/test_gpu_cache_attention.py (the arithmetic is the masked attention's), and, bit for
+bit, against the masked attention of the same rows laid end to end."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+from oracle import paged as op
+from tests.test_gpu_cache_attention import TREE26, _check, _f
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _i(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def _inputs(seed, B, n, Hq, Hkv, D, page, max_pages, lens, spare=3):
+    """Pages in any order; what belongs to no sequence holds NaN, and so do the rows behind a sequence's end."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = (torch.randn(B, n, Hq, D, generator=g, device=DEV) * 1.5).to(torch.bfloat16)
+    held = [-(-L // page) for L in lens]
+    total = sum(held) + spare
+    order = torch.randperm(total, generator=g, device=DEV).tolist()
+    pages = [torch.randn(total, page, Hkv, D, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    table, at = [[-1] * max_pages for _ in range(B)], 0
+    for b, h in enumerate(held):
+        table[b][:h] = order[at:at + h]
+        at += h
+        if lens[b] % page:
+            for t in pages:
+                t[table[b][h - 1], lens[b] % page:] = float("nan")
+    for t in pages:
+        t[order[at:]] = float("nan")
+    return q, pages, _i(table), _i(lens)
+
+
+def _flat(pages, table, lens, Lmax):
+    """The sequences' rows end to end, [B, Lmax, Hkv, D]; zeros behind them."""
+    out = []
+    for t in pages:
+        c = torch.zeros(len(lens), Lmax, *t.shape[2:], dtype=t.dtype, device=DEV)
+        for b, L in enumerate(lens.tolist()):
+            ids = table[b, :-(-L // t.shape[1])].long()
+            c[b, :L] = t[ids].flatten(0, 1)[:L]
+        out.append(c)
+    return tuple(out)
+
+
+def _call(q, pages, table, lens, expect=0, **how):
+    import target_model_verify_gb300 as tv
+    B, n, Hq, D = q.shape
+    ws = torch.empty(tv.paged_attention_workspace_bytes(B, n, Hq, pages[0].shape[2], D, *pages[0].shape[:2],
+                                                        table.shape[1]), dtype=torch.uint8, device=DEV)
+    out = tv.verify_attention_paged(q, *pages, table, lens, workspace=ws, **how)
+    assert tv.read_status(ws) == expect
+    return out
+
+
+def _run(q, pages, table, lens, **how):
+    import target_model_verify_gb300 as tv
+    out = _call(q, pages, table, lens, **how)
+    flat = _flat(pages, table, lens, table.shape[1] * pages[0].shape[1])
+    assert torch.equal(out, tv.verify_attention_masked(q, *flat, lens, **how))
+    _check("masked", q, flat, lens, out, **how)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("n,Hq,Hkv,D", [
+    (1, 1, 1, 128),               # one head
+    (1, 32, 8, 128),              # a drafter's token, Llama grouping
+    (5, 8, 2, 64),
+    (3, 4, 4, 256),               # wide heads, no grouping
+    (9, 16, 2, 128),              # 72 rows: two groups
+    (40, 2, 2, 64),               # 64 lanes of rows
+])
+def test_matches_oracle_and_masked(page, n, Hq, Hkv, D):
+    lens = [n, 0, n + 15, n + 16, n + 17, 127, 128, 129, 300, 511]
+    q, pages, table, lens = _inputs(page + D, len(lens), n, Hq, Hkv, D, page, 512 // page + 1, lens)
+    _run(q, pages, table, lens)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("how", [
+    {"softcap": 5.0}, {"window": 1}, {"window": 37}, {"window": 200, "softcap": 30.0, "scale": 0.2},
+    {"slopes": True}, {"slopes": True, "window": 64, "softcap": 20.0},
+    {"parent": TREE26}, {"parent": TREE26, "window": 3}, {"parent": TREE26, "slopes": True, "softcap": 10.0},
+], ids=str)
+def test_options(page, D, how):
+    n = 26 if "parent" in how else 4
+    how = dict(how)
+    if how.get("slopes"):
+        how["slopes"] = torch.tensor([0.5, 0.25, 0.1, 0.01], device=DEV)
+    q, pages, table, lens = _inputs(D + n, 3, n, 4, 2, D, page, 320 // page, [310, n, 129])
+    _run(q, pages, table, lens, **how)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_one_long_sequence_and_many_short_ones(page):
+    q, pages, table, lens = _inputs(1, 1, 1, 8, 2, 128, page, 20000 // page + 1, [19999])
+    _run(q, pages, table, lens)
+    many = [1 + 37 * b % 500 for b in range(70)]
+    q, pages, table, lens = _inputs(2, 70, 1, 16, 8, 64, page, 512 // page, many)
+    _run(q, pages, table, lens)
+
+
+def test_pages_behind_the_window_may_be_gone():
+    """What no position sees is not looked up: entries of pages given back hold anything."""
+    q, pages, table, lens = _inputs(3, 2, 3, 4, 2, 128, 16, 70, [1100, 600])
+    want = _call(q, pages, table, lens, window=100)
+    gone = table.clone()
+    gone[0, :(1100 - 3 - 100 + 1) // 16] = -1
+    gone[1, :(600 - 3 - 100 + 1) // 16] = 1 << 30
+    assert torch.equal(_call(q, pages, gone, lens, window=100), want)
+
+
+def test_pages_outside_the_pool_count_as_zeros():
+    for bad in (-1, 1 << 30, 2 ** 31 - 1, -2 ** 31):
+        q, pages, table, lens = _inputs(4, 2, 2, 4, 2, 64, 16, 20, [310, 200])
+        if bad == 1 << 30:
+            bad = pages[0].shape[0]                      # the first that there is not
+        table[0, 4] = table[1, 12] = table[0, 19] = bad
+        out = _call(q, pages, table, lens, expect=op.INVALID)
+        host = table.tolist()
+        k, v = (np.stack([np.pad(op.gather(_f(t), host[b], L), ((0, 320 - L), (0, 0), (0, 0)))
+                          for b, L in enumerate((310, 200))]) for t in pages)
+        want = oc.masked_attention(_f(q), k, v, [310, 200])
+        # the output's rounding, the weights', and the scores' well within it
+        assert (np.abs(_f(out) - want) <= 2.0 ** -8 * np.abs(want) + 3 * 2.0 ** -8 * np.abs(v).max()).all()
+        table[0, 4] = table[1, 12] = table[0, 19] = 0
+        _call(q, pages, table, lens)
+
+
+def test_values_that_are_no_numbers():
+    """They reach the positions that see them and no others, found through the table."""
+    q, pages, table, lens = _inputs(5, 1, 4, 4, 2, 128, 16, 10, [150])
+    for row, col, x in ((147, 3, float("inf")), (148, 5, float("nan")), (149, 7, -float("inf"))):
+        pages[1][table[0, row // 16], row % 16, 0, col] = x
+    out = _f(_call(q, pages, table, lens))[0]
+    for i in range(4):
+        for row, col, x in ((147, 3, np.inf), (148, 5, np.nan), (149, 7, -np.inf)):
+            for h in range(2):
+                got = out[i, h, col]
+                if row <= 146 + i:
+                    assert np.isnan(got) if np.isnan(x) else got == x
+                else:
+                    assert np.isfinite(got)
+            assert np.isfinite(out[i, 2:, col]).all()
+
+
+def test_bad_lengths():
+    q, pages, table, lens = _inputs(6, 4, 2, 4, 2, 64, 16, 4, [64, 30, 20, 33])
+    good = _call(q, pages, table, lens)
+    out = _call(q, pages, table, _i([65, -1, 1, 33]), expect=op.INVALID)
+    assert not out[:3].any() and torch.equal(out[3], good[3])
+
+
+def test_strided_queries_streams_and_graphs():
+    import target_model_verify_gb300 as tv
+    q, pages, table, lens = _inputs(7, 3, 2, 8, 2, 128, 32, 12, [300, 2, 77])
+    want = _call(q, pages, table, lens)
+    wide = torch.randn(3, 2, 12, 128, device=DEV).to(torch.bfloat16)
+    wide[:, :, :8] = q
+    assert torch.equal(_call(wide[:, :, :8], pages, table, lens), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = tv.verify_attention_paged(q, *pages, table, lens, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tv.verify_attention_paged(q, *pages, table, lens)
+    for _ in range(2):
+        q.copy_(q.flip(1))
+        lens.copy_(lens.roll(1))
+        table.copy_(table.roll(1, 0))
+        graph.replay()
+        assert torch.equal(out, _call(q, pages, table, lens))
