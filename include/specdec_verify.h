@@ -484,6 +484,42 @@ int specdec_verify_attention_paged(const void* q, long long q_stride, const void
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * Causal attention over packed prompts, the step that fills a cache: sequences
+ * of different lengths end to end.
+ *   q          [T, Hq, D]   bf16   row t at element t * q_stride
+ *   k, v       [T, Hkv, D]  bf16   at t * k_stride, t * v_stride (each stride a
+ *                                  multiple of 8, at least its row, below
+ *                                  2^31: slices of a fused projection serve)
+ *   cu_seqlens [B + 1]      int32  (device) sequence b is rows cu_seqlens[b] ..
+ *                                  cu_seqlens[b + 1] - 1; empty ones may occur
+ *   slopes     [Hq] fp32 (device) or NULL, scale, softcap, window: as in
+ *                                  specdec_verify_attention_masked(), distance
+ *                                  being the difference of rows
+ *   out        [T, Hq, D]   bf16   o_i = sum_j softmax_j(s_ij) v_j over the rows
+ *                                  j <= i of i's sequence, i - j < window;
+ *                                  rows of no sequence are left as they were
+ * Query head h reads KV head h / (Hq / Hkv). Rows that a position does not see
+ * never reach its output, whatever they hold; an infinity or a NaN in a value
+ * row makes that column infinite or NaN where the row is seen. Softmax
+ * statistics and outputs in fp32, the probabilities enter the value product
+ * as bf16.
+ * A cu_seqlens that is not ascending within 0 .. T sets
+ * SPECDEC_ERR_INVALID_ARG in the status word and nothing is written; a
+ * device-side wait that ran out sets SPECDEC_ERR_TIMEOUT, and no output is to
+ * be used. Limits: D = 64, 128 or 256; Hq % Hkv == 0, Hq / Hkv <= 128, Hq <=
+ * 2^20; T <= 2^30, T * Hq * D < 2^40, (T / (128 / (Hq / Hkv)) + B) * Hkv <
+ * 2^31 - 4096; scale and softcap as there; q, k, v and out 16-byte aligned. B
+ * or T of 0 is a no-op. out must not overlap the inputs. Asynchronous; the
+ * workspace grows with T / (128 / (Hq / Hkv)) + B, 16 bytes each.
+ */
+size_t specdec_prompt_attention_workspace_size(int B, int T, int Hq, int Hkv, int D);
+int specdec_prompt_attention(const void* q, long long q_stride, const void* k, long long k_stride,
+                             const void* v, long long v_stride, const int32_t* cu_seqlens,
+                             const float* slopes, int B, int T, int Hq, int Hkv, int D,
+                             float scale, float softcap, int window, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * The drafter's clustered LM head ("多詞元預測視覺化指南", section 高效嵌入器):
  * cluster logits y = h E^T, the top_k clusters of every row (largest y, ties
  * to the lower index), token logits z = h . W_r for the kept clusters'

@@ -387,6 +387,33 @@ def verify_attention_paged(q, k_pages, v_pages, table, seq_lens, scale=0.0, soft
     return out
 
 
+def prompt_attention_workspace_bytes(B, T, Hq, Hkv, D) -> int:
+    """Workspace of prompt_attention."""
+    return _b.specdec_prompt_attention_workspace_size(B, T, Hq, Hkv, D)
+
+
+def prompt_attention(q, k, v, cu_seqlens, scale=0.0, softcap=0.0, window=0, slopes=None, out=None, workspace=None,
+                     stream=None):
+    """Causal attention of one layer over packed prompts (include/specdec_verify.h,
+    specdec_prompt_attention).
+
+    q [T, Hq, D], k and v [T, Hkv, D] bf16 (slices of a fused projection are taken as they are),
+    cu_seqlens [B + 1] int32: sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1. softcap,
+    window and slopes as in verify_attention_masked(). Returns out [T, Hq, D] bf16; rows of no
+    sequence are left as they were (uninitialised without `out`). A cu_seqlens that does not fit
+    (nothing is written) and a device-side timeout are seen only in read_status() of a workspace that
+    the caller brought.
+    """
+    if stream is not None:
+        with _on(stream, q):
+            got = prompt_attention(q, k, v, cu_seqlens, scale, softcap, window, slopes, out, workspace)
+        return _handed_over(got, out)
+    rc, out = _b.native().prompt_attention(q, k, v, cu_seqlens, scale, softcap, window, slopes, out, workspace)
+    if rc != 0:
+        _b._check(rc, "specdec_prompt_attention")
+    return out
+
+
 def cluster_head(hidden, cluster_emb, W_sorted, starts, token_of_row, top_k=1, max_cluster=None,
                  temperature=1.0, seed=0, position=0, mode=SAMPLE, logits_out=None,
                  workspace=None, stream=None):

@@ -78,6 +78,9 @@ _SIGNATURES = {
     "specdec_verify_attention_paged_workspace_size": (_sz, [_i] * 8),
     "specdec_verify_attention_paged": (_i, [_vp, _ll] + [_vp] * 6 + [_i] * 8 + [_f, _f, _i, _vp, _vp,
                                                                                 _sz, _vp]),
+    "specdec_prompt_attention_workspace_size": (_sz, [_i] * 5),
+    "specdec_prompt_attention": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp] + [_i] * 5 + [_f, _f, _i, _vp, _vp, _sz,
+                                                                                          _vp]),
     "specdec_shard_record_bytes": (_sz, [_i, _i]),
     "specdec_shard_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "specdec_shard_score": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp,
@@ -256,6 +259,14 @@ def specdec_verify_attention_paged_workspace_size(B, n_new, Hq, Hkv, D, n_pages,
 def specdec_verify_attention_paged(*args) -> int:
     """Attention over a paged cache (the parent array is a host int32 array)."""
     return int(lib().specdec_verify_attention_paged(*args))
+
+
+def specdec_prompt_attention_workspace_size(B, T, Hq, Hkv, D) -> int:
+    return int(lib().specdec_prompt_attention_workspace_size(B, T, Hq, Hkv, D))
+
+
+def specdec_prompt_attention(*args) -> int:
+    return int(lib().specdec_prompt_attention(*args))
 
 
 def specdec_cluster_head_workspace_size(M, n_c, top_k, max_cluster) -> int:

@@ -263,6 +263,29 @@ cudaError_t launch_cache_attention_paged(const CacheAttnLaunch& A, int D, const 
                                          const CUtensorMap& tmap_v, const CUtensorMap& tmap_q,
                                          cudaStream_t stream);
 
+// Causal attention over packed prompts (prompt_attention.cu).
+struct PromptLaunch {
+  int B, T, Hq, Hkv, G;
+  int tile_tokens;                   // tokens of a tile: 128 / G
+  int window, cost_shift;            // the list's order is by blocks >> cost_shift
+  long long max_items;               // of a KV head, at most
+  long long v_stride;                // elements from one token's values to the next's
+  float scale, cap, cap_exp;
+  const float* slopes;               // [Hq] or null
+  const int32_t* cu_seqlens;         // [B + 1]
+  const uint16_t* v;
+  __nv_bfloat16* out;                // [T, Hq, D]
+  int4* items;                       // [max_items] (first row, first token, length)
+  int* n_items;
+  int* next;                         // the next (item, KV head) nobody has taken
+  int* status;
+};
+// Tiles of an item, and keys per block.
+constexpr int prompt_tiles(int D) { return D <= 128 ? 2 : 1; }
+constexpr int prompt_block(int D) { return D <= 128 ? 128 : 64; }
+cudaError_t launch_prompt_attention(const PromptLaunch& A, int D, const CUtensorMap& tmap_q,
+                                    const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, cudaStream_t stream);
+
 // Quantise new positions' keys and values into an e4m3 cache.
 struct Kv8AppendLaunch {
   int B, n, Hkv, D, Lmax, n_scale, max_blocks;

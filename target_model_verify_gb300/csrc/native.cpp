@@ -298,9 +298,61 @@ int append_paged(const Tensor& k_new, const Tensor& v_new, const Tensor& k_pages
                               c10::cuda::getCurrentCUDAStream(k_new.device().index()).stream());
 }
 
+std::pair<int, Tensor> prompt_attention(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu_seqlens,
+                                        double scale, double softcap, int64_t window, const OptTensor& slopes,
+                                        const OptTensor& out_given, const OptTensor& workspace) {
+  for (const Tensor* t : {&q, &k, &v})
+    check_type(t->scalar_type() == at::kBFloat16 && t->is_cuda() && t->dim() == 3,
+               "q, k and v must be bfloat16 CUDA tensors [T, heads, D]");
+  const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = k.size(1);
+  check_value(k.sizes() == v.sizes() && k.size(0) == T && k.size(2) == D,
+              "q [T, Hq, D] and k, v [T, Hkv, D] do not fit");
+  check_type(cu_seqlens.scalar_type() == at::kInt && cu_seqlens.is_contiguous() && cu_seqlens.is_cuda() &&
+                 cu_seqlens.dim() == 1,
+             "cu_seqlens must be a contiguous int32 CUDA tensor [B + 1]");
+  check_value(cu_seqlens.size(0) >= 1, "cu_seqlens must have at least one entry");
+  if (slopes) {
+    check_type(slopes->scalar_type() == at::kFloat && slopes->is_contiguous() && slopes->is_cuda(),
+               "slopes must be a contiguous float32 CUDA tensor");
+    check_value(slopes->sizes() == at::IntArrayRef{Hq}, "slopes must have one entry per query head");
+  }
+  for (const Tensor* t : {&k, &v, &cu_seqlens}) same_device(q, *t);
+  same_device(q, slopes);
+  same_device(q, out_given);
+  same_device(q, workspace);
+  const int64_t B = cu_seqlens.size(0) - 1;
+  auto stride = [&](const Tensor& t) { return T ? row_stride(t.unsqueeze(0)) : t.size(1) * D; };
+  const long long qs = stride(q), ks = stride(k), vs = stride(v);
+  const c10::cuda::CUDAGuard guard(q.device());
+  Tensor out;
+  if (out_given) {
+    check_type(out_given->scalar_type() == at::kBFloat16 && out_given->sizes() == q.sizes() &&
+                   out_given->is_contiguous(),
+               "out must be a contiguous bfloat16 CUDA tensor of q's shape");
+    out = *out_given;
+  } else {
+    out = at::empty({T, Hq, D}, q.options());
+  }
+  size_t bytes = 0;
+  if (!workspace) {
+    bytes = specdec_prompt_attention_workspace_size(narrow(B), narrow(T), narrow(Hq), narrow(Hkv), narrow(D));
+    if (bytes == 0) return {SPECDEC_ERR_UNSUPPORTED, out};
+  }
+  c10::DataPtr own;
+  size_t have;
+  void* ws = workspace_of(workspace, bytes, own, have);
+  const int win = window > INT32_MAX ? 0 : window < 0 ? -1 : (int)window;
+  const int rc = specdec_prompt_attention(
+      q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, ptr<int32_t>(cu_seqlens), ptr<float>(slopes), narrow(B),
+      narrow(T), narrow(Hq), narrow(Hkv), narrow(D), to_float(scale), to_float(softcap), win, out.data_ptr(), ws, have,
+      c10::cuda::getCurrentCUDAStream(q.device().index()).stream());
+  return {rc, out};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_native, m) {
+  m.def("prompt_attention", &prompt_attention);
   m.def("plan_pages", &plan_pages);
   m.def("append_paged", &append_paged);
   m.def("append_kv8", &append_kv8);
