@@ -17,9 +17,9 @@
 // first kernel lists a head's items with the longest first; CTAs, one per SM,
 // take them off that list one by one, so that unequal prompts end together.
 //
-// CTA (up to 128 dims): warps 0-3 and 4-7 softmax of one tile each, then one
-// warp each to load and to issue, and two that look through value blocks with
-// keys that not every row sees.
+// CTA (up to 128 dims): warps 0-3 and 4-7 softmax of one tile each, then a
+// warp that loads, one for each tile that issues its products, and one that
+// looks through value blocks with keys that not every row sees.
 //   S = Q K^T, M = 128, N = 128 keys, both operands in shared memory, into
 //     the tile's 128 columns of tensor memory;
 //   softmax: lane = row. The reference of the exponents moves only when a
@@ -85,7 +85,7 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[128]) {
 
 constexpr int kPlanThreads = 1024, kPlanBuckets = 1024;
 constexpr int kSoftRegs = 208, kRoleRegs = 88;      // registers a thread, of 168 at launch (384 threads)
-constexpr int kRoleWarps = 4;                       // behind the softmax warps: loads, issue, and two for values
+constexpr int kRoleWarps = 4;                       // behind the softmax warps: loads, issue, values
 
 template <int kD>
 struct PromptShape {
@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
   using S = PromptShape<kD>;
   constexpr int kBlk = S::kBlk, kR = S::kRing, kTiles = S::kTiles, kSoft = S::kSoft;
-  constexpr int kLoad = kSoft, kIssue = kSoft + 1, kCheck = kSoft + 2, kCheckWarps = 2;      // warp indices
-  constexpr uint32_t kReaders = kSoft + 1 + kCheckWarps;        // warps that are told of an item
+  constexpr int kLoad = kSoft, kIssue = kSoft + 1, kCheck = kIssue + kTiles;     // warp indices
+  constexpr int kCheckWarps = kRoleWarps - 1 - kTiles;
+  constexpr uint32_t kReaders = kSoft + kTiles + kCheckWarps;   // warps that are told of an item
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw);
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
   auto told = [&](int e) { return bar(3 * kR + 10 + e); };
   auto heard = [&](int e) { return bar(3 * kR + 12 + e); };
   const uint32_t drained = bar(3 * kR + 14);
-  const uint32_t board = bar(3 * kR + 17) & ~15u;               // [2] (row0, t0, L, KV head or -1)
+  auto turn = [&](int u) { return bar(3 * kR + 15 + u); };
+  const uint32_t board = bar(3 * kR + 18) & ~15u;               // [2] (row0, t0, L, KV head or -1)
   uint8_t* const words = smem_raw + (board + 32 - raw);
   volatile int* const abort = reinterpret_cast<volatile int*>(words);
   volatile int* const odd = abort + 1;                          // a value that is no number was held back
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kR; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 1 + kCheckWarps);
+      mbar_init(empty(s), kTiles + kCheckWarps);
       mbar_init(v_clean(s), kCheckWarps);
     }
     for (int u = 0; u < 2; ++u) {
@@ -246,10 +248,11 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       mbar_init(s_full(u), 1);
       mbar_init(p_full(u), 4);
       mbar_init(o_done(u), 1);
+      mbar_init(turn(u), 1);
       mbar_init(told(u), 1);
       mbar_init(heard(u), kReaders);
     }
-    mbar_init(drained, 1);
+    mbar_init(drained, kTiles);
     *abort = 0;
     *odd = 0;
     fence_mbar_init();
@@ -349,117 +352,119 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
         }
         next = __shfl_sync(0xffffffffu, next, 0);
       }
-    } else if (warp == kIssue) {
+    } else if (warp < kCheck) {
       // ----------------------------------------------------------- issue --
+      // A warp to a tile: behind MMAs that wait for their turn, even a wait
+      // with nothing to wait for takes 200 cycles, which the other's fill. So
+      // all that a block's products need is waited for ahead of them. The two
+      // take turns, a P V and the next Q K^T each: side by side, both tiles'
+      // products would end late, and their softmax leave the tensor core idle.
       constexpr uint32_t id_qk = instr_desc(1, false, kBlk), id_pv = instr_desc(1, true, kD);
-      const uint64_t q_desc = operand_desc<128>(qb, 16), k_desc = operand_desc<128>(ring, 16);
+      const int u = warp - kIssue;
+      const uint64_t q_desc = operand_desc<128>(qb + u * S::kQTile, 16), k_desc = operand_desc<128>(ring, 16);
       const uint64_t v_desc = operand_desc<128>(ring, kBlk * 128);
+      const uint32_t acc = tmem + S::kColO + u * kD;
       int s = 0;
-      uint32_t ph = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean_ph = 0, n = 0;
+      uint32_t ph = 0, nq = 0, clean_ph = 0, n = 0, n_turn = 0;
       Item<kD> w;
-      // The ring's next block: K or V of the item; false when a wait ran out.
-      auto arrived = [&](bool needs_check) {
-        if (!(ok = warp_wait(full(s), ph))) return false;
-        if (needs_check) {
-          if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) return false;
-          clean_ph ^= 1u << s;
-        }
-        return true;
+      auto my_turn = [&]() {                     // the second tile's begins with the first one's end
+        ok = warp_wait(turn(u), (n_turn++ & 1) ^ (u == 0 ? 1u : 0u));
+        return ok;
       };
-      auto release = [&]() {                     // once what was issued so far is done
-        if (elect_one()) tc_commit(empty(s));
-        __syncwarp();
+      auto pass_turn = [&]() {
+        if (lane == 0) mbar_arrive(turn(u ^ 1));
+      };
+      auto step = [&]() {
         if (++s == kR) {
           s = 0;
           ph ^= 1u;
         }
       };
-      auto scores = [&](int u, int buf, bool last) {      // of tile u against the ring's block
+      auto release = [&](bool used) {            // once what was issued so far is done
+        if (elect_one()) {
+          if (used)
+            tc_commit(empty(s));
+          else
+            mbar_arrive(empty(s));
+        }
+        __syncwarp();
+        step();
+      };
+      auto scores = [&](int buf, bool last) {    // against the ring's block
         tc_fence_after();
         if (elect_one()) {
           const uint64_t kd = k_desc + (uint64_t)((uint32_t)(s * S::kSlotBytes) >> 4);
-          const uint64_t qd = q_desc + (uint64_t)((uint32_t)(u * S::kQTile) >> 4);
 #pragma unroll
           for (int p = 0; p < S::kPanels; ++p)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss<false>(tmem + S::kColS + buf * kBlk, qd + (uint64_t)((p * 128 * 128 + k * 32) >> 4),
+              mma_ss<false>(tmem + S::kColS + buf * kBlk, q_desc + (uint64_t)((p * 128 * 128 + k * 32) >> 4),
                             kd + (uint64_t)((p * kBlk * 128 + k * 32) >> 4), id_qk, p + k > 0);
           tc_commit(s_full(buf));
           if (last) tc_commit(q_empty(u));
         }
         __syncwarp();
       };
-      auto values = [&](int u, int buf, bool more, bool last) {   // more: adds to what is there
+      auto values = [&](int buf, bool more, bool last) {       // more: adds to what is there
         tc_fence_after();
         if (elect_one()) {
           const uint64_t vd = v_desc + (uint64_t)((uint32_t)(s * S::kSlotBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < kBlk / 16; ++k)
-            mma_ts<false>(tmem + S::kColO + u * kD, tmem + S::kColS + buf * kBlk + k * 8,
-                          vd + (uint64_t)(k * 2048 >> 4), id_pv, more || k > 0);
+            mma_ts<false>(acc, tmem + S::kColS + buf * kBlk + k * 8, vd + (uint64_t)(k * 2048 >> 4), id_pv,
+                          more || k > 0);
           if (last) tc_commit(o_done(kTiles == 2 ? u : buf));
         }
         __syncwarp();
       };
+      // V of block i is in the ring's slot.
+      auto arrived_v = [&](int i) {
+        if (!(ok = warp_wait(full(s), ph))) return false;
+        if (!w.clean(i)) {
+          if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) return false;
+          clean_ph ^= 1u << s;
+        }
+        return true;
+      };
       while (ok && hear(w)) {
-#pragma unroll
-        for (int u = 0; u < kTiles; ++u)
-          if (ok && w.tile(u)) {
-            ok = warp_wait(q_full(u), nq[u] & 1);
-            ++nq[u];
-          }
-        if (!ok || !arrived(false)) break;
+        if (w.tile(u) && !(ok = warp_wait(q_full(u), nq++ & 1))) break;
+        if (!(ok = warp_wait(full(s), ph))) break;
         if constexpr (kTiles == 2) {
-#pragma unroll
-          for (int u = 0; u < kTiles; ++u)
-            if (w.on(u, w.first)) scores(u, u, w.first + 1 == w.end(u));
-          release();
-          for (int i = w.first; ok && i < w.last; ++i) {
-            // V i is in the ring's slot s, K i + 1 in the next
-            if (!arrived(!w.clean(i))) break;
-            const int sv = s;
-            const uint32_t phv = ph;
-            bool have_k = false;
-#pragma unroll
-            for (int u = 0; u < kTiles; ++u) {
-              if (!ok) continue;
-              if (w.on(u, i)) {
-                if (!(ok = warp_wait(p_full(u), np[u] & 1))) continue;
-                ++np[u];
-                values(u, u, i > w.begin(u), i + 1 == w.end(u));
-              }
-              if (w.on(u, i + 1)) {
-                if (++s == kR) {
-                  s = 0;
-                  ph ^= 1u;
-                }
-                if (!have_k && !arrived(false)) continue;
-                have_k = true;
-                scores(u, u, i + 2 == w.end(u));
-                s = sv;
-                ph = phv;
-              }
+          if (!my_turn()) break;
+          if (w.on(u, w.first)) scores(u, w.first + 1 == w.end(u));
+          pass_turn();
+          release(w.on(u, w.first));
+          for (int i = w.first; i < w.last; ++i) {
+            const bool here = w.on(u, i), then = i + 1 < w.last;
+            if (!arrived_v(i)) break;
+            if (then && !(ok = warp_wait(full(s + 1 == kR ? 0 : s + 1), s + 1 == kR ? ph ^ 1u : ph))) break;
+            if (here && !(ok = warp_wait(p_full(u), n++ & 1))) break;
+            if (!my_turn()) break;
+            if (here) values(u, i > w.begin(u), i + 1 == w.end(u));
+            release(here);
+            if (then) {
+              if (w.on(u, i + 1)) scores(u, i + 2 == w.end(u));
+              pass_turn();
+              release(w.on(u, i + 1));
+            } else {
+              pass_turn();
             }
-            if (!ok) break;
-            release();
-            if (i + 1 < w.last) release();
           }
         } else {
-          // scores up to two blocks ahead, in buffers taken in turn
-          scores(0, n & 1, w.first + 1 == w.last);
-          release();
-          for (int i = w.first; ok && i < w.last; ++i, ++n) {
+          // scores a block ahead, in buffers taken in turn
+          scores(n & 1, w.first + 1 == w.last);
+          release(true);
+          for (int i = w.first; i < w.last; ++i, ++n) {
             if (i + 1 < w.last) {
-              if (!arrived(false)) break;
+              if (!(ok = warp_wait(full(s), ph))) break;
               // (its buffer's P was read by the product issued last)
-              scores(0, (n + 1) & 1, i + 2 == w.last);
-              release();
+              scores((n + 1) & 1, i + 2 == w.last);
+              release(true);
             }
-            if (!arrived(!w.clean(i))) break;
+            if (!arrived_v(i)) break;
             if (!(ok = warp_wait(p_full(n & 1), (n >> 1) & 1))) break;
-            values(0, n & 1, i > w.first, true);
-            release();
+            values(n & 1, i > w.first, true);
+            release(true);
           }
         }
       }
@@ -479,25 +484,34 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       auto pass = [&](bool look) {
         if (!(ok = warp_wait(full(s), ph))) return;
         if (look) {
-          for (int e = at; e < S::kSlotBytes / 16; e += 32 * kCheckWarps) {
-            const uint32_t a = ring + s * S::kSlotBytes + e * 16;
-            const uint4 v = lds128(a);
-            uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            bool put = false;
+          constexpr int kBatch = 8;
+          static_assert(S::kSlotBytes / 16 % (32 * kCheckWarps * kBatch) == 0, "whole batches");
+#pragma unroll 1
+          for (int e0 = at; e0 < S::kSlotBytes / 16; e0 += 32 * kCheckWarps * kBatch) {
+            uint4 v[kBatch];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((x[k] & 0x7f80u) == 0x7f80u) {
-                x[k] &= 0xffff0000u;
-                put = true;
+            for (int y = 0; y < kBatch; ++y)
+              v[y] = lds128(ring + s * S::kSlotBytes + (e0 + y * 32 * kCheckWarps) * 16);
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+              const uint32_t a = ring + s * S::kSlotBytes + (e0 + y * 32 * kCheckWarps) * 16;
+              uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+              bool put = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((x[k] & 0x7f80u) == 0x7f80u) {
+                  x[k] &= 0xffff0000u;
+                  put = true;
+                }
+                if ((x[k] & 0x7f800000u) == 0x7f800000u) {
+                  x[k] &= 0x0000ffffu;
+                  put = true;
+                }
               }
-              if ((x[k] & 0x7f800000u) == 0x7f800000u) {
-                x[k] &= 0x0000ffffu;
-                put = true;
+              if (put) {
+                sts128(a, x[0], x[1], x[2], x[3]);
+                *odd = 1;
               }
-            }
-            if (put) {
-              sts128(a, x[0], x[1], x[2], x[3]);
-              *odd = 1;
             }
           }
           fence_proxy_async_smem();
