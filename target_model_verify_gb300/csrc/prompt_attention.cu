@@ -484,34 +484,34 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       auto pass = [&](bool look) {
         if (!(ok = warp_wait(full(s), ph))) return;
         if (look) {
-          constexpr int kBatch = 8;
-          static_assert(S::kSlotBytes / 16 % (32 * kCheckWarps * kBatch) == 0, "whole batches");
+          // 16 bytes of each of kBatch runs at a time: an exponent of ones
+          // carries into the sign's place
+          constexpr int kBatch = 8, kStep = 32 * kCheckWarps * 16;
+          static_assert(S::kSlotBytes % (kStep * kBatch) == 0, "whole batches");
 #pragma unroll 1
-          for (int e0 = at; e0 < S::kSlotBytes / 16; e0 += 32 * kCheckWarps * kBatch) {
+          for (uint32_t a0 = ring + s * S::kSlotBytes + at * 16, end = a0 + S::kSlotBytes; a0 < end;
+               a0 += kStep * kBatch) {
             uint4 v[kBatch];
 #pragma unroll
+            for (int y = 0; y < kBatch; ++y) v[y] = lds128(a0 + y * kStep);
+            uint32_t any = 0;
+#pragma unroll
             for (int y = 0; y < kBatch; ++y)
-              v[y] = lds128(ring + s * S::kSlotBytes + (e0 + y * 32 * kCheckWarps) * 16);
+              any |= ((v[y].x & 0x7fff7fffu) + 0x00800080u) | ((v[y].y & 0x7fff7fffu) + 0x00800080u) |
+                     ((v[y].z & 0x7fff7fffu) + 0x00800080u) | ((v[y].w & 0x7fff7fffu) + 0x00800080u);
+            if (__builtin_expect((any & 0x80008000u) != 0, 0)) {
+#pragma unroll 1
+              for (int y = 0; y < kBatch; ++y) {
+                const uint4 z = lds128(a0 + y * kStep);
+                uint32_t x[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-              const uint32_t a = ring + s * S::kSlotBytes + (e0 + y * 32 * kCheckWarps) * 16;
-              uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-              bool put = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((x[k] & 0x7f80u) == 0x7f80u) {
-                  x[k] &= 0xffff0000u;
-                  put = true;
+                for (int k = 0; k < 4; ++k) {
+                  if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u;
+                  if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0x0000ffffu;
                 }
-                if ((x[k] & 0x7f800000u) == 0x7f800000u) {
-                  x[k] &= 0x0000ffffu;
-                  put = true;
-                }
+                sts128(a0 + y * kStep, x[0], x[1], x[2], x[3]);
               }
-              if (put) {
-                sts128(a, x[0], x[1], x[2], x[3]);
-                *odd = 1;
-              }
+              *odd = 1;
             }
           }
           fence_proxy_async_smem();
@@ -645,11 +645,13 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       ++n_items;
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // NaN stays
-      __nv_bfloat16* const out = A.out + ((size_t)(w.row0 + tok) * A.Hq + (size_t)w.h * A.G + gq) * kD;
+      // Where each row of the lane's eight goes (see below); none: not this call's.
+      const long long none = -1;
+      const long long my_row = mine ? ((long long)(w.row0 + tok) * A.Hq + w.h * A.G + gq) * kD : none;
       const bool has_odd = *odd != 0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kD; c0 += 32) {
-        uint32_t o[32];
+      for (int c0 = 0; c0 < kD; c0 += 64) {
+        uint32_t o[64];
         tmem_load(tl + S::kColO + u * kD + c0, o);
         if (__builtin_expect(has_odd, 0) && mine) {
           // Infinities and NaN that were held back (rare), where they are seen
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
             for (int j = max(low, i * kBlk); j <= min(tok, i * kBlk + kBlk - 1); ++j) {
               const uint16_t* v = A.v + (size_t)(w.row0 + j) * A.v_stride + (size_t)w.h * kD + c0;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
+              for (int k = 0; k < 64; ++k) {
                 const uint32_t bits = (uint32_t)v[k] << 16;
                 if ((bits & 0x7f800000u) == 0x7f800000u)
                   o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(bits));
@@ -667,15 +669,33 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
             }
           }
         }
-        if (mine) {
+        __syncwarp();
+        // 16-byte pieces change places among eight lanes, so that a store
+        // writes 128 bytes of each of four rows: with a row to a lane, each
+        // touches 32 lines, and the two tiles' outputs took 5000 cycles.
+        uint32_t y[8][4];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t p[4];
+        for (int k = 0; k < 64; k += 2)
+          y[k / 8][k / 2 % 4] = pack2<false>(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              p[x] = pack2<false>(__uint_as_float(o[k + 2 * x]) * inv, __uint_as_float(o[k + 2 * x + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + c0 + k) = make_uint4(p[0], p[1], p[2], p[3]);
+        for (int b = 1; b < 8; b <<= 1) {
+          const bool upper = lane & b;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (k & b) continue;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? y[k][x] : y[k | b][x], b);
+              y[k][x] = upper ? got : y[k][x];
+              y[k | b][x] = upper ? y[k | b][x] : got;
+            }
           }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const long long to = __shfl_sync(0xffffffffu, my_row, (lane & 24) | k);
+          if (to != none)
+            *reinterpret_cast<uint4*>(A.out + to + c0 + (lane & 7) * 8) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
         }
         __syncwarp();                        // the next load is the whole warp's
       }
