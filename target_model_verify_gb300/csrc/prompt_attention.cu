@@ -84,18 +84,20 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&x)[128]) {
 }
 
 constexpr int kPlanThreads = 1024, kPlanBuckets = 1024;
-constexpr int kSoftRegs = 208, kRoleRegs = 88;      // registers a thread, of 168 at launch (384 threads)
+constexpr int kSoftRegs = 208, kRoleRegs = 88;      // registers a thread, of 168 at launch (two tiles: 384 threads)
 constexpr int kRoleWarps = 4;                       // behind the softmax warps: loads, issue, values
 
 template <int kD>
 struct PromptShape {
   static constexpr int kTiles = prompt_tiles(kD);               // of an item, a softmax warpgroup each
   static constexpr int kBlk = prompt_block(kD);                 // keys per block
-  static constexpr int kSoft = 4 * kTiles;                      // softmax warps
+  static constexpr int kHalves = kTiles == 2 ? 1 : 2;           // warps that share a row's keys of a block
+  static constexpr int kSoft = 4 * kHalves * kTiles;            // softmax warps
   static constexpr int kThreads = 32 * (kSoft + kRoleWarps);
   static constexpr int kPanels = kD / 64;                       // 128-byte runs of a row
   static constexpr int kSlotBytes = kBlk * kD * 2;              // a block of K, or of V
   static constexpr int kQTile = 128 * kD * 2;
+  static constexpr int kKeys = kBlk / kHalves;                  // of a block, to a softmax thread
   static constexpr int kFixed = 1024 + kTiles * kQTile + 1024;
   static constexpr int kRingMax = (kSmemLimit - kFixed) / kSlotBytes;
   static constexpr int kRing = kRingMax < 8 ? kRingMax : 8;     // blocks (K and V alike) in flight
@@ -104,6 +106,19 @@ struct PromptShape {
   static constexpr int kColS = 0, kColO = 2 * kBlk;             // two buffers of scores, then the outputs
   static_assert(kColO + kTiles * kD <= 512, "tensor memory");
 };
+
+// A barrier that counts the threads with x.
+__device__ __forceinline__ int bar_count(int id, int nthreads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.popc.u32 %0, %2, %3, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(nthreads)
+      : "memory");
+  return (int)r;
+}
 
 // An item as its roles see it.
 template <int kD>
@@ -207,7 +222,8 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ PromptLaunch A, const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
   using S = PromptShape<kD>;
-  constexpr int kBlk = S::kBlk, kR = S::kRing, kTiles = S::kTiles, kSoft = S::kSoft;
+  constexpr int kBlk = S::kBlk, kKeys = S::kKeys, kR = S::kRing, kTiles = S::kTiles, kHalves = S::kHalves,
+                kSoft = S::kSoft;
   constexpr int kLoad = kSoft, kIssue = kSoft + 1, kCheck = kIssue + kTiles;     // warp indices
   constexpr int kCheckWarps = kRoleWarps - 1 - kTiles;
   constexpr uint32_t kReaders = kSoft + kTiles + kCheckWarps;   // warps that are told of an item
@@ -231,6 +247,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
   const uint32_t drained = bar(3 * kR + 14);
   auto turn = [&](int u) { return bar(3 * kR + 15 + u); };
   const uint32_t board = bar(3 * kR + 18) & ~15u;               // [2] (row0, t0, L, KV head or -1)
+  const uint32_t rows_tab = board + 64;                         // [128] what a row's halves tell each other
   uint8_t* const words = smem_raw + (board + 32 - raw);
   volatile int* const abort = reinterpret_cast<volatile int*>(words);
   volatile int* const odd = abort + 1;                          // a value that is no number was held back
@@ -246,7 +263,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       mbar_init(q_full(u), 1);
       mbar_init(q_empty(u), 1);
       mbar_init(s_full(u), 1);
-      mbar_init(p_full(u), 4);
+      mbar_init(p_full(u), 4 * kHalves);
       mbar_init(o_done(u), 1);
       mbar_init(turn(u), 1);
       mbar_init(told(u), 1);
@@ -354,45 +371,36 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       }
     } else if (warp < kCheck) {
       // ----------------------------------------------------------- issue --
-      // A warp to a tile: behind MMAs that wait for their turn, even a wait
+      // A thread to a tile: behind MMAs that wait for their place, even a wait
       // with nothing to wait for takes 200 cycles, which the other's fill. So
       // all that a block's products need is waited for ahead of them. The two
       // take turns, a P V and the next Q K^T each: side by side, both tiles'
       // products would end late, and their softmax leave the tensor core idle.
       constexpr uint32_t id_qk = instr_desc(1, false, kBlk), id_pv = instr_desc(1, true, kD);
-      const int u = warp - kIssue;
-      const uint64_t q_desc = operand_desc<128>(qb + u * S::kQTile, 16), k_desc = operand_desc<128>(ring, 16);
-      const uint64_t v_desc = operand_desc<128>(ring, kBlk * 128);
-      const uint32_t acc = tmem + S::kColO + u * kD;
-      int s = 0;
-      uint32_t ph = 0, nq = 0, clean_ph = 0, n = 0, n_turn = 0;
-      Item<kD> w;
-      auto my_turn = [&]() {                     // the second tile's begins with the first one's end
-        ok = warp_wait(turn(u), (n_turn++ & 1) ^ (u == 0 ? 1u : 0u));
-        return ok;
-      };
-      auto pass_turn = [&]() {
-        if (lane == 0) mbar_arrive(turn(u ^ 1));
-      };
-      auto step = [&]() {
-        if (++s == kR) {
-          s = 0;
-          ph ^= 1u;
-        }
-      };
-      auto release = [&](bool used) {            // once what was issued so far is done
-        if (elect_one()) {
+      if (elect_one()) {
+        const int u = warp - kIssue;
+        const uint64_t q_desc = operand_desc<128>(qb + u * S::kQTile, 16), k_desc = operand_desc<128>(ring, 16);
+        const uint64_t v_desc = operand_desc<128>(ring, kBlk * 128);
+        const uint32_t acc = tmem + S::kColO + u * kD;
+        int s = 0;
+        uint32_t ph = 0, nq = 0, clean_ph = 0, n = 0, n_turn = 0;
+        Item<kD> w;
+        auto wait = [&](uint32_t b, uint32_t parity) { return ok = mbar_wait<true>(b, parity, abort, A.status); };
+        auto my_turn = [&]() {                   // the second tile's begins with the first one's end
+          return wait(turn(u), (n_turn++ & 1) ^ (u == 0 ? 1u : 0u));
+        };
+        auto pass_turn = [&]() { mbar_arrive(turn(u ^ 1)); };
+        auto release = [&](bool used) {          // once what was issued so far is done
           if (used)
             tc_commit(empty(s));
           else
             mbar_arrive(empty(s));
-        }
-        __syncwarp();
-        step();
-      };
-      auto scores = [&](int buf, bool last) {    // against the ring's block
-        tc_fence_after();
-        if (elect_one()) {
+          if (++s == kR) {
+            s = 0;
+            ph ^= 1u;
+          }
+        };
+        auto scores = [&](int buf, bool last) {  // against the ring's block
           const uint64_t kd = k_desc + (uint64_t)((uint32_t)(s * S::kSlotBytes) >> 4);
 #pragma unroll
           for (int p = 0; p < S::kPanels; ++p)
@@ -402,75 +410,77 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
                             kd + (uint64_t)((p * kBlk * 128 + k * 32) >> 4), id_qk, p + k > 0);
           tc_commit(s_full(buf));
           if (last) tc_commit(q_empty(u));
-        }
-        __syncwarp();
-      };
-      auto values = [&](int buf, bool more, bool last) {       // more: adds to what is there
-        tc_fence_after();
-        if (elect_one()) {
+        };
+        auto values = [&](int buf, bool more, bool last) {     // more: adds to what is there
           const uint64_t vd = v_desc + (uint64_t)((uint32_t)(s * S::kSlotBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < kBlk / 16; ++k)
             mma_ts<false>(acc, tmem + S::kColS + buf * kBlk + k * 8, vd + (uint64_t)(k * 2048 >> 4), id_pv,
                           more || k > 0);
           if (last) tc_commit(o_done(kTiles == 2 ? u : buf));
-        }
-        __syncwarp();
-      };
-      // V of block i is in the ring's slot.
-      auto arrived_v = [&](int i) {
-        if (!(ok = warp_wait(full(s), ph))) return false;
-        if (!w.clean(i)) {
-          if (!(ok = warp_wait(v_clean(s), (clean_ph >> s) & 1))) return false;
-          clean_ph ^= 1u << s;
-        }
-        return true;
-      };
-      while (ok && hear(w)) {
-        if (w.tile(u) && !(ok = warp_wait(q_full(u), nq++ & 1))) break;
-        if (!(ok = warp_wait(full(s), ph))) break;
-        if constexpr (kTiles == 2) {
-          if (!my_turn()) break;
-          if (w.on(u, w.first)) scores(u, w.first + 1 == w.end(u));
-          pass_turn();
-          release(w.on(u, w.first));
-          for (int i = w.first; i < w.last; ++i) {
-            const bool here = w.on(u, i), then = i + 1 < w.last;
-            if (!arrived_v(i)) break;
-            if (then && !(ok = warp_wait(full(s + 1 == kR ? 0 : s + 1), s + 1 == kR ? ph ^ 1u : ph))) break;
-            if (here && !(ok = warp_wait(p_full(u), n++ & 1))) break;
-            if (!my_turn()) break;
-            if (here) values(u, i > w.begin(u), i + 1 == w.end(u));
-            release(here);
-            if (then) {
-              if (w.on(u, i + 1)) scores(u, i + 2 == w.end(u));
-              pass_turn();
-              release(w.on(u, i + 1));
-            } else {
-              pass_turn();
-            }
+        };
+        // V of block i is in the ring's slot.
+        auto arrived_v = [&](int i) {
+          if (!wait(full(s), ph)) return false;
+          if (!w.clean(i)) {
+            if (!wait(v_clean(s), (clean_ph >> s) & 1)) return false;
+            clean_ph ^= 1u << s;
           }
-        } else {
-          // scores a block ahead, in buffers taken in turn
-          scores(n & 1, w.first + 1 == w.last);
-          release(true);
-          for (int i = w.first; i < w.last; ++i, ++n) {
-            if (i + 1 < w.last) {
-              if (!(ok = warp_wait(full(s), ph))) break;
-              // (its buffer's P was read by the product issued last)
-              scores((n + 1) & 1, i + 2 == w.last);
+          return true;
+        };
+        while (ok && wait(told(n_told & 1), (n_told >> 1) & 1)) {
+          const uint4 it = lds128(board + 16 * (n_told & 1));
+          mbar_arrive(heard(n_told++ & 1));
+          if ((int)it.w < 0) break;
+          w.set(A, make_int4((int)it.x, (int)it.y, (int)it.z, 0), (int)it.w);
+          if (w.tile(u) && !wait(q_full(u), nq++ & 1)) break;
+          if (!wait(full(s), ph)) break;
+          if constexpr (kTiles == 2) {
+            if (!my_turn()) break;
+            tc_fence_after();
+            const bool begins = w.on(u, w.first);
+            if (begins) scores(u, w.first + 1 == w.end(u));
+            pass_turn();
+            release(begins);
+            for (int i = w.first; i < w.last; ++i) {
+              const bool here = w.on(u, i), then = i + 1 < w.last, more = then && w.on(u, i + 1);
+              if (!arrived_v(i)) break;
+              if (then && !wait(full(s + 1 == kR ? 0 : s + 1), s + 1 == kR ? ph ^ 1u : ph)) break;
+              if (here && !wait(p_full(u), n++ & 1)) break;
+              if (!my_turn()) break;
+              tc_fence_after();
+              if (here) values(u, i > w.begin(u), i + 1 == w.end(u));
+              release(here);
+              if (more) scores(u, i + 2 == w.end(u));
+              pass_turn();
+              if (then) release(more);
+            }
+          } else {
+            // scores a block ahead, in buffers taken in turn
+            tc_fence_after();
+            scores(n & 1, w.first + 1 == w.last);
+            release(true);
+            for (int i = w.first; i < w.last; ++i, ++n) {
+              if (i + 1 < w.last) {
+                if (!wait(full(s), ph)) break;
+                tc_fence_after();
+                // (its buffer's P was read by the product issued last)
+                scores((n + 1) & 1, i + 2 == w.last);
+                release(true);
+              }
+              if (!arrived_v(i)) break;
+              if (!wait(p_full(n & 1), (n >> 1) & 1)) break;
+              tc_fence_after();
+              values(n & 1, i > w.first, true);
               release(true);
             }
-            if (!arrived_v(i)) break;
-            if (!(ok = warp_wait(p_full(n & 1), (n >> 1) & 1))) break;
-            values(n & 1, i > w.first, true);
-            release(true);
           }
         }
+        // every product has to be done before the tensor memory is given back
+        tc_commit(drained);
+        wait_drain(drained, 0);
       }
-      // every product has to be done before the tensor memory is given back
-      if (elect_one()) tc_commit(drained);
-      wait_drain(drained, 0);
+      __syncwarp();
     } else {
       // ---------------------------------------------------------- values --
       // Blocks with keys that not every row sees: an infinity or a NaN there
@@ -536,12 +546,35 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
   } else {
     // --------------------------------------------------------------- softmax --
     if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int u = kTiles == 2 ? warp >> 2 : 0, row = (warp & 3) * 32 + lane;
+    const int u = warp / (4 * kHalves), half = (warp >> 2) % kHalves, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);      // this warp's lanes
     const int tok_of_row = row / A.G, gq = row % A.G;
+    // Two warps of the same rows meet at a barrier of their own once for every
+    // item and block, whatever became of their waits, and so go on, or give up,
+    // together.
+    const int pair_bar = 1 + (warp & 3);
+    auto any_of_row = [&](bool x) {
+      return kHalves == 1 ? __any_sync(0xffffffffu, x) != 0 : bar_count(pair_bar, 32 * kHalves, x) > 0;
+    };
+    // A row's value from both halves.
+    auto joined = [&](float x, auto join) {
+      if (kHalves == 1) return x;
+      const uint32_t at = rows_tab + row * 4;
+      if (half == 1) sts32(at, __float_as_uint(x));
+      named_bar_sync(pair_bar, 32 * kHalves);
+      if (half == 0) {
+        x = join(x, __uint_as_float(lds32(at)));
+        sts32(at, __float_as_uint(x));
+      }
+      named_bar_sync(pair_bar, 32 * kHalves);
+      return half == 0 ? x : __uint_as_float(lds32(at));
+    };
     uint32_t n = 0, n_items = 0;       // this tile's blocks and items
     Item<kD> w;
-    while (ok && hear(w)) {
+    for (;;) {
+      const bool more = ok && hear(w);
+      if (kHalves > 1 && any_of_row(!ok)) ok = false;
+      if (!ok || !more) break;
       if (!w.tile(u)) continue;
       const int ta = w.t0 + u * A.tile_tokens, tok = ta + tok_of_row;
       const bool mine = tok_of_row < A.tile_tokens && tok < w.L;
@@ -549,14 +582,15 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       for (int i = w.begin(u); i < w.end(u); ++i, ++n) {
         const int buf = kTiles == 2 ? u : (int)(n & 1);
-        const int j0 = i * kBlk;
-        if (!(ok = warp_wait(s_full(buf), kTiles == 2 ? n & 1 : (n >> 1) & 1))) break;
+        const int j0 = i * kBlk + half * kKeys;
+        ok = warp_wait(s_full(buf), kTiles == 2 ? n & 1 : (n >> 1) & 1);
+        if (kHalves == 1 && !ok) break;
         tc_fence_after();
         union {
-          uint32_t u[kBlk];
-          float f[kBlk];
+          uint32_t u[kKeys];
+          float f[kKeys];
         } x;
-        tmem_load(tl + S::kColS + buf * kBlk, x.u);
+        tmem_load(tl + S::kColS + buf * kBlk + half * kKeys, x.u);
         float c = A.scale * kLog2e, top = -INFINITY;
         if constexpr (kExtra) {
           // cap and bias: the scores become exponents
@@ -564,17 +598,17 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           if (A.cap > 0.f) {
             const float cl = A.cap * kLog2e, ce = A.scale * A.cap_exp;
 #pragma unroll
-            for (int k = 0; k < kBlk; ++k) x.f[k] = capped(x.f[k] * ce, cl, cl + fmaf(slope, (float)k, b0));
+            for (int k = 0; k < kKeys; ++k) x.f[k] = capped(x.f[k] * ce, cl, cl + fmaf(slope, (float)k, b0));
           } else {
 #pragma unroll
-            for (int k = 0; k < kBlk; ++k) x.f[k] = fmaf(x.f[k], c, fmaf(slope, (float)k, b0));
+            for (int k = 0; k < kKeys; ++k) x.f[k] = fmaf(x.f[k], c, fmaf(slope, (float)k, b0));
           }
           c = 1.f;
         }
         if (__builtin_expect(!w.clean(i), 0)) {
-          const int hi = tok - j0, lo = A.window > 0 ? hi - A.window + 1 : 0;     // keys lo .. hi of the block
+          const int hi = tok - j0, lo = A.window > 0 ? hi - A.window + 1 : 0;     // keys lo .. hi of the thread's
 #pragma unroll
-          for (int k0 = 0; k0 < kBlk; k0 += 32) {
+          for (int k0 = 0; k0 < kKeys; k0 += 32) {
             const int a = lo - k0, b = hi - k0;
             uint32_t m = b < 0 ? 0u : b >= 31 ? 0xffffffffu : (2u << b) - 1u;
             if (a > 0) m &= a >= 32 ? 0u : 0xffffffffu << a;
@@ -583,20 +617,27 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           }
         }
 #pragma unroll
-        for (int k = 0; k < kBlk; k += 32) top = fmaxf(top, largest<32>(x.f + k));
+        for (int k = 0; k < kKeys; k += 32) top = fmaxf(top, largest<32>(x.f + k));
         top *= c;
         // ---- the reference follows the maximum when it has to ----
-        const bool up = mine && top > m_ref + kHeadroom;
-        if (__builtin_expect(__any_sync(0xffffffffu, up), 0)) {
+        // (Behind the barrier both halves have their scores, which P overwrites.)
+        if (kHalves > 1) tc_fence_before();
+        const bool rare = any_of_row((kHalves > 1 && !ok) || (mine && top > m_ref + kHeadroom));
+        if (kHalves > 1) tc_fence_after();
+        if (__builtin_expect(rare, 0)) {
+          if (kHalves > 1 && any_of_row(!ok)) ok = false;
+          if (!ok) break;
+          top = joined(top, [](float a, float b) { return fmaxf(a, b); });
+          const bool up = mine && top > m_ref + kHeadroom;
           const float alpha = up ? ex2(m_ref - top) : 1.f;
           if (up) m_ref = top;
           l *= alpha;
           if (i > w.begin(u)) {
             // the products so far are done: with two tiles these scores came behind them
-            if (kTiles == 1 && !(ok = warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1))) break;
+            if (kTiles == 1) ok = warp_wait(o_done((n - 1) & 1), ((n - 1) >> 1) & 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < kD; c0 += 16) {
+            for (int c0 = half * (kD / kHalves); c0 < (half + 1) * (kD / kHalves); c0 += 16) {
               uint32_t v[16];
               tmem_load(tl + S::kColO + u * kD + c0, v);
 #pragma unroll
@@ -613,13 +654,13 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           // Exponents of 2^20 and more are rounded before the subtraction, as the
           // reference was: a fused one would bring out the reference's rounding.
 #pragma unroll
-          for (int k = 0; k < kBlk; ++k) x.f[k] = __fadd_rn(__fmul_rn(x.f[k], c), sub);
+          for (int k = 0; k < kKeys; ++k) x.f[k] = __fadd_rn(__fmul_rn(x.f[k], c), sub);
           c = 1.f;
           sub = 0.f;
         }
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int k0 = 0; k0 < kBlk; k0 += 32) {
+        for (int k0 = 0; k0 < kKeys; k0 += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
@@ -630,7 +671,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
             pk[k / 2] = pack2<false>(y0, y1);
             add2(s0, s1, y0, y1);
           }
-          tmem_store(tl + S::kColS + buf * kBlk + k0 / 2, pk, Cols<16>{});
+          tmem_store(tl + S::kColS + buf * kBlk + (half * kKeys + k0) / 2, pk, Cols<16>{});
         }
         l += s0 + s1;
         tmem_wait_store();
@@ -638,19 +679,22 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(buf));
       }
-      if (!ok) break;
       // ---- the tile's output ----
-      const uint32_t done = kTiles == 2 ? o_done(u) : o_done((n - 1) & 1);
-      if (!(ok = warp_wait(done, kTiles == 2 ? n_items & 1 : ((n - 1) >> 1) & 1))) break;
+      if (ok) {
+        const uint32_t done = kTiles == 2 ? o_done(u) : o_done((n - 1) & 1);
+        ok = warp_wait(done, kTiles == 2 ? n_items & 1 : ((n - 1) >> 1) & 1);
+      }
+      if (kHalves > 1 && any_of_row(!ok)) ok = false;
+      if (!ok) continue;                         // to the barrier behind which both leave
       ++n_items;
       tc_fence_after();
+      l = joined(l, [](float a, float b) { return a + b; });
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // NaN stays
-      // Where each row of the lane's eight goes (see below); none: not this call's.
       const long long none = -1;
       const long long my_row = mine ? ((long long)(w.row0 + tok) * A.Hq + w.h * A.G + gq) * kD : none;
       const bool has_odd = *odd != 0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kD; c0 += 64) {
+      for (int c0 = half * (kD / kHalves); c0 < (half + 1) * (kD / kHalves); c0 += 64) {
         uint32_t o[64];
         tmem_load(tl + S::kColO + u * kD + c0, o);
         if (__builtin_expect(has_odd, 0) && mine) {
