@@ -190,6 +190,9 @@ int attention(bool e4m3, const Pages* pages, const void* q, long long q_stride, 
   A.n_pages = pages ? pages->n_pages : 0;
   A.flags = pages ? reinterpret_cast<int*>(ws + pl.off_flags) : nullptr;
   A.n_flags = 0;                             // the launch knows
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (pages && cache_attn_by_few(A, D))
+    return launch_cache_attention_few(A, D, k_cache, stream) == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
   CUtensorMap tk, tv, tq;
   int block = cache_attn_block(D, cache_attn_rows(pl.group_pos * G)), seqs = B, rows = Lmax;
   if (pages) {
@@ -204,7 +207,6 @@ int attention(bool e4m3, const Pages* pages, const void* q, long long q_stride, 
     tq = tk;                                   // not read: the kernel converts the queries itself
   else if (!encode_queries(&tq, q, q_stride, B, n_new, Hq, G, D, pl.group_pos))
     return SPECDEC_ERR_CUDA;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   const cudaError_t e = pages ? launch_cache_attention_paged(A, D, tk, tv, tq, stream)
                         : e4m3 ? launch_cache_attention_kv8(A, D, tk, tv, tq, stream)
                                : launch_cache_attention_bf16(A, D, tk, tv, tq, stream);

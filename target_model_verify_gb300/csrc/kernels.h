@@ -300,6 +300,28 @@ struct Kv8AppendLaunch {
 };
 cudaError_t launch_kv8_append(const Kv8AppendLaunch& A, cudaStream_t stream);
 
+// The paged form for little work (cache_attention_few.cu): up to 16 query rows
+// per KV head, all (sequence, KV head) tiles at once, in clusters of up to
+// eight CTAs, and few enough chunks of 16 cache rows to a warp that the longest
+// sequence there may be, alone, ends before the other form would (measured
+// there). A distance bias or a cap makes a chunk cost half as much again.
+constexpr int kCacheAttnFewRows = 16;
+constexpr int cache_attn_few_warps(int D) { return D == 256 ? 4 : 8; }
+constexpr int cache_attn_few_slots(int D) { return (D == 64 ? 3 : 1) * kCacheAttnCtas; }   // CTAs that run at once
+inline int cache_attn_few_ctas(long long tiles, int D) {
+  const int slots = cache_attn_few_slots(D);
+  return tiles * 8 <= slots ? 8 : tiles * 4 <= slots ? 4 : tiles * 2 <= slots ? 2 : 1;
+}
+inline bool cache_attn_by_few(const CacheAttnLaunch& A, int D) {
+  const long long tiles = (long long)A.B * A.Hkv + 1;
+  if (A.n_new * A.G > kCacheAttnFewRows || tiles > cache_attn_few_slots(D)) return false;
+  const long long rows = A.window > 0 && A.window < A.Lmax - A.n_new ? (long long)A.window + A.n_new + 15 : A.Lmax;
+  const long long warps = (long long)cache_attn_few_ctas(tiles, D) * cache_attn_few_warps(D);
+  const int most = D == 256 ? 4 : A.cap > 0.f || A.slopes ? 5 : 8;
+  return (rows + 15) / 16 <= most * warps;
+}
+cudaError_t launch_cache_attention_few(const CacheAttnLaunch& A, int D, const void* k_pages, cudaStream_t stream);
+
 // log2 of a page's rows; -1 for sizes that are not offered.
 inline int page_log2(int page) {
   return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : page == 256 ? 8 : -1;

@@ -1,6 +1,7 @@
 """Attention over a paged bf16 cache (verify_attention_paged) on the GPU: against the fp64 oracle with the
-tolerances of tests/test_gpu_cache_attention.py (the arithmetic is the masked attention's), and, bit for
-bit, against the masked attention of the same rows laid end to end."""
+tolerances of tests/test_gpu_cache_attention.py (the arithmetic is the masked attention's), and, for more
+query rows than the form for little work takes, bit for bit against the masked attention of the same rows
+laid end to end."""
 import numpy as np
 import pytest
 import torch
@@ -63,7 +64,8 @@ def _run(q, pages, table, lens, **how):
     import target_model_verify_gb300 as tv
     out = _call(q, pages, table, lens, **how)
     flat = _flat(pages, table, lens, table.shape[1] * pages[0].shape[1])
-    assert torch.equal(out, tv.verify_attention_masked(q, *flat, lens, **how))
+    if q.shape[1] * q.shape[2] // pages[0].shape[2] > 16:
+        assert torch.equal(out, tv.verify_attention_masked(q, *flat, lens, **how))
     _check("masked", q, flat, lens, out, **how)
 
 
