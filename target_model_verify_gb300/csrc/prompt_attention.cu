@@ -98,7 +98,8 @@ struct PromptShape {
   static constexpr int kSlotBytes = kBlk * kD * 2;              // a block of K, or of V
   static constexpr int kQTile = 128 * kD * 2;
   static constexpr int kKeys = kBlk / kHalves;                  // of a block, to a softmax thread
-  static constexpr int kFixed = 1024 + kTiles * kQTile + 1024;
+  static constexpr int kStage = 32 * 128;                       // a softmax warp's rows, 64 columns of the output
+  static constexpr int kFixed = 1024 + kTiles * kQTile + kSoft * kStage + 1024;
   static constexpr int kRingMax = (kSmemLimit - kFixed) / kSlotBytes;
   static constexpr int kRing = kRingMax < 8 ? kRingMax : 8;     // blocks (K and V alike) in flight
   static constexpr int kSmem = kFixed + kRing * kSlotBytes;
@@ -107,6 +108,11 @@ struct PromptShape {
   static_assert(kColO + kTiles * kD <= 512, "tensor memory");
 };
 
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
 // A barrier that counts the threads with x.
 __device__ __forceinline__ int bar_count(int id, int nthreads, bool x) {
   uint32_t r;
@@ -118,6 +124,16 @@ __device__ __forceinline__ int bar_count(int id, int nthreads, bool x) {
       : "r"((uint32_t)x), "r"(id), "r"(nthreads)
       : "memory");
   return (int)r;
+}
+
+// capped() of two scores with one reciprocal, which takes as long as two
+// exponentials: 1 / a = b / (a b). The bound keeps the product finite; behind it
+// the tanh is 1 to 2^-59.
+__device__ __forceinline__ void capped2(float& x, float& y, float cap_exp, float cap_log2e, float plus_x, float plus_y) {
+  const float a = 1.f + ex2(min_or_nan(x * cap_exp, 60.f)), b = 1.f + ex2(min_or_nan(y * cap_exp, 60.f));
+  const float r = rcp(a * b) * (-2.f * cap_log2e);
+  x = fmaf(r, b, plus_x);
+  y = fmaf(r, a, plus_y);
 }
 
 // An item as its roles see it.
@@ -232,7 +248,8 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t qb = (raw + 1023u) & ~1023u;
   const uint32_t ring = qb + kTiles * S::kQTile;
-  const uint32_t bars = ring + kR * S::kSlotBytes;
+  const uint32_t stage = ring + kR * S::kSlotBytes;
+  const uint32_t bars = stage + kSoft * S::kStage;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   auto full = [&](int s) { return bar(s); };
   auto empty = [&](int s) { return bar(kR + s); };
@@ -598,7 +615,8 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           if (A.cap > 0.f) {
             const float cl = A.cap * kLog2e, ce = A.scale * A.cap_exp;
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k) x.f[k] = capped(x.f[k] * ce, cl, cl + fmaf(slope, (float)k, b0));
+            for (int k = 0; k < kKeys; k += 2)
+              capped2(x.f[k], x.f[k + 1], ce, cl, cl + fmaf(slope, (float)k, b0), cl + fmaf(slope, (float)(k + 1), b0));
           } else {
 #pragma unroll
             for (int k = 0; k < kKeys; ++k) x.f[k] = fmaf(x.f[k], c, fmaf(slope, (float)k, b0));
@@ -690,8 +708,10 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       tc_fence_after();
       l = joined(l, [](float a, float b) { return a + b; });
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // NaN stays
-      const long long none = -1;
-      const long long my_row = mine ? ((long long)(w.row0 + tok) * A.Hq + w.h * A.G + gq) * kD : none;
+      // where a lane's row goes, in 16-byte pieces from the tile's first row (P Hq rows' pieces are below 2^32)
+      const uint32_t my_row = (uint32_t)(((long long)tok_of_row * A.Hq + gq) * (kD / 8));
+      const uint32_t rows_mine = __ballot_sync(0xffffffffu, mine);
+      uint4* const out = reinterpret_cast<uint4*>(A.out) + ((size_t)(w.row0 + ta) * A.Hq + (size_t)w.h * A.G) * (kD / 8);
       const bool has_odd = *odd != 0;
 #pragma unroll 1
       for (int c0 = half * (kD / kHalves); c0 < (half + 1) * (kD / kHalves); c0 += 64) {
@@ -714,32 +734,25 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           }
         }
         __syncwarp();
-        // 16-byte pieces change places among eight lanes, so that a store
-        // writes 128 bytes of each of four rows: with a row to a lane, each
-        // touches 32 lines, and the two tiles' outputs took 5000 cycles.
-        uint32_t y[8][4];
-#pragma unroll
-        for (int k = 0; k < 64; k += 2)
-          y[k / 8][k / 2 % 4] = pack2<false>(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
-#pragma unroll
-        for (int b = 1; b < 8; b <<= 1) {
-          const bool upper = lane & b;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k & b) continue;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? y[k][x] : y[k | b][x], b);
-              y[k][x] = upper ? got : y[k][x];
-              y[k | b][x] = upper ? y[k | b][x] : got;
-            }
-          }
-        }
+        // Through shared memory, so that a store writes 128 bytes of each of four
+        // rows: with a row to a lane, each touches 32 lines, and the two tiles'
+        // outputs took 5000 cycles.
+        const uint32_t mine_at = stage + warp * S::kStage + lane * 128;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const long long to = __shfl_sync(0xffffffffu, my_row, (lane & 24) | k);
-          if (to != none)
-            *reinterpret_cast<uint4*>(A.out + to + c0 + (lane & 7) * 8) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+          uint32_t y[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            y[x] = pack2<false>(__uint_as_float(o[8 * k + 2 * x]) * inv, __uint_as_float(o[8 * k + 2 * x + 1]) * inv);
+          sts128(mine_at + ((k ^ (lane & 7)) << 4), y[0], y[1], y[2], y[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = k * 4 + (lane >> 3);
+          const uint4 y = lds128(stage + warp * S::kStage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          const uint32_t to = __shfl_sync(0xffffffffu, my_row, r);
+          if ((rows_mine >> r) & 1u) out[to + (uint32_t)(c0 / 8 + (lane & 7))] = y;
         }
         __syncwarp();                        // the next load is the whole warp's
       }
