@@ -109,19 +109,28 @@ def test_one_long_sequence_and_many_short_ones(page):
     _run(q, pages, table, lens)
 
 
-def test_pages_behind_the_window_may_be_gone():
+# 2 query heads per KV head: up to 8 new positions go to the form for little work, 9 to the other
+FORMS = pytest.mark.parametrize("n", [3, 9])
+
+
+@FORMS
+def test_pages_behind_the_window_may_be_gone(n):
     """What no position sees is not looked up: entries of pages given back hold anything."""
-    q, pages, table, lens = _inputs(3, 2, 3, 4, 2, 128, 16, 70, [1100, 600])
+    q, pages, table, lens = _inputs(3, 2, n, 4, 2, 128, 16, 70, [1100, 600])
     want = _call(q, pages, table, lens, window=100)
     gone = table.clone()
-    gone[0, :(1100 - 3 - 100 + 1) // 16] = -1
-    gone[1, :(600 - 3 - 100 + 1) // 16] = 1 << 30
+    gone[0, :(1100 - n - 100 + 1) // 16] = -1
+    gone[1, :(600 - n - 100 + 1) // 16] = 1 << 30
     assert torch.equal(_call(q, pages, gone, lens, window=100), want)
+    gone[1, (600 - n - 100 + 1) // 16] = -1
+    _call(q, pages, gone, lens, window=100, expect=op.INVALID)
 
 
-def test_pages_outside_the_pool_count_as_zeros():
+@FORMS
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_pages_outside_the_pool_count_as_zeros(n, D):
     for bad in (-1, 1 << 30, 2 ** 31 - 1, -2 ** 31):
-        q, pages, table, lens = _inputs(4, 2, 2, 4, 2, 64, 16, 20, [310, 200])
+        q, pages, table, lens = _inputs(4, 2, n, 4, 2, D, 16, 20, [310, 200])
         if bad == 1 << 30:
             bad = pages[0].shape[0]                      # the first that there is not
         table[0, 4] = table[1, 12] = table[0, 19] = bad
@@ -136,35 +145,39 @@ def test_pages_outside_the_pool_count_as_zeros():
         _call(q, pages, table, lens)
 
 
-def test_values_that_are_no_numbers():
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,Hq", [(4, 4), (4, 12)])           # 8 rows, 24 rows
+def test_values_that_are_no_numbers(n, Hq, D):
     """They reach the positions that see them and no others, found through the table."""
-    q, pages, table, lens = _inputs(5, 1, 4, 4, 2, 128, 16, 10, [150])
+    q, pages, table, lens = _inputs(5, 1, n, Hq, 2, D, 16, 10, [150])
     for row, col, x in ((147, 3, float("inf")), (148, 5, float("nan")), (149, 7, -float("inf"))):
         pages[1][table[0, row // 16], row % 16, 0, col] = x
     out = _f(_call(q, pages, table, lens))[0]
     for i in range(4):
         for row, col, x in ((147, 3, np.inf), (148, 5, np.nan), (149, 7, -np.inf)):
-            for h in range(2):
+            for h in range(Hq // 2):
                 got = out[i, h, col]
                 if row <= 146 + i:
                     assert np.isnan(got) if np.isnan(x) else got == x
                 else:
                     assert np.isfinite(got)
-            assert np.isfinite(out[i, 2:, col]).all()
+            assert np.isfinite(out[i, Hq // 2:, col]).all()
 
 
-def test_bad_lengths():
-    q, pages, table, lens = _inputs(6, 4, 2, 4, 2, 64, 16, 4, [64, 30, 20, 33])
+@FORMS
+def test_bad_lengths(n):
+    q, pages, table, lens = _inputs(6, 4, n, 4, 2, 64, 16, 4, [64, 30, 20, 33])
     good = _call(q, pages, table, lens)
-    out = _call(q, pages, table, _i([65, -1, 1, 33]), expect=op.INVALID)
+    out = _call(q, pages, table, _i([65, -1, n - 1, 33]), expect=op.INVALID)
     assert not out[:3].any() and torch.equal(out[3], good[3])
 
 
-def test_strided_queries_streams_and_graphs():
+@pytest.mark.parametrize("n", [2, 5])                        # 8 rows, 20 rows
+def test_strided_queries_streams_and_graphs(n):
     import target_model_verify_gb300 as tv
-    q, pages, table, lens = _inputs(7, 3, 2, 8, 2, 128, 32, 12, [300, 2, 77])
+    q, pages, table, lens = _inputs(7, 3, n, 8, 2, 128, 32, 12, [300, n, 77])
     want = _call(q, pages, table, lens)
-    wide = torch.randn(3, 2, 12, 128, device=DEV).to(torch.bfloat16)
+    wide = torch.randn(3, n, 12, 128, device=DEV).to(torch.bfloat16)
     wide[:, :, :8] = q
     assert torch.equal(_call(wide[:, :, :8], pages, table, lens), want)
     side = torch.cuda.Stream()
@@ -181,3 +194,75 @@ def test_strided_queries_streams_and_graphs():
         table.copy_(table.roll(1, 0))
         graph.replay()
         assert torch.equal(out, _call(q, pages, table, lens))
+
+
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,capacity,lens", [
+    (1, 1, 4, 1, 128, 8192, [8192]),             # eight CTAs, eight chunks a warp
+    (1, 16, 1, 1, 64, 8192, [8000]),             # sixteen positions of one head
+    (18, 1, 16, 8, 128, 1024, None),             # a CTA to a tile, the most tiles at once less a few
+    (9, 1, 16, 8, 128, 2048, None),              # two
+    (4, 1, 16, 8, 128, 4096, None),              # four
+    (50, 2, 18, 9, 64, 256, None),               # 64 dims: three CTAs to an SM
+    (2, 3, 10, 2, 256, 2048, [2048, 3]),
+    (37, 1, 4, 4, 256, 256, None),
+])
+@pytest.mark.parametrize("how", [{}, {"window": 77}, {"slopes": True, "softcap": 20.0}], ids=str)
+def test_little_work(B, n, Hq, Hkv, D, capacity, lens, how):
+    """The form for little work at each size of its clusters, up to the longest that it takes."""
+    how = dict(how)
+    if how.get("slopes"):
+        how["slopes"] = torch.exp2(-torch.arange(1, Hq + 1, device=DEV, dtype=torch.float32))
+    if lens is None:
+        lens = [n + 131 * b % (capacity - n) for b in range(B)]
+        lens[0] = capacity
+    q, pages, table, lens = _inputs(B + D, B, n, Hq, Hkv, D, 16, capacity // 16, lens)
+    _run(q, pages, table, lens, **how)
+
+
+@pytest.mark.parametrize("n,parent", [(1, False), (8, False), (26, True)])
+def test_small_trees_and_lengths(n, parent):
+    """Every length from the new positions' count on, across the first chunks' edges."""
+    lens = list(range(n, n + 36))
+    q, pages, table, lens = _inputs(8, len(lens), n, 2, 2, 128, 16, 5, lens)
+    _run(q, pages, table, lens, **({"parent": TREE26[:n]} if parent else {}))
+
+
+def test_a_small_tree_in_the_form_for_little_work():
+    for how in ({}, {"window": 3}, {"slopes": torch.tensor([0.5, 0.1], device=DEV)}):
+        q, pages, table, lens = _inputs(9, 4, 14, 2, 2, 128, 32, 5, [14, 31, 60, 137])
+        _run(q, pages, table, lens, parent=TREE26[:14], **how)
+
+
+def test_two_graphs_share_a_workspace():
+    """Steps of two layers, captured apart with one workspace, replayed in turn."""
+    import target_model_verify_gb300 as tv
+    graphs, outs, wants = [], [], []
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    for layer, n in ((0, 1), (1, 9)):
+        q, pages, table, lens = _inputs(20 + layer, 3, n, 8, 2, 128, 16, 40, [600, 77, 300])
+        wants.append(_call(q, pages, table, lens))
+        out, g = torch.zeros_like(q), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tv.verify_attention_paged(q, *pages, table, lens, out=out, workspace=ws)
+        graphs.append((g, q, pages, table, lens))
+        outs.append(out)
+    for _ in range(3):
+        for g, *_ in graphs:
+            g.replay()
+    assert tv.read_status(ws) == 0
+    for out, want in zip(outs, wants):
+        assert torch.equal(out, want)
+
+
+def test_two_calls_at_once():
+    """On streams of their own, each with its own workspace."""
+    import target_model_verify_gb300 as tv
+    calls = [_inputs(30, 2, n, 8, 2, 128, 16, 300, [4000, 900]) for n in (1, 1, 9, 9)]
+    want = [_call(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        outs = [tv.verify_attention_paged(c[0], *c[1], c[2], c[3], stream=s) for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)

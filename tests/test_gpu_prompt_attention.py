@@ -220,3 +220,44 @@ def test_graphs_streams_and_repeats(D):
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(other, out)
         _check(q, k, v, offsets, out)
+
+
+def test_two_graphs_share_a_workspace():
+    import target_model_verify_gb300 as tv
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for D, lens in ((128, [300, 77]), (256, [5, 140]), (64, [900])):
+        q, k, v, cu = _inputs(18, lens, 8, 2, D)
+        want = _call(q, k, v, cu)
+        out, g, offsets = torch.zeros_like(want), torch.cuda.CUDAGraph(), _i(cu)
+        with torch.cuda.graph(g):
+            tv.prompt_attention(q, k, v, offsets, out=out, workspace=ws)
+        graphs.append((g, out, want, (q, k, v, offsets)))
+    for _ in range(3):
+        for g, *_ in graphs:
+            g.replay()
+    assert tv.read_status(ws) == 0
+    for _, out, want, _ in graphs:
+        assert torch.equal(out, want)
+
+
+def test_two_calls_at_once():
+    """On streams of their own, each with its own workspace."""
+    import target_model_verify_gb300 as tv
+    calls = [_inputs(19 + x, lens, 8, 2, D) for x, (D, lens) in enumerate(((128, [2000]), (64, [300] * 5), (256, [700])))]
+    want = [_call(*c) for c in calls]
+    offsets = [_i(c[3]) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        outs = [tv.prompt_attention(*c[:3], cu, stream=s) for c, cu, s in zip(calls, offsets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+
+
+def test_many_short_sequences():
+    """More sequences than threads of the kernel that lists the work, empty ones among them."""
+    lens = [(7 * x) % 5 for x in range(3000)]
+    q, k, v, cu = _inputs(23, lens, 4, 2, 64)
+    _check(q, k, v, cu, _call(q, k, v, cu))
