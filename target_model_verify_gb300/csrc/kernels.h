@@ -275,7 +275,7 @@ struct PromptLaunch {
   const int32_t* cu_seqlens;         // [B + 1]
   const uint16_t* v;
   __nv_bfloat16* out;                // [T, Hq, D]
-  int4* items;                       // [max_items] (first row, first token, length)
+  int4* items;                       // [max_items] (first row, first token, length); null: no list
   int* n_items;
   int* next;                         // the next (item, KV head) nobody has taken
   int* status;

@@ -16,6 +16,8 @@
 // tiles (one for 256 dims) of a KV head and the blocks of keys they see. A
 // first kernel lists a head's items with the longest first; CTAs, one per SM,
 // take them off that list one by one, so that unequal prompts end together.
+// (Without a list where a CTA has two items at most, and few sequences: each
+// finds its own in the offsets.)
 //
 // CTA (up to 128 dims): warps 0-3 and 4-7 softmax of one tile each, then a
 // warp that loads, one for each tile that issues its products, and one that
@@ -323,7 +325,46 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
     if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
     if (warp == kLoad) {
       // ----------------------------------------------------------- loads --
-      const int total = *reinterpret_cast<const volatile int*>(A.n_items) * A.Hkv;     // < 2^31 (host)
+      // The items come from the list, or, where there is none, from the
+      // offsets themselves, in their order: a warp's running count of items.
+      const int span = kTiles * A.tile_tokens;
+      auto count_items = [&](int b) { return b < A.B ? (A.cu_seqlens[b + 1] - A.cu_seqlens[b] + span - 1) / span : 0; };
+      auto find_item = [&](int item) {
+        for (int b0 = 0, before = 0;; b0 += 32) {
+          const int mine = count_items(b0 + lane);
+          int run = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += x;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, item < before + run);
+          if (hit) {
+            const int l = __ffs(hit) - 1, t = item - before - __shfl_sync(0xffffffffu, run - mine, l);
+            const int row0 = A.cu_seqlens[b0 + l];
+            return make_int4(row0, t * span, A.cu_seqlens[b0 + l + 1] - row0, 0);
+          }
+          before += __shfl_sync(0xffffffffu, run, 31);
+        }
+      };
+      int total;                                                 // < 2^31 (host)
+      if (A.items) {
+        total = *reinterpret_cast<const volatile int*>(A.n_items) * A.Hkv;
+      } else {
+        bool broken = false;
+        int n_items = 0;
+        for (int b = lane; b < A.B; b += 32) {
+          const int lo = A.cu_seqlens[b], hi = A.cu_seqlens[b + 1];
+          broken |= lo < 0 || hi < lo || hi > A.T;
+        }
+        broken = __any_sync(0xffffffffu, broken);
+        if (!broken)
+          for (int b = lane; b < A.B; b += 32) n_items += count_items(b);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n_items += __shfl_xor_sync(0xffffffffu, n_items, o);
+        total = n_items * A.Hkv;
+        if (blockIdx.x == 0 && lane == 0) *A.status = broken ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
+      }
       int s = 0;
       uint32_t ph = 0, nq[2] = {0, 0};
       int next = blockIdx.x;
@@ -349,7 +390,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
         if (!(ok = warp_wait(heard(e), ((n_told >> 1) & 1) ^ 1u))) break;
         int4 it = make_int4(0, 0, 0, -1);
         if (next < total) {
-          it = __ldcg(A.items + next / A.Hkv);
+          it = A.items ? __ldcg(A.items + next / A.Hkv) : find_item(next / A.Hkv);
           it.w = next % A.Hkv;
         }
         if (lane == 0) {
@@ -359,7 +400,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
         __syncwarp();
         ++n_told;
         if (it.w < 0) break;
-        if (lane == 0) next = atomicAdd(A.next, 1);          // looked at an item later
+        if (lane == 0) next = A.items ? atomicAdd(A.next, 1) : next + (int)gridDim.x;      // looked at an item later
         Item<kD> w;
         w.set(A, it, it.w);
         load(w, false, w.first);
@@ -802,10 +843,12 @@ cudaError_t launch_prompt(const PromptLaunch& A, const CUtensorMap& tq, const CU
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
-  e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel<kD>, A, ctas);
-  if (e != cudaSuccess) return e;
+  if (A.items) {
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel<kD>, A, ctas);
+    if (e != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
