@@ -124,7 +124,7 @@ _native = None
 
 
 def native():
-    """The compiled module that marshals the cache operators (raises if it has not been built)."""
+    """The compiled module that marshals the cache and prompt operators (raises if it has not been built)."""
     global _native
     if _native is None:
         lib()

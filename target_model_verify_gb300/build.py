@@ -157,8 +157,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         except (ImportError, RuntimeError, OSError) as e:
             if os.path.exists(NATIVE_PATH):                # of older sources
                 os.remove(NATIVE_PATH)
-            sys.stderr.write(f"warning: _native.so was not built, append_kv8() and the cache attention "
-                             f"will raise from Python:\n{e}\n")
+            sys.stderr.write(f"warning: _native.so was not built, append_kv8(), the cache, paged and "
+                             f"prompt operators will raise from Python:\n{e}\n")
     return LIB_PATH
 
 

@@ -66,6 +66,11 @@
 //     shared-memory tile, since P needs f16's 11 bits and both operands share
 //     a type; bf16 values are used as they land, and P is bf16 for the same
 //     reason (the sum takes it as rounded, see below).
+//
+// Paged (bf16): the producers' lanes look up a block's pages, a block ahead, and
+// load one box each; nothing else knows of pages. One token over 64 x 4096 rows
+// in pages of 16: 165 us for 1074 MB, 0.96 of the copy peak; over 1 x 131072 in
+// pages of 64 83 us, 0.95.
 #pragma once
 
 #include <cuda_fp16.h>

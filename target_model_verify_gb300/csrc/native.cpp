@@ -1,4 +1,4 @@
-// Argument checks and marshalling of the cache operators for Python: the same
+// Argument checks and marshalling of the cache and prompt operators for Python: the same
 // C ABI as the ctypes binding, reached without its per-call cost (20 to 35 us
 // of interpreter time on a Grace core for a dozen tensors, against 3 to 10 us
 // of GPU time for a small batch's step; here about 3 us).

@@ -14,6 +14,10 @@
 // the map's old entries. Larger plans run as a cluster whose CTAs compute the
 // same sums and share the entries out: first the pages given back, then, behind
 // a barrier, the pages taken and the map, which reads those off the stack too.
+// Measured (graph replays): 3.5 us for a step's plan of 8 sequences x 5 rows
+// (7.4 with a trip and a barrier per phase), 19 us for 128k rows of 256 prompts
+// planned and given back (29 with one CTA for a call without a map and the map
+// behind the table's barrier).
 #include "kernels.h"
 
 namespace specdec {
