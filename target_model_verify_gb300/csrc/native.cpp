@@ -57,6 +57,15 @@ long long row_stride(const Tensor& t) {
   return sn;
 }
 
+// The same of packed rows t [T, H, D].
+long long packed_stride(const Tensor& t) {
+  const int64_t T = t.size(0), H = t.size(1), D = t.size(2);
+  const int64_t sn = T > 1 ? t.stride(0) : H * D;
+  check_value(!((t.stride(2) != 1 && D > 1) || (t.stride(1) != D && H > 1) || sn < H * D || sn % 8 != 0),
+              "the heads of a row must be contiguous, and rows a multiple of 8 elements apart");
+  return sn;
+}
+
 void check_ints(const Tensor& t, at::IntArrayRef shape, const char* type, const char* size) {
   check_type(t.scalar_type() == at::kInt && t.is_contiguous() && t.is_cuda(), type);
   check_value(t.sizes() == shape, size);
@@ -279,15 +288,17 @@ int append_paged(const Tensor& k_new, const Tensor& v_new, const Tensor& k_pages
   check_cache(k_pages, v_pages, at::kBFloat16, kPool);
   check_value(k_new.sizes() == v_new.sizes() && k_new.size(-2) == k_pages.size(2) && k_new.size(-1) == k_pages.size(3),
               "k_new and v_new must have one shape, and the heads of the cache [pages, page, Hkv, D]");
-  const Tensor k = k_new.dim() == 3 ? k_new.unsqueeze(0) : k_new, v = v_new.dim() == 3 ? v_new.unsqueeze(0) : v_new;
-  const int64_t B = k.size(0), n = k.size(1), Hkv = k.size(2), D = k.size(3);
+  const bool packed = k_new.dim() == 3;
+  const int64_t B = packed ? 1 : k_new.size(0), n = k_new.size(packed ? 0 : 1), Hkv = k_new.size(-2),
+                D = k_new.size(-1);
   const at::IntArrayRef lead = k_new.sizes().slice(0, k_new.dim() - 2);
   check_ints(slots, lead, "slots must be a contiguous int32 CUDA tensor", "slots must have one entry per new row");
   if (rows) check_ints(*rows, lead, "rows must be a contiguous int32 CUDA tensor", "rows must have one entry per slot");
   for (const Tensor* t : {&v_new, &k_pages, &v_pages, &slots}) same_device(k_new, *t);
   same_device(k_new, rows);
   same_device(k_new, workspace);
-  const long long ks = B && n ? row_stride(k) : Hkv * D, vs = B && n ? row_stride(v) : Hkv * D;
+  auto stride = [&](const Tensor& t) { return !B || !n ? Hkv * D : packed ? packed_stride(t) : row_stride(t); };
+  const long long ks = stride(k_new), vs = stride(v_new);
   const c10::cuda::CUDAGuard guard(k_new.device());
   c10::DataPtr own;
   size_t have;
@@ -321,8 +332,8 @@ std::pair<int, Tensor> prompt_attention(const Tensor& q, const Tensor& k, const 
   same_device(q, out_given);
   same_device(q, workspace);
   const int64_t B = cu_seqlens.size(0) - 1;
-  auto stride = [&](const Tensor& t) { return T ? row_stride(t.unsqueeze(0)) : t.size(1) * D; };
-  const long long qs = stride(q), ks = stride(k), vs = stride(v);
+  const long long qs = T ? packed_stride(q) : Hq * D, ks = T ? packed_stride(k) : Hkv * D,
+                  vs = T ? packed_stride(v) : Hkv * D;
   const c10::cuda::CUDAGuard guard(q.device());
   Tensor out;
   if (out_given) {

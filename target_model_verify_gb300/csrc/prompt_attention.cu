@@ -239,7 +239,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     *A.status = broken ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
   }
   __syncthreads();
-  if (!broken) each([&](int bucket, int4 it) { A.items[atomicAdd(place + bucket, 1)] = it; });
+  // (within the list, should the offsets have changed since they were counted)
+  if (!broken)
+    each([&](int bucket, int4 it) {
+      const int at = atomicAdd(place + bucket, 1);
+      const bool fits = it.x >= 0 && it.x <= A.T && it.z <= A.T - it.x;
+      if (at < A.max_items) A.items[at] = fits ? it : make_int4(0, 0, 0, 0);
+    });
 }
 
 template <int kD, bool kExtra>
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       const int span = kTiles * A.tile_tokens;
       auto count_items = [&](int b) { return b < A.B ? (A.cu_seqlens[b + 1] - A.cu_seqlens[b] + span - 1) / span : 0; };
       auto find_item = [&](int item) {
-        for (int b0 = 0, before = 0;; b0 += 32) {
+        for (int b0 = 0, before = 0; b0 < A.B; b0 += 32) {
           const int mine = count_items(b0 + lane);
           int run = mine;
 #pragma unroll
@@ -348,11 +354,13 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           const unsigned hit = __ballot_sync(0xffffffffu, item < before + run);
           if (hit) {
             const int l = __ffs(hit) - 1, t = item - before - __shfl_sync(0xffffffffu, run - mine, l);
-            const int row0 = A.cu_seqlens[b0 + l];
-            return make_int4(row0, t * span, A.cu_seqlens[b0 + l + 1] - row0, 0);
+            const int row0 = A.cu_seqlens[b0 + l], L = A.cu_seqlens[b0 + l + 1] - row0;
+            if (row0 < 0 || row0 > A.T || L > A.T - row0 || t * span >= L) break;
+            return make_int4(row0, t * span, L, 0);
           }
           before += __shfl_sync(0xffffffffu, run, 31);
         }
+        return make_int4(0, 0, 0, 0);          // the offsets have changed since they were counted: an empty item
       };
       int total;                                                 // < 2^31 (host)
       if (A.items) {

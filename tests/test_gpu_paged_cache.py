@@ -99,6 +99,29 @@ def test_what_is_given_back_serves_the_same_call():
     assert batch.gpu[3].item() == 0
 
 
+@pytest.mark.parametrize("B,page", [(300, 16), (1500, 16), (40, 32)])
+def test_a_cluster_gives_and_takes_at_once(B, page):
+    """Requests that shrink, end, stay, grow and begin, in one plan with a map of many rows."""
+    r = random.Random(B)
+    most = 6 * page
+    batch = Batch(B, 7, 4 * B, page)
+    lens = [r.randint(0, most) if b % 2 else 0 for b in range(B)]
+    while sum(-(-x // page) for x in lens) > 4 * B:
+        lens[r.randrange(B)] = 0
+    batch.plan([0] * B, lens)
+    for _ in range(3):
+        start = [r.choice((0, x, x // 2)) for x in lens]
+        counts = [r.choice((0, 1, r.randint(0, most - s))) for s in start]
+        cu = [0]
+        for c in counts:
+            cu.append(cu[-1] + c + r.randint(0, 1))
+        while sum(-(-(s + c) // page) for s, c in zip(start, counts)) > 4 * B:
+            b = r.randrange(B)
+            start[b] = counts[b] = 0
+        batch.plan(start, counts, cu_rows=cu, n_slots=cu[-1])
+        lens = [s + c for s, c in zip(start, counts)]
+
+
 def test_too_few_pages_change_nothing():
     batch = Batch(3, 8, 9, 16)
     batch.plan([0, 0, 0], [33, 40, 16], n=40)
