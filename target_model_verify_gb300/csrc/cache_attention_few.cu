@@ -45,6 +45,20 @@ struct FewShape {
   static_assert(kCacheAttnFewRows * kD * 4 <= kWarpBytes, "a warp's part of the output fits its ring");
 };
 
+// What the kernel needs of a call (CacheAttnLaunch's tree alone is 2 KB to hand over).
+struct FewLaunch {
+  int B, n_new, Hq, Hkv, G, Lmax, window, tree, max_depth, max_pages, page_log2, n_pages;
+  float scale, cap, cap_exp;
+  long long q_stride;
+  const __nv_bfloat16 *q, *k, *v;
+  const float* slopes;
+  const int32_t *seq_lens, *table;
+  __nv_bfloat16* out;
+  int* status;
+  uint16_t anc[kCacheAttnFewRows];   // bit a of entry i: new position i sees new position a
+  uint8_t depth[kCacheAttnFewRows];
+};
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
@@ -80,7 +94,7 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t a) {
 
 template <int kD, bool kExtra>
 __global__ void __launch_bounds__(FewShape<kD>::kThreads)
-    few_attn_kernel(const __grid_constant__ CacheAttnLaunch A, const __nv_bfloat16* __restrict__ k_pages, int ctas) {
+    few_attn_kernel(const __grid_constant__ FewLaunch A, int ctas) {
   using S = FewShape<kD>;
   constexpr int kRows = kCacheAttnFewRows, kWarps = S::kWarps, kThreads = S::kThreads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -155,13 +169,13 @@ __global__ void __launch_bounds__(FewShape<kD>::kThreads)
       constexpr int kStep = 32 / S::kPieces;                    // rows that the warp copies at a time
       const int r0 = lane / S::kPieces, c = lane % S::kPieces;
       const size_t at = ((row0 + r0) * A.Hkv + h) * kD + c * 8, step = (size_t)kStep * A.Hkv * kD;
-      const __nv_bfloat16 *ks = k_pages + at, *vs = static_cast<const __nv_bfloat16*>(A.v) + at;
+      const __nv_bfloat16 *ks = A.k + at, *vs = A.v + at;
 #pragma unroll
       for (int r = r0; r < kFewKeys + r0; r += kStep, ks += step, vs += step) {
         const bool take = good && j0 + r < L;                   // (else the address is not read)
         const uint32_t dst = to + r * S::kRowBytes + ((c ^ (r & 7)) << 4);
-        cp_async16(dst, take ? ks : k_pages, take);
-        cp_async16(dst + S::kChunk, take ? vs : k_pages, take);
+        cp_async16(dst, take ? ks : A.k, take);
+        cp_async16(dst + S::kChunk, take ? vs : A.v, take);
       }
     }
     cp_async_commit();
@@ -203,7 +217,7 @@ __global__ void __launch_bounds__(FewShape<kD>::kThreads)
     const int d = A.tree && a >= 0 ? A.depth[a] : a;           // where it stands, from the first new one
     if (A.window > 0 && (int)dep[x] - d >= A.window) return false;
     if (a < 0) return true;
-    return A.tree ? ((A.anc[i][a >> 5] >> (a & 31)) & 1u) != 0 : a <= i;
+    return A.tree ? ((A.anc[i] >> a) & 1u) != 0 : a <= i;
   };
   const int clean_hi = P0 + 1;         // chunks that end here or before, and begin at clean_lo or behind,
   const int clean_lo = A.window > 0 ? P0 + A.max_depth - A.window + 1 : 0;      // are seen whole by every row
@@ -393,7 +407,7 @@ __global__ void __launch_bounds__(FewShape<kD>::kThreads)
 }
 
 template <int kD, bool kExtra>
-cudaError_t launch_few(const CacheAttnLaunch& A, const void* k_pages, cudaStream_t stream) {
+cudaError_t launch_few(const FewLaunch& A, cudaStream_t stream) {
   using S = FewShape<kD>;
   static std::atomic<int> smem_set[64];
   int dev = 0;
@@ -419,22 +433,51 @@ cudaError_t launch_few(const CacheAttnLaunch& A, const void* k_pages, cudaStream
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, few_attn_kernel<kD, kExtra>, A, static_cast<const __nv_bfloat16*>(k_pages), ctas);
+  return cudaLaunchKernelEx(&cfg, few_attn_kernel<kD, kExtra>, A, ctas);
 }
 
 template <int kD>
-cudaError_t launch_few_dim(const CacheAttnLaunch& A, const void* k_pages, cudaStream_t stream) {
-  return A.cap > 0.f || A.slopes ? launch_few<kD, true>(A, k_pages, stream)
-                                 : launch_few<kD, false>(A, k_pages, stream);
+cudaError_t launch_few_dim(const FewLaunch& A, cudaStream_t stream) {
+  return A.cap > 0.f || A.slopes ? launch_few<kD, true>(A, stream) : launch_few<kD, false>(A, stream);
 }
 
 }  // namespace cache_attn
 
 cudaError_t launch_cache_attention_few(const CacheAttnLaunch& A, int D, const void* k_pages, cudaStream_t stream) {
+  cache_attn::FewLaunch F;
+  F.B = A.B;
+  F.n_new = A.n_new;
+  F.Hq = A.Hq;
+  F.Hkv = A.Hkv;
+  F.G = A.G;
+  F.Lmax = A.Lmax;
+  F.window = A.window;
+  F.tree = A.tree;
+  F.max_depth = A.max_depth;
+  F.max_pages = A.max_pages;
+  F.page_log2 = A.page_log2;
+  F.n_pages = A.n_pages;
+  F.scale = A.scale;
+  F.cap = A.cap;
+  F.cap_exp = A.cap_exp;
+  F.q_stride = A.q_stride;
+  F.q = A.q;
+  F.k = static_cast<const __nv_bfloat16*>(k_pages);
+  F.v = static_cast<const __nv_bfloat16*>(A.v);
+  F.slopes = A.slopes;
+  F.seq_lens = A.seq_lens;
+  F.table = A.table;
+  F.out = A.out;
+  F.status = A.status;
+  for (int i = 0; i < kCacheAttnFewRows; ++i) {
+    const bool node = A.tree && i < A.n_new;
+    F.anc[i] = node ? (uint16_t)A.anc[i][0] : 0;
+    F.depth[i] = node ? A.depth[i] : 0;
+  }
   switch (D) {
-    case 64: return cache_attn::launch_few_dim<64>(A, k_pages, stream);
-    case 128: return cache_attn::launch_few_dim<128>(A, k_pages, stream);
-    case 256: return cache_attn::launch_few_dim<256>(A, k_pages, stream);
+    case 64: return cache_attn::launch_few_dim<64>(F, stream);
+    case 128: return cache_attn::launch_few_dim<128>(F, stream);
+    case 256: return cache_attn::launch_few_dim<256>(F, stream);
   }
   return cudaErrorInvalidValue;
 }
