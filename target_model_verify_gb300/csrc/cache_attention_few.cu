@@ -116,18 +116,27 @@ __global__ void __launch_bounds__(FewShape<kD>::kThreads)
 
   if (tile == A.B * A.Hkv) {
     // ---- the last cluster alone looks through the call's tables and writes the status word ----
+    // (sequence, page) pairs dealt out over the threads, four at a time, so that
+    // many sequences take no longer than the attention
     int bad = 0;
-    for (int b = 0; b < A.B; ++b) {
-      const int L = A.seq_lens[b];
-      if (L == 0) continue;
-      if (L < A.n_new || L > A.Lmax) {
-        bad = 1;
-        continue;
+    const int per = A.window > 0 ? min(A.max_pages, (A.window + A.n_new + page - 1) / page + 1) : A.max_pages;
+    const int pairs = A.B * per, step = ctas * kThreads;
+    for (int e0 = rank * kThreads + threadIdx.x; e0 < pairs; e0 += 4 * step) {
+      int L[4], id[4], p[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = e0 + x * step, b = e / per;
+        L[x] = 0;
+        if (e >= pairs) continue;
+        L[x] = A.seq_lens[b];
+        p[x] = e - b * per + (A.window > 0 ? max(0, L[x] - A.n_new - A.window + 1) >> A.page_log2 : 0);
+        id[x] = p[x] < A.max_pages ? A.table[(size_t)b * A.max_pages + p[x]] : 0;
       }
-      const int low = A.window > 0 ? max(0, L - A.n_new - A.window + 1) : 0;
-      for (int p = (low >> A.page_log2) + rank * kThreads + threadIdx.x; p <= (L - 1) >> A.page_log2;
-           p += ctas * kThreads)
-        bad |= (unsigned)A.table[(size_t)b * A.max_pages + p] >= (unsigned)A.n_pages;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (L[x] != 0)
+          bad |= L[x] < A.n_new || L[x] > A.Lmax ||
+                 (p[x] <= (L[x] - 1) >> A.page_log2 && (unsigned)id[x] >= (unsigned)A.n_pages);
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) flag = bad;

@@ -4,9 +4,11 @@
 // Bound: HBM (8 bytes moved for a key and a value element), latency for a
 // step's few rows. A warp (or part of one, for short rows) copies one row of
 // K or of V in 16-byte pieces, four in flight to a lane, with the slot's load
-// beside the row's. Measured (8 KV heads of 128): 3.1 us for 256 x 5 rows (10.5
-// MB), 11.1 us for 20.5k rows of 16 prompts (84 MB, 7580 GB/s with the writes in
-// L2; 16.8 us, 5000 GB/s, from cold caches).
+// beside the row's. Measured (8 KV heads of 128, graph replays): 3.1 us for 256 x
+// 5 rows (10.5 MB), 8.2 us for 20.5k rows of 16 prompts (84 MB, which stay in L2;
+// 11.1 with the check of the map in the last CTA, which then began last, an entry
+// at a time), 60 us for 65k rows (537 MB, 8900 GB/s with a part in L2; 95); one
+// head of 64: 65k rows in 6.2 us (24).
 #include "kernels.h"
 
 namespace specdec {
@@ -19,18 +21,40 @@ template <int kLanes>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendLaunch A) {
   grid_launch_dependents();          // the next kernel may get ready, and wait for this one's end
   grid_dependency_wait();
-  if (blockIdx.x == gridDim.x - 1) {
-    // the last CTA alone checks the map of the call and writes the status word
+  if (blockIdx.x == 0) {
+    // The first CTA alone checks the map of the call and writes the status word:
+    // eight loads of four entries in flight to a thread, so that it keeps up with
+    // the copies of short rows.
     int bad = 0;
-    for (long long i = threadIdx.x; i < A.rows_total; i += kThreads) {
-      const int slot = A.slots[i];
-      if (slot < -1 || slot >= A.pool_rows || (slot >= 0 && A.rows && (unsigned)A.rows[i] >= (unsigned)A.n)) bad = 1;
+    const long long quads = !A.rows && ((uintptr_t)A.slots & 15u) == 0 ? A.rows_total / 4 : 0;
+    for (long long i0 = threadIdx.x; i0 < quads; i0 += 8 * kThreads) {
+      int4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = i0 + k * kThreads < quads ? reinterpret_cast<const int4*>(A.slots)[i0 + k * kThreads]
+                                         : make_int4(-1, -1, -1, -1);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        bad |= min(min(v[k].x, v[k].y), min(v[k].z, v[k].w)) < -1 ||
+               max(max(v[k].x, v[k].y), max(v[k].z, v[k].w)) >= A.pool_rows;
+    }
+    for (long long i0 = 4 * quads + threadIdx.x; i0 < A.rows_total; i0 += 8 * kThreads) {
+      int slot[8], row[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const long long i = i0 + k * kThreads;
+        slot[k] = i < A.rows_total ? A.slots[i] : -1;
+        row[k] = A.rows && i < A.rows_total ? A.rows[i] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        bad |= slot[k] < -1 || slot[k] >= A.pool_rows || (slot[k] >= 0 && (unsigned)row[k] >= (unsigned)A.n);
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *A.status = bad ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
     return;
   }
-  const long long item = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const long long item = (long long)(blockIdx.x - 1) * (kThreads / kLanes) + threadIdx.x / kLanes;
   const long long i = item >> 1;
   if (i >= A.rows_total) return;
   const int kv = (int)(item & 1), c0 = threadIdx.x % kLanes;
