@@ -137,7 +137,8 @@ __device__ __forceinline__ int bar_count(int id, int nthreads, bool x) {
 
 // capped() of two scores with one reciprocal, which takes as long as two
 // exponentials: 1 / a = b / (a b). The bound keeps the product finite; behind it
-// the tanh is 1 to 2^-59.
+// the tanh is 1 to 2^-59. A NaN in either is one in both, so both have to be
+// scores that the row sees, or numbers.
 __device__ __forceinline__ void capped2(float& x, float& y, float cap_exp, float cap_log2e, float plus_x, float plus_y) {
   const float a = 1.f + ex2(min_or_nan(x * cap_exp, 60.f)), b = 1.f + ex2(min_or_nan(y * cap_exp, 60.f));
   const float r = rcp(a * b) * (-2.f * cap_log2e);
@@ -664,12 +665,26 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           float f[kKeys];
         } x;
         tmem_load(tl + S::kColS + buf * kBlk + half * kKeys, x.u);
+        // Keys that the thread's row does not see, in a block that has some.
+        const bool masked = __builtin_expect(!w.clean(i), 0);
+        auto unseen = [&](float score) {
+          const int hi = tok - j0, lo = A.window > 0 ? hi - A.window + 1 : 0;     // it sees lo .. hi of its own
+#pragma unroll
+          for (int k0 = 0; k0 < kKeys; k0 += 32) {
+            const int a = lo - k0, b = hi - k0;
+            uint32_t m = b < 0 ? 0u : b >= 31 ? 0xffffffffu : (2u << b) - 1u;
+            if (a > 0) m &= a >= 32 ? 0u : 0xffffffffu << a;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x.f[k0 + k] = (m >> k) & 1u ? x.f[k0 + k] : score;
+          }
+        };
         float c = A.scale * kLog2e, top = -INFINITY;
         if constexpr (kExtra) {
           // cap and bias: the scores become exponents
           const float b0 = slope * (float)(j0 - tok);
           if (A.cap > 0.f) {
             const float cl = A.cap * kLog2e, ce = A.scale * A.cap_exp;
+            if (masked) unseen(0.f);             // a NaN there would reach the key that shares its reciprocal
 #pragma unroll
             for (int k = 0; k < kKeys; k += 2)
               capped2(x.f[k], x.f[k + 1], ce, cl, cl + fmaf(slope, (float)k, b0), cl + fmaf(slope, (float)(k + 1), b0));
@@ -679,17 +694,7 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           }
           c = 1.f;
         }
-        if (__builtin_expect(!w.clean(i), 0)) {
-          const int hi = tok - j0, lo = A.window > 0 ? hi - A.window + 1 : 0;     // keys lo .. hi of the thread's
-#pragma unroll
-          for (int k0 = 0; k0 < kKeys; k0 += 32) {
-            const int a = lo - k0, b = hi - k0;
-            uint32_t m = b < 0 ? 0u : b >= 31 ? 0xffffffffu : (2u << b) - 1u;
-            if (a > 0) m &= a >= 32 ? 0u : 0xffffffffu << a;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x.f[k0 + k] = (m >> k) & 1u ? x.f[k0 + k] : -INFINITY;
-          }
-        }
+        if (masked) unseen(-INFINITY);
 #pragma unroll
         for (int k = 0; k < kKeys; k += 32) top = fmaxf(top, largest<32>(x.f + k));
         top *= c;
