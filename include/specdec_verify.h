@@ -504,7 +504,9 @@ int specdec_verify_attention_paged(const void* q, long long q_stride, const void
  * statistics and outputs in fp32, the probabilities enter the value product
  * as bf16.
  * A cu_seqlens that is not ascending within 0 .. T sets
- * SPECDEC_ERR_INVALID_ARG in the status word and nothing is written; a
+ * SPECDEC_ERR_INVALID_ARG in the status word and nothing is written. It must
+ * not change during the call: outputs are unspecified then, though nothing
+ * outside the arguments is read or written, and the next call is as any. A
  * device-side wait that ran out sets SPECDEC_ERR_TIMEOUT, and no output is to
  * be used. Limits: D = 64, 128 or 256; Hq % Hkv == 0, Hq / Hkv <= 128, Hq <=
  * 2^20; T <= 2^30, T * Hq * D < 2^40, (T / (128 / (Hq / Hkv)) + B) * Hkv <

@@ -183,6 +183,15 @@ struct Item {
   __device__ __forceinline__ bool clean(int i) const { return i >= clean_lo && i < clean_hi; }
 };
 
+// The rows of a sequence, (first, length); a length of -1 where the offsets do
+// not fit. Each is read once where it is used: what was looked at is what counts,
+// should they change during the call.
+__device__ __forceinline__ int2 rows_of(const PromptLaunch& A, int b) {
+  const volatile int32_t* const cu = A.cu_seqlens + b;
+  const int lo = cu[0], hi = cu[1];
+  return lo < 0 || hi < lo || hi > A.T ? make_int2(0, -1) : make_int2(lo, hi - lo);
+}
+
 // The list of a head's items, longest first (equals in any order: no item's
 // outcome depends on another's), and the status word.
 template <int kD>
@@ -194,15 +203,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
   place[tid] = 0;
   grid_dependency_wait();
   bool broken = false;
-  for (int b = tid; b < A.B; b += kPlanThreads) {
-    const int lo = A.cu_seqlens[b], hi = A.cu_seqlens[b + 1];
-    broken |= lo < 0 || hi < lo || hi > A.T;
-  }
+  for (int b = tid; b < A.B; b += kPlanThreads) broken |= rows_of(A, b).y < 0;
   broken = __syncthreads_or(broken);
   const int span = S::kTiles * A.tile_tokens;
   auto each = [&](auto&& take) {
     for (int b = warp; b < A.B; b += kPlanThreads / 32) {
-      const int row0 = A.cu_seqlens[b], L = A.cu_seqlens[b + 1] - row0;
+      const int2 rows = rows_of(A, b);
+      const int row0 = rows.x, L = rows.y;
       for (int t0 = lane * span; t0 < L; t0 += 32 * span) {
         const int t_end = min(t0 + span, L) - 1;
         const int low = A.window > 0 ? max(0, t0 - A.window + 1) / S::kBlk : 0;
@@ -235,17 +242,17 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
   run += warp ? warp_sum[warp - 1] : 0;
   place[tid] = run - mine;
   if (tid == kPlanThreads - 1) {
-    *A.n_items = run;
+    *A.n_items = (int)(run < A.max_items ? run : A.max_items);
     *A.next = ctas;                  // every CTA begins with the item of its own number
     *A.status = broken ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
   }
   __syncthreads();
-  // (within the list, should the offsets have changed since they were counted)
+  // (within the list, should the offsets have changed since they were counted;
+  // entries that are not written then are looked at where they are taken)
   if (!broken)
     each([&](int bucket, int4 it) {
       const int at = atomicAdd(place + bucket, 1);
-      const bool fits = it.x >= 0 && it.x <= A.T && it.z <= A.T - it.x;
-      if (at < A.max_items) A.items[at] = fits ? it : make_int4(0, 0, 0, 0);
+      if (at < A.max_items) A.items[at] = it;
     });
 }
 
@@ -342,10 +349,11 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
       // The items come from the list, or, where there is none, from the
       // offsets themselves, in their order: a warp's running count of items.
       const int span = kTiles * A.tile_tokens;
-      auto count_items = [&](int b) { return b < A.B ? (A.cu_seqlens[b + 1] - A.cu_seqlens[b] + span - 1) / span : 0; };
+      auto count_items = [&](int2 rows) { return (max(rows.y, 0) + span - 1) / span; };
       auto find_item = [&](int item) {
         for (int b0 = 0, before = 0; b0 < A.B; b0 += 32) {
-          const int mine = count_items(b0 + lane);
+          const int2 rows = b0 + lane < A.B ? rows_of(A, b0 + lane) : make_int2(0, 0);
+          const int mine = count_items(rows);
           int run = mine;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -355,13 +363,16 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
           const unsigned hit = __ballot_sync(0xffffffffu, item < before + run);
           if (hit) {
             const int l = __ffs(hit) - 1, t = item - before - __shfl_sync(0xffffffffu, run - mine, l);
-            const int row0 = A.cu_seqlens[b0 + l], L = A.cu_seqlens[b0 + l + 1] - row0;
-            if (row0 < 0 || row0 > A.T || L > A.T - row0 || t * span >= L) break;
-            return make_int4(row0, t * span, L, 0);
+            return make_int4(__shfl_sync(0xffffffffu, rows.x, l), t * span, __shfl_sync(0xffffffffu, rows.y, l), 0);
           }
           before += __shfl_sync(0xffffffffu, run, 31);
         }
-        return make_int4(0, 0, 0, 0);          // the offsets have changed since they were counted: an empty item
+        return make_int4(0, 0, 0, 0);          // the offsets have changed since they were counted
+      };
+      // Rows of the batch and a token among them: not so only where the offsets
+      // have changed since the items were counted. Such an item is nobody's.
+      auto lies = [&](int4 it) {
+        return it.x >= 0 && it.x <= A.T && it.z <= A.T - it.x && it.y >= 0 && it.y < it.z;
       };
       int total;                                                 // < 2^31 (host)
       if (A.items) {
@@ -370,15 +381,14 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
         bool broken = false;
         int n_items = 0;
         for (int b = lane; b < A.B; b += 32) {
-          const int lo = A.cu_seqlens[b], hi = A.cu_seqlens[b + 1];
-          broken |= lo < 0 || hi < lo || hi > A.T;
+          const int2 rows = rows_of(A, b);
+          broken |= rows.y < 0;
+          n_items += count_items(rows);
         }
         broken = __any_sync(0xffffffffu, broken);
-        if (!broken)
-          for (int b = lane; b < A.B; b += 32) n_items += count_items(b);
 #pragma unroll
         for (int o = 16; o; o >>= 1) n_items += __shfl_xor_sync(0xffffffffu, n_items, o);
-        total = n_items * A.Hkv;
+        total = broken ? 0 : (int)(n_items < A.max_items ? n_items : A.max_items) * A.Hkv;
         if (blockIdx.x == 0 && lane == 0) *A.status = broken ? SPECDEC_ERR_INVALID_ARG : SPECDEC_OK;
       }
       int s = 0;
@@ -405,9 +415,13 @@ __global__ void __launch_bounds__(PromptShape<kD>::kThreads, 1)
         const int e = n_told & 1;
         if (!(ok = warp_wait(heard(e), ((n_told >> 1) & 1) ^ 1u))) break;
         int4 it = make_int4(0, 0, 0, -1);
-        if (next < total) {
+        while (next < total) {
           it = A.items ? __ldcg(A.items + next / A.Hkv) : find_item(next / A.Hkv);
           it.w = next % A.Hkv;
+          if (__builtin_expect(lies(it), 1)) break;
+          it.w = -1;
+          if (lane == 0) next = A.items ? atomicAdd(A.next, 1) : next + (int)gridDim.x;
+          next = __shfl_sync(0xffffffffu, next, 0);
         }
         if (lane == 0) {
           sts128(board + 16 * e, it.x, it.y, it.z, it.w);
