@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) page_plan_kernel(const __grid_con
       chunks([&](int b0, int rank) {
         const int lane = tid & 31, warps = all / 32;
         for (int s = me / 32; s < min(kThreads, A.B - b0); s += warps)
-          for (int t = C.begin[s] + lane; t < C.end[s]; t += 32) {
-            const int row = C.start[s] + t - C.begin[s];
+          for (long long t = C.begin[s] + (long long)lane; t < C.end[s]; t += 32) {      // (past 2^31 at the last step)
+            const int row = C.start[s] + (int)(t - C.begin[s]);
             A.slots[t] = slot_of(page_at(b0, rank, s, row >> A.page_log2), row);
           }
         return C.take_upto[kThreads - 1];
