@@ -418,10 +418,12 @@ int specdec_verify_attention_masked(const void* q, long long q_stride, const voi
  * (negative, past max_pages * page, more rows than the map has room for) is
  * left as it is, its rows of the map are -1, and the status word gets
  * SPECDEC_ERR_INVALID_ARG; so does a row of the map whose table entry is not
- * a page (-1 there). A cu_rows that is not ascending within 0 .. n_slots, or a
- * stack that could not hold what is given back, sets it too: nothing changes
- * then, and the map is -1 throughout. Limits: page = 16, 32, 64, 128 or 256; max_pages * page
- * and n_pages * page <= 2^30; n_slots < 2^31 - 4. B = 0 with a map fills it
+ * a page (-1 there), and an entry outside the pool among those given back or
+ * taken (it changes hands as a page would). Pages that stand in two places are
+ * not found. A cu_rows that is not ascending within 0 .. n_slots, or a stack
+ * that could not hold what is given back, sets it too: nothing changes then,
+ * and the map is -1 throughout. Limits: page = 16, 32, 64, 128 or 256;
+ * max_pages * page and n_pages * page <= 2^30; n_slots < 2^31 - 4. B = 0 with a map fills it
  * with -1. The tensors must not overlap. Asynchronous; the workspace holds
  * the status word only.
  */

@@ -43,12 +43,16 @@ def plan(table, held, free, n_free, start, counts, page, n=None, cu_rows=None, n
     if len(more) > n_free + len(back):
         return table, held, free, n_free, slots if mapped else None, NO_PAGES
     for b, x in back:
+        if not 0 <= table[b][x] < n_pages:
+            status = INVALID
         free[n_free] = table[b][x]
         table[b][x] = -1
         n_free += 1
     for b, x in more:
         n_free -= 1
         table[b][x] = free[n_free]
+        if not 0 <= table[b][x] < n_pages:
+            status = INVALID
     held = want
     if mapped:
         for b in range(B):

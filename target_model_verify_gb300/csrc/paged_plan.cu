@@ -163,6 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_plan_kernel(const __grid_con
     return entry(b0, s, C.have[s] + m - (s ? C.take_upto[s - 1] : 0));
   };
   bool odd = false;
+  auto moved = [&](int id) {               // a page that changes hands
+    odd |= (unsigned)id >= (unsigned)A.n_pages;
+    return id;
+  };
   auto slot_of = [&](int id, int row) {
     if ((unsigned)id < (unsigned)A.n_pages) return (id << A.page_log2) + (row & mask);
     odd = true;
@@ -221,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) page_plan_kernel(const __grid_con
     __syncthreads();
     if (from) {
       *from = -1;
-      A.free_pages[n_free + tid] = given_id;
+      A.free_pages[n_free + tid] = moved(given_id);
     }
-    if (to) *to = taken_id;
+    if (to) *to = moved(taken_id);
     if (enough && tid < A.B && C.want[tid] != C.have[tid]) A.held[tid] = C.want[tid];
     if (tid == 0 && (give || take)) *A.n_free = top - take;
     if (4 * tid < n_slots) {
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_plan_kernel(const __grid_con
       const int here = C.give_upto[kThreads - 1];
       for (int m = me; m < here; m += all) {
         int32_t* const from = given(b0, m);
-        A.free_pages[n_free + rank + m] = __ldcg(from);
+        A.free_pages[n_free + rank + m] = moved(__ldcg(from));
         *from = -1;
       }
       return here;
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_plan_kernel(const __grid_con
   if (take > 0)
     chunks([&](int b0, int rank) {
       const int here = C.take_upto[kThreads - 1];
-      for (int m = me; m < here; m += all) *taken(b0, m) = __ldcg(A.free_pages + top - 1 - rank - m);
+      for (int m = me; m < here; m += all) *taken(b0, m) = moved(__ldcg(A.free_pages + top - 1 - rank - m));
       return here;
     });
   // ---- the map: pages that were there from the table, others from the stack as well ----

@@ -1,8 +1,11 @@
 """Plans of a paged cache at the ends of what they take, and of tables that hold what they should not."""
+import random
+
 import pytest
 import torch
 
-from tests.test_gpu_paged_cache import _i
+from oracle import paged as op
+from tests.test_gpu_paged_cache import Batch, _i
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -31,3 +34,37 @@ def test_the_largest_map(B):
     for part in slots[2:-3].split(1 << 28):
         assert (part == -1).all()
     assert tables[1].tolist() == [2] + [1] * (B - 2) + [2]
+
+
+@pytest.mark.parametrize("max_pages", [8, 9000])              # one CTA, and a cluster
+@pytest.mark.parametrize("entry", [-1, 40, 2 ** 31 - 1])
+def test_entries_that_are_no_pages_are_told(entry, max_pages):
+    """They go onto the stack and off it again as pages would; the status word says so each time, with a map
+    and without, and not of a plan that moves others."""
+    batch = Batch(3, max_pages, 40, 16)
+    batch.plan([0, 0, 0], [40, 30, 50])
+    batch.gpu[0][1, 1] = entry
+    batch.load()
+    batch.plan([40, 0, 50], [20, 20, 0], n=20, expect=op.INVALID)      # a row on it
+    batch.plan([60, 0, 50], [0, 32, 0], n=32, expect=op.INVALID)
+    batch.plan([0, 0, 50], [35, 20, 0])                                # it stays where it is
+    batch.plan([0, 0, 50], [35, 16, 0], expect=op.INVALID)             # given back
+    batch.plan([35, 16, 50], [0, 0, 16], expect=op.INVALID)            # taken again
+    batch.plan([35, 16, 0], [0, 0, 66])                                # it stays there
+    batch.plan([0, 0, 0], [0, 0, 0], expect=op.INVALID)
+
+
+def test_two_pools_hold_all_their_pages_after_many_plans():
+    """Steps and admissions of two batches in turn: no page is lost, and none is in two places."""
+    r = random.Random(3)
+    batches = [Batch(B, 40, pages, 16) for B, pages in ((5, 100), (300, 2000))]
+    for step in range(60):
+        for batch in batches:
+            B, pages = batch.gpu[0].shape[0], batch.gpu[2].shape[0]
+            lens = [r.randint(0, 400) if r.random() < 0.6 else 0 for _ in range(B)]
+            while sum(-(-x // 16) for x in lens) > pages:
+                lens[r.randrange(B)] = 0
+            batch.plan([0] * B, lens, **({} if step % 3 else {"n": 400}))
+            table, held, free, n_free = batch.host
+            there = [p for row, h in zip(table, held) for p in row[:h]] + free[:n_free]
+            assert sorted(there) == list(range(pages))
