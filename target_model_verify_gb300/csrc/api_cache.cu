@@ -171,7 +171,7 @@ int attention(bool e4m3, const Pages* pages, const void* q, long long q_stride, 
   A.n_scale = (Lmax + SPECDEC_KV8_BLOCK - 1) / SPECDEC_KV8_BLOCK;
   A.scale = scale > 0.f ? scale : 1.f / std::sqrt((float)D);
   A.cap = softcap;
-  A.cap_exp = softcap > 0.f ? 2.f * kLog2e / softcap : 0.f;
+  A.cap_exp = cap_factor(softcap, A.scale);
   A.q_stride = q_stride;
   A.q = static_cast<const __nv_bfloat16*>(q);
   A.v = v_cache;

@@ -99,7 +99,7 @@ int specdec_prompt_attention(const void* q, long long q_stride, const void* k, l
   A.v_stride = v_stride;
   A.scale = scale > 0.f ? scale : 1.f / std::sqrt((float)D);
   A.cap = softcap;
-  A.cap_exp = softcap > 0.f ? 2.f * kLog2e / softcap : 0.f;
+  A.cap_exp = cap_factor(softcap, A.scale);
   A.slopes = slopes;
   A.cu_seqlens = cu_seqlens;
   A.v = static_cast<const uint16_t*>(v);

@@ -187,6 +187,15 @@ cudaError_t launch_attention(const AttnLaunch& A, const CUtensorMap& tmap_k,
 int attn_n_stages(int B, int n_new, int Hq, int Hkv);
 int attn_smem_bytes(int n_mt, int n_stages);
 
+// 2 log2(e) / cap: the exponent of a capped score's tanh is this times the scale
+// times q . k. That product of the two stays a number, so that a score of 0 stays
+// 0; where it would not, the cap is below 1e-8, and what is lost of it nothing.
+inline float cap_factor(float cap, float scale) {
+  if (!(cap > 0.f)) return 0.f;
+  const float f = 2.f * kLog2e / cap, most = 3e38f / scale;
+  return f < most ? f : most;
+}
+
 // Verify-step attention with caps, biases, windows and token trees, over a
 // bf16 or an e4m3 cache (cache_attention.cuh).
 constexpr int kCacheAttnCtas = 152;       // CTAs at most: one per SM of a 152-SM part,
@@ -200,7 +209,7 @@ struct CacheAttnLaunch {
   int n_scale;                       // scales per (sequence, KV head)
   int head_lanes;                    // CTAs beside each other on a part: Hkv, or 1
   int note_tiles;                    // a note per tile (this many), or 0: per CTA
-  float scale, cap, cap_exp;         // cap_exp = 2 log2(e) / cap
+  float scale, cap, cap_exp;         // cap_factor()
   long long q_stride;                // elements from one position's queries to the next's
   const __nv_bfloat16* q;            // [B, n_new, Hq, D]
   const void* v;                     // the value cache
@@ -270,7 +279,7 @@ struct PromptLaunch {
   int window, cost_shift;            // the list's order is by blocks >> cost_shift
   long long max_items;               // of a KV head, at most
   long long v_stride;                // elements from one token's values to the next's
-  float scale, cap, cap_exp;
+  float scale, cap, cap_exp;         // cap_factor()
   const float* slopes;               // [Hq] or null
   const int32_t* cu_seqlens;         // [B + 1]
   const uint16_t* v;
