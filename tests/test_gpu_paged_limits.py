@@ -68,3 +68,26 @@ def test_two_pools_hold_all_their_pages_after_many_plans():
             table, held, free, n_free = batch.host
             there = [p for row, h in zip(table, held) for p in row[:h]] + free[:n_free]
             assert sorted(there) == list(range(pages))
+
+
+@pytest.mark.parametrize("at", [1, 2, 3])
+@pytest.mark.parametrize("B,n", [(3, 5), (40, 130)])          # one CTA, and a cluster
+def test_maps_at_any_entry(at, B, n):
+    """A map that does not begin on 16 bytes is filled, and read, as any; what is around it stays."""
+    import target_model_verify_gb300 as tv
+    batch = Batch(B, 12, 10 * B, 16)
+    big = torch.full((B * n + 8,), 77, dtype=torch.int32, device=DEV)
+    slots = big[at:at + B * n].view(B, n)
+    counts = [n - b % 3 for b in range(B)]
+    *_, want, status = op.plan(*batch.host, [7] * B, counts, 16, n)
+    tv.plan_pages(*batch.gpu, _i([7] * B), _i(counts), 16, slots=slots, workspace=batch.ws)
+    assert tv.read_status(batch.ws) == status == op.OK
+    assert slots.flatten().tolist() == want
+    assert (big[:at] == 77).all() and (big[at + B * n:] == 77).all()
+    new = [torch.randn(B, n, 2, 64, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    pool = tv.alloc_paged_cache(10 * B, 16, 2, 64, device=DEV)
+    tv.append_paged(*new, *pool, slots, workspace=batch.ws)
+    assert tv.read_status(batch.ws) == op.OK
+    live = slots.flatten() >= 0
+    for t, x in zip(pool, new):
+        assert torch.equal(t.view(-1, 2, 64)[slots.flatten()[live].long()], x.view(-1, 2, 64)[live])
