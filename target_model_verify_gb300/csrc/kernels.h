@@ -313,7 +313,10 @@ cudaError_t launch_kv8_append(const Kv8AppendLaunch& A, cudaStream_t stream);
 // per KV head, all (sequence, KV head) tiles at once, in clusters of up to
 // eight CTAs, and few enough chunks of 16 cache rows to a warp that the longest
 // sequence there may be, alone, ends before the other form would (measured
-// there). A distance bias or a cap makes a chunk cost half as much again.
+// there). How long that is the host knows from the table's width only: one
+// sequence of 517 rows takes 5.6 us under a table of up to 8192 rows (8 KV heads
+// of 128), and 11.2 in the other form under a wider one. A distance bias or a
+// cap makes a chunk cost half as much again.
 constexpr int kCacheAttnFewRows = 16;
 constexpr int cache_attn_few_warps(int D) { return D == 256 ? 4 : 8; }
 constexpr int cache_attn_few_slots(int D) { return (D == 64 ? 3 : 1) * kCacheAttnCtas; }   // CTAs that run at once

@@ -5,7 +5,7 @@
 // step's few rows. A warp (or part of one, for short rows) copies one row of
 // K or of V in 16-byte pieces, four in flight to a lane, with the slot's load
 // beside the row's. Measured (8 KV heads of 128, graph replays): 3.1 us for 256 x
-// 5 rows (10.5 MB), 8.2 us for 20.5k rows of 16 prompts (84 MB, which stay in L2;
+// 5 rows (10.5 MB), 8.2 us for 10.3k rows of 16 prompts (84 MB, which stay in L2;
 // 11.1 with the check of the map in the last CTA, which then began last, an entry
 // at a time), 60 us for 65k rows (537 MB, 8900 GB/s with a part in L2; 95); one
 // head of 64: 65k rows in 6.2 us (24).

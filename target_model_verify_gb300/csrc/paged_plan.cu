@@ -17,7 +17,8 @@
 // Measured (graph replays): 3.5 us for a step's plan of 8 sequences x 5 rows
 // (7.4 with a trip and a barrier per phase), 19 us for 128k rows of 256 prompts
 // planned and given back (29 with one CTA for a call without a map and the map
-// behind the table's barrier).
+// behind the table's barrier). A step's call without a map, 8 sequences: 1.7 us,
+// and 3.7 as a cluster, which it becomes with more than 16,384 table entries.
 #include "kernels.h"
 
 namespace specdec {

@@ -8,10 +8,10 @@
 //
 // Bound: the tensor cores (4 D operations per visible pair and query head), and,
 // as long beside them, the exponentials. Measured (32 query / 8 KV heads of 128,
-// graph replays): one prompt of 8192 tokens 350 us, 1570 TFLOP/s, 0.80 of the
-// measured bf16 rate; 24 ragged prompts of up to 2500 tokens 143 us (1100); 64
+// graph replays): one prompt of 8192 tokens 350 us, 1570 TFLOP/s, 0.82 of the
+// measured bf16 rate; 24 ragged prompts of up to 2500 tokens 143 to 149 us (1080); 64
 // dims, 8192 tokens 292 us (942); 256 dims (8 / 4 heads) 190 us (1440), 2 x 4001
-// tokens of it with a window of 1024 and a cap 77 us (758). A block of 128 keys
+// tokens of it with a window of 1024 and a cap 80 us (730). A block of 128 keys
 // takes 2740 cycles for the two tiles: each one's products 1180 (16 MMAs of 64
 // cycles, and the change between the two kinds), the hand-over of the turn 190,
 // each one's softmax 1180 beside the other's products.
